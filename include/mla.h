@@ -184,6 +184,132 @@ mla_status mla_cache_append(const void* c_new, void* kv_cache, float* kv_scale,
                             int num_pages, mla_dtype kv_dtype, void* stream);
 
 /*
+ * Position rotation, where an entry point takes `rope_turns` [d_rope / 2] uint64: pair i of a rope
+ * part at position p is turned by p * rope_turns[i] * 2^-64 turns (mod 1, exactly, for any int32 p),
+ * so rope_turns[i] = round(inv_freq_i / (2 pi) * 2^64) mod 2^64.  interleaved != 0: pair i is
+ * columns (2i, 2i + 1); otherwise (i, i + d_rope / 2).  (x, y) becomes
+ * (x cos - y sin, y cos + x sin).
+ *
+ * RMS norm, where an entry point takes a norm weight w: y = w x / sqrt(mean(x^2) + eps).  Sums,
+ * norms and rotations are computed in fp32 and rounded once to the stored type.
+ */
+
+/*
+ * mla_rope_append -- mla_cache_append of raw rows: the latent's RMS norm and the rope key's
+ * rotation are applied on the way into the cache.
+ *
+ *   c_new       q_len rows for each of B sequences, d_latent + d_rope bf16 each, c_stride
+ *               elements from one row to the next (>= d_latent + d_rope, a multiple of 8): the
+ *               projection's output, its rope part not yet rotated
+ *   norm_weight [d_latent] bf16, or NULL: the latent part is stored as it is
+ *   positions   [B, q_len] int32, or NULL -- the position a row's rope part is rotated to; NULL
+ *               takes the row's place in its sequence.  (Tokens of a drafted tree sit at their
+ *               depth, not at their place.)
+ *   new_lens    [B] int32, or NULL (q_len for every sequence) -- n_b, the new tokens of sequence
+ *               b: row t < n_b goes to place L_b - n_b + t, rows t >= n_b are padding and are not
+ *               written.  n_b <= 0 writes nothing; n_b > q_len is reported through
+ *               MLA_ERR_DEVICE_CHECK and writes nothing.
+ * kv_cache, kv_scale, page_table, cache_lens, the e4m3 quantisation (of the fp32 row: no rounding
+ * to bf16 in between; a NaN stays NaN), the treatment of places below 0 and of bad pages, and the
+ * supported sizes are those of mla_cache_append.  No two rows of a call may name the same place
+ * of the cache.
+ */
+mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm_weight, float eps,
+                           const int* positions, const void* rope_turns, int interleaved,
+                           void* kv_cache, float* kv_scale, const int* page_table,
+                           const int* cache_lens, const int* new_lens, int B, int q_len,
+                           int d_latent, int d_rope, int page_size, int max_pages_per_seq,
+                           int num_pages, mla_dtype kv_dtype, void* stream);
+
+/*
+ * mla_decode_tree -- mla_decode for a tree of drafted tokens: the q_len new tokens of a sequence
+ * are nodes of a tree (several drafted continuations of its prefix) instead of one chain.
+ *
+ *   tree_mask   bit words, uint32 [B, q_len, ceil(q_len / 32)] (or one [q_len, ceil(q_len / 32)]
+ *               for the whole batch): bit j % 32 of word j / 32 of row t says whether token t sees
+ *               drafted token j (its ancestors and itself, usually; no bit is implied)
+ *   tree_mask_stride  words from one sequence's mask to the next; 0 for one mask for all
+ *   new_lens    [B] int32, or NULL (q_len for every sequence) -- n_b, the drafted tokens of
+ *               sequence b, clamped to 0 .. q_len.  They occupy places L_b - n_b .. L_b - 1 of the
+ *               cache (mla_rope_append writes them there); rows t >= n_b are padding: O = 0,
+ *               LSE = -inf.
+ * Token t < n_b sees every key of the prefix, 0 .. L_b - n_b - 1, and the drafted keys its bits
+ * name.  A row that sees no key gets O = 0 and LSE = -inf.  A drafted key whose cached row (or
+ * scale) is not finite makes the rows that see it NaN and leaves the others alone.
+ * Everything else -- layouts, cache types, lengths, bad pages, out, lse, the workspace
+ * (mla_decode_workspace_size) and the limits -- is as for mla_decode, with num_pages * page_size
+ * and B * q_len * H below 2^31.
+ */
+mla_status mla_decode_tree(const void* q_latent, const void* q_rope, const void* kv_cache,
+                           const float* kv_scale, const int* page_table, const int* cache_lens,
+                           const void* tree_mask, int64_t tree_mask_stride, const int* new_lens,
+                           void* out, float* lse, int B, int H, int q_len, int d_latent,
+                           int d_rope, int page_size, int max_pages_per_seq, int num_pages,
+                           float softmax_scale, mla_dtype kv_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * mla_qk_norm_rope -- RMS norms of queries and keys for each head with the position rotation in
+ * the same pass: the step between the projections and mla_prefill (or, queries only, mla_absorb
+ * and mla_decode).  It also splits q into the two parts those take.
+ *
+ *   q       `rows` tokens of H heads of d_nope + d_rope bf16 (nope part first); q_row_stride and
+ *           q_head_stride elements from one token / head to the next
+ *   k_nope  `rows` x H x d_nope bf16, with strides of its own (e.g. the key half of a joint key and
+ *           value projection);  k_rope  `rows` x d_rope bf16, one shared rope key per token
+ *           Each of q, k_nope, k_rope may be NULL (then so are its weights; its outputs are not
+ *           written).  Strides are multiples of 8 elements, >= 0 (0 repeats an operand).
+ *   q_nope_weight, k_nope_weight [d_nope] bf16, q_rope_weight, k_rope_weight [d_rope] bf16 -- the
+ *           nope and the rope part of a head are normalised separately, each by its weight; NULL:
+ *           that part is not normalised
+ *   positions [rows] int32
+ *   q_nope_out [rows, H, d_nope], q_rope_out [rows, H, d_rope], k_nope_out [rows, H, d_nope],
+ *   k_rope_out [rows, d_rope] bf16, contiguous; they must not overlap the inputs
+ * Supported: d_nope = 128, d_rope = 64, H <= 65535, rows * ceil(H / 4) <= 0x70000000.
+ */
+mla_status mla_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* k_nope, int64_t k_nope_row_stride,
+                            int64_t k_nope_head_stride, const void* k_rope,
+                            int64_t k_rope_row_stride, const void* q_nope_weight,
+                            const void* q_rope_weight, const void* k_nope_weight,
+                            const void* k_rope_weight, const int* positions, const void* rope_turns,
+                            float eps, int interleaved, void* q_nope_out, void* q_rope_out,
+                            void* k_nope_out, void* k_rope_out, int64_t rows, int H, int d_nope,
+                            int d_rope, void* stream);
+
+/*
+ * mla_qk_norm_rope_backward_workspace_size -- bytes of device workspace
+ * mla_qk_norm_rope_backward needs when any weight is given (0 for sizes it refuses).
+ */
+size_t mla_qk_norm_rope_backward_workspace_size(int64_t rows, int H);
+
+/*
+ * mla_qk_norm_rope_backward -- gradients of mla_qk_norm_rope, taking what mla_prefill_backward
+ * gives:
+ *   dq_nope, dq_rope, dk_nope bf16, dk_rope fp32 -- upstream gradients, in the contiguous layouts
+ *           of the forward's outputs
+ *   q .. interleaved -- the forward's inputs
+ *   dq, dk_nope_in, dk_rope_in bf16 -- gradients of q, k_nope, k_rope, laid out with the same
+ *           strides as those (only the operands' own elements are written); strides that let
+ *           elements overlap (a repeated operand) are refused.  They must not overlap the inputs.
+ *   dq_nope_weight .. dk_rope_weight fp32 -- gradients of the weights, summed over rows and heads
+ *           in a fixed order; given exactly where the weight is
+ *   workspace  at least mla_qk_norm_rope_backward_workspace_size() bytes; not needed (NULL) when
+ *           no weight is given
+ * Supported sizes as for mla_qk_norm_rope.
+ */
+mla_status mla_qk_norm_rope_backward(
+    const void* dq_nope, const void* dq_rope, const void* dk_nope, const float* dk_rope,
+    const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
+    int64_t k_nope_row_stride, int64_t k_nope_head_stride, const void* k_rope,
+    int64_t k_rope_row_stride, const void* q_nope_weight, const void* q_rope_weight,
+    const void* k_nope_weight, const void* k_rope_weight, const int* positions,
+    const void* rope_turns, float eps, int interleaved, void* dq, void* dk_nope_in,
+    void* dk_rope_in, float* dq_nope_weight, float* dq_rope_weight, float* dk_nope_weight,
+    float* dk_rope_weight, int64_t rows, int H, int d_nope, int d_rope, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * mla_absorb -- the per-head absorption product either side of absorbed decode:
  *     y[r, h, :] = x[r, h, :] @ w[h]      (fp32 accumulation, bf16 round-to-nearest-even out)
  *   x [R, H, K] bf16, w [H, K, N] bf16, y [R, H, N] bf16 (all contiguous, 16-byte aligned).

@@ -29,6 +29,11 @@
 //               (O_half / l, log-sum-exp), column quads of 32 rows per 512-byte store, and,
 //               in the CTA that completes a (sequence, column half), merge its splits into
 //               the bf16 output and the LSE
+// A third instance of each kernel serves a tree of drafted tokens (kTree): which of the n newest
+// keys a row sees comes from a bit mask a token instead of the diagonal, and the pages that hold
+// drafted keys pass through the preparation warps, which take non-finite values out of them (a
+// zero weight times such a value would reach rows that do not see the key) and flag their keys,
+// so that the rows that see them, and no others, come out as NaN.
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
 #include <cuda.h>
@@ -96,6 +101,11 @@ struct Params {
   int NQT, TQ;  // query tiles per sequence (T*H rows in tiles of 128) and rows per tile
   int n_slots;  // partial slots: G + B * NQT
   float scale_log2;
+  // drafted tree: bit j of row t says whether token t sees drafted key j
+  const uint32_t* tree_mask;  // [B or 1][T][mask_words]
+  long long mask_stride;      // words from one sequence's mask to the next (0: one for all)
+  int mask_words;
+  const int* new_lens;        // [B] drafted tokens of each sequence, or null (T each)
   int page_box;  // 1: a page is one box of the 3-D cache map (else nine boxes of the 2-D one)
   int item_cost;  // flat pages the split plan charges per work item (see decode_plan.cuh)
   // buffer sizes for the store checks of the bounds-checked build
@@ -123,7 +133,38 @@ struct Bars {
   int abort_flag;
   Plan plan;
   float kscale[kStages][kPage];
+  float key_nan[kStages][kPage];  // tree: NaN where a drafted key holds a non-finite value, else 0
 };
+
+// Drafted tokens of virtual sequence v: the newest n keys; rows of tokens n .. T - 1 are padding.
+__device__ __forceinline__ int drafted(const Params& p, int vseq) {
+  return p.new_lens ? min(max(__ldg(p.new_lens + vseq / p.NQT), 0), p.T) : p.T;
+}
+
+// Bits j .. j + 63 of a row's tree mask, 0 past its words (j >= 0).
+__device__ __forceinline__ unsigned long long mask_bits(const uint32_t* row, int words, int j) {
+  const int w = j >> 5, sh = j & 31;
+  auto word = [&](int i) { return i < words ? __ldg(row + i) : 0u; };
+  const uint32_t a = word(w), b = word(w + 1), c = word(w + 2);
+  return __funnelshift_r(a, b, sh) | static_cast<unsigned long long>(__funnelshift_r(b, c, sh)) << 32;
+}
+
+// Does a 16-byte granule hold a non-finite value (bf16: NaN or infinity; e4m3: NaN)?
+template <bool kFp8>
+__device__ __forceinline__ bool granule_nonfinite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kFp8) {
+      // a byte is NaN iff its low 7 bits are all set: adding 1 to them carries into bit 7
+      bad |= (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+    } else {
+      bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+    }
+  }
+  return bad;
+}
 
 __device__ __forceinline__ int page_of(const Params& p, int vseq, int pg) {
   return __ldg(p.page_table + (size_t)(vseq / p.NQT) * p.max_pages + pg);
@@ -136,7 +177,7 @@ __device__ __forceinline__ int page_row(const Params& p, int vseq, int pg) {
   return row_of_page(p, page_of(p, vseq, pg));
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tm_cache,
                         const __grid_constant__ CUtensorMap tm_page,
@@ -168,6 +209,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   const int TH = p.T * p.H, TQ = p.TQ;
   // first Q row of virtual sequence v: its sequence's rows, then 128 per query tile
   auto q_row0 = [&](int v) { return (v / p.NQT) * TH + (v % p.NQT) * kRows; };
+  // bf16: keys of sequence v up to here go from the copy straight to the MMA; a page that reaches
+  // further (past the sequence's end, or into its drafted keys) passes the preparation warps
+  auto clean_keys = [&](int v, int len) { return kTree ? max(len - drafted(p, v), 0) : len; };
 
   if (threadIdx.x == 0) {
     // the descriptors are fetched while the barriers are set up and the plan is made: a TMA
@@ -439,6 +483,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if (!(ok = ptx::mbar_wait(&bars.q_hi_full, nseg & 1, abort_flag, p.err))) break;
         ptx::tc_fence_after();
         const int g_end = g + (hi - lo), g_first = g;
+        const int clean = clean_keys(seq, L);
         int gs = g, gp = g;  // next page whose S / whose PV is to be issued
         int sp = 0;          // next part of S(gs)
         bool zero_asked = false;  // bf16: the partial page gs was handed to the preparation warps
@@ -464,7 +509,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           if (gs < g_end && gs <= gp + 1) {
             if constexpr (kFp8) {
               can = ptx::mbar_test_wait(&bars.stage_ready[gs % kStages][sp], (gs / kStages) & 1);
-            } else if ((lo + (gs - g_first) + 1) * kPage <= L) {
+            } else if ((lo + (gs - g_first) + 1) * kPage <= clean) {
               can = sp == 0 ? ptx::mbar_test_wait(&bars.spart_full, gs & 1)
                             : ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1);
             } else if (sp == 1) {
@@ -523,6 +568,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     int g = 0, n_zero = 0;
     bool ok = true;
     while (ok && segs.next(seq, L, lo, hi)) {
+      const int clean = clean_keys(seq, L);
       for (int pg = lo; pg < hi; ++pg, ++g) {
         const int s = g % kStages;
         unsigned char* st = sm + kOffStage + s * kStageBytes;
@@ -539,9 +585,32 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           // parts land it hands the page over (zero_go); rows valid..63 of its nine chunks
           // are zeroed (16-byte granules; whole rows, so the swizzle is immaterial) and handed
           // back (zeroed).  Full pages go straight from the copy to the MMA.
-          if (valid < kPage) {
+          if ((pg + 1) * kPage > clean) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero & 1, abort_flag, p.err));
             if (!ok) break;
+            if constexpr (kTree) {
+              // drafted keys first .. valid - 1 of the page: non-finite granules are zeroed and the
+              // key flagged; a warp scans a whole row (72 granules), the two warps every other row
+              const int first = max(clean - pg * kPage, 0);
+              if (tid < kPage && (tid < first || tid >= valid)) bars.key_nan[g & 1][tid] = 0.f;
+              for (int rw = first + (tid >> 5); rw < valid; rw += n_prep / 32) {
+                bool bad_row = false;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                  const int e = (tid & 31) + 32 * i, c = e >> 3;
+                  if (e >= 72) continue;
+                  unsigned char* base = sm + (c < 5 ? kOffSPart + c * kPageChunk
+                                                    : kOffVPart + (g % kVSlots) * kVPartBytes + (c - 5) * kPageChunk);
+                  uint4* gr = reinterpret_cast<uint4*>(base + rw * 128 + (e & 7) * 16);
+                  if (granule_nonfinite<false>(*gr)) {
+                    *gr = make_uint4(0, 0, 0, 0);
+                    bad_row = true;
+                  }
+                }
+                bad_row = __any_sync(0xffffffffu, bad_row);
+                if ((tid & 31) == 0) bars.key_nan[g & 1][rw] = bad_row ? __int_as_float(0x7fc00000) : 0.f;
+              }
+            }
             const int nrow = kPage - valid;
             for (int part = 0; part < 2; ++part) {
               const int nch = part == 0 ? 5 : 4;
@@ -559,6 +628,15 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         } else {
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.stage_full[s], (g / kStages) & 1, abort_flag, p.err));
           if (!ok) break;
+          const bool tree_page = kTree && (pg + 1) * kPage > clean;
+          if constexpr (kTree) {
+            if (tid < kPage) {
+              const bool fin = fabsf(ksc) < INFINITY;
+              bars.key_nan[s][row] = fin ? 0.f : __int_as_float(0x7fc00000);
+              // (only where the mask may hide the key; elsewhere every row sees the scale as it is)
+              if (tree_page && !fin) ksc = 0.f;
+            }
+          }
           if (tid < kPage) bars.kscale[s][row] = ksc;
           // Widen in place, in three lockstep steps of three chunks (four 16-byte granules
           // per thread per step).  bf16 chunk c (bytes [8c, 8c+8) KB) overlaps raw chunks 2c-9
@@ -579,10 +657,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                            ? *reinterpret_cast<const uint4*>(st + kRawOffset + c * kRawChunk + gi * 16)
                            : make_uint4(0, 0, 0, 0);
             }
+            uint32_t hit = 0;  // tree: granules that hold a NaN, zeroed here, flagged below
+            if (tree_page) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (granule_nonfinite<true>(raw[q])) {
+                  raw[q] = make_uint4(0, 0, 0, 0);
+                  hit |= 1u << q;
+                }
+            }
             __syncwarp();
             if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bars.conv_sync);
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.conv_sync, (3 * g + k) & 1, abort_flag, p.err));
             if (!ok) break;
+            if (kTree && hit) {  // after the barrier: the flags' reset above came before it
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (hit >> q & 1) bars.key_nan[s][((tid + n_prep * q) & 255) >> 2] = __int_as_float(0x7fc00000);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int G = tid + n_prep * q, c = 3 * k + (G >> 8), gi = G & 255;
@@ -632,9 +724,26 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const int gr = (seq % p.NQT) * kRows + r;  // row within the sequence's T*H rows
       const int t_row = gr / p.H;
       const int last_visible = p.causal ? (L - p.T + t_row) : (L - 1);  // keys <= this are visible
+      const int n_new = kTree ? drafted(p, seq) : 0;
+      const int first_new = L - n_new;  // tree: the first drafted key (negative if L < n_new)
+      const bool pad_row = kTree && t_row >= n_new;
+      const uint32_t* mask_row =
+          kTree ? p.tree_mask + (seq / p.NQT) * p.mask_stride + (long long)t_row * p.mask_words : nullptr;
       float m = -INFINITY, l = 0.f, lr = 0.f;  // exact row sum (LSE) and bf16-rounded (PV)
       const uint32_t o_addr = tmem + lane_off + 256;
       for (int pg = lo; pg < hi; ++pg, ++g) {
+        const bool tree_page = kTree && (pg + 1) * kPage > first_new;
+        unsigned long long vis = ~0ull;  // tree: bit x says whether this row sees key pg * 64 + x
+        if (tree_page) {
+          const int off = pg * kPage - first_new;  // drafted index of the page's first key, > -64
+          if (pad_row)
+            vis = 0;
+          else if (off >= 0)
+            vis = mask_bits(mask_row, p.mask_words, off);
+          else
+            vis = mask_bits(mask_row, p.mask_words, 0) << -off | ((1ull << -off) - 1);
+          if (L - pg * kPage < kPage) vis &= (1ull << (L - pg * kPage)) - 1;
+        }
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.s_full[g & 1], (g >> 1) & 1, abort_flag, p.err));
         if (!ok) break;
         ptx::tc_fence_after();
@@ -659,7 +768,19 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           s2[x] = ptx::f2(s[2 * x], s[2 * x + 1]);
           if constexpr (kFp8) s2[x] = ptx::mul2(s2[x], ptx::f2(ks[2 * x], ks[2 * x + 1]));
         }
-        if (key0 + kPage - 1 > lim) {  // a partial page (or a bad one): mask invisible keys
+        if constexpr (kTree) {
+          if (bad) vis = 0;
+          if (tree_page || bad) {
+            const float* kn = bars.key_nan[kFp8 ? g % kStages : g & 1];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const uint32_t two = static_cast<uint32_t>(vis >> (2 * x));
+              const float lo_nan = tree_page ? kn[2 * x] : 0.f, hi_nan = tree_page ? kn[2 * x + 1] : 0.f;
+              s2[x] = ptx::f2(two & 1 ? ptx::f2_lo(s2[x]) + lo_nan : -INFINITY,
+                              two & 2 ? ptx::f2_hi(s2[x]) + hi_nan : -INFINITY);
+            }
+          }
+        } else if (key0 + kPage - 1 > lim) {  // a partial page (or a bad one): mask invisible keys
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             s2[x] = ptx::f2(key0 + 2 * x <= lim ? ptx::f2_lo(s2[x]) : -INFINITY,
@@ -742,8 +863,14 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const size_t slot = (size_t)unit + seq;
-      const float inv = lr > 0.f ? 1.f / lr : 0.f;
-      const float lse_own = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (pad_row) l = lr = 0.f;
+      // (tree: a NaN sum stays one, and a row without keys is zero whatever its accumulator holds)
+      const float inv = (kTree ? lr != 0.f : lr > 0.f) ? 1.f / lr : 0.f;
+      const float lse_own = (kTree ? l != 0.f : l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      auto own_o = [&](uint32_t v) {
+        const float o = __uint_as_float(v) * inv;
+        return kTree && lr == 0.f ? 0.f : o;
+      };
       const bool row_live = r < TQ && gr < TH;
       // The work units that cover this virtual sequence write their partials of this column
       // half into slots c + seq, c_first <= c <= c_first + nsplit - 1; this one is k_own.
@@ -814,9 +941,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                 float4* d4 = dst + (size_t)((c + h2) * 8 + x) * TQ;
                 if (MLA_STORE_OK(d4, p.part_o, p.part_o_bytes, p.err))
                   ptx::st_l2_hint(d4,
-                                  make_float4(__uint_as_float(v[h2][4 * x]) * inv, __uint_as_float(v[h2][4 * x + 1]) * inv,
-                                              __uint_as_float(v[h2][4 * x + 2]) * inv,
-                                              __uint_as_float(v[h2][4 * x + 3]) * inv),
+                                  make_float4(own_o(v[h2][4 * x]), own_o(v[h2][4 * x + 1]), own_o(v[h2][4 * x + 2]),
+                                              own_o(v[h2][4 * x + 3])),
                                   keep);
               }
           }
@@ -875,12 +1001,15 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
 #pragma unroll
         for (int k = 0; k < kLseRegs; ++k) mxl = fmaxf(mxl, lse_r[k]);
         for (int k = kLseRegs; k < nsplit; ++k) mxl = fmaxf(mxl, lse_of(k));
-        auto wraw = [&](float ls) { return (mxl == -INFINITY || ls == -INFINITY) ? 0.f : __expf(ls - mxl); };
+        auto wraw = [&](float ls) {
+          if (kTree && ls != ls) return ls;
+          return (mxl == -INFINITY || ls == -INFINITY) ? 0.f : __expf(ls - mxl);
+        };
         float wsum = 0.f;
 #pragma unroll
         for (int k = 0; k < kLseRegs; ++k) wsum += wraw(lse_r[k]);
         for (int k = kLseRegs; k < nsplit; ++k) wsum += wraw(lse_of(k));
-        const float winv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const float winv = (kTree ? wsum != 0.f : wsum > 0.f) ? 1.f / wsum : 0.f;
         float w_r[kLseRegs];
 #pragma unroll
         for (int k = 0; k < kLseRegs; ++k) w_r[k] = wraw(lse_r[k]) * winv;
@@ -923,10 +1052,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
               ptx::tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                x[j] = make_float4(__uint_as_float(v[j >> 3][4 * (j & 7)]) * inv,
-                                   __uint_as_float(v[j >> 3][4 * (j & 7) + 1]) * inv,
-                                   __uint_as_float(v[j >> 3][4 * (j & 7) + 2]) * inv,
-                                   __uint_as_float(v[j >> 3][4 * (j & 7) + 3]) * inv);
+                x[j] = make_float4(own_o(v[j >> 3][4 * (j & 7)]), own_o(v[j >> 3][4 * (j & 7) + 1]),
+                                   own_o(v[j >> 3][4 * (j & 7) + 2]), own_o(v[j >> 3][4 * (j & 7) + 3]));
             } else if (bulk) {  // the other split of two, copied into shared memory
 #pragma unroll
               for (int j = 0; j < 16; ++j)
@@ -971,7 +1098,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         }
         float* lp = p.lse + ((size_t)(seq / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
         if (half == 0 && row_live && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err))
-          *lp = wsum > 0.f ? mxl + logf(wsum) : -INFINITY;
+          *lp = (kTree ? wsum != 0.f : wsum > 0.f) ? mxl + logf(wsum) : -INFINITY;
       }
       // the accumulator was read: the next segment's first PV product may overwrite it
       ptx::tc_fence_before();
@@ -1006,8 +1133,8 @@ cudaError_t load_decode_kernels() {
   cudaFuncAttributes fa;
   cudaError_t e = load_decode_t_kernels();
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncGetAttributes(&fa, decode_split_kernel<false>)) != cudaSuccess) return e;
-  if ((e = cudaFuncGetAttributes(&fa, decode_split_kernel<true>)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, decode_split_kernel<false, false>)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, decode_split_kernel<true, false>)) != cudaSuccess) return e;
   return cudaFuncGetAttributes(&fa, zero_counters_kernel);
 }
 
@@ -1019,6 +1146,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
                                 const float* kv_scale, const int* page_table,
                                 const int* cache_lens, int B, int H, int T, int max_pages,
                                 int num_pages, float softmax_scale, int causal, bool fp8,
+                                const void* tree_mask, long long mask_stride, const int* new_lens,
                                 float* part_o, float* part_lse, int* counters, void* out,
                                 float* lse, int G, unsigned int* err, cudaStream_t stream) {
   using namespace sm103_decode;
@@ -1084,6 +1212,10 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   p.causal = causal;
   p.G = G;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.tree_mask = static_cast<const uint32_t*>(tree_mask);
+  p.mask_stride = mask_stride;
+  p.mask_words = (T + 31) / 32;
+  p.new_lens = new_lens;
   p.page_box = page_box ? 1 : 0;
   // one flat page charged per work item (its Q load, epilogue and merge; measured against
   // 0, 2 and 4 on uniform and ragged batches: the same time for 64 sequences of 4096 keys,
@@ -1111,8 +1243,8 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto go = [&](auto kern) -> cudaError_t {
-    static unsigned long long smem_set[2] = {0, 0};
-    const cudaError_t e2 = smem_attr_once(kern, kSmemAlloc, &smem_set[fp8 ? 1 : 0]);
+    static unsigned long long smem_set[4] = {0, 0, 0, 0};
+    const cudaError_t e2 = smem_attr_once(kern, kSmemAlloc, &smem_set[(fp8 ? 1 : 0) + (tree_mask ? 2 : 0)]);
     if (e2 != cudaSuccess) return e2;
     // programmatic dependent of the zeroing kernel: the prologue (barriers, TMEM, plan, first
     // loads) overlaps it
@@ -1128,7 +1260,8 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, tm, tm_page, tm_c4, tm_c5, tm_qlat, tm_qrope, p);
   };
-  return fp8 ? go(decode_split_kernel<true>) : go(decode_split_kernel<false>);
+  if (tree_mask) return fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>);
+  return fp8 ? go(decode_split_kernel<true, false>) : go(decode_split_kernel<false, false>);
 }
 
 }  // namespace mla

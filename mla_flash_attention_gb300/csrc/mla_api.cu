@@ -28,6 +28,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
                                 const float* kv_scale, const int* page_table,
                                 const int* cache_lens, int B, int H, int T, int max_pages,
                                 int num_pages, float softmax_scale, int causal, bool fp8,
+                                const void* tree_mask, long long mask_stride, const int* new_lens,
                                 float* part_o, float* part_lse, int* counters, void* out,
                                 float* lse, int G, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_decode_t_sm103(const void* q_latent, const void* q_rope, const void* kv_cache,
@@ -50,6 +51,25 @@ cudaError_t launch_cache_append(const void* c_new, void* cache, float* kv_scale,
                                 const int* page_table, const int* cache_lens, int B, int T,
                                 int max_pages, int num_pages, bool fp8, unsigned int* err,
                                 cudaStream_t stream);
+cudaError_t launch_rope_append(const void* c_new, long long row_stride, const void* w, float eps,
+                               const int* positions, const void* turns, bool pairs, void* cache, float* kv_scale,
+                               const int* page_table, const int* cache_lens, const int* new_lens, int B, int T,
+                               int max_pages, int num_pages, bool fp8, unsigned int* err, cudaStream_t stream);
+size_t norm_rope_grad_workspace_bytes(long long rows, int H, int sms);
+cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_head, const void* kn,
+                                   long long kn_row, long long kn_head, const void* kr, long long kr_row,
+                                   const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
+                                   const int* pos, const void* turns, float eps, bool pairs, long long rows,
+                                   int H, void* qn_out, void* qr_out, void* kn_out, void* kr_out, int sms,
+                                   unsigned int* err, cudaStream_t stream);
+cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const float* dkr,
+                                        const void* q, long long q_row, long long q_head, const void* kn,
+                                        long long kn_row, long long kn_head, const void* kr, long long kr_row,
+                                        const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
+                                        const int* pos, const void* turns, float eps, bool pairs, long long rows,
+                                        int H, void* dq, void* dk_nope, void* dk_rope, float* dw_qn, float* dw_qr,
+                                        float* dw_kn, float* dw_kr, float* workspace, int sms, unsigned int* err,
+                                        cudaStream_t stream);
 }  // namespace mla
 
 namespace {
@@ -155,6 +175,38 @@ DecodeWorkspace decode_workspace_layout_t(void* base, int B, int TH, int d_laten
   w.counters = reinterpret_cast<int*>(static_cast<char*>(base) + o_bytes + l_bytes);
   w.bytes = o_bytes + l_bytes + c_bytes;
   return w;
+}
+
+// What mla_qk_norm_rope and its backward share: the operands present and their strides.
+mla_status check_qk_norm_rope(const char* fn, const void* q, long long q_row, long long q_head, const void* k_nope,
+                              long long kn_row, long long kn_head, const void* k_rope, long long kr_row,
+                              const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
+                              const int* positions, const void* rope_turns, float eps, long long rows, int H,
+                              int d_nope, int d_rope) {
+  if (!q && !k_nope && !k_rope) return fail(MLA_ERR_INVALID_ARG, "%s: q, k_nope and k_rope are all NULL", fn);
+  if (!positions || !rope_turns) return fail(MLA_ERR_INVALID_ARG, "%s: positions and rope_turns must not be NULL", fn);
+  if ((!q && (w_qn || w_qr)) || (!k_nope && w_kn) || (!k_rope && w_kr))
+    return fail(MLA_ERR_INVALID_ARG, "%s: a norm weight was given for an operand that is NULL", fn);
+  if (rows <= 0 || H <= 0) return fail(MLA_ERR_INVALID_ARG, "%s: rows and H must be positive (got %lld, %d)", fn, rows, H);
+  if (d_nope != 128 || d_rope != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: only d_nope=128, d_rope=64 are built (got %d, %d)", fn, d_nope, d_rope);
+  // the kernels number (row, group of four heads) pairs in 32 bits, a grid's step below the top
+  if (H > 65535 || rows > 0x70000000LL / ((H + 3) / 4))
+    return fail(MLA_ERR_UNSUPPORTED, "%s: H must be at most 65535 and rows * ceil(H / 4) at most 0x70000000", fn);
+  if (!std::isfinite(eps) || eps < 0.f) return fail(MLA_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  const void* ptrs[] = {q, k_nope, k_rope, w_qn, w_qr, w_kn, w_kr};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(rope_turns) & 7))
+    return fail(MLA_ERR_INVALID_ARG, "%s: positions must be 4-byte and rope_turns 8-byte aligned", fn);
+  const long long strides[] = {q ? q_row : 0, q ? q_head : 0, k_nope ? kn_row : 0, k_nope ? kn_head : 0,
+                               k_rope ? kr_row : 0};
+  for (long long s : strides)
+    if (s < 0 || s % 8 != 0)
+      return fail(MLA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements and not negative (got %lld)", fn, s);
+  if ((double)rows * ((double)strides[0] + strides[2] + strides[4]) + (double)H * ((double)strides[1] + strides[3]) >= 4.0e18)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: strides too large", fn);
+  return MLA_OK;
 }
 
 }  // namespace
@@ -366,7 +418,7 @@ mla_status mla_decode(const void* q_latent, const void* q_rope, const void* kv_c
                                       g_wait_limit.load(), g_skip_unit.load(), st)
          : mla::launch_decode_sm103(q_latent, q_rope, kv_cache, kv_scale, page_table, cache_lens, B, H,
                                     q_len, max_pages_per_seq, num_pages, softmax_scale, causal != 0, fp8,
-                                    ws.part_o, ws.part_lse, ws.counters, out, lse, G, err, st);
+                                    nullptr, 0, nullptr, ws.part_o, ws.part_lse, ws.counters, out, lse, G, err, st);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode launch");
   return MLA_OK;
 }
@@ -422,6 +474,195 @@ mla_status mla_cache_append(const void* c_new, void* kv_cache, float* kv_scale,
                                            q_len, max_pages_per_seq, num_pages, fp8, err,
                                            static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "mla_cache_append launch");
+  return MLA_OK;
+}
+
+mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm_weight, float eps,
+                           const int* positions, const void* rope_turns, int interleaved, void* kv_cache,
+                           float* kv_scale, const int* page_table, const int* cache_lens, const int* new_lens, int B,
+                           int q_len, int d_latent, int d_rope, int page_size, int max_pages_per_seq, int num_pages,
+                           mla_dtype kv_dtype, void* stream) {
+  if (!c_new || !rope_turns || !kv_cache || !page_table || !cache_lens)
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: null tensor pointer");
+  if (B <= 0 || q_len <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: B, q_len, max_pages_per_seq, num_pages must be positive");
+  if (d_latent != 512 || d_rope != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: only d_latent=512, d_rope=64 are built (got %d, %d)", d_latent, d_rope);
+  if (page_size != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: only page_size=64 is built (got %d)", page_size);
+  if ((long long)B * q_len > 0x7fffffffLL / 4)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: B*q_len too large");
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: max_pages_per_seq*page_size overflows int32");
+  if (c_stride < d_latent + d_rope || c_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: c_stride must be a multiple of 8 and at least %d (got %lld)",
+                d_latent + d_rope, (long long)c_stride);
+  if (!std::isfinite(eps) || eps < 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: eps must be finite and not negative");
+  const bool fp8 = kv_dtype == MLA_FP8_E4M3;
+  if (kv_dtype != MLA_BF16 && !fp8)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: kv_dtype must be MLA_BF16 or MLA_FP8_E4M3");
+  if (fp8 != (kv_scale != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: kv_scale is required for fp8 and must be NULL for bf16");
+  const void* ptrs[] = {c_new, norm_weight, kv_cache};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: tensors must be 16-byte aligned");
+  const void* words[] = {kv_scale, positions, page_table, cache_lens, new_lens};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3)
+      return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: scales and integer tensors must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(rope_turns) & 7)
+    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: rope_turns must be 8-byte aligned");
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "mla_rope_append: device error word not reachable");
+  cudaError_t e = mla::launch_rope_append(c_new, c_stride, norm_weight, eps, positions, rope_turns, interleaved != 0,
+                                          kv_cache, kv_scale, page_table, cache_lens, new_lens, B, q_len,
+                                          max_pages_per_seq, num_pages, fp8, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_rope_append launch");
+  return MLA_OK;
+}
+
+mla_status mla_decode_tree(const void* q_latent, const void* q_rope, const void* kv_cache, const float* kv_scale,
+                           const int* page_table, const int* cache_lens, const void* tree_mask,
+                           int64_t tree_mask_stride, const int* new_lens, void* out, float* lse, int B, int H,
+                           int q_len, int d_latent, int d_rope, int page_size, int max_pages_per_seq, int num_pages,
+                           float softmax_scale, mla_dtype kv_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (!q_latent || !q_rope || !kv_cache || !page_table || !cache_lens || !tree_mask || !out || !lse)
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: null tensor pointer");
+  if (B <= 0 || H <= 0 || q_len <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: B, H, q_len, max_pages_per_seq, num_pages must be positive");
+  if (d_latent != 512 || d_rope != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: only d_latent=512, d_rope=64 are built (got %d, %d)", d_latent, d_rope);
+  if (page_size != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: only page_size=64 is built (got %d)", page_size);
+  if ((long long)H * q_len > 65536)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: q_len*H must be at most 65536 (got %lld)", (long long)H * q_len);
+  if (B > 65535) return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: B must be at most 65535");
+  if ((long long)B * ((H * q_len + 127) / 128) > (1LL << 24) || (long long)B * H * q_len > 0x7fffffffLL)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: B * ceil(q_len*H / 128) must be at most 2^24 and B*q_len*H below 2^31");
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: max_pages_per_seq*page_size overflows int32");
+  if ((long long)num_pages * page_size > 0x7fffffffLL)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: num_pages*page_size overflows int32");
+  const int words = (q_len + 31) / 32;
+  if (tree_mask_stride != 0 && tree_mask_stride < (int64_t)q_len * words)
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: tree_mask_stride must be 0 or at least q_len * ceil(q_len / 32) = %lld words",
+                (long long)q_len * words);
+  if (!std::isfinite(softmax_scale) || softmax_scale <= 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: softmax_scale must be finite and positive");
+  const bool fp8 = kv_dtype == MLA_FP8_E4M3;
+  if (kv_dtype != MLA_BF16 && !fp8)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode_tree: kv_dtype must be MLA_BF16 or MLA_FP8_E4M3");
+  if (fp8 != (kv_scale != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: kv_scale is required for fp8 and must be NULL for bf16");
+  const void* ptrs[] = {q_latent, q_rope, kv_cache, kv_scale, out, lse, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: tensors must be 16-byte aligned");
+  const void* ints[] = {page_table, cache_lens, tree_mask, new_lens};
+  for (const void* p : ints)
+    if (reinterpret_cast<uintptr_t>(p) & 3)
+      return fail(MLA_ERR_INVALID_ARG, "mla_decode_tree: integer tensors must be 4-byte aligned");
+  const int G = decode_units();
+  if (G <= 0) return fail(MLA_ERR_CUDA, "mla_decode_tree: cannot query the SM count");
+  const DecodeWorkspace ws = decode_workspace_layout(workspace, B, H * q_len, d_latent, G);
+  if (!workspace || workspace_bytes < ws.bytes)
+    return fail(MLA_ERR_WORKSPACE, "mla_decode_tree: workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, ws.bytes);
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "mla_decode_tree: device error word not reachable");
+  cudaError_t e = mla::launch_decode_sm103(q_latent, q_rope, kv_cache, kv_scale, page_table, cache_lens, B, H, q_len,
+                                           max_pages_per_seq, num_pages, softmax_scale, 1, fp8, tree_mask,
+                                           tree_mask_stride, new_lens, ws.part_o, ws.part_lse, ws.counters, out, lse, G,
+                                           err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_decode_tree launch");
+  return MLA_OK;
+}
+
+mla_status mla_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
+                            int64_t k_nope_row_stride, int64_t k_nope_head_stride, const void* k_rope,
+                            int64_t k_rope_row_stride, const void* q_nope_weight, const void* q_rope_weight,
+                            const void* k_nope_weight, const void* k_rope_weight, const int* positions,
+                            const void* rope_turns, float eps, int interleaved, void* q_nope_out, void* q_rope_out,
+                            void* k_nope_out, void* k_rope_out, int64_t rows, int H, int d_nope, int d_rope,
+                            void* stream) {
+  const mla_status st = check_qk_norm_rope("mla_qk_norm_rope", q, q_row_stride, q_head_stride, k_nope,
+                                           k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
+                                           q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions,
+                                           rope_turns, eps, rows, H, d_nope, d_rope);
+  if (st != MLA_OK) return st;
+  if ((q && (!q_nope_out || !q_rope_out)) || (k_nope && !k_nope_out) || (k_rope && !k_rope_out))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qk_norm_rope: an output of a given operand is NULL");
+  const void* outs[] = {q_nope_out, q_rope_out, k_nope_out, k_rope_out};
+  for (const void* p : outs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_qk_norm_rope: tensors must be 16-byte aligned");
+  const int sms = num_sms_current();
+  unsigned int* err = device_error_word();
+  if (!err || sms <= 0) return fail(MLA_ERR_CUDA, "mla_qk_norm_rope: device error word not reachable");
+  cudaError_t e = mla::launch_norm_rope_sm103(
+      q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
+      q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, eps, interleaved != 0, rows, H,
+      q_nope_out, q_rope_out, k_nope_out, k_rope_out, sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_qk_norm_rope launch");
+  return MLA_OK;
+}
+
+size_t mla_qk_norm_rope_backward_workspace_size(int64_t rows, int H) {
+  if (rows <= 0 || H <= 0 || H > 65535 || rows > 0x70000000LL / ((H + 3) / 4)) return 0;
+  const int sms = num_sms_current();
+  return sms > 0 ? mla::norm_rope_grad_workspace_bytes(rows, H, sms) : 0;
+}
+
+mla_status mla_qk_norm_rope_backward(const void* dq_nope, const void* dq_rope, const void* dk_nope,
+                                     const float* dk_rope, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                     const void* k_nope, int64_t k_nope_row_stride, int64_t k_nope_head_stride,
+                                     const void* k_rope, int64_t k_rope_row_stride, const void* q_nope_weight,
+                                     const void* q_rope_weight, const void* k_nope_weight, const void* k_rope_weight,
+                                     const int* positions, const void* rope_turns, float eps, int interleaved,
+                                     void* dq, void* dk_nope_in, void* dk_rope_in, float* dq_nope_weight,
+                                     float* dq_rope_weight, float* dk_nope_weight, float* dk_rope_weight,
+                                     int64_t rows, int H, int d_nope, int d_rope, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  const char* fn = "mla_qk_norm_rope_backward";
+  const mla_status st = check_qk_norm_rope(fn, q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
+                                           k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight,
+                                           q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, eps,
+                                           rows, H, d_nope, d_rope);
+  if (st != MLA_OK) return st;
+  if ((q && (!dq_nope || !dq_rope || !dq)) || (k_nope && (!dk_nope || !dk_nope_in)) || (k_rope && (!dk_rope || !dk_rope_in)))
+    return fail(MLA_ERR_INVALID_ARG, "%s: a gradient of a given operand is NULL", fn);
+  if ((q_nope_weight != nullptr) != (dq_nope_weight != nullptr) || (q_rope_weight != nullptr) != (dq_rope_weight != nullptr) ||
+      (k_nope_weight != nullptr) != (dk_nope_weight != nullptr) || (k_rope_weight != nullptr) != (dk_rope_weight != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "%s: a weight's gradient must be given exactly where the weight is", fn);
+  const void* ptrs[] = {dq_nope, dq_rope, dk_nope, dk_rope, dq, dk_nope_in, dk_rope_in, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const void* dws[] = {dq_nope_weight, dq_rope_weight, dk_nope_weight, dk_rope_weight};
+  for (const void* p : dws)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(MLA_ERR_INVALID_ARG, "%s: weight gradients must be 4-byte aligned", fn);
+  // gradients share their operand's strides: every element needs a place of its own
+  auto overlaps = [&](int64_t row, int64_t head, int d) {
+    return (H > 1 && head < d) || (rows > 1 && row < d) ||
+           (rows > 1 && H > 1 && row < (int64_t)(H - 1) * head + d && head < (rows - 1) * row + d);
+  };
+  if ((q && overlaps(q_row_stride, q_head_stride, d_nope + d_rope)) ||
+      (k_nope && overlaps(k_nope_row_stride, k_nope_head_stride, d_nope)) ||
+      (k_rope && rows > 1 && k_rope_row_stride < d_rope))
+    return fail(MLA_ERR_INVALID_ARG, "%s: an operand's strides make its elements overlap, so its gradient has no such layout", fn);
+  const bool weights = dq_nope_weight || dq_rope_weight || dk_nope_weight || dk_rope_weight;
+  const int sms = num_sms_current();
+  if (sms <= 0) return fail(MLA_ERR_CUDA, "%s: cannot query the SM count", fn);
+  const size_t need = weights ? mla::norm_rope_grad_workspace_bytes(rows, H, sms) : 0;
+  if (weights && (!workspace || workspace_bytes < need))
+    return fail(MLA_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", fn, workspace_bytes, need);
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
+  cudaError_t e = mla::launch_norm_rope_grad_sm103(
+      dq_nope, dq_rope, dk_nope, dk_rope, q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
+      k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+      positions, rope_turns, eps, interleaved != 0, rows, H, dq, dk_nope_in, dk_rope_in, dq_nope_weight, dq_rope_weight,
+      dk_nope_weight, dk_rope_weight, static_cast<float*>(workspace), sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_qk_norm_rope_backward launch");
   return MLA_OK;
 }
 

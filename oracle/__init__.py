@@ -19,6 +19,7 @@ from .mla_ref import (  # noqa: F401
     decode_gather,
     decode_b,
     mla_decode,
+    mla_decode_tree,
     lse_combine,
 )
 from .cache_ref import (  # noqa: F401
@@ -28,3 +29,4 @@ from .cache_ref import (  # noqa: F401
 )
 from .absorb_ref import absorb  # noqa: F401
 from .backward_ref import prefill_backward_bh, mla_prefill_backward  # noqa: F401
+from . import norm_rope_ref  # noqa: F401

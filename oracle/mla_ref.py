@@ -212,6 +212,32 @@ def mla_decode(inp):
     return O, Ls
 
 
+def mla_decode_tree(inp, sees, new_lens=None):
+    """Decode of drafted trees: O [B,T,H,d_latent], LSE [B,H,T].
+
+    ``sees`` [B, T, T] bool: whether token t sees drafted token j.  ``new_lens`` [B] (default T):
+    the drafted tokens of each sequence, at its last places; the rows behind them are padding
+    and see nothing.  Every drafted token sees the whole prefix.
+    """
+    O = np.zeros((inp.B, inp.T, inp.H, inp.d_latent))
+    Ls = np.full((inp.B, inp.H, inp.T), -np.inf)
+    for b in range(inp.B):
+        L = int(inp.cache_lens[b])
+        n = inp.T if new_lens is None else int(new_lens[b])
+        C = decode_gather(inp, b)
+        for t in range(n):
+            visible = np.ones(L, bool)
+            for j in range(n):  # drafted token j sits at place L - n + j (not cached if below 0)
+                if L - n + j >= 0:
+                    visible[L - n + j] = sees[b, t, j]
+            Q = np.concatenate([_dq(inp.q_latent[b, t], False), _dq(inp.q_rope[b, t], False)], axis=1)
+            # keys that are not seen are left out, so that nothing they hold can matter
+            rows = C[visible]
+            O[b, t], Ls[b, :, t] = attention_rows(Q, rows, rows[:, :inp.d_latent],
+                                                  np.ones((inp.H, len(rows)), bool), inp.softmax_scale)[:2]
+    return O, Ls
+
+
 def lse_combine(o_parts, lse_parts):
     """Merge attention results computed over disjoint key sets.
 

@@ -1,0 +1,271 @@
+"""GPU parity of mla_decode_tree (through the C ABI) against the fp64 oracle.
+
+Tolerances are mla_decode's: the arithmetic is the same, only the mask differs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gen import make_decode
+from tests.parity import TOL_O_BF16, TOL_O_FP8, check
+
+pytestmark = pytest.mark.gpu
+
+
+def random_parents(B, T, seed):
+    rng = np.random.default_rng(seed)
+    return np.array([[int(rng.integers(max(-1, t - 4), t)) if t else -1 for t in range(T)] for _ in range(B)])
+
+
+def sees_of(mask, T):
+    m = mask.cpu().numpy().astype(np.int64)
+    j = np.arange(T)
+    return (m[..., j // 32] >> (j % 32) & 1).astype(bool)
+
+
+class Problem:
+    def __init__(self, H, T, lens, fp8, seed, new=None, shared=False, mask=None, extra_pages=1):
+        from mla_flash_attention_gb300 import binding
+        from mla_flash_attention_gb300.testing import decode_to_device
+
+        B = len(lens)
+        self.inp = inp = make_decode(B, H, T, lens, fp8=fp8, seed=seed, extra_pages=extra_pages)
+        if mask is None:
+            mask, _ = binding.tree_mask_from_parents(random_parents(1 if shared else B, T, seed))
+            mask = mask[0] if shared else mask
+        self.mask = mask.cuda()
+        self.sees = np.broadcast_to(sees_of(mask, T), (B, T, T))
+        self.new = None if new is None else torch.tensor(new, dtype=torch.int32, device="cuda")
+        d = decode_to_device(inp, torch.device("cuda"))
+        self.args, self.kv_scale = d["args"], d["kwargs"]["kv_scale"]
+
+    def run(self, lib, **kw):
+        return lib.mla_decode_tree(*self.args, self.mask, kv_scale=self.kv_scale, new_lens=self.new,
+                                   softmax_scale=self.inp.softmax_scale, **kw)
+
+    def check(self, out, lse, what=""):
+        n = None if self.new is None else self.new.cpu().numpy().clip(0, self.inp.T)
+        O, L = oracle.mla_decode_tree(self.inp, self.sees, n)
+        check(out.float().cpu().numpy(), O, lse.cpu().numpy(), L, TOL_O_FP8 if self.inp.fp8 else TOL_O_BF16, what=what)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,T,lens,new", [
+    (1, 1, [1], None),                                    # the smallest call
+    (16, 1, [1, 64, 65, 700], None),                      # single tokens
+    (8, 4, [3, 4, 64, 66, 67, 130], None),                # trees across a page's end; fewer keys than nodes
+    (16, 8, [1000, 8, 72, 64], [8, 3, 5, 1]),             # ragged trees, padding rows
+    (4, 33, [33, 90, 400], None),                         # two mask words
+    (128, 3, [300, 65], None),                            # three tiles of query rows
+    (16, 13, [13, 500, 64, 0, 77], [13, 0, 7, 5, 13]),    # no drafted token, an empty sequence
+    (3, 64, [64, 63, 200], [64, 64, 50]),                 # 64 nodes: a whole page of drafted keys
+    (2, 150, [140, 600], [150, 131]),                     # five mask words over three pages
+])
+def test_trees(lib, H, T, lens, new, fp8):
+    p = Problem(H, T, lens, fp8, seed=H * 100 + T, new=new)
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    p.check(out, lse, "H=%d T=%d fp8=%d" % (H, T, fp8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_mask_for_the_batch(lib, fp8):
+    p = Problem(16, 9, [9, 70, 128, 1000], fp8, seed=5, shared=True)
+    assert p.mask.dim() == 2
+    p.check(*p.run(lib))
+    lib.check_device_error()
+
+
+@pytest.mark.parametrize("fp8,H,T", [(False, 128, 1), (False, 16, 2), (False, 40, 5), (True, 64, 2), (True, 128, 4)])
+def test_a_chain_is_mla_decode_bit_for_bit(lib, fp8, H, T):
+    # (fp8 with more than 32 query rows: mla_decode takes the same kernel there)
+    mask, depth = lib.tree_mask_from_parents(torch.arange(T) - 1)
+    assert depth.tolist() == list(range(T))
+    p = Problem(H, T, [T, 64, 65, 3000], fp8, seed=6, mask=mask)
+    out, lse = p.run(lib)
+    o, l = lib.mla_decode(*p.args, kv_scale=p.kv_scale, softmax_scale=p.inp.softmax_scale)
+    lib.check_device_error()
+    assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_that_see_nothing_or_anything(lib, fp8):
+    # bits are taken as they are: empty rows, rows that see later tokens, bits past the tree
+    T = 40
+    rng = np.random.default_rng(3)
+    mask = torch.from_numpy(rng.integers(-2 ** 31, 2 ** 31, (3, T, 2)).astype(np.int32))
+    mask[:, 5] = 0
+    mask[1, :20] = 0
+    p = Problem(4, T, [T, 25, 300], fp8, seed=7, mask=mask, new=[T, 30, 33])
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    p.check(out, lse)
+    assert bool((out[0, 5] == 0).all()) and bool(torch.isneginf(lse[0, :, 5]).all())  # no prefix, no bit
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("H,T", [(4, 6), (128, 6)])
+def test_non_finite_drafted_keys_reach_only_rows_that_see_them(lib, fp8, value, H, T):
+    if fp8 and value != value:
+        spots = ("code", "scale")
+    elif fp8:
+        spots = ("scale",)  # e4m3 has no infinity
+    else:
+        spots = ("latent", "rope")
+    for spot in spots:
+        lens = [64 + 3, 30, 400]
+        p = Problem(H, T, lens, fp8, seed=8, shared=True)
+        clean_out, clean_lse = p.run(lib)
+        node = 2
+        for b, L in enumerate(lens):
+            place = L - T + node
+            page, row = int(p.inp.page_table[b, place // 64]), place % 64
+            if spot == "scale":
+                p.kv_scale[page, row] = value
+            elif spot == "code":
+                p.args[2].view(torch.uint8)[page, row, 77] = 0xFF
+            else:
+                p.args[2][page, row, 300 if spot == "latent" else 570] = value
+        out, lse = p.run(lib)
+        lib.check_device_error()
+        hit = torch.from_numpy(p.sees[0, :, node].copy()).cuda()
+        assert bool(hit.any()) and not bool(hit.all())
+        assert bool(torch.isnan(out[:, hit]).all()) and bool(torch.isnan(lse[:, :, hit]).all()), spot
+        assert torch.equal(out[:, ~hit], clean_out[:, ~hit]), spot
+        assert torch.equal(lse[:, :, ~hit], clean_lse[:, :, ~hit]), spot
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_padding_rows_are_zero_whatever_the_prefix_holds(lib, fp8):
+    p = Problem(8, 5, [200], fp8, seed=9, new=[2])
+    page = int(p.inp.page_table[0, 0])
+    if fp8:
+        p.args[2].view(torch.uint8)[page, 3, 5] = 0x7F
+    else:
+        p.args[2][page, 3, 5] = float("nan")
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    assert bool((out[0, 2:] == 0).all()) and bool(torch.isneginf(lse[0, :, 2:]).all())
+    assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isnan(lse[0, :, :2]).all())
+
+
+def test_counts_outside_the_range_are_clamped(lib):
+    p = Problem(16, 4, [100, 100], False, seed=10, new=[9, -3])
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    p.check(out, lse)
+
+
+def test_long_sequence_split_over_every_unit(lib):
+    p = Problem(16, 12, [32768, 1], False, seed=11, new=[12, 1])
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    p.check(out, lse)
+    again = p.run(lib)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_many_short_sequences(lib):
+    rng = np.random.default_rng(4)
+    new = rng.integers(0, 6, 300)
+    p = Problem(4, 5, list(np.maximum(new, rng.integers(1, 130, 300))), True, seed=12, new=list(new.clip(0, 5)))
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    p.check(out, lse)
+
+
+def test_bad_page_is_reported(lib):
+    p = Problem(4, 3, [100, 100], False, seed=13)
+    p.args[3][1, 1] = p.inp.num_pages + 5
+    p.run(lib)
+    with pytest.raises(lib.MLAError, match="DEVICE_CHECK"):
+        lib.check_device_error()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_writes_only_out_lse_and_workspace(lib, fp8):
+    from tests.test_gpu_canaries import Guarded
+
+    p = Problem(40, 5, [5, 130, 777], fp8, seed=14, new=[5, 2, 4])
+    inp = p.inp
+    out = Guarded((inp.B, inp.T, inp.H, 512), torch.bfloat16)
+    lse = Guarded((inp.B, inp.H, inp.T), torch.float32)
+    ws = Guarded((lib.decode_workspace_size(inp.B, inp.H, inp.T),), torch.uint8)
+    before = p.args[2].view(torch.uint8).clone()
+    p.run(lib, out=out.t, lse=lse.t, workspace=ws.t)
+    lib.check_device_error()
+    assert out.intact() and lse.intact() and ws.intact()
+    assert torch.equal(p.args[2].view(torch.uint8), before)
+    p.check(out.t, lse.t)
+
+
+def test_captured_and_replayed_with_new_lengths_and_masks(lib):
+    p = Problem(16, 7, [500, 130], False, seed=15, new=[7, 4])
+    other = Problem(16, 7, [410, 128], False, seed=15, new=[2, 7])
+    ws = torch.empty(lib.decode_workspace_size(2, 16, 7), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p.run(lib, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = p.run(lib, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    p.check(out, lse)
+    for a, b in zip(p.args, other.args):
+        a.zero_()
+        a.view(-1)[:b.numel()].copy_(b.reshape(-1)) if a is p.args[2] else a.copy_(
+            torch.nn.functional.pad(b, (0, a.shape[-1] - b.shape[-1])))
+    p.mask.copy_(other.mask)
+    p.new.copy_(other.new)
+    graph.replay()
+    torch.cuda.synchronize()
+    lib.check_device_error()
+    other.check(out, lse)
+
+
+def test_two_calls_at_once_on_two_streams(lib):
+    ps = [Problem(16, 6, [3000, 900, 64], bool(i % 2), seed=16 + i) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[p.run(lib, stream=s) for p, s in zip(ps, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    lib.check_device_error()
+    for r in got:
+        for p, (out, lse) in zip(ps, r):
+            p.check(out, lse)
+
+
+def test_refusals_of_the_binding(lib):
+    p = Problem(4, 3, [100], False, seed=17)
+    with pytest.raises(ValueError, match="tree_mask"):
+        lib.mla_decode_tree(*p.args, p.mask[:, :2].contiguous(), softmax_scale=0.1)
+    with pytest.raises(TypeError, match="tree_mask"):
+        lib.mla_decode_tree(*p.args, p.mask.long(), softmax_scale=0.1)
+    with pytest.raises(ValueError, match="new_lens"):
+        lib.mla_decode_tree(*p.args, p.mask, new_lens=torch.ones(1, dtype=torch.int32), softmax_scale=0.1)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.mla_decode_tree(*p.args, p.mask, softmax_scale=0.1, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(lib.MLAError, match="WORKSPACE"):
+        lib.mla_decode_tree(*p.args, p.mask, softmax_scale=0.1,
+                            workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(lib.MLAError, match="UNSUPPORTED"):
+        cache = p.args[2].view(-1, 32, 576)
+        lib.mla_decode_tree(p.args[0], p.args[1], cache, *p.args[3:], p.mask, softmax_scale=0.1)
+
+
+def test_offsets_past_32_bits(lib):
+    # 60000 pages hold 2.2e9 values: the sequence's pages lie at both ends of the pool
+    p = Problem(16, 4, [130], False, seed=18)
+    pages = 60000
+    pool = torch.zeros(pages, 64, 576, device="cuda", dtype=torch.bfloat16)
+    where = torch.tensor([pages - 1, 0, pages - 2], device="cuda")
+    pool[where] = p.args[2][p.args[3][0].long()]
+    want = p.run(lib)
+    out, lse = lib.mla_decode_tree(p.args[0], p.args[1], pool, where.to(torch.int32)[None], p.args[4], p.mask,
+                                   softmax_scale=p.inp.softmax_scale)
+    lib.check_device_error()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
