@@ -265,7 +265,7 @@ mla_status mla_decode_tree(const void* q_latent, const void* q_rope, const void*
  *   positions [rows] int32
  *   q_nope_out [rows, H, d_nope], q_rope_out [rows, H, d_rope], k_nope_out [rows, H, d_nope],
  *   k_rope_out [rows, d_rope] bf16, contiguous; they must not overlap the inputs
- * Supported: d_nope = 128, d_rope = 64, H <= 65535, rows * ceil(H / 4) <= 0x70000000.
+ * Supported: d_nope = 128, d_rope = 64, H <= 65535, rows * H <= 0x70000000.
  */
 mla_status mla_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                             const void* k_nope, int64_t k_nope_row_stride,

@@ -190,15 +190,15 @@ mla_status check_qk_norm_rope(const char* fn, const void* q, long long q_row, lo
   if (rows <= 0 || H <= 0) return fail(MLA_ERR_INVALID_ARG, "%s: rows and H must be positive (got %lld, %d)", fn, rows, H);
   if (d_nope != 128 || d_rope != 64)
     return fail(MLA_ERR_UNSUPPORTED, "%s: only d_nope=128, d_rope=64 are built (got %d, %d)", fn, d_nope, d_rope);
-  // the kernels number (row, group of four heads) pairs in 32 bits, a grid's step below the top
-  if (H > 65535 || rows > 0x70000000LL / ((H + 3) / 4))
-    return fail(MLA_ERR_UNSUPPORTED, "%s: H must be at most 65535 and rows * ceil(H / 4) at most 0x70000000", fn);
+  // the kernels number (row, head) pairs in 32 bits
+  if (H > 65535 || rows > 0x70000000LL / H)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: H must be at most 65535 and rows * H at most 0x70000000", fn);
   if (!std::isfinite(eps) || eps < 0.f) return fail(MLA_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
-  const void* ptrs[] = {q, k_nope, k_rope, w_qn, w_qr, w_kn, w_kr};
+  const void* ptrs[] = {q, k_nope, k_rope, w_qn, w_qr, w_kn, w_kr, rope_turns};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
-  if ((reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(rope_turns) & 7))
-    return fail(MLA_ERR_INVALID_ARG, "%s: positions must be 4-byte and rope_turns 8-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(positions) & 3)
+    return fail(MLA_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", fn);
   const long long strides[] = {q ? q_row : 0, q ? q_head : 0, k_nope ? kn_row : 0, k_nope ? kn_head : 0,
                                k_rope ? kr_row : 0};
   for (long long s : strides)
@@ -504,15 +504,13 @@ mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm
     return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: kv_dtype must be MLA_BF16 or MLA_FP8_E4M3");
   if (fp8 != (kv_scale != nullptr))
     return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: kv_scale is required for fp8 and must be NULL for bf16");
-  const void* ptrs[] = {c_new, norm_weight, kv_cache};
+  const void* ptrs[] = {c_new, norm_weight, kv_cache, rope_turns};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: tensors must be 16-byte aligned");
   const void* words[] = {kv_scale, positions, page_table, cache_lens, new_lens};
   for (const void* p : words)
     if (reinterpret_cast<uintptr_t>(p) & 3)
       return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: scales and integer tensors must be 4-byte aligned");
-  if (reinterpret_cast<uintptr_t>(rope_turns) & 7)
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: rope_turns must be 8-byte aligned");
   unsigned int* err = device_error_word();
   if (!err) return fail(MLA_ERR_CUDA, "mla_rope_append: device error word not reachable");
   cudaError_t e = mla::launch_rope_append(c_new, c_stride, norm_weight, eps, positions, rope_turns, interleaved != 0,
@@ -608,7 +606,7 @@ mla_status mla_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_
 }
 
 size_t mla_qk_norm_rope_backward_workspace_size(int64_t rows, int H) {
-  if (rows <= 0 || H <= 0 || H > 65535 || rows > 0x70000000LL / ((H + 3) / 4)) return 0;
+  if (rows <= 0 || H <= 0 || H > 65535 || rows > 0x70000000LL / H) return 0;
   const int sms = num_sms_current();
   return sms > 0 ? mla::norm_rope_grad_workspace_bytes(rows, H, sms) : 0;
 }

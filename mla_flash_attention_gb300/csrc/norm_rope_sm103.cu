@@ -8,14 +8,19 @@
 //   (dx = g where w is absent).
 //
 // One pass over memory bounds it: 2 bytes in and out an element (forward), 6 (gradient), about
-// ten operations each.  A warp takes four heads of one row at a time, every load 16 bytes a
-// lane: two loads of 128-wide parts (16 lanes a head) for q and two for k_nope, one of the four
-// rope parts (8 lanes a head), all issued before the first is used; the sums are shuffles inside
-// the 16 or 8 lanes.  Each lane makes the cos and sin of one of the 32 frequencies and the
-// others fetch it by shuffle.  Everything between load and store is fp32, rounded once.
-// The gradient's weight sums stay in registers over a warp's whole share of the rows, are joined
-// per block in shared memory and written as one partial row of 384 a block; a second kernel adds
-// the partial rows in a fixed order, so the result does not depend on the run.
+// ten operations each.  The work is a list of warp tasks of four kinds, walked in a grid stride:
+// four (row, head) pairs of q's nope part, the same of k_nope (16 lanes a pair, 16 bytes a lane),
+// the rope parts of eight of q's heads in one row (8 lanes a head), one row's rope key.  One kind at a time keeps few values live, so that the SM holds enough warps
+// to cover memory's latency: 16384 tokens of 128 heads, q and keys, 424 us (6.3 TB/s, 93 % of the
+// measured copy rate); the gradient of 4096 tokens of 64 heads 90 us (5.6 TB/s, 82 %).  With q and
+// k_nope of four heads in one task the registers (104 and 152 a thread) left too few warps: 520 and
+// 175 us.  A task's loads issued while the one before is worked on cost more in registers than they
+// gave (429 and 91 us at 64 and 80 registers).  The sums are shuffles inside the 16 or 8 lanes; each lane makes the cos and sin of one of
+// the 32 frequencies and the others fetch it by shuffle.  Everything between load and store is
+// fp32, rounded once.
+// The gradient's weight sums stay in registers while a warp's tasks are of one kind, then go to
+// the warp's own row in shared memory; a block writes its warps' sum as one partial row of 384, and
+// a second kernel adds the partial rows in a fixed order, so the result does not depend on the run.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,9 +31,13 @@ namespace norm_rope {
 
 constexpr int kDn = 128, kDr = rope::kDr, kDq = kDn + kDr;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kHeads = 4;                       // heads of a row a warp takes at a time
+constexpr int kPairs4 = 4;                      // (row, head) pairs of a nope task
+constexpr int kRopeHeads = 8;                   // heads of a rope task
 constexpr int kDw = 2 * (kDn + kDr);            // weight gradients: q nope, q rope, k nope, k rope
 constexpr int kOffQr = kDn, kOffKn = kDq, kOffKr = kDq + kDn;
+
+// Blocks a SM holds (their registers' share); the grid is at most that many a SM.
+constexpr int kForwardBlocks = 5, kGradBlocks = 4;
 
 struct Params {
   // inputs (any of the three may be absent) and their strides in elements
@@ -39,8 +48,11 @@ struct Params {
   const unsigned long long* turns;
   float eps;
   int H;
-  int groups;  // ceil(H / 4)
-  int tasks;   // R * groups
+  unsigned pairs;        // rows * H
+  unsigned n_qn, n_kn;   // nope tasks of q and of k_nope
+  unsigned n_qr, n_kr;   // rope tasks: rope_groups a row for q, one for the rope key
+  unsigned rope_groups;  // ceil(H / 8)
+  int q_linear, kn_linear;  // row stride == H * head stride: pair i is i head strides in
   // forward: contiguous outputs; gradient: dx with the operands' strides
   uint16_t *qn_out, *qr_out, *kn_out, *kr_out;
   // gradient: contiguous upstream gradients
@@ -110,162 +122,170 @@ __device__ __forceinline__ void norm8_grad(float (&g)[8], const float (&x)[8], c
   }
 }
 
-template <bool kPairs>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const int c16 = lane & 15, c8 = lane & 7;
-  const uint4 w_qn = weights8(p.w_qn, c16), w_qr = weights8(p.w_qr, c8);
-  const uint4 w_kn = weights8(p.w_kn, c16), w_kr = weights8(p.w_kr, c8);
-  const unsigned long long turns = __ldg(p.turns + lane);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (long long task = blockIdx.x * kWarps + (threadIdx.x >> 5); task < p.tasks; task += gridDim.x * kWarps) {
-    const unsigned row32 = static_cast<unsigned>(task) / static_cast<unsigned>(p.groups);
-    const int g = static_cast<int>(static_cast<unsigned>(task) - row32 * p.groups), h0 = g * kHeads;
-    const long long row = row32;
-    const int hn[2] = {h0 + (lane >> 4), h0 + 2 + (lane >> 4)};  // heads of the two nope loads
-    const int hr = h0 + (lane >> 3);                             // head of the rope load
-    const bool rope_key = p.kr && g == 0;
-    uint4 qn[2], kn[2], qr = zero, kr = zero;
+// Element offset of pair i (row * H + head) in an operand with these strides.
+__device__ __forceinline__ long long pair_offset(unsigned i, int H, long long row_stride, long long head_stride,
+                                                 int linear) {
+  if (linear) return i * head_stride;
+  const unsigned row = i / H;
+  return row * row_stride + (i - row * H) * head_stride;
+}
+
+// The nope tasks u, u + step, ... < n of one operand; returns the first u past them.
+template <bool kGrad>
+__device__ __forceinline__ unsigned nope_tasks(const Params& p, unsigned u, unsigned n, unsigned step,
+                                               const uint16_t* x, long long row_stride, long long head_stride,
+                                               int linear, const uint16_t* w, const uint16_t* dy, uint16_t* out,
+                                               size_t out_bytes, float* dw_row) {
+  if (u >= n) return u;
+  const int lane = threadIdx.x & 31, c16 = lane & 15;
+  const uint4 w16 = weights8(w, c16), zero = make_uint4(0, 0, 0, 0);
+  float dw[8] = {};
+  for (; u < n; u += step) {
+    unsigned pair[2];
+    long long off[2];
+    uint4 in[2], up[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      qn[i] = p.q && hn[i] < p.H ? load16(p.q + row * p.q_row + hn[i] * p.q_head + 8 * c16) : zero;
-      kn[i] = p.kn && hn[i] < p.H ? load16(p.kn + row * p.kn_row + hn[i] * p.kn_head + 8 * c16) : zero;
+      pair[i] = u * kPairs4 + 2 * i + (lane >> 4);
+      off[i] = pair_offset(pair[i], p.H, row_stride, head_stride, linear) + 8 * c16;
+      in[i] = pair[i] < p.pairs ? load16(x + off[i]) : zero;
+      if (kGrad) up[i] = pair[i] < p.pairs ? load16(dy + (size_t)pair[i] * kDn + 8 * c16) : zero;
     }
-    if (p.q && hr < p.H) qr = load16(p.q + row * p.q_row + hr * p.q_head + kDn + 8 * c8);
-    if (rope_key && lane < 8) kr = load16(p.kr + row * p.kr_row + 8 * c8);
-    float c, s;
-    rope::cos_sin(__ldg(p.pos + row), turns, c, s);
-    float x[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (p.q) {
-        rope::unpack8(qn[i], x);
-        norm8<16>(x, w_qn, p.w_qn, p.eps);
-        uint4* dst = reinterpret_cast<uint4*>(p.qn_out + (row * p.H + hn[i]) * kDn + 8 * c16);
-        if (hn[i] < p.H && MLA_STORE_OK(dst, p.qn_out, p.qn_bytes, p.err)) *dst = rope::pack8(x);
+      float v[8], g[8];
+      rope::unpack8(in[i], v);
+      uint4* dst;
+      if constexpr (kGrad) {
+        rope::unpack8(up[i], g);
+        norm8_grad<16>(g, v, w16, w, p.eps, pair[i] < p.pairs, dw);
+        dst = reinterpret_cast<uint4*>(out + off[i]);
+      } else {
+        norm8<16>(v, w16, w, p.eps);
+        dst = reinterpret_cast<uint4*>(out + (size_t)pair[i] * kDn + 8 * c16);
       }
-      if (p.kn) {
-        rope::unpack8(kn[i], x);
-        norm8<16>(x, w_kn, p.w_kn, p.eps);
-        uint4* dst = reinterpret_cast<uint4*>(p.kn_out + (row * p.H + hn[i]) * kDn + 8 * c16);
-        if (hn[i] < p.H && MLA_STORE_OK(dst, p.kn_out, p.kn_bytes, p.err)) *dst = rope::pack8(x);
-      }
-    }
-    if (p.q) {
-      rope::unpack8(qr, x);
-      norm8<8>(x, w_qr, p.w_qr, p.eps);
-      rope::rotate8<kPairs, false>(x, c, s, lane);
-      uint4* dst = reinterpret_cast<uint4*>(p.qr_out + (row * p.H + hr) * kDr + 8 * c8);
-      if (hr < p.H && MLA_STORE_OK(dst, p.qr_out, p.qr_bytes, p.err)) *dst = rope::pack8(x);
-    }
-    if (rope_key) {
-      rope::unpack8(kr, x);
-      norm8<8>(x, w_kr, p.w_kr, p.eps);
-      rope::rotate8<kPairs, false>(x, c, s, lane);
-      uint4* dst = reinterpret_cast<uint4*>(p.kr_out + row * kDr + 8 * c8);
-      if (lane < 8 && MLA_STORE_OK(dst, p.kr_out, p.kr_bytes, p.err)) *dst = rope::pack8(x);
+      if (pair[i] < p.pairs && MLA_STORE_OK(dst, out, out_bytes, p.err)) *dst = rope::pack8(kGrad ? g : v);
     }
   }
+  if (kGrad && dw_row) {  // the two lanes that hold the same columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], 16);
+      if (lane < 16) dw_row[8 * lane + i] = dw[i];
+    }
+  }
+  return u;
+}
+
+// The rope tasks u, u + step, ... < n: of q (eight heads of a row, groups tasks a row) or of the
+// rope key (kKey: one "head" a row, and its upstream gradient in fp32).
+template <bool kGrad, bool kPairs, bool kKey>
+__device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsigned n, unsigned step,
+                                               const uint16_t* x, long long row_stride, long long head_stride,
+                                               int heads, unsigned groups, const uint16_t* w, const void* dy,
+                                               uint16_t* out, size_t out_bytes, float* dw_row) {
+  if (u >= n) return u;
+  const int lane = threadIdx.x & 31, c8 = lane & 7;
+  const uint4 w8 = weights8(w, c8), zero = make_uint4(0, 0, 0, 0);
+  const unsigned long long turns = __ldg(p.turns + lane);
+  constexpr int kLoads = kKey ? 1 : 2;
+  float dw[8] = {};
+  for (; u < n; u += step) {
+    const unsigned row32 = kKey || groups == 1 ? u : u / groups;
+    const int h0 = kKey ? 0 : (u - row32 * groups) * kRopeHeads + (lane >> 3);
+    const long long row = row32;
+    const bool mine = !kKey || lane < 8;
+    uint4 in[kLoads], up[kLoads];
+    float4 uk[2] = {};
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int h = h0 + 4 * i;
+      const bool live = mine && h < heads;
+      in[i] = live ? load16(x + row * row_stride + h * head_stride + 8 * c8) : zero;
+      if constexpr (kGrad && kKey) {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(dy) + row * kDr + 8 * c8);
+        if (live) {
+          uk[0] = __ldg(src);
+          uk[1] = __ldg(src + 1);
+        }
+      } else if constexpr (kGrad) {
+        up[i] = live ? load16(static_cast<const uint16_t*>(dy) + (row * heads + h) * kDr + 8 * c8) : zero;
+      }
+    }
+    float c, s;
+    rope::cos_sin(__ldg(p.pos + row), turns, c, s);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int h = h0 + 4 * i;
+      const bool live = mine && h < heads;
+      if (!__any_sync(0xffffffffu, live)) break;
+      float v[8], d[8];
+      rope::unpack8(in[i], v);
+      uint4* dst;
+      if constexpr (kGrad) {
+        if constexpr (kKey) {
+          d[0] = uk[0].x; d[1] = uk[0].y; d[2] = uk[0].z; d[3] = uk[0].w;
+          d[4] = uk[1].x; d[5] = uk[1].y; d[6] = uk[1].z; d[7] = uk[1].w;
+        } else {
+          rope::unpack8(up[i], d);
+        }
+        rope::rotate8<kPairs, true>(d, c, s, lane);
+        norm8_grad<8>(d, v, w8, w, p.eps, live, dw);
+        dst = reinterpret_cast<uint4*>(out + row * row_stride + h * head_stride + 8 * c8);
+      } else {
+        norm8<8>(v, w8, w, p.eps);
+        rope::rotate8<kPairs, false>(v, c, s, lane);
+        dst = reinterpret_cast<uint4*>(out + (row * heads + h) * kDr + 8 * c8);
+      }
+      if (live && MLA_STORE_OK(dst, out, out_bytes, p.err)) *dst = rope::pack8(kGrad ? d : v);
+    }
+  }
+  if (kGrad && dw_row) {  // the four lanes that hold the same columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], 16);
+      dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], 8);
+      if (lane < 8) dw_row[8 * lane + i] = dw[i];
+    }
+  }
+  return u;
+}
+
+// The four kinds of tasks of warp `u` of `step`.
+template <bool kGrad, bool kPairs>
+__device__ __forceinline__ void all_tasks(const Params& p, unsigned u, unsigned step, float* dw_row) {
+  auto at = [&](int off) { return dw_row ? dw_row + off : nullptr; };
+  u = nope_tasks<kGrad>(p, u, p.n_qn, step, p.q, p.q_row, p.q_head, p.q_linear, p.w_qn, p.dqn, p.qn_out, p.qn_bytes,
+                        at(0)) - p.n_qn;
+  u = nope_tasks<kGrad>(p, u, p.n_kn, step, p.kn, p.kn_row, p.kn_head, p.kn_linear, p.w_kn, p.dkn, p.kn_out,
+                        p.kn_bytes, at(kOffKn)) - p.n_kn;
+  // (the gradient of q's rope part lies behind its nope part, as in q)
+  u = rope_tasks<kGrad, kPairs, false>(p, u, p.n_qr, step, p.q + kDn, p.q_row, p.q_head, p.H, p.rope_groups, p.w_qr,
+                                       p.dqr, kGrad ? p.qn_out + kDn : p.qr_out,
+                                       kGrad ? p.qn_bytes - 2 * kDn : p.qr_bytes, at(kOffQr)) - p.n_qr;
+  rope_tasks<kGrad, kPairs, true>(p, u, p.n_kr, step, p.kr, p.kr_row, 0, 1, 1, p.w_kr, p.dkr, p.kr_out, p.kr_bytes,
+                                  at(kOffKr));
 }
 
 template <bool kPairs>
-__global__ void __launch_bounds__(kThreads) norm_rope_grad_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_rope_kernel(const Params p) {
+  const unsigned step = gridDim.x * kWarps;
+  all_tasks<false, kPairs>(p, blockIdx.x * kWarps + (threadIdx.x >> 5), step, nullptr);
+}
+
+template <bool kPairs>
+__global__ void __launch_bounds__(kThreads, kGradBlocks) norm_rope_grad_kernel(const Params p) {
   __shared__ float joined[kWarps][kDw];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c16 = lane & 15, c8 = lane & 7;
-  const uint4 w_qn = weights8(p.w_qn, c16), w_qr = weights8(p.w_qr, c8);
-  const uint4 w_kn = weights8(p.w_kn, c16), w_kr = weights8(p.w_kr, c8);
-  const unsigned long long turns = __ldg(p.turns + lane);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  float dw_qn[8] = {}, dw_qr[8] = {}, dw_kn[8] = {}, dw_kr[8] = {};
-  for (long long task = blockIdx.x * kWarps + warp; task < p.tasks; task += gridDim.x * kWarps) {
-    const unsigned row32 = static_cast<unsigned>(task) / static_cast<unsigned>(p.groups);
-    const int g = static_cast<int>(static_cast<unsigned>(task) - row32 * p.groups), h0 = g * kHeads;
-    const long long row = row32;
-    const int hn[2] = {h0 + (lane >> 4), h0 + 2 + (lane >> 4)};
-    const int hr = h0 + (lane >> 3);
-    const bool rope_key = p.kr && g == 0;
-    uint4 qn[2], kn[2], dqn[2], dkn[2], qr = zero, dqr = zero;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool q_in = p.q && hn[i] < p.H, k_in = p.kn && hn[i] < p.H;
-      qn[i] = q_in ? load16(p.q + row * p.q_row + hn[i] * p.q_head + 8 * c16) : zero;
-      dqn[i] = q_in ? load16(p.dqn + (row * p.H + hn[i]) * kDn + 8 * c16) : zero;
-      kn[i] = k_in ? load16(p.kn + row * p.kn_row + hn[i] * p.kn_head + 8 * c16) : zero;
-      dkn[i] = k_in ? load16(p.dkn + (row * p.H + hn[i]) * kDn + 8 * c16) : zero;
-    }
-    if (p.q && hr < p.H) {
-      qr = load16(p.q + row * p.q_row + hr * p.q_head + kDn + 8 * c8);
-      dqr = load16(p.dqr + (row * p.H + hr) * kDr + 8 * c8);
-    }
-    float c, s;
-    rope::cos_sin(__ldg(p.pos + row), turns, c, s);
-    float x[8], d[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool live = hn[i] < p.H;
-      if (p.q) {
-        rope::unpack8(qn[i], x);
-        rope::unpack8(dqn[i], d);
-        norm8_grad<16>(d, x, w_qn, p.w_qn, p.eps, live, dw_qn);
-        uint4* dst = reinterpret_cast<uint4*>(p.qn_out + row * p.q_row + hn[i] * p.q_head + 8 * c16);
-        if (live && MLA_STORE_OK(dst, p.qn_out, p.qn_bytes, p.err)) *dst = rope::pack8(d);
-      }
-      if (p.kn) {
-        rope::unpack8(kn[i], x);
-        rope::unpack8(dkn[i], d);
-        norm8_grad<16>(d, x, w_kn, p.w_kn, p.eps, live, dw_kn);
-        uint4* dst = reinterpret_cast<uint4*>(p.kn_out + row * p.kn_row + hn[i] * p.kn_head + 8 * c16);
-        if (live && MLA_STORE_OK(dst, p.kn_out, p.kn_bytes, p.err)) *dst = rope::pack8(d);
-      }
-    }
-    if (p.q) {
-      rope::unpack8(qr, x);
-      rope::unpack8(dqr, d);
-      rope::rotate8<kPairs, true>(d, c, s, lane);
-      norm8_grad<8>(d, x, w_qr, p.w_qr, p.eps, hr < p.H, dw_qr);
-      uint4* dst = reinterpret_cast<uint4*>(p.qn_out + row * p.q_row + hr * p.q_head + kDn + 8 * c8);
-      if (hr < p.H && MLA_STORE_OK(dst, p.qn_out, p.qn_bytes, p.err)) *dst = rope::pack8(d);
-    }
-    if (rope_key) {
-      uint4 kr = zero;
-      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-      if (lane < 8) {
-        kr = load16(p.kr + row * p.kr_row + 8 * c8);
-        const float4* src = reinterpret_cast<const float4*>(p.dkr + row * kDr + 8 * c8);
-        lo = __ldg(src);
-        hi = __ldg(src + 1);
-      }
-      rope::unpack8(kr, x);
-      d[0] = lo.x; d[1] = lo.y; d[2] = lo.z; d[3] = lo.w;
-      d[4] = hi.x; d[5] = hi.y; d[6] = hi.z; d[7] = hi.w;
-      rope::rotate8<kPairs, true>(d, c, s, lane);
-      norm8_grad<8>(d, x, w_kr, p.w_kr, p.eps, lane < 8, dw_kr);
-      uint4* dst = reinterpret_cast<uint4*>(p.kr_out + row * p.kr_row + 8 * c8);
-      if (lane < 8 && MLA_STORE_OK(dst, p.kr_out, p.kr_bytes, p.err)) *dst = rope::pack8(d);
-    }
+  const int warp = threadIdx.x >> 5;
+  const unsigned step = gridDim.x * kWarps;
+  float* mine = nullptr;
+  if (p.partial) {  // a warp need not meet every kind of task
+    mine = joined[warp];
+    for (int i = threadIdx.x & 31; i < kDw; i += 32) mine[i] = 0.f;
+    __syncwarp();
   }
+  all_tasks<true, kPairs>(p, blockIdx.x * kWarps + warp, step, mine);
   if (!p.partial) return;
-  // the lanes of a warp that hold the same columns, then the block's warps in order
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    dw_qn[i] += __shfl_xor_sync(0xffffffffu, dw_qn[i], 16);
-    dw_kn[i] += __shfl_xor_sync(0xffffffffu, dw_kn[i], 16);
-    dw_qr[i] += __shfl_xor_sync(0xffffffffu, dw_qr[i], 16);
-    dw_qr[i] += __shfl_xor_sync(0xffffffffu, dw_qr[i], 8);
-  }
-  float* mine = joined[warp];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (lane < 16) {
-      mine[8 * lane + i] = dw_qn[i];
-      mine[kOffKn + 8 * lane + i] = dw_kn[i];
-    }
-    if (lane < 8) {
-      mine[kOffQr + 8 * lane + i] = dw_qr[i];
-      mine[kOffKr + 8 * lane + i] = dw_kr[i];
-    }
-  }
   __syncthreads();
   for (int col = threadIdx.x; col < kDw; col += kThreads) {
     float v = 0.f;
@@ -303,9 +323,10 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restri
   }
 }
 
-// Blocks of a persistent launch: at most four (forward) or three (gradient) a SM, what their
-// registers leave room for.
-constexpr int kForwardBlocks = 4, kGradBlocks = 3;
+inline unsigned nope_count(long long rows, int H) { return static_cast<unsigned>((rows * H + kPairs4 - 1) / kPairs4); }
+inline unsigned rope_count(long long rows, int H) { return static_cast<unsigned>(rows * ((H + kRopeHeads - 1) / kRopeHeads)); }
+
+inline long long task_count(const Params& p) { return (long long)p.n_qn + p.n_kn + p.n_qr + p.n_kr; }
 
 inline int blocks_for(long long tasks, int per_sm, int sms) {
   return static_cast<int>(std::min<long long>((tasks + kWarps - 1) / kWarps, (long long)per_sm * sms));
@@ -313,9 +334,11 @@ inline int blocks_for(long long tasks, int per_sm, int sms) {
 
 }  // namespace norm_rope
 
+// Partial rows of the largest launch for these sizes (all operands given).
 size_t norm_rope_grad_workspace_bytes(long long rows, int H, int sms) {
   using namespace norm_rope;
-  return (size_t)blocks_for(rows * ((H + kHeads - 1) / kHeads), kGradBlocks, sms) * kDw * sizeof(float);
+  const long long tasks = 2LL * nope_count(rows, H) + rope_count(rows, H) + rows;
+  return (size_t)blocks_for(tasks, kGradBlocks, sms) * kDw * sizeof(float);
 }
 
 namespace {
@@ -342,8 +365,14 @@ norm_rope::Params shared_params(const void* q, long long q_row, long long q_head
   p.turns = static_cast<const unsigned long long*>(turns);
   p.eps = eps;
   p.H = H;
-  p.groups = (H + norm_rope::kHeads - 1) / norm_rope::kHeads;
-  p.tasks = static_cast<int>(rows * p.groups);  // the caller keeps rows * groups below 2^31
+  p.pairs = static_cast<unsigned>(rows * H);  // the caller keeps rows * H at most 0x70000000
+  p.n_qn = q ? norm_rope::nope_count(rows, H) : 0;
+  p.n_kn = kn ? norm_rope::nope_count(rows, H) : 0;
+  p.n_qr = q ? norm_rope::rope_count(rows, H) : 0;
+  p.n_kr = kr ? static_cast<unsigned>(rows) : 0;
+  p.rope_groups = (H + norm_rope::kRopeHeads - 1) / norm_rope::kRopeHeads;
+  p.q_linear = q_row == H * q_head;
+  p.kn_linear = kn_row == H * kn_head;
   p.err = err;
   return p;
 }
@@ -368,7 +397,7 @@ cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_h
   p.qr_bytes = (size_t)rows * H * kDr * 2;
   p.kn_bytes = (size_t)rows * H * kDn * 2;
   p.kr_bytes = (size_t)rows * kDr * 2;
-  const int grid = blocks_for(p.tasks, kForwardBlocks, sms);
+  const int grid = blocks_for(task_count(p), kForwardBlocks, sms);
   if (pairs)
     norm_rope_kernel<true><<<grid, kThreads, 0, stream>>>(p);
   else
@@ -398,7 +427,7 @@ cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const 
   p.qn_bytes -= std::min(p.qn_bytes, testing_out_shrink());
   p.kn_bytes = ((rows - 1) * kn_row + (H - 1) * kn_head + kDn) * 2;
   p.kr_bytes = ((rows - 1) * kr_row + kDr) * 2;
-  const int grid = blocks_for(p.tasks, kGradBlocks, sms);
+  const int grid = blocks_for(task_count(p), kGradBlocks, sms);
   const bool weights = dw_qn || dw_qr || dw_kn || dw_kr;
   p.partial = weights ? workspace : nullptr;
   p.partial_bytes = (size_t)grid * kDw * sizeof(float);

@@ -15,11 +15,16 @@ namespace rope {
 
 constexpr int kDr = 64, kFreqs = kDr / 2;
 
-// cos and sin of frequency `turns` at position `pos` (any int32, negative ones included)
+// cos and sin of frequency `turns` at position `pos` (any int32, negative ones included).  The
+// angle lies in [-pi, pi), where the fast sine and cosine are within 2^-21 of the true ones: results
+// are rounded to 8 bits or fewer, and the accurate functions took a quarter of the append's
+// instructions.
 __device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float& c, float& s) {
   const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
-  // the top 32 bits, as a signed fraction of a turn in [-1/2, 1/2); sincospif takes half turns
-  sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);
+  // the top 32 bits, as a signed fraction of a turn in [-1/2, 1/2): times 2 pi 2^-32
+  const float angle = static_cast<float>(static_cast<int>(phase >> 32)) * 1.4629180792671596e-9f;
+  s = __sinf(angle);
+  c = __cosf(angle);
 }
 
 // Eight consecutive bf16 as floats, and back (round to nearest even).
