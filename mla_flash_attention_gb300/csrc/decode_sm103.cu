@@ -82,6 +82,9 @@ constexpr int kSmemAlloc = kSmemBytes + 1024;
 // bf16: 8 warps; fp8: 12 (four more page-widening warps)
 template <bool kFp8> constexpr int kThreadsOf = kFp8 ? 384 : 256;
 template <bool kFp8> constexpr int kPrepOf = kFp8 ? 192 : 64;
+// a tree's item in at most this many splits is merged by the split that finishes last, from its
+// accumulator and one bulk copy
+constexpr int kFusedSplits = 2;
 constexpr int kPrefetchAhead = 4;             // pages warmed in L2 ahead of their load
 
 struct Params {
@@ -93,6 +96,10 @@ struct Params {
   const int* cache_lens;
   float* part_o;
   float* part_lse;   // [2][n_slots][TQ]: each column half writes its own copy
+  // [G] tree: {item + 1, its splits} if the item whose second split is unit c's is left to the merge
+  // kernel, else 0, zeroed per call.  They lie in the last of the n_slots slots of part_o, which no
+  // split uses (unit c and item v share slot c + v <= G - 1 + B * NQT - 1).
+  int2* deferred;
   int* counters;     // [B * NQT][2]: finished splits per (virtual sequence, half), zeroed per call
   uint16_t* out;     // [B, T, H, 512] bf16
   float* lse;        // [B, H, T]
@@ -878,6 +885,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const int c_first = segs.flat0 / bars.plan.chunk;
       const int nsplit = (segs.flat0 + n_pages - 1) / bars.plan.chunk - c_first + 1;
       const int k_own = unit - c_first;
+      // a tree's item in more splits than that is merged by the kernel behind this one
+      const bool deferred = kTree && nsplit > kFusedSplits;
       // Merge path.  A split that finds every other split of this (sequence, column half)
       // counted in (always so for a sequence with one split) merges at once, its own share
       // read from the accumulator.  Otherwise it writes its partial (O_half / l, LSE), makes
@@ -895,7 +904,13 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       }
       if (r == 0) {
         int fast = 1, bulk = 0;
-        if (nsplit > 1) {
+        if (deferred) {
+          fast = 0;
+          if (half == 0 && k_own == 1) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // zeroed before
+            p.deferred[unit] = make_int2(seq + 1, nsplit);
+          }
+        } else if (nsplit > 1) {
           // the counters were zeroed by the kernel this one was launched behind
           asm volatile("griddepcontrol.wait;" ::: "memory");
           fast = ptx::ld_acquire_gpu(p.counters + (size_t)seq * 2 + half) == nsplit - 1;
@@ -949,6 +964,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         }
         float* plp = p.part_lse + ((size_t)half * p.n_slots + slot) * TQ + r;
         if (row_live && MLA_STORE_OK(plp, p.part_lse, p.part_lse_bytes, p.err)) *plp = lse_own;
+      }
+      if (!own_in_tmem && !deferred) {
         __threadfence();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bars.part_done);
@@ -1114,10 +1131,88 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   }
 }
 
+// Merges the tree items that went into more than kFusedSplits splits, all over the GPU: block
+// (c, y) takes 32 rows and 32 column quads of the item whose second split is unit c's, if there is
+// one.  Left to the split that finishes last, the merge reads every partial through one SM, about
+// 4 us a split: one sequence of 1000 keys and 128 rows, in 16 splits, took 68 us, 50 of them there.
+// The splits are weighed and summed in split order, as in the split kernel's own merge.
+constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeQuads = 32;
+constexpr int kMaxSplits = 128;
+static_assert(kMaxSplits * sizeof(int2) <= kDl * sizeof(float), "a slot of one row holds the deferred items");
+
+__global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Params p) {
+  __shared__ float weight[kMaxSplits][kMergeRows];
+  const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel is done
+  const int2 d = __ldcg(p.deferred + unit);
+  if (d.x == 0) return;
+  const int item = d.x - 1, nsplit = d.y, c_first = unit - 1;
+  const int r = (blockIdx.y & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
+  const bool live = r < p.TQ && gr < p.T * p.H;
+  const int q0 = (blockIdx.y >> 2) * kMergeQuads, half = q0 / 64;
+  const float* lsp = p.part_lse + ((size_t)half * p.n_slots + c_first + item) * p.TQ + r;
+  if (warp == 0) {
+    float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < nsplit; ++k) {
+      const float ls = live ? ptx::ld_l2(lsp + (size_t)k * p.TQ) : -INFINITY;
+      weight[k][lane] = ls;
+      mx = fmaxf(mx, ls);
+    }
+    for (int k = 0; k < nsplit; ++k) {
+      const float ls = weight[k][lane];
+      const float w = ls != ls ? ls : ls == -INFINITY ? 0.f : __expf(ls - mx);
+      weight[k][lane] = w;
+      sum += w;
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    for (int k = 0; k < nsplit; ++k) weight[k][lane] *= inv;
+    float* lp = p.lse + ((size_t)(item / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
+    if (q0 == 0 && live && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err))
+      *lp = sum != 0.f ? mx + logf(sum) : -INFINITY;
+  }
+  __syncthreads();
+  if (!live) return;
+  // four column quads (32 bytes of a bf16 row) a thread, four splits' loads in flight
+  const int q = q0 + 4 * warp;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((size_t)(c_first + item) * 128 + q) * p.TQ + r;
+  const size_t slot_stride = (size_t)128 * p.TQ;
+  float4 acc[4] = {};
+  for (int k0 = 0; k0 < nsplit; k0 += 4) {
+    float4 x[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[kk][j] = k0 + kk < nsplit ? ptx::ld_l2(src + (k0 + kk) * slot_stride + (size_t)j * p.TQ)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const float w = k0 + kk < nsplit ? weight[k0 + kk][lane] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j].x = fmaf(w, x[kk][j].x, acc[j].x);
+        acc[j].y = fmaf(w, x[kk][j].y, acc[j].y);
+        acc[j].z = fmaf(w, x[kk][j].z, acc[j].z);
+        acc[j].w = fmaf(w, x[kk][j].w, acc[j].w);
+      }
+    }
+  }
+  uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)(item / p.NQT) * p.T * p.H + gr) * kDl + q * 4);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (MLA_STORE_OK(o + j, p.out, p.out_bytes, p.err))
+      o[j] = make_uint4(ptx::pack_bf16x2(acc[2 * j].x, acc[2 * j].y), ptx::pack_bf16x2(acc[2 * j].z, acc[2 * j].w),
+                        ptx::pack_bf16x2(acc[2 * j + 1].x, acc[2 * j + 1].y),
+                        ptx::pack_bf16x2(acc[2 * j + 1].z, acc[2 * j + 1].w));
+}
+
 // Zeroes the split counters of a decode call; the split kernel is launched behind it as a
 // programmatic dependent and waits for it only where it first touches a counter.
-__global__ void __launch_bounds__(256) zero_counters_kernel(int* __restrict__ c, int n) {
+__global__ void __launch_bounds__(256) zero_counters_kernel(int* __restrict__ c, int n,
+                                                               int2* __restrict__ deferred, int units) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x < units) deferred[threadIdx.x] = make_int2(0, 0);
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) c[i] = 0;
 }
 
@@ -1159,6 +1254,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
       &tm, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_cache,
       dims, strides, box, /*swizzle128=*/!fp8);
   if (e != cudaSuccess) return e;
+  if (tree_mask && G > kMaxSplits) return cudaErrorNotSupported;  // the merge kernel's tables
   // The same bytes as a 3-D tensor (64 columns of a chunk, row, chunk of 64 columns): a box
   // of 64 x 64 x n is n consecutive 64-column chunks of a page, landing chunk-major exactly as
   // n 2-D boxes do (one TMA instruction instead of n): fp8 pages take one box of nine chunks,
@@ -1216,6 +1312,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   p.mask_stride = mask_stride;
   p.mask_words = (T + 31) / 32;
   p.new_lens = new_lens;
+  p.deferred = reinterpret_cast<int2*>(part_o + (size_t)(p.n_slots - 1) * TQ * kDl);
   p.page_box = page_box ? 1 : 0;
   // one flat page charged per work item (its Q load, epilogue and merge; measured against
   // 0, 2 and 4 on uniform and ragged batches: the same time for 64 sequences of 4096 keys,
@@ -1240,7 +1337,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     __atomic_store_n(&carveout_set, 1, __ATOMIC_RELEASE);
   }
   const int zero_blocks = (int)std::min<long long>((n_cnt + 2047) / 2048, 1024);
-  zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt);
+  zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt, p.deferred, tree_mask ? G : 0);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto go = [&](auto kern) -> cudaError_t {
     static unsigned long long smem_set[4] = {0, 0, 0, 0};
@@ -1260,7 +1357,19 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, tm, tm_page, tm_c4, tm_c5, tm_qlat, tm_qrope, p);
   };
-  if (tree_mask) return fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>);
+  if (tree_mask) {
+    if ((e = fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G, (kRows / kMergeRows) * (128 / kMergeQuads));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p);
+  }
   return fp8 ? go(decode_split_kernel<true, false>) : go(decode_split_kernel<false, false>);
 }
 
