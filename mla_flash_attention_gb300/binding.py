@@ -8,13 +8,18 @@ module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
 from typing import Optional
 
 import torch
+
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("the marshalling module is not built (%s); run "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`" % e) from e
 
 # MLA_GB300_LIB selects another build of the same library, e.g. the bounds-checked
 # libmla_gb300_debug.so (mla_flash_attention_gb300.build.build(debug=True))
@@ -381,54 +386,28 @@ def mla_decode_noalloc(q_latent, q_rope, kv_cache, page_table, cache_lens, kv_sc
 
 # ------------------------------------------------- around the attention: norms, rotation, trees
 
-_HERE = contextlib.nullcontext()
+# Their arguments are checked, their outputs and workspaces allocated and the C entry points
+# called by the compiled module _marshal (csrc/marshal.cpp): in Python that took several times as
+# long as the kernels of a decode step.
+
+def _address(f) -> int:
+    return ctypes.cast(f, ctypes.c_void_p).value
 
 
-def _launching(dev, stream):
-    """The context of a call on tensors of `dev`: that device current, `stream` (if one is given)
-    the stream that outputs and workspaces are allocated and the kernels launched on."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("stream must be on the tensors' device %s (got %s)" % (dev, stream.device))
-        return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+_marshal.connect(_address(_lib.mla_qk_norm_rope), _address(_lib.mla_qk_norm_rope_backward),
+                 _address(_lib.mla_qk_norm_rope_backward_workspace_size), _address(_lib.mla_rope_append),
+                 _address(_lib.mla_decode_tree), _address(_lib.mla_decode_workspace_size), _check)
 
 
-def _take(t, name, dtype, shape, dev=None, strided=False):
-    """_need for a tensor that may also have to be on device `dev`; strided: any strides with the
-    last dimension contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must have dtype %s (got %s)" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if dev is not None and t.device != dev:
-        raise ValueError("%s must be on %s (got %s)" % (name, dev, t.device))
-    if strided:
-        if t.stride(-1) != 1 and t.shape[-1] != 1:
-            raise ValueError("%s must have a contiguous last dimension" % name)
-    elif not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-
-
-def _scratch(t, dev):
-    """Checks a workspace passed in: contiguous bytes on the device of the call."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-
-
-def _row_stride(t, name):
-    """Elements from one token of t [B, S, ...] to the next, over all B * S tokens."""
-    B, S = t.shape[:2]
-    sb, ss = t.stride()[:2]
-    if S == 1:
-        return sb if B > 1 else t.shape[-1]  # a single token's strides may be anything
-    if B > 1 and sb != S * ss:
-        raise ValueError("%s: the B and S dimensions must have one stride (got %d and %d)" % (name, sb, ss))
-    return ss
+def _call(stream, tensor, f, *args):
+    """f(*args) with `stream` (a torch.cuda.Stream) the stream that outputs and workspaces are
+    allocated and the kernels launched on; None: the current stream of the tensors' device."""
+    if stream is None:
+        return f(*args)
+    if isinstance(tensor, torch.Tensor) and stream.device != tensor.device:
+        raise ValueError("stream must be on the tensors' device %s (got %s)" % (tensor.device, stream.device))
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def rope_turns(inv_freq, device=None) -> torch.Tensor:
@@ -469,40 +448,6 @@ def tree_mask_from_parents(parents):
     return words.to(dev), (sees.sum(-1).to(torch.int32) - 1).to(dev)
 
 
-def _qk_operands(q, k_nope, k_rope, weights, positions, turns):
-    """Checks the operands the norm-and-rotation calls share; returns (B, S, H, dn, dr, device,
-    the C arguments q .. k_rope_row_stride)."""
-    bf = torch.bfloat16
-    some = q if q is not None else k_nope if k_nope is not None else k_rope
-    if some is None:
-        raise ValueError("one of q, k_nope, k_rope must be given")
-    for t, n, dims in ((q, "q", 4), (k_nope, "k_nope", 4), (k_rope, "k_rope", 3)):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != dims):
-            raise ValueError("%s must be a tensor of %d dimensions" % (n, dims))
-    B, S = some.shape[:2]
-    H = some.shape[2] if some.dim() == 4 else 1
-    dr = 2 * turns.numel() if isinstance(turns, torch.Tensor) else 64
-    dn = q.shape[3] - dr if q is not None else k_nope.shape[3] if k_nope is not None else 128
-    dev = some.device
-    args = []
-    for t, n, shape in ((q, "q", (B, S, H, dn + dr)), (k_nope, "k_nope", (B, S, H, dn)),
-                        (k_rope, "k_rope", (B, S, dr))):
-        if t is None:
-            args += [None, 0, 0] if n != "k_rope" else [None, 0]
-            continue
-        _take(t, n, bf, shape, dev, strided=True)
-        args += [t.data_ptr(), _row_stride(t, n)]
-        if n != "k_rope":
-            args.append(t.stride(2) if H > 1 else t.shape[3])
-    for w, n, d in zip(weights, ("q_nope_weight", "q_rope_weight", "k_nope_weight", "k_rope_weight"),
-                       (dn, dr, dn, dr)):
-        if w is not None:
-            _take(w, n, bf, (d,), dev)
-    _take(positions, "positions", torch.int32, (B, S), dev)
-    _take(turns, "rope_turns", torch.int64, (dr // 2,), dev)
-    return B, S, H, dn, dr, dev, args
-
-
 def mla_qk_norm_rope(q=None, k_nope=None, k_rope=None, *, positions, rope_turns, q_nope_weight=None,
                      q_rope_weight=None, k_nope_weight=None, k_rope_weight=None, eps: float = 1e-6,
                      interleaved: bool = True, out=None, stream=None):
@@ -514,21 +459,9 @@ def mla_qk_norm_rope(q=None, k_nope=None, k_rope=None, *, positions, rope_turns,
     positions [B,S] int32; rope_turns from ``rope_turns()``.  Returns (q_nope [B,S,H,dn],
     q_rope [B,S,H,dr], k_nope, k_rope), contiguous bf16, None for operands not given; ``out``
     may pass those four preallocated."""
-    weights = (q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight)
-    B, S, H, dn, dr, dev, args = _qk_operands(q, k_nope, k_rope, weights, positions, rope_turns)
-    shapes = ((B, S, H, dn) if q is not None else None, (B, S, H, dr) if q is not None else None,
-              (B, S, H, dn) if k_nope is not None else None, (B, S, dr) if k_rope is not None else None)
-    with _launching(dev, stream):
-        if out is None:
-            out = tuple(None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
-        else:
-            for t, n, s in zip(out, ("out[0]", "out[1]", "out[2]", "out[3]"), shapes):
-                if s is not None:
-                    _take(t, n, torch.bfloat16, s, dev)
-        _check(_lib.mla_qk_norm_rope(
-            *args, *(_ptr(w) for w in weights), _ptr(positions), _ptr(rope_turns), float(eps), int(bool(interleaved)),
-            *(None if s is None else _ptr(t) for t, s in zip(out, shapes)), B * S, H, dn, dr, _stream(stream)))
-    return tuple(None if s is None else t for t, s in zip(out, shapes))
+    return _call(stream, q if q is not None else k_nope if k_nope is not None else k_rope, _marshal.qk_norm_rope,
+                 q, k_nope, k_rope, positions, rope_turns, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+                 eps, interleaved, out)
 
 
 def qk_norm_rope_backward_workspace_size(rows: int, H: int) -> int:
@@ -545,46 +478,10 @@ def mla_qk_norm_rope_backward(dq_nope, dq_rope, dk_nope, dk_rope, q=None, k_nope
     dq_rope_weight, dk_nope_weight, dk_rope_weight): bf16 with the operands' own strides, the
     weights' in fp32, None for what was not given.  ``grads`` may pass those seven
     preallocated (e.g. dk_nope as a view of a joint key and value gradient)."""
-    bf, f32 = torch.bfloat16, torch.float32
-    weights = (q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight)
-    B, S, H, dn, dr, dev, args = _qk_operands(q, k_nope, k_rope, weights, positions, rope_turns)
-    ups = []
-    for t, n, given, dt, s in ((dq_nope, "dq_nope", q, bf, (B, S, H, dn)), (dq_rope, "dq_rope", q, bf, (B, S, H, dr)),
-                               (dk_nope, "dk_nope", k_nope, bf, (B, S, H, dn)),
-                               (dk_rope, "dk_rope", k_rope, f32, (B, S, dr))):
-        if given is not None:
-            _take(t, n, dt, s, dev)
-        ups.append(None if given is None else _ptr(t))
-    with _launching(dev, stream):
-        if grads is None:
-            grads = [None if t is None else torch.empty_strided(t.shape, t.stride(), dtype=bf, device=dev)
-                     for t in (q, k_nope, k_rope)]
-            grads += [None if w is None else torch.empty(w.shape, dtype=f32, device=dev) for w in weights]
-        else:
-            grads = list(grads)
-            if len(grads) != 7:
-                raise ValueError("grads must hold seven tensors (None for those not given)")
-            for i, t in enumerate((q, k_nope, k_rope)):
-                if t is not None:
-                    _take(grads[i], "grads[%d]" % i, bf, t.shape, dev, strided=True)
-                    if any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), grads[i].stride())):
-                        raise ValueError("grads[%d] must have its operand's strides" % i)
-            for i, w in enumerate(weights):
-                if w is not None:
-                    _take(grads[3 + i], "grads[%d]" % (3 + i), f32, w.shape, dev)
-        given = (q, k_nope, k_rope) + weights
-        grads = tuple(None if g is None else t for t, g in zip(grads, given))
-        if workspace is not None:
-            _scratch(workspace, dev)
-        elif any(w is not None for w in weights):
-            workspace = torch.empty(max(qk_norm_rope_backward_workspace_size(B * S, H), 16), dtype=torch.uint8,
-                                    device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(_lib.mla_qk_norm_rope_backward(
-            *ups, *args, *(_ptr(w) for w in weights), _ptr(positions), _ptr(rope_turns), float(eps),
-            int(bool(interleaved)), *(_ptr(g) for g in grads), B * S, H, dn, dr, _ptr(workspace), ws_bytes,
-            _stream(stream)))
-    return grads
+    return _call(stream, q if q is not None else k_nope if k_nope is not None else k_rope,
+                 _marshal.qk_norm_rope_backward, q, k_nope, k_rope, positions, rope_turns, q_nope_weight,
+                 q_rope_weight, k_nope_weight, k_rope_weight, eps, interleaved, dq_nope, dq_rope, dk_nope, dk_rope,
+                 grads, workspace)
 
 
 def mla_rope_append(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, rope_turns, norm_weight=None,
@@ -595,38 +492,8 @@ def mla_rope_append(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, r
     token's place in its sequence); new_lens int32 [B] (None: q_len): the tokens of each
     sequence that are real, its rows behind them padding.  Modifies kv_cache (and kv_scale) in
     place and returns them."""
-    bf, i32 = torch.bfloat16, torch.int32
-    if not isinstance(c_new, torch.Tensor) or c_new.dim() != 3:
-        raise ValueError("c_new must be a tensor of 3 dimensions")
-    if not isinstance(kv_cache, torch.Tensor) or kv_cache.dim() != 3:
-        raise ValueError("kv_cache must be a tensor of 3 dimensions")
-    B, T, D = c_new.shape
-    num_pages, page_size, _ = kv_cache.shape
-    dev = c_new.device
-    fp8 = kv_cache.dtype == torch.float8_e4m3fn
-    _take(c_new, "c_new", bf, (B, T, D), strided=True)
-    _take(kv_cache, "kv_cache", torch.float8_e4m3fn if fp8 else bf, (num_pages, page_size, D), dev)
-    if fp8:
-        _take(kv_scale, "kv_scale", torch.float32, (num_pages, page_size), dev)
-    elif kv_scale is not None:
-        raise ValueError("kv_scale is only used with an fp8 cache")
-    max_pages = page_table.shape[1]
-    _take(page_table, "page_table", i32, (B, max_pages), dev)
-    _take(cache_lens, "cache_lens", i32, (B,), dev)
-    dr = 2 * rope_turns.numel()
-    _take(rope_turns, "rope_turns", torch.int64, (dr // 2,), dev)
-    if norm_weight is not None:
-        _take(norm_weight, "norm_weight", bf, (D - dr,), dev)
-    if positions is not None:
-        _take(positions, "positions", i32, (B, T), dev)
-    if new_lens is not None:
-        _take(new_lens, "new_lens", i32, (B,), dev)
-    with _launching(dev, stream):
-        _check(_lib.mla_rope_append(
-            _ptr(c_new), _row_stride(c_new, "c_new"), _ptr(norm_weight), float(eps),
-            _ptr(positions), _ptr(rope_turns), int(bool(interleaved)), _ptr(kv_cache), _ptr(kv_scale),
-            _ptr(page_table), _ptr(cache_lens), _ptr(new_lens), B, T, D - dr, dr, page_size, max_pages, num_pages,
-            MLA_FP8_E4M3 if fp8 else MLA_BF16, _stream(stream)))
+    _call(stream, c_new, _marshal.rope_append, c_new, kv_cache, kv_scale, page_table, cache_lens, new_lens, rope_turns,
+          norm_weight, eps, positions, interleaved)
     return kv_cache, kv_scale
 
 
@@ -637,43 +504,5 @@ def mla_decode_tree(q_latent, q_rope, kv_cache, page_table, cache_lens, tree_mas
     says whether token t sees drafted token j; the prefix is seen by all.  new_lens int32 [B]
     (None: q_len): the drafted tokens of each sequence, the newest of its cache; the rows behind
     them are padding (O = 0, LSE = -inf).  The rest is as for mla_decode."""
-    bf, i32 = torch.bfloat16, torch.int32
-    B, T, H, dl = q_latent.shape
-    dr = q_rope.shape[-1]
-    num_pages, page_size, _ = kv_cache.shape
-    dev = q_latent.device
-    fp8 = kv_cache.dtype == torch.float8_e4m3fn
-    _take(q_latent, "q_latent", bf, (B, T, H, dl))
-    _take(q_rope, "q_rope", bf, (B, T, H, dr), dev)
-    _take(kv_cache, "kv_cache", torch.float8_e4m3fn if fp8 else bf, (num_pages, page_size, dl + dr), dev)
-    if fp8:
-        _take(kv_scale, "kv_scale", torch.float32, (num_pages, page_size), dev)
-    elif kv_scale is not None:
-        raise ValueError("kv_scale is only used with an fp8 cache")
-    max_pages = page_table.shape[1]
-    _take(page_table, "page_table", i32, (B, max_pages), dev)
-    _take(cache_lens, "cache_lens", i32, (B,), dev)
-    words = (T + 31) // 32
-    shared = isinstance(tree_mask, torch.Tensor) and tree_mask.dim() == 2
-    _take(tree_mask, "tree_mask", i32, (T, words) if shared else (B, T, words), dev)
-    if new_lens is not None:
-        _take(new_lens, "new_lens", i32, (B,), dev)
-    with _launching(dev, stream):
-        if out is None:
-            out = torch.empty((B, T, H, dl), dtype=bf, device=dev)
-        else:
-            _take(out, "out", bf, (B, T, H, dl), dev)
-        if lse is None:
-            lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-        else:
-            _take(lse, "lse", torch.float32, (B, H, T), dev)
-        if workspace is None:
-            workspace = torch.empty(max(decode_workspace_size(B, H, T, dl), 16), dtype=torch.uint8, device=dev)
-        else:
-            _scratch(workspace, dev)
-        _check(_lib.mla_decode_tree(
-            _ptr(q_latent), _ptr(q_rope), _ptr(kv_cache), _ptr(kv_scale), _ptr(page_table), _ptr(cache_lens),
-            _ptr(tree_mask), 0 if shared else T * words, _ptr(new_lens), _ptr(out), _ptr(lse), B, H, T, dl, dr,
-            page_size, max_pages, num_pages, float(softmax_scale), MLA_FP8_E4M3 if fp8 else MLA_BF16,
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
-    return out, lse
+    return _call(stream, q_latent, _marshal.decode_tree, q_latent, q_rope, kv_cache, kv_scale, page_table, cache_lens,
+                 new_lens, tree_mask, softmax_scale, out, lse, workspace)
