@@ -29,11 +29,17 @@
 //               (O_half / l, log-sum-exp), column quads of 32 rows per 512-byte store, and,
 //               in the CTA that completes a (sequence, column half), merge its splits into
 //               the bf16 output and the LSE
-// A third instance of each kernel serves a tree of drafted tokens (kTree): which of the n newest
-// keys a row sees comes from a bit mask a token instead of the diagonal, and the pages that hold
-// drafted keys pass through the preparation warps, which take non-finite values out of them (a
-// zero weight times such a value would reach rows that do not see the key) and flag their keys,
-// so that the rows that see them, and no others, come out as NaN.
+// Two further instances serve a tree of drafted tokens (kTree): which of the n newest keys a row
+// sees comes from a bit mask a token instead of the diagonal, and the pages that hold drafted keys
+// pass through the preparation warps, which take non-finite values out of them (a zero weight
+// times such a value would reach rows that do not see the key) and flag their keys, so that the
+// rows that see them, and no others, come out as NaN.
+// The tree over an fp8 cache (kF8) widens nothing: the e4m3 page is the MMA's operand as it lies.
+// Its other operands are sums of two e4m3 terms: a bf16 query, scaled by a power of two into
+// [128, 256) at its row's largest value, is hi + lo exactly (8 significant bits, 4 + 4) down to 2^-10
+// of that value, and a weight P'' = p ks is hi + lo to 2^-8.  Twice the k-steps at twice the rate: the
+// tensor work is bf16's, pages take half the bytes, and four fit instead of two; each page is its
+// own stage, released by its PV product.  The preparation warps make the query terms.
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
 #include <cuda.h>
@@ -79,7 +85,17 @@ __host__ __device__ constexpr int chunk_idx(int c, int half) {
   return ((c >> 2) == half && c < 8) ? c - 4 * half : (half == 0 ? c - 4 : (c < 4 ? c : 4));
 }
 constexpr int kSmemAlloc = kSmemBytes + 1024;
-// bf16: 8 warps; fp8: 12 (four more page-widening warps)
+// kF8: pages of four 128-column chunks (64 rows x 128 bytes, 128B-swizzled) and the rope columns
+// (64 rows x 64 bytes, 64B-swizzled), four of them; Q's smem part: latent 256..511 as two hi and two lo
+// chunks of 128 columns, then one chunk with the rope's hi and lo terms
+constexpr int kF8Page = 4 * kPageChunk + kPage * 64;  // 36 KB
+constexpr int kF8Stages = 4;
+static_assert(kF8Stages * kF8Page <= kStages * kStageBytes, "fp8 tree pages fit the stages");
+constexpr int kF8PrepWarps = 6;                 // warps 2-3 and 8-11
+// registers a thread: 384 threads launched at kF8RegsLaunch, then traded between the warpgroups
+constexpr int kF8RegsLaunch = 168, kF8RegsHigh = 232, kF8RegsLow = 136;
+static_assert(128 * kF8RegsHigh + 256 * kF8RegsLow <= 384 * kF8RegsLaunch, "register split");
+// bf16: 8 warps; fp8: 12 (four more preparation warps)
 template <bool kFp8> constexpr int kThreadsOf = kFp8 ? 384 : 256;
 template <bool kFp8> constexpr int kPrepOf = kFp8 ? 192 : 64;
 // a tree's item in at most this many splits is merged by the split that finishes last, from its
@@ -119,6 +135,16 @@ struct Params {
   size_t out_bytes, lse_bytes, part_o_bytes, part_lse_bytes, counters_bytes;
 };
 
+struct F8Bars {
+  uint64_t full[kF8Stages], empty[kF8Stages];
+  signed char q_exp[2][kRows];              // the power of two a query row was scaled by, by segment parity
+  float ks[kRows / 32][kPage], lk[kRows / 32][kPage];  // a page's key scales and their log2, a copy a softmax warp
+};
+struct NoBars {};
+template <bool kF8> struct F8Part { using type = NoBars; };
+template <> struct F8Part<true> { using type = F8Bars; };
+
+template <bool kFp8, bool kTree>
 struct Bars {
   // stage_ready[s][k]: bf16 pages are ready at once (k = 0); fp8 pages in three parts, k = 0..2
   // covering 64-column chunks 3k..3k+2, as the in-place widening completes them
@@ -139,9 +165,13 @@ struct Bars {
   uint32_t tmem_base;
   int abort_flag;
   Plan plan;
-  float kscale[kStages][kPage];
-  float key_nan[kStages][kPage];  // tree: NaN where a drafted key holds a non-finite value, else 0
+  float kscale[kFp8 && !kTree ? kStages : 1][kFp8 && !kTree ? kPage : 1];
+  unsigned char key_nan[kTree ? 2 : 1][kPage];  // tree: 1 where a drafted key holds a non-finite value
+  typename F8Part<kFp8 && kTree>::type f8;
 };
+
+// with 224 KB of dynamic shared memory and no slack, what the fp8 tree's block has left
+static_assert(sizeof(Bars<true, true>) <= 3072, "static shared memory of the fp8 tree");
 
 // Drafted tokens of virtual sequence v: the newest n keys; rows of tokens n .. T - 1 are padding.
 __device__ __forceinline__ int drafted(const Params& p, int vseq) {
@@ -184,6 +214,146 @@ __device__ __forceinline__ int page_row(const Params& p, int vseq, int pg) {
   return row_of_page(p, page_of(p, vseq, pg));
 }
 
+// Eight bf16 (times alpha) as their hi and lo e4m3 terms.
+__device__ __forceinline__ void split8(const uint4& w, float alpha, uint2& hi, uint2& lo) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ptx::split_e4m3x2(ptx::pack_f16x2(__uint_as_float(in[i] << 16) * alpha, __uint_as_float(in[i] & 0xffff0000u) * alpha),
+                      h[i], l[i]);
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// 8 bytes at byte b of row r of a 128B-swizzled chunk of 128-byte rows
+__device__ __forceinline__ void store_swz128(unsigned char* chunk, int r, int b, const uint2& v) {
+  *reinterpret_cast<uint2*>(chunk + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 8)) = v;
+}
+
+constexpr int kQNonFinite = 127;  // q_exp of a row with a NaN or an infinity: all its terms are NaN
+
+// The factor 2^k of a row's terms.
+__device__ __forceinline__ float q_factor(int k) {
+  return k == kQNonFinite ? __int_as_float(0x7fc00000) : __int_as_float((k + 127) << 23);
+}
+
+// The preparation warps of the tree over an fp8 cache: the query terms of every segment, in two
+// steps through the same shared memory (latent 0..255, copied on to TMEM by the MMA thread; then the
+// rest, which stays), and the pages that end a sequence or hold drafted keys.
+template <typename B>
+__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, Segments segs, unsigned char* sm, int TH) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pw = warp < 4 ? warp - 2 : warp - 6;  // 0 .. kF8PrepWarps - 1
+  volatile int* abort_flag = &bars.abort_flag;
+  unsigned char* qa = sm + kOffQhi;
+  int seq, L, lo, hi, g = 0, nseg = 0, n_zero = 0;
+  auto wait = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, abort_flag, p.err)) != 0;
+  };
+  auto done = [&](uint64_t* bar) {
+    ptx::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+  };
+  while (segs.next(seq, L, lo, hi)) {
+    if (nseg > 0 && !wait(&bars.q_free, nseg - 1)) return;
+    const int tile0 = (seq % p.NQT) * kRows, live = min(p.TQ, TH - tile0);
+    const size_t r0 = (size_t)(seq / p.NQT) * TH + tile0;
+    signed char* q_exp = bars.f8.q_exp[nseg & 1];
+    constexpr int kBatch = 4;  // rows a warp has in flight
+    for (int base = pw; base < kRows; base += kBatch * kF8PrepWarps) {
+      uint4 a[kBatch], b[kBatch], c[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rw = base + i * kF8PrepWarps;
+        a[i] = b[i] = c[i] = make_uint4(0, 0, 0, 0);
+        if (rw < live) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q_latent + (r0 + rw) * kDl);
+          a[i] = __ldg(src + lane);
+          b[i] = __ldg(src + 32 + lane);
+          if (lane < 8) c[i] = __ldg(reinterpret_cast<const uint4*>(p.q_rope + (r0 + rw) * 64) + lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rw = base + i * kF8PrepWarps;
+        if (rw >= kRows) break;
+        // the largest magnitude's bits, as integers
+        uint32_t mx = 0;
+        const uint32_t w[12] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w, c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+        for (int x = 0; x < 12; ++x) mx = __vmaxu2(mx, w[x] & 0x7fff7fffu);
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+        const int field = bits >> 7;  // exponent + 127; 255: NaN or infinity
+        const int k = field == 255 ? kQNonFinite : bits == 0 ? 0 : min(max(134 - field, -120), 120);
+        if (lane == 0) q_exp[rw] = static_cast<signed char>(k);
+        uint2 h, l;
+        split8(a[i], q_factor(k), h, l);
+        store_swz128(qa + (lane >> 4) * kQChunk, rw, 8 * (lane & 15), h);
+        store_swz128(qa + (2 + (lane >> 4)) * kQChunk, rw, 8 * (lane & 15), l);
+      }
+    }
+    done(&bars.q_lo_full);
+    if (!wait(&bars.q_cp_done, nseg)) return;
+    for (int base = pw; base < kRows; base += kBatch * kF8PrepWarps) {
+      uint4 b[kBatch], c[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rw = base + i * kF8PrepWarps;
+        b[i] = c[i] = make_uint4(0, 0, 0, 0);
+        if (rw < live) {
+          b[i] = __ldg(reinterpret_cast<const uint4*>(p.q_latent + (r0 + rw) * kDl) + 32 + lane);
+          if (lane < 8) c[i] = __ldg(reinterpret_cast<const uint4*>(p.q_rope + (r0 + rw) * 64) + lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int rw = base + i * kF8PrepWarps;
+        if (rw >= kRows) break;
+        const float f = q_factor(q_exp[rw]);
+        uint2 h, l;
+        split8(b[i], f, h, l);
+        store_swz128(qa + (lane >> 4) * kQChunk, rw, 8 * (lane & 15), h);
+        store_swz128(qa + (2 + (lane >> 4)) * kQChunk, rw, 8 * (lane & 15), l);
+        if (lane < 8) {
+          split8(c[i], f, h, l);
+          store_swz128(qa + 4 * kQChunk, rw, 8 * lane, h);
+          store_swz128(qa + 4 * kQChunk, rw, 64 + 8 * lane, l);
+        }
+      }
+    }
+    done(&bars.q_hi_full);
+    ++nseg;
+    // pages past the clean keys: granules of drafted keys that hold a NaN are zeroed and the key
+    // flagged, the rows past the sequence's end are zeroed (whole rows, so the swizzles are immaterial)
+    const int clean = max(L - drafted(p, seq), 0);
+    for (int pg = max(lo, clean / kPage); pg < hi; ++pg) {
+      if (!wait(&bars.zero_go, n_zero++)) return;
+      const int gg = g + pg - lo, first = max(clean - pg * kPage, 0), valid = min(kPage, L - pg * kPage);
+      unsigned char* st = sm + kOffStage + (gg % kF8Stages) * kF8Page;
+      unsigned char* flags = bars.key_nan[gg & 1];
+      for (int rw = pw; rw < kPage; rw += kF8PrepWarps) {
+        uint4* g0 = reinterpret_cast<uint4*>(st + (lane >> 3) * kPageChunk + rw * 128 + (lane & 7) * 16);
+        uint4* g1 = reinterpret_cast<uint4*>(st + 4 * kPageChunk + rw * 64 + (lane & 3) * 16);
+        bool hit0 = rw >= valid, hit1 = hit0;
+        if (rw >= first && rw < valid) {
+          hit0 = granule_nonfinite<true>(*g0);
+          hit1 = lane < 4 && granule_nonfinite<true>(*g1);
+          const bool any = __any_sync(0xffffffffu, hit0 || hit1);
+          if (lane == 0) flags[rw] = any;
+        } else if (lane == 0) {
+          flags[rw] = 0;
+        }
+        if (hit0) *g0 = make_uint4(0, 0, 0, 0);
+        if (hit1 && lane < 4) *g1 = make_uint4(0, 0, 0, 0);
+      }
+      done(&bars.zeroed);
+    }
+    g += hi - lo;
+  }
+}
+
 template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tm_cache,
@@ -195,16 +365,22 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ Bars bars;
+  __shared__ Bars<kFp8, kTree> bars;
+  constexpr bool kF8 = kFp8 && kTree;       // e4m3 operands throughout
+  constexpr bool kWiden = kFp8 && !kTree;   // e4m3 pages widened to bf16
+  if (kF8 && sm != smem_raw) {  // allocated without the slack of the others (never taken: it is 1024-aligned)
+    if (threadIdx.x == 0) latch_error(p.err, kErrBounds);
+    return;
+  }
   constexpr int kThreads = kThreadsOf<kFp8>;
   // fp8: with fewer than 128 query rows per tile, softmax warps whose 32 rows are all padding
   // of the M = 128 MMA (never stored) widen pages instead: warps 4 .. 4 + n_soft - 1 run the
   // softmax, warps 4 + n_soft .. 7 join the preparation warps (2-3 and 8-11)
-  const int n_soft = kFp8 ? (p.TQ + 31) / 32 : kRows / 32;
-  const int n_prep = kPrepOf<kFp8> + (kFp8 ? 32 * (kRows / 32 - n_soft) : 0);
+  const int n_soft = kWiden ? (p.TQ + 31) / 32 : kRows / 32;
+  const int n_prep = kPrepOf<kFp8> + (kWiden ? 32 * (kRows / 32 - n_soft) : 0);
   // readiness parts of a page stage: fp8 three groups of three widened chunks; bf16 the
   // score-only part, then the value part
-  constexpr int kParts = kFp8 ? 3 : 2;
+  constexpr int kParts = kF8 ? 1 : kFp8 ? 3 : 2;
   // the first sequence's Q latent 0..255 (four 16 KB chunks) is staged where pages 1 (fp8)
   // or 1 and 2 (bf16: value slots 1 and 2) land
   auto q_stage_off = [&](int c) -> int {
@@ -226,6 +402,13 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::prefetch_tensormap(&tm_qlat);
     ptx::prefetch_tensormap(&tm_qrope);
     if (kFp8 || p.page_box) ptx::prefetch_tensormap(&tm_page);
+    if constexpr (kF8) {
+      ptx::prefetch_tensormap(&tm_c4);
+      for (int s = 0; s < kF8Stages; ++s) {
+        ptx::mbar_init(&bars.f8.full[s], 1);
+        ptx::mbar_init(&bars.f8.empty[s], 1);
+      }
+    }
     if (!kFp8 && p.page_box) {
       ptx::prefetch_tensormap(&tm_c4);
       ptx::prefetch_tensormap(&tm_c5);
@@ -252,9 +435,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::mbar_init(&bars.o_done, 1);
     ptx::mbar_init(&bars.seg_done, 1);
     ptx::mbar_init(&bars.q_free, 1);
-    ptx::mbar_init(&bars.q_lo_full, 1);
+    ptx::mbar_init(&bars.q_lo_full, kF8 ? kF8PrepWarps : 1);
     ptx::mbar_init(&bars.q_cp_done, 1);
-    ptx::mbar_init(&bars.q_hi_full, 1);
+    ptx::mbar_init(&bars.q_hi_full, kF8 ? kF8PrepWarps : 1);
     ptx::mbar_init(&bars.q0_copied, 1);
     ptx::mbar_init(&bars.conv_sync, n_prep / 32);  // one arrival per preparation warp
     ptx::mbar_init(&bars.part_done, n_soft);
@@ -279,7 +462,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   segs.init(p, bars.plan);
   int seq, L, lo, hi;
 
-  if (warp == 0) {
+  if (warp < 4 || warp >= 8 || warp >= 4 + n_soft) {
+   if constexpr (kF8) ptx::regs_dec<kF8RegsLow>();
+   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
     // One lane issues Q, the pages in order (fp8: whole pages; bf16: the value part as soon
     // as its ring slot frees, then the score-only part once the previous page's scores are
@@ -292,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         // the first page's table entry is read before Q is issued, so its latency overlaps
         // the Q copies instead of delaying the page's own
         const int page_first = page_of(p, seq, lo);
-        {
+        if constexpr (!kF8) {  // (kF8: the preparation warps bring Q)
           if (nseg == 0) {
             // first sequence: Q latent 0..255 staged in the (still unused) second page
             // stage, the rest of Q straight into the Q area, all at once
@@ -327,12 +512,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         };
         for (int pg = lo; pg < hi; ++pg, ++g) {
           const int s = g % kStages;
-          if (kFp8 && !(ok = ptx::mbar_wait(&bars.stage_empty[s], ((g / kStages) & 1) ^ 1, abort_flag, p.err)))
+          if (kWiden && !(ok = ptx::mbar_wait(&bars.stage_empty[s], ((g / kStages) & 1) ^ 1, abort_flag, p.err)))
             break;
           // the first sequence's staged Q stays in place until it is copied to TMEM
-          if (kFp8 && g == 1 && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
+          if (kWiden && g == 1 && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
           const int y = pg == lo ? row_of_page(p, page_first) : page_row(p, seq, pg);
-          if constexpr (kFp8) {
+          if constexpr (kF8) {
+            const int t = g % kF8Stages;
+            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((g / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
+            unsigned char* dst = sm + kOffStage + t * kF8Page;
+            ptx::mbar_arrive_expect_tx(&bars.f8.full[t], kF8Page);
+            if (p.page_box) {
+              ptx::tma_load_3d(dst, &tm_page, &bars.f8.full[t], 0, y, 0);
+            } else {
+              for (int c = 0; c < 4; ++c)
+                ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, &bars.f8.full[t], c * 128, y);
+            }
+            ptx::tma_load_2d(dst + 4 * kPageChunk, &tm_c4, &bars.f8.full[t], 512, y);
+          } else if constexpr (kFp8) {
             unsigned char* dst = sm + kOffStage + s * kStageBytes + kRawOffset;
             ptx::mbar_arrive_expect_tx(&bars.stage_full[s], 9 * kRawChunk);
             if (p.page_box) {
@@ -387,7 +584,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         }
       }
     }
-  } else if (warp == 1) {
+   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
     if (ptx::elect_one()) {
       constexpr uint32_t kIdS = ptx::make_idesc(1, kRows, kPage, 0, 0);
@@ -422,7 +619,31 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       // of S(gg) starts the accumulator.
       auto issue_s = [&](int gg, int part) {
         const uint32_t d = tmem + 128 + (gg & 1) * 64;
-        if constexpr (kFp8) {
+        if constexpr (kF8) {
+          // 18 k-steps of 32 columns, the query's hi term and its lo term
+          constexpr uint32_t kIdS8 = ptx::make_idesc(0, kRows, kPage, 0, 0);
+          const uint64_t st = b0 + (gg % kF8Stages) * (kF8Page / 16);
+          const uint64_t rp = ptx::smem_desc(smb + kOffStage + (gg % kF8Stages) * kF8Page + 4 * kPageChunk, 16, 512,
+                                             ptx::kSwz64);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // latent 0..255: A from TMEM
+            const uint64_t db = st + 512 * (j >> 2) + 2 * (j & 3);
+            ptx::mma_f8_ts(d, tmem + j * 8, db, kIdS8, j > 0 ? 1u : 0u);
+            ptx::mma_f8_ts(d, tmem + 64 + j * 8, db, kIdS8, 1u);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // latent 256..511: A from shared memory
+            const uint64_t db = st + 512 * (2 + (j >> 2)) + 2 * (j & 3);
+            const uint64_t da = qd + 1024 * (j >> 2) + 2 * (j & 3);
+            ptx::mma_f8_ss(d, da, db, kIdS8, 1u);
+            ptx::mma_f8_ss(d, da + 2048, db, kIdS8, 1u);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {  // rope
+            ptx::mma_f8_ss(d, qd + 4096 + 2 * j, rp + 2 * j, kIdS8, 1u);
+            ptx::mma_f8_ss(d, qd + 4096 + 4 + 2 * j, rp + 2 * j, kIdS8, 1u);
+          }
+        } else if constexpr (kFp8) {
           const uint64_t st = (gg % kStages) ? b1 : b0;
           if (part == 0) {
 #pragma unroll
@@ -459,6 +680,19 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       // PV: B = this half's 256 latent columns (four chunks 8 KB apart), 16 keys per k-step
       auto issue_pv = [&](int gg, bool first) {
         uint32_t st;
+        if constexpr (kF8) {
+          // two 128-column chunks 8 KB apart, 32 keys per k-step; P'' hi in 16 TMEM columns, lo in 16 more
+          constexpr uint32_t kIdPV8 = ptx::make_idesc(0, kRows, 256, 0, 1);
+          const uint64_t vd8 = ptx::sw128_desc(smb + kOffStage + (gg % kF8Stages) * kF8Page + 2 * half * kPageChunk,
+                                               kPageChunk, 1024);
+          const uint32_t pa8 = tmem + 128 + (gg & 1) * 64;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            ptx::mma_f8_ts(o_tm, pa8 + k * 8, vd8 + 256 * k, kIdPV8, (!first || k > 0) ? 1u : 0u);
+            ptx::mma_f8_ts(o_tm, pa8 + 16 + k * 8, vd8 + 256 * k, kIdPV8, 1u);
+          }
+          return;
+        }
         if constexpr (kFp8) st = kOffStage + (gg % kStages) * kStageBytes + 4 * half * kPageChunk;
         else st = kOffVPart + (gg % kVSlots) * kVPartBytes;
         const uint64_t vd = ptx::sw128_desc(smb + st, kPageChunk, 1024);
@@ -475,12 +709,12 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         // the first sequence's Q latent 0..255 was staged in the second page stage
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const uint32_t qc = nseg == 0 ? smb + q_stage_off(k >> 2) : qhi + (k >> 2) * kQChunk;
+          const uint32_t qc = !kF8 && nseg == 0 ? smb + q_stage_off(k >> 2) : qhi + (k >> 2) * kQChunk;
           ptx::tmem_cp_128x256b(tmem + k * 8, ptx::sw128_desc(qc + (k & 3) * 32, 16, 1024));
         }
         ptx::mma_commit(&bars.q_cp_done);
         if (nseg == 0) ptx::mma_commit(&bars.q0_copied);
-        if (nseg > 0) {  // the rest of Q over the staging copy (the producer loaded the first)
+        if (!kF8 && nseg > 0) {  // the rest of Q over the staging copy (the producer loaded the first)
           if (!(ok = ptx::mbar_wait(&bars.q_cp_done, nseg & 1, abort_flag, p.err))) break;
           ptx::mbar_arrive_expect_tx(&bars.q_hi_full, 5 * TQ * 128);
           for (int c = 0; c < 4; ++c)
@@ -504,7 +738,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             ptx::mma_commit(&bars.o_done);
             // fp8: the whole stage; bf16: the value part (the score-only part was released
             // after the scores)
-            ptx::mma_commit(kFp8 ? &bars.stage_empty[gp % kStages] : &bars.vpart_empty[gp % kVSlots]);
+            if constexpr (kF8) ptx::mma_commit(&bars.f8.empty[gp % kF8Stages]);
+            else ptx::mma_commit(kFp8 ? &bars.stage_empty[gp % kStages] : &bars.vpart_empty[gp % kVSlots]);
             ++gp;
             progress = true;
           }
@@ -514,7 +749,19 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           // landed and comes back with the rows past the end zeroed.
           bool can = false;
           if (gs < g_end && gs <= gp + 1) {
-            if constexpr (kFp8) {
+            if constexpr (kF8) {
+              if (!zero_asked && ptx::mbar_test_wait(&bars.f8.full[gs % kF8Stages], (gs / kF8Stages) & 1)) {
+                can = (lo + (gs - g_first) + 1) * kPage <= clean;
+                if (!can) {
+                  ptx::mbar_arrive(&bars.zero_go);
+                  zero_asked = progress = true;
+                }
+              } else if (zero_asked && ptx::mbar_test_wait(&bars.zeroed, n_zeroed & 1)) {
+                can = true;
+                zero_asked = false;
+                ++n_zeroed;
+              }
+            } else if constexpr (kFp8) {
               can = ptx::mbar_test_wait(&bars.stage_ready[gs % kStages][sp], (gs / kStages) & 1);
             } else if ((lo + (gs - g_first) + 1) * kPage <= clean) {
               can = sp == 0 ? ptx::mbar_test_wait(&bars.spart_full, gs & 1)
@@ -565,7 +812,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         ++nseg;
       }
     }
-  } else if (warp < 4 || warp >= 8 || warp >= 4 + n_soft) {
+   } else if constexpr (kF8) {
+    prepare_f8(p, bars, segs, sm, TH);
+   } else {
     // -------------------------------------------------------------- stage preparation
     // 0 .. n_prep - 1: warps 2-3, then 8-11, then the softmax warps that joined
     const int tid = warp < 4 ? threadIdx.x - 64
@@ -599,7 +848,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
               // drafted keys first .. valid - 1 of the page: non-finite granules are zeroed and the
               // key flagged; a warp scans a whole row (72 granules), the two warps every other row
               const int first = max(clean - pg * kPage, 0);
-              if (tid < kPage && (tid < first || tid >= valid)) bars.key_nan[g & 1][tid] = 0.f;
+              if (tid < kPage && (tid < first || tid >= valid)) bars.key_nan[g & 1][tid] = 0;
               for (int rw = first + (tid >> 5); rw < valid; rw += n_prep / 32) {
                 bool bad_row = false;
 #pragma unroll
@@ -615,7 +864,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                   }
                 }
                 bad_row = __any_sync(0xffffffffu, bad_row);
-                if ((tid & 31) == 0) bars.key_nan[g & 1][rw] = bad_row ? __int_as_float(0x7fc00000) : 0.f;
+                if ((tid & 31) == 0) bars.key_nan[g & 1][rw] = bad_row;
               }
             }
             const int nrow = kPage - valid;
@@ -635,15 +884,6 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         } else {
           ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.stage_full[s], (g / kStages) & 1, abort_flag, p.err));
           if (!ok) break;
-          const bool tree_page = kTree && (pg + 1) * kPage > clean;
-          if constexpr (kTree) {
-            if (tid < kPage) {
-              const bool fin = fabsf(ksc) < INFINITY;
-              bars.key_nan[s][row] = fin ? 0.f : __int_as_float(0x7fc00000);
-              // (only where the mask may hide the key; elsewhere every row sees the scale as it is)
-              if (tree_page && !fin) ksc = 0.f;
-            }
-          }
           if (tid < kPage) bars.kscale[s][row] = ksc;
           // Widen in place, in three lockstep steps of three chunks (four 16-byte granules
           // per thread per step).  bf16 chunk c (bytes [8c, 8c+8) KB) overlaps raw chunks 2c-9
@@ -664,24 +904,10 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                            ? *reinterpret_cast<const uint4*>(st + kRawOffset + c * kRawChunk + gi * 16)
                            : make_uint4(0, 0, 0, 0);
             }
-            uint32_t hit = 0;  // tree: granules that hold a NaN, zeroed here, flagged below
-            if (tree_page) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (granule_nonfinite<true>(raw[q])) {
-                  raw[q] = make_uint4(0, 0, 0, 0);
-                  hit |= 1u << q;
-                }
-            }
             __syncwarp();
             if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bars.conv_sync);
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.conv_sync, (3 * g + k) & 1, abort_flag, p.err));
             if (!ok) break;
-            if (kTree && hit) {  // after the barrier: the flags' reset above came before it
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (hit >> q & 1) bars.key_nan[s][((tid + n_prep * q) & 255) >> 2] = __int_as_float(0x7fc00000);
-            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int G = tid + n_prep * q, c = 3 * k + (G >> 8), gi = G & 255;
@@ -707,8 +933,10 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         }
       }
     }
+   }
   } else {
     // -------------------------------------------------------------- softmax / epilogue
+    if constexpr (kF8) ptx::regs_inc<kF8RegsHigh>();
     const int r = threadIdx.x - 128;  // query row == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int g = 0, n_epi = 0, n_part = 0, n_bulk = 0, n_bulk_issued = 0;
@@ -738,6 +966,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           kTree ? p.tree_mask + (seq / p.NQT) * p.mask_stride + (long long)t_row * p.mask_words : nullptr;
       float m = -INFINITY, l = 0.f, lr = 0.f;  // exact row sum (LSE) and bf16-rounded (PV)
       const uint32_t o_addr = tmem + lane_off + 256;
+      // kF8: each lane has the scales of keys 2 lane and 2 lane + 1 of the next page on their way, and
+      // the page-table entry of the one after
+      float f8_scale = 0.f;  // softmax scale in the exponent over the row's power of two
+      int tab[2] = {-1, -1};
+      float2 ks_next = make_float2(0.f, 0.f);
+      auto entry = [&](int pg) {
+        return pg < hi ? __ldg(p.page_table + (size_t)(seq / p.NQT) * p.max_pages + pg) : -1;
+      };
+      auto scales = [&](int page) {
+        return page >= 0 && page < p.num_pages
+                   ? __ldg(reinterpret_cast<const float2*>(p.kv_scale + (size_t)page * kPage) + (r & 31))
+                   : make_float2(0.f, 0.f);
+      };
+      if constexpr (kF8) {
+        tab[0] = entry(lo);
+        tab[1] = entry(lo + 1);
+        ks_next = scales(tab[0]);
+      }
       for (int pg = lo; pg < hi; ++pg, ++g) {
         const bool tree_page = kTree && (pg + 1) * kPage > first_new;
         unsigned long long vis = ~0ull;  // tree: bit x says whether this row sees key pg * 64 + x
@@ -751,6 +997,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             vis = mask_bits(mask_row, p.mask_words, 0) << -off | ((1ull << -off) - 1);
           if (L - pg * kPage < kPage) vis &= (1ull << (L - pg * kPage)) - 1;
         }
+        int page8 = -1;
+        if constexpr (kF8) {
+          page8 = tab[0];
+          const int key = pg * kPage + 2 * (r & 31);
+          float2 k2 = make_float2(key < L ? ks_next.x : 0.f, key + 1 < L ? ks_next.y : 0.f);
+          // log2 of the scale, floored (a scale of 0 gives weights of 0); NaN flags a drafted key whose
+          // scale is not finite
+          float2 l2 = make_float2(fmaxf(__log2f(k2.x), -100.f), fmaxf(__log2f(k2.y), -100.f));
+          if (tree_page && !(fabsf(k2.x) < INFINITY)) k2.x = 0.f, l2.x = __int_as_float(0x7fc00000);
+          if (tree_page && !(fabsf(k2.y) < INFINITY)) k2.y = 0.f, l2.y = __int_as_float(0x7fc00000);
+          __syncwarp();  // the warp has read the page before's
+          *reinterpret_cast<float2*>(&bars.f8.ks[warp - 4][2 * (r & 31)]) = k2;
+          *reinterpret_cast<float2*>(&bars.f8.lk[warp - 4][2 * (r & 31)]) = l2;
+          __syncwarp();
+          tab[0] = tab[1];
+          tab[1] = entry(pg + 2);
+          ks_next = scales(tab[0]);
+        }
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.s_full[g & 1], (g >> 1) & 1, abort_flag, p.err));
         if (!ok) break;
         ptx::tc_fence_after();
@@ -762,29 +1026,45 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           ptx::tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(su + 32));
           ptx::tmem_ld_wait();
         }
-        const int page = __ldg(p.page_table + (size_t)(seq / p.NQT) * p.max_pages + pg);
+        const int page = kF8 ? page8 : __ldg(p.page_table + (size_t)(seq / p.NQT) * p.max_pages + pg);
         const bool bad = page < 0 || page >= p.num_pages;
+        if constexpr (kF8) {
+          if (bad && r == 0 && seq % p.NQT == 0) latch_error(p.err, kErrBadPage);
+          if (pg == lo)  // written before this segment's first scores were issued
+            f8_scale = p.scale_log2 * __int_as_float((127 - bars.f8.q_exp[n_epi & 1][r]) << 23);
+        }
         const int key0 = pg * kPage;
         const int lim = bad ? -1 : min(last_visible, L - 1);  // visible keys: key0+x <= lim
         // unscaled scores (fp8: times the key's scale), two keys per packed instruction; the
         // softmax scale is applied in the exponent argument
-        const float* ks = bars.kscale[g % kStages];
+        // (kF8: scaled scores, in the exponent's units)
+        const float* ks;
+        if constexpr (kF8) ks = bars.f8.ks[warp - 4];
+        else ks = bars.kscale[kFp8 ? g % kStages : 0];
         uint64_t s2[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
           s2[x] = ptx::f2(s[2 * x], s[2 * x + 1]);
-          if constexpr (kFp8) s2[x] = ptx::mul2(s2[x], ptx::f2(ks[2 * x], ks[2 * x + 1]));
+          if constexpr (kF8)
+            s2[x] = ptx::mul2(ptx::mul2(s2[x], *reinterpret_cast<const uint64_t*>(ks + 2 * x)), ptx::f2(f8_scale, f8_scale));
+          else if constexpr (kFp8) s2[x] = ptx::mul2(s2[x], ptx::f2(ks[2 * x], ks[2 * x + 1]));
         }
         if constexpr (kTree) {
           if (bad) vis = 0;
           if (tree_page || bad) {
-            const float* kn = bars.key_nan[kFp8 ? g % kStages : g & 1];
+            const unsigned char* kn = bars.key_nan[g & 1];
+            const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
               const uint32_t two = static_cast<uint32_t>(vis >> (2 * x));
-              const float lo_nan = tree_page ? kn[2 * x] : 0.f, hi_nan = tree_page ? kn[2 * x + 1] : 0.f;
-              s2[x] = ptx::f2(two & 1 ? ptx::f2_lo(s2[x]) + lo_nan : -INFINITY,
-                              two & 2 ? ptx::f2_hi(s2[x]) + hi_nan : -INFINITY);
+              float a = ptx::f2_lo(s2[x]), b = ptx::f2_hi(s2[x]);
+              if (tree_page && kn[2 * x]) a = nan;
+              if (tree_page && kn[2 * x + 1]) b = nan;
+              if constexpr (kF8) {  // 0, or NaN where the scale was flagged
+                a += bars.f8.lk[warp - 4][2 * x] - bars.f8.lk[warp - 4][2 * x];
+                b += bars.f8.lk[warp - 4][2 * x + 1] - bars.f8.lk[warp - 4][2 * x + 1];
+              }
+              s2[x] = ptx::f2(two & 1 ? a : -INFINITY, two & 2 ? b : -INFINITY);
             }
           }
         } else if (key0 + kPage - 1 > lim) {  // a partial page (or a bad one): mask invisible keys
@@ -793,16 +1073,28 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             s2[x] = ptx::f2(key0 + 2 * x <= lim ? ptx::f2_lo(s2[x]) : -INFINITY,
                             key0 + 2 * x + 1 <= lim ? ptx::f2_hi(s2[x]) : -INFINITY);
         }
-        float mx4[4] = {ptx::f2_lo(s2[0]), ptx::f2_hi(s2[0]), ptx::f2_lo(s2[1]), ptx::f2_hi(s2[1])};
+        // kF8: the weights P'' = p ks are what has to fit e4m3, so the maximum is that of their exponents,
+        // and it is mapped to 2^5: they lie in (0, 2^8], their lo terms' steps 2^-15 of the row's largest
+        auto exponents = [&](int x) {
+          if constexpr (kF8) return ptx::add2(s2[x], *reinterpret_cast<const uint64_t*>(&bars.f8.lk[warp - 4][2 * x]));
+          else return s2[x];
+        };
+        constexpr float kTop = kF8 ? 5.f : 0.f;
+        const uint64_t e0 = exponents(0), e1 = exponents(1);
+        float mx4[4] = {ptx::f2_lo(e0), ptx::f2_hi(e0), ptx::f2_lo(e1), ptx::f2_hi(e1)};
 #pragma unroll
-        for (int x = 2; x < 32; ++x) mx4[x & 3] = ptx::fmax3(mx4[x & 3], ptx::f2_lo(s2[x]), ptx::f2_hi(s2[x]));
+        for (int x = 2; x < 32; ++x) {
+          const uint64_t ex = exponents(x);
+          mx4[x & 3] = ptx::fmax3(mx4[x & 3], ptx::f2_lo(ex), ptx::f2_hi(ex));
+        }
         // tile maximum in the exponent domain (the scale is positive; -inf stays -inf)
-        const float mx = ptx::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * p.scale_log2;
+        const float mx = kF8 ? ptx::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) - kTop
+                             : ptx::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * p.scale_log2;
         float m_use = m;
         if (pg == lo) {
           m_use = mx;
         } else {
-          const bool grow = mx > m + 8.0f;
+          const bool grow = mx > m + (8.0f - kTop);
           if (__any_sync(0xffffffffu, grow)) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.o_done, (g - 1) & 1, abort_flag, p.err));
             if (!ok) break;
@@ -833,8 +1125,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         uint64_t ps2[2] = {ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f)};
         float pr[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[32];
+        if constexpr (kF8) {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < 32; x += 2) {  // four keys: one word of hi codes, one of lo codes
+            uint32_t h[2], lo8[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint64_t a2 = ptx::add2(s2[x + y], nm2);
+              const uint64_t pp = ptx::f2(ptx::ex2(ptx::f2_lo(a2)), ptx::ex2(ptx::f2_hi(a2)));
+              ps2[y] = ptx::add2(ps2[y], pp);
+              const uint64_t ab = ptx::mul2(pp, *reinterpret_cast<const uint64_t*>(ks + 2 * (x + y)));
+              ptx::split_e4m3x2(ptx::pack_f16x2(ptx::f2_lo(ab), ptx::f2_hi(ab)), h[y], lo8[y]);
+            }
+            pk[x / 2] = h[0] | h[1] << 16;
+            pk[16 + x / 2] = lo8[0] | lo8[1] << 16;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < (kF8 ? 0 : 32); ++x) {
           const uint64_t a2 = ptx::fma2(s2[x], sc2, nm2);
           const uint64_t pp = ptx::f2(ptx::ex2(ptx::f2_lo(a2)), ptx::ex2(ptx::f2_hi(a2)));
           ps2[x & 1] = ptx::add2(ps2[x & 1], pp);
@@ -1236,6 +1544,9 @@ cudaError_t load_decode_kernels() {
 cudaError_t encode_tensor_map_swz(CUtensorMap* map, CUtensorMapDataType dt, int rank,
                                   const void* ptr, const uint64_t* dims, const uint64_t* strides,
                                   const uint32_t* box, bool swizzle128);
+cudaError_t encode_tensor_map_swizzle(CUtensorMap* map, CUtensorMapDataType dt, int rank,
+                                      const void* ptr, const uint64_t* dims, const uint64_t* strides,
+                                      const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const void* kv_cache,
                                 const float* kv_scale, const int* page_table,
@@ -1247,12 +1558,14 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   using namespace sm103_decode;
   CUtensorMap tm;
   // the cache as a 2-D tensor [num_pages * 64 rows, 576 columns]; boxes of 64 x 64
+  // (the tree over an fp8 cache: 128 columns, swizzled as operands, and the rope columns on their own)
+  const bool f8 = fp8 && tree_mask;
   uint64_t dims[2] = {(uint64_t)kDc, (uint64_t)num_pages * kPage};
   uint64_t strides[1] = {(uint64_t)kDc * (fp8 ? 1 : 2)};
-  uint32_t box[2] = {64, kPage};
+  uint32_t box[2] = {f8 ? 128u : 64u, kPage};
   cudaError_t e = encode_tensor_map_swz(
       &tm, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_cache,
-      dims, strides, box, /*swizzle128=*/!fp8);
+      dims, strides, box, /*swizzle128=*/!fp8 || f8);
   if (e != cudaSuccess) return e;
   if (tree_mask && G > kMaxSplits) return cudaErrorNotSupported;  // the merge kernel's tables
   // The same bytes as a 3-D tensor (64 columns of a chunk, row, chunk of 64 columns): a box
@@ -1268,8 +1581,18 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     uint32_t pbox[3] = {64, (uint32_t)kPage, nchunks};
     return encode_tensor_map_swz(m, pdt, 3, kv_cache, pdims, pstrides, pbox, /*swizzle128=*/!fp8) == cudaSuccess;
   };
-  const bool page_box = enc3(&tm_page, 9) && (fp8 || (enc3(&tm_c4, 4) && enc3(&tm_c5, 5)));
-  if (!page_box) tm_page = tm_c4 = tm_c5 = tm;
+  bool page_box;
+  if (f8) {
+    const uint64_t d3[3] = {128, (uint64_t)num_pages * kPage, 4}, s3[2] = {(uint64_t)kDc, 128};
+    const uint32_t b3[3] = {128, (uint32_t)kPage, 4}, br[2] = {64, (uint32_t)kPage};
+    page_box = encode_tensor_map_swz(&tm_page, pdt, 3, kv_cache, d3, s3, b3, true) == cudaSuccess;
+    if (!page_box) tm_page = tm;
+    if ((e = encode_tensor_map_swizzle(&tm_c4, pdt, 2, kv_cache, dims, strides, br, CU_TENSOR_MAP_SWIZZLE_64B)) != cudaSuccess)
+      return e;
+  } else {
+    page_box = enc3(&tm_page, 9) && (fp8 || (enc3(&tm_c4, 4) && enc3(&tm_c5, 5)));
+    if (!page_box) tm_page = tm_c4 = tm_c5 = tm;
+  }
   // Q as 2-D tensors [B*T*H rows, 512 | 64 columns]; boxes of 64 columns x T*H rows
   // (one sequence), 128B-swizzled like the operand tiles
   const int TH = T * H;
@@ -1341,14 +1664,15 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto go = [&](auto kern) -> cudaError_t {
     static unsigned long long smem_set[4] = {0, 0, 0, 0};
-    const cudaError_t e2 = smem_attr_once(kern, kSmemAlloc, &smem_set[(fp8 ? 1 : 0) + (tree_mask ? 2 : 0)]);
+    const int smem = f8 ? kSmemBytes : kSmemAlloc;
+    const cudaError_t e2 = smem_attr_once(kern, smem, &smem_set[(fp8 ? 1 : 0) + (tree_mask ? 2 : 0)]);
     if (e2 != cudaSuccess) return e2;
     // programmatic dependent of the zeroing kernel: the prologue (barriers, TMEM, plan, first
     // loads) overlaps it
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * G);
     cfg.blockDim = dim3(fp8 ? kThreadsOf<true> : kThreadsOf<false>);
-    cfg.dynamicSmemBytes = kSmemAlloc;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1358,6 +1682,16 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     return cudaLaunchKernelEx(&cfg, kern, tm, tm_page, tm_c4, tm_c5, tm_qlat, tm_qrope, p);
   };
   if (tree_mask) {
+    if (fp8) {
+      // the register split between its warpgroups draws on what the launch holds
+      static int regs = 0;
+      if (!__atomic_load_n(&regs, __ATOMIC_ACQUIRE)) {
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, decode_split_kernel<true, true>)) != cudaSuccess) return e;
+        __atomic_store_n(&regs, fa.numRegs, __ATOMIC_RELEASE);
+      }
+      if (regs < kF8RegsLaunch) return cudaErrorInvalidDeviceFunction;
+    }
     if ((e = fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(G, (kRows / kMergeRows) * (128 / kMergeQuads));

@@ -296,6 +296,16 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
+// D[tmem] (+)= A[tmem] * B[smem], 8-bit operands (four consecutive k of A a TMEM column)
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
 // Copy 128 rows x 256 bits from a shared-memory matrix (descriptor as for the MMA
 // operands) into TMEM: row i lands in lane i, eight consecutive 32-bit columns from taddr.
 // Asynchronous like the MMA; completion is tracked by mma_commit.
@@ -475,6 +485,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// A packed f16 pair as a sum of two e4m3 pairs: hi = e4m3(v), lo = e4m3(v - hi), the difference exact
+// in f16.  16 bits each, first value low.  v within +-448; a NaN gives NaN codes.
+__device__ __forceinline__ void split_e4m3x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, r;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
+      "sub.rn.f16x2 r, %2, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n\t"
+      "cvt.u32.u16 %0, h;\n\t"
+      "cvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "r"(v));
 }
 
 // max of three (one instruction)
