@@ -9,7 +9,9 @@
 // partial result of unit c for item v goes to slot c + v, which is unique because consecutive
 // units never move backwards through the items; there are at most G + (items) - 1 slots.
 // A parameter struct passed to make_plan / Segments::init provides cache_lens, B, NQT
-// (query tiles per sequence), max_pages, G and item_cost (flat pages charged per item).
+// (query tiles per sequence), max_pages, G and item_cost (flat pages charged per item).  An
+// adaptive plan charges at most a unit's even share of the real pages, so that with few pages
+// whole units are not spent on flat pages without keys; Plan::item_cost is what it charges.
 #pragma once
 
 #include "common.cuh"
@@ -26,6 +28,7 @@ struct Plan {
   // the unit's first segment, as Segments::next finds it (valid if seg_ok): sequence b0 of
   // length seg_L, pages [seg_lo, seg_hi); lets the roles start without reloading lengths
   int seg_L, seg_lo, seg_hi, seg_ok;
+  int item_cost;
 };
 
 __device__ __forceinline__ int clamp_len(int L, int max_pages) {
@@ -40,18 +43,19 @@ __device__ __forceinline__ int warp_sum(int v) {
 
 // The Plan of work unit `unit`, computed by one warp with coalesced loads of the lengths
 // (256 at a time) and warp scans.
-template <typename Prm>
+template <bool kAdaptive = false, typename Prm>
 __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
   const int lane = threadIdx.x & 31;
   const int B = prm.B * prm.NQT;  // work is planned per (sequence, query tile)
   auto len_at = [&](int bb) {
     return bb < B ? clamp_len(__ldg(prm.cache_lens + bb / prm.NQT), prm.max_pages) : 0;
   };
+  int cost = kAdaptive ? 0 : prm.item_cost;
   auto flat_of = [&](int Lb) {
     const int n = pages_of(Lb, kPage);
-    return n > 0 ? n + prm.item_cost : 0;
+    return n > 0 ? n + cost : 0;
   };
-  int total = 0;
+  int total = 0, items = 0;
   int l0s[8];  // the first 256 items' lengths, kept for the second pass
   for (int base = 0; base < B; base += 256) {
     int l[8], sum = 0;
@@ -64,6 +68,14 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += flat_of(l[i]);
     total += warp_sum(sum);
+    if (kAdaptive) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) items += __popc(__ballot_sync(0xffffffffu, l[i] > 0));
+    }
+  }
+  if (kAdaptive) {
+    cost = max(1, min(prm.item_cost, total / prm.G));
+    total += items * cost;
   }
   const int chunk = total > 0 ? (total + prm.G - 1) / prm.G : 1;
   const int start = min(total, unit * chunk), end = min(total, start + chunk);
@@ -105,7 +117,7 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
     seg_hi = min(min(end, pb0 + nv) - pb0, n);
     seg_ok = seg_lo < seg_hi ? 1 : 0;
   }
-  if (lane == 0) *out = Plan{start, end, b0, pb0, chunk, L0, seg_lo, seg_hi, seg_ok};
+  if (lane == 0) *out = Plan{start, end, b0, pb0, chunk, L0, seg_lo, seg_hi, seg_ok, cost};
 }
 
 // Walks the (sequence, page range) segments of this CTA's work unit in order; every
@@ -119,7 +131,7 @@ struct Segments {
     NQT = prm.NQT;
     B = prm.B * prm.NQT;
     max_pages = prm.max_pages;
-    item_cost = prm.item_cost;
+    item_cost = plan.item_cost;
     start = plan.start;
     end = plan.end;
     b = plan.b0;

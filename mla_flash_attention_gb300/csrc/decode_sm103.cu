@@ -86,11 +86,16 @@ __host__ __device__ constexpr int chunk_idx(int c, int half) {
 }
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 // kF8: pages of four 128-column chunks (64 rows x 128 bytes, 128B-swizzled) and the rope columns
-// (64 rows x 64 bytes, 64B-swizzled), four of them; Q's smem part: latent 256..511 as two hi and two lo
-// chunks of 128 columns, then one chunk with the rope's hi and lo terms
+// (64 rows x 64 bytes, 64B-swizzled), four of them; Q's smem part: latent 256..383 as a hi and a lo
+// chunk, latent 384..511 likewise, then one chunk with the rope's hi and lo terms
 constexpr int kF8Page = 4 * kPageChunk + kPage * 64;  // 36 KB
 constexpr int kF8Stages = 4;
 static_assert(kF8Stages * kF8Page <= kStages * kStageBytes, "fp8 tree pages fit the stages");
+// Flat pages the tree's split plan charges for an item's start and end (its queries, the epilogue, and
+// for fp8 the query terms), at most: a page of keys takes 1.4 us (bf16) and 1.2 us (fp8).  64 ragged
+// sequences of up to 16384 keys, fp8: 404, 384, 364, 354, 345 and 346 us for 1, 4, 8, 12, 16 and 19; 16
+// sequences of 4096 keys and 16 x 128 rows, bf16: 371, 372, 368 and 367 us for 1, 3, 5 and 8.
+constexpr int kF8ItemCost = 16, kTreeItemCost = 6;
 constexpr int kF8PrepWarps = 6;                 // warps 2-3 and 8-11
 // registers a thread: 384 threads launched at kF8RegsLaunch, then traded between the warpgroups
 constexpr int kF8RegsLaunch = 168, kF8RegsHigh = 232, kF8RegsLow = 136;
@@ -112,10 +117,10 @@ struct Params {
   const int* cache_lens;
   float* part_o;
   float* part_lse;   // [2][n_slots][TQ]: each column half writes its own copy
-  // [G] tree: {item + 1, its splits} if the item whose second split is unit c's is left to the merge
-  // kernel, else 0, zeroed per call.  They lie in the last of the n_slots slots of part_o, which no
-  // split uses (unit c and item v share slot c + v <= G - 1 + B * NQT - 1).
-  int2* deferred;
+  // tree: how many items are left to the merge kernel (.x of the first entry, zeroed per call), then
+  // {item, first unit, splits} of each, at most one a unit.  They lie in the last of the n_slots
+  // slots of part_o, which no split uses (unit c and item v share slot c + v <= G - 1 + B * NQT - 1).
+  int4* deferred;
   int* counters;     // [B * NQT][2]: finished splits per (virtual sequence, half), zeroed per call
   uint16_t* out;     // [B, T, H, 512] bf16
   float* lse;        // [B, H, T]
@@ -137,6 +142,7 @@ struct Params {
 
 struct F8Bars {
   uint64_t full[kF8Stages], empty[kF8Stages];
+  uint64_t q_raw, q_sync;                   // raw query rows landed; warpgroup 2 has read them
   signed char q_exp[2][kRows];              // the power of two a query row was scaled by, by segment parity
   float ks[kRows / 32][kPage], lk[kRows / 32][kPage];  // a page's key scales and their log2, a copy a softmax warp
 };
@@ -214,21 +220,16 @@ __device__ __forceinline__ int page_row(const Params& p, int vseq, int pg) {
   return row_of_page(p, page_of(p, vseq, pg));
 }
 
-// Eight bf16 (times alpha) as their hi and lo e4m3 terms.
-__device__ __forceinline__ void split8(const uint4& w, float alpha, uint2& hi, uint2& lo) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t h[4], l[4];
+// Sixteen bf16 (times alpha) as their hi and lo e4m3 terms, 16 bytes each.
+__device__ __forceinline__ void split16(const uint4& w0, const uint4& w1, float alpha, uint4& hi, uint4& lo) {
+  const uint32_t in[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  uint32_t h[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
     ptx::split_e4m3x2(ptx::pack_f16x2(__uint_as_float(in[i] << 16) * alpha, __uint_as_float(in[i] & 0xffff0000u) * alpha),
                       h[i], l[i]);
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-}
-
-// 8 bytes at byte b of row r of a 128B-swizzled chunk of 128-byte rows
-__device__ __forceinline__ void store_swz128(unsigned char* chunk, int r, int b, const uint2& v) {
-  *reinterpret_cast<uint2*>(chunk + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 8)) = v;
+  hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
 }
 
 constexpr int kQNonFinite = 127;  // q_exp of a row with a NaN or an infinity: all its terms are NaN
@@ -238,13 +239,17 @@ __device__ __forceinline__ float q_factor(int k) {
   return k == kQNonFinite ? __int_as_float(0x7fc00000) : __int_as_float((k + 127) << 23);
 }
 
-// The preparation warps of the tree over an fp8 cache: the query terms of every segment, in two
-// steps through the same shared memory (latent 0..255, copied on to TMEM by the MMA thread; then the
-// rest, which stays), and the pages that end a sequence or hold drafted keys.
-template <typename B>
-__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, Segments segs, unsigned char* sm, int TH) {
+// The preparation warps of the tree over an fp8 cache.  All six prepare the pages that end a sequence
+// or hold drafted keys; warpgroup 2 (kQ) makes the query terms of every segment, in two steps through
+// the same shared memory (latent 0..255, copied on to TMEM by the MMA thread; then the rest, which
+// stays): raw rows by TMA, turned in place into terms by one thread a row (128 columns: 256 bytes of
+// bf16 become 128 of hi and 128 of lo).  A row's power of two needs all its columns, so the second
+// part is loaded twice, first for its largest value.
+template <bool kQ, typename B>
+__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, Segments segs, unsigned char* sm, int TH,
+                                           const CUtensorMap& tm_qlat, const CUtensorMap& tm_qrope) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pw = warp < 4 ? warp - 2 : warp - 6;  // 0 .. kF8PrepWarps - 1
+  const int pw = kQ ? warp - 6 : warp - 2;  // 0 .. kF8PrepWarps - 1
   volatile int* abort_flag = &bars.abort_flag;
   unsigned char* qa = sm + kOffQhi;
   int seq, L, lo, hi, g = 0, nseg = 0, n_zero = 0;
@@ -256,74 +261,88 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, Segments se
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
   };
+  auto first_row = [&](int v) { return (size_t)(v / p.NQT) * TH + (v % p.NQT) * kRows; };
+  auto live_rows = [&](int v) { return min(p.TQ, TH - (v % p.NQT) * kRows); };
+  // row r's raw chunks 2 c, 2 c + 1 (64 columns of bf16 each) become its hi and its lo chunk
+  const int r = (warp & 3) * 32 + lane;
+  auto granule = [&](int chunk, int i) {
+    return reinterpret_cast<uint4*>(qa + chunk * kQChunk + r * 128 + ((i ^ (r & 7)) << 4));
+  };
+  auto turn = [&](int c, float f, bool live) {
+    uint4 raw[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) raw[i] = live ? *granule(2 * c + (i >> 3), i & 7) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 h, l;
+      split16(raw[2 * i], raw[2 * i + 1], f, h, l);
+      *granule(2 * c, i) = h;
+      *granule(2 * c + 1, i) = l;
+    }
+  };
+  // all of warpgroup 2 is done with what is in the query area
+  int n_sync = 0;
+  auto sync = [&]() {
+    done(&bars.f8.q_sync);
+    return wait(&bars.f8.q_sync, n_sync++);
+  };
+  uint32_t mx = 0;  // the largest magnitude's bits of the row, as integers
+  auto largest = [&](int chunk) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 w = *granule(chunk, i);
+      mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu),
+                    __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    }
+  };
   while (segs.next(seq, L, lo, hi)) {
-    if (nseg > 0 && !wait(&bars.q_free, nseg - 1)) return;
-    const int tile0 = (seq % p.NQT) * kRows, live = min(p.TQ, TH - tile0);
-    const size_t r0 = (size_t)(seq / p.NQT) * TH + tile0;
-    signed char* q_exp = bars.f8.q_exp[nseg & 1];
-    constexpr int kBatch = 4;  // rows a warp has in flight
-    for (int base = pw; base < kRows; base += kBatch * kF8PrepWarps) {
-      uint4 a[kBatch], b[kBatch], c[kBatch];
+    if constexpr (kQ) {
+      if (nseg > 0 && !wait(&bars.q_free, nseg - 1)) return;
+      const int r0 = (seq / p.NQT) * TH + (seq % p.NQT) * kRows;
+      const bool live = r < min(p.TQ, TH - (seq % p.NQT) * kRows);
+      auto load = [&](int col) {  // latent col .. col + 255, and the rope columns with the second half
+        if (threadIdx.x != 8 * 32) return;
+        ptx::mbar_arrive_expect_tx(&bars.f8.q_raw, (col ? 5 : 4) * p.TQ * 128);
+        for (int c = 0; c < 4; ++c) ptx::tma_load_2d(qa + c * kQChunk, &tm_qlat, &bars.f8.q_raw, col + c * 64, r0);
+        if (col) ptx::tma_load_2d(qa + 4 * kQChunk, &tm_qrope, &bars.f8.q_raw, 0, r0);
+      };
+      load(256);
+      if (!wait(&bars.f8.q_raw, 3 * nseg)) return;
+      mx = 0;
+#pragma unroll 1
+      for (int c = 0; c < 5; ++c) largest(c);
+      if (!sync()) return;
+      load(0);
+      if (!wait(&bars.f8.q_raw, 3 * nseg + 1)) return;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) largest(c);
+      const uint32_t bits = max(mx & 0xffffu, mx >> 16);
+      const int field = bits >> 7;  // exponent + 127; 255: NaN or infinity
+      const int k = field == 255 ? kQNonFinite : bits == 0 ? 0 : min(max(134 - field, -120), 120);
+      bars.f8.q_exp[nseg & 1][r] = static_cast<signed char>(k);
+      const float f = q_factor(k);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) turn(c, f, live);
+      done(&bars.q_lo_full);
+      if (!wait(&bars.q_cp_done, nseg)) return;
+      load(256);
+      if (!wait(&bars.f8.q_raw, 3 * nseg + 2)) return;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) turn(c, f, live);
+      {  // rope: 64 columns, hi and lo in one chunk
+        uint4 raw[8];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rw = base + i * kF8PrepWarps;
-        a[i] = b[i] = c[i] = make_uint4(0, 0, 0, 0);
-        if (rw < live) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q_latent + (r0 + rw) * kDl);
-          a[i] = __ldg(src + lane);
-          b[i] = __ldg(src + 32 + lane);
-          if (lane < 8) c[i] = __ldg(reinterpret_cast<const uint4*>(p.q_rope + (r0 + rw) * 64) + lane);
+        for (int i = 0; i < 8; ++i) raw[i] = live ? *granule(4, i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 h, l;
+          split16(raw[2 * i], raw[2 * i + 1], f, h, l);
+          *granule(4, i) = h;
+          *granule(4, 4 + i) = l;
         }
       }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rw = base + i * kF8PrepWarps;
-        if (rw >= kRows) break;
-        // the largest magnitude's bits, as integers
-        uint32_t mx = 0;
-        const uint32_t w[12] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w, c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-        for (int x = 0; x < 12; ++x) mx = __vmaxu2(mx, w[x] & 0x7fff7fffu);
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-        const int field = bits >> 7;  // exponent + 127; 255: NaN or infinity
-        const int k = field == 255 ? kQNonFinite : bits == 0 ? 0 : min(max(134 - field, -120), 120);
-        if (lane == 0) q_exp[rw] = static_cast<signed char>(k);
-        uint2 h, l;
-        split8(a[i], q_factor(k), h, l);
-        store_swz128(qa + (lane >> 4) * kQChunk, rw, 8 * (lane & 15), h);
-        store_swz128(qa + (2 + (lane >> 4)) * kQChunk, rw, 8 * (lane & 15), l);
-      }
+      done(&bars.q_hi_full);
     }
-    done(&bars.q_lo_full);
-    if (!wait(&bars.q_cp_done, nseg)) return;
-    for (int base = pw; base < kRows; base += kBatch * kF8PrepWarps) {
-      uint4 b[kBatch], c[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rw = base + i * kF8PrepWarps;
-        b[i] = c[i] = make_uint4(0, 0, 0, 0);
-        if (rw < live) {
-          b[i] = __ldg(reinterpret_cast<const uint4*>(p.q_latent + (r0 + rw) * kDl) + 32 + lane);
-          if (lane < 8) c[i] = __ldg(reinterpret_cast<const uint4*>(p.q_rope + (r0 + rw) * 64) + lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int rw = base + i * kF8PrepWarps;
-        if (rw >= kRows) break;
-        const float f = q_factor(q_exp[rw]);
-        uint2 h, l;
-        split8(b[i], f, h, l);
-        store_swz128(qa + (lane >> 4) * kQChunk, rw, 8 * (lane & 15), h);
-        store_swz128(qa + (2 + (lane >> 4)) * kQChunk, rw, 8 * (lane & 15), l);
-        if (lane < 8) {
-          split8(c[i], f, h, l);
-          store_swz128(qa + 4 * kQChunk, rw, 8 * lane, h);
-          store_swz128(qa + 4 * kQChunk, rw, 64 + 8 * lane, l);
-        }
-      }
-    }
-    done(&bars.q_hi_full);
     ++nseg;
     // pages past the clean keys: granules of drafted keys that hold a NaN are zeroed and the key
     // flagged, the rows past the sequence's end are zeroed (whole rows, so the swizzles are immaterial)
@@ -408,6 +427,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         ptx::mbar_init(&bars.f8.full[s], 1);
         ptx::mbar_init(&bars.f8.empty[s], 1);
       }
+      ptx::mbar_init(&bars.f8.q_raw, 1);
+      ptx::mbar_init(&bars.f8.q_sync, 4);
     }
     if (!kFp8 && p.page_box) {
       ptx::prefetch_tensormap(&tm_c4);
@@ -435,9 +456,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::mbar_init(&bars.o_done, 1);
     ptx::mbar_init(&bars.seg_done, 1);
     ptx::mbar_init(&bars.q_free, 1);
-    ptx::mbar_init(&bars.q_lo_full, kF8 ? kF8PrepWarps : 1);
+    ptx::mbar_init(&bars.q_lo_full, kF8 ? 4 : 1);  // kF8: the warps of warpgroup 2
     ptx::mbar_init(&bars.q_cp_done, 1);
-    ptx::mbar_init(&bars.q_hi_full, kF8 ? kF8PrepWarps : 1);
+    ptx::mbar_init(&bars.q_hi_full, kF8 ? 4 : 1);
     ptx::mbar_init(&bars.q0_copied, 1);
     ptx::mbar_init(&bars.conv_sync, n_prep / 32);  // one arrival per preparation warp
     ptx::mbar_init(&bars.part_done, n_soft);
@@ -447,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::fence_barrier_init();
   }
   // the plan's length loads go out first; the other warps set up meanwhile
-  if (warp == 3) make_plan(p, unit, &bars.plan);
+  if (warp == 3) make_plan<kTree>(p, unit, &bars.plan);
   // Q rows T*H..127 are never loaded: keep them zero (finite scores in the padded rows)
   for (int i = threadIdx.x; i < 5 * kQChunk / 16; i += kThreads)
     reinterpret_cast<uint4*>(sm + kOffQhi)[i] = make_uint4(0, 0, 0, 0);
@@ -628,15 +649,16 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // latent 0..255: A from TMEM
             const uint64_t db = st + 512 * (j >> 2) + 2 * (j & 3);
-            ptx::mma_f8_ts(d, tmem + j * 8, db, kIdS8, j > 0 ? 1u : 0u);
-            ptx::mma_f8_ts(d, tmem + 64 + j * 8, db, kIdS8, 1u);
+            const uint32_t qa = tmem + (j >> 2) * 64 + (j & 3) * 8;
+            ptx::mma_f8_ts(d, qa, db, kIdS8, j > 0 ? 1u : 0u);
+            ptx::mma_f8_ts(d, qa + 32, db, kIdS8, 1u);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // latent 256..511: A from shared memory
             const uint64_t db = st + 512 * (2 + (j >> 2)) + 2 * (j & 3);
-            const uint64_t da = qd + 1024 * (j >> 2) + 2 * (j & 3);
+            const uint64_t da = qd + 2048 * (j >> 2) + 2 * (j & 3);
             ptx::mma_f8_ss(d, da, db, kIdS8, 1u);
-            ptx::mma_f8_ss(d, da + 2048, db, kIdS8, 1u);
+            ptx::mma_f8_ss(d, da + 1024, db, kIdS8, 1u);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // rope
@@ -813,7 +835,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       }
     }
    } else if constexpr (kF8) {
-    prepare_f8(p, bars, segs, sm, TH);
+    if (warp < 4) prepare_f8<false>(p, bars, segs, sm, TH, tm_qlat, tm_qrope);
+    else prepare_f8<true>(p, bars, segs, sm, TH, tm_qlat, tm_qrope);
    } else {
     // -------------------------------------------------------------- stage preparation
     // 0 .. n_prep - 1: warps 2-3, then 8-11, then the softmax warps that joined
@@ -1216,7 +1239,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           fast = 0;
           if (half == 0 && k_own == 1) {
             asm volatile("griddepcontrol.wait;" ::: "memory");  // zeroed before
-            p.deferred[unit] = make_int2(seq + 1, nsplit);
+            p.deferred[1 + atomicAdd(&p.deferred[0].x, 1)] = make_int4(seq, c_first, nsplit, 0);
           }
         } else if (nsplit > 1) {
           // the counters were zeroed by the kernel this one was launched behind
@@ -1439,88 +1462,86 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   }
 }
 
-// Merges the tree items that went into more than kFusedSplits splits, all over the GPU: block
-// (c, y) takes 32 rows and 32 column quads of the item whose second split is unit c's, if there is
-// one.  Left to the split that finishes last, the merge reads every partial through one SM, about
-// 4 us a split: one sequence of 1000 keys and 128 rows, in 16 splits, took 68 us, 50 of them there.
-// The splits are weighed and summed in split order, as in the split kernel's own merge.
-constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeQuads = 32;
-constexpr int kMaxSplits = 128;
-static_assert(kMaxSplits * sizeof(int2) <= kDl * sizeof(float), "a slot of one row holds the deferred items");
+// Merges the tree items that went into more than kFusedSplits splits, all over the GPU: the split
+// kernel lists them (Params::deferred), the blocks here share the list's slices of 32 rows and 16
+// column quads.  Left to the split that finishes last, the merge reads every partial through one SM,
+// about 4 us a split: one sequence of 1000 keys and 128 rows, in 16 splits, took 68 us, 50 of them
+// there.  The splits are weighed and summed in split order, as in the split kernel's own merge.
+constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeQuads = 16;  // two quads a thread
+constexpr int kMergeSlices = (kRows / kMergeRows) * (128 / kMergeQuads);
+constexpr int kMergeBlocks = 304;
 
-__global__ void __launch_bounds__(kMergeThreads, 4) tree_merge_kernel(const Params p) {
-  __shared__ float weight[kMaxSplits][kMergeRows];
-  const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Params p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel is done
-  const int2 d = __ldcg(p.deferred + unit);
-  if (d.x == 0) return;
-  const int item = d.x - 1, nsplit = d.y, c_first = unit - 1;
-  const int r = (blockIdx.y & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
-  const bool live = r < p.TQ && gr < p.T * p.H;
-  const int q0 = (blockIdx.y >> 2) * kMergeQuads, half = q0 / 64;
-  const float* lsp = p.part_lse + ((size_t)half * p.n_slots + c_first + item) * p.TQ + r;
-  if (warp == 0) {
+  const int work = __ldcg(&p.deferred[0].x) * kMergeSlices;
+  for (int w = blockIdx.x; w < work; w += gridDim.x) {
+    const int4 d = __ldcg(reinterpret_cast<const int4*>(p.deferred + 1) + w / kMergeSlices);
+    const int item = d.x, c_first = d.y, nsplit = d.z, slice = w % kMergeSlices;
+    const int r = (slice & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
+    const bool live = r < p.TQ && gr < p.T * p.H;
+    const int q = (slice >> 2) * kMergeQuads + 2 * warp, half = q / 64;
+    if (!live) continue;  // (no warp-collective step below)
+    const float* lsp = p.part_lse + ((size_t)half * p.n_slots + c_first + item) * p.TQ + r;
+    constexpr int kBatch = 8;  // splits in flight
     float mx = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < nsplit; ++k) {
-      const float ls = live ? ptx::ld_l2(lsp + (size_t)k * p.TQ) : -INFINITY;
-      weight[k][lane] = ls;
-      mx = fmaxf(mx, ls);
+    for (int k0 = 0; k0 < nsplit; k0 += 2 * kBatch) {
+      float ls[2 * kBatch];
+#pragma unroll
+      for (int k = 0; k < 2 * kBatch; ++k) ls[k] = k0 + k < nsplit ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 2 * kBatch; ++k) mx = fmaxf(mx, ls[k]);
     }
-    for (int k = 0; k < nsplit; ++k) {
-      const float ls = weight[k][lane];
-      const float w = ls != ls ? ls : ls == -INFINITY ? 0.f : __expf(ls - mx);
-      weight[k][lane] = w;
-      sum += w;
+    auto weight = [&](float ls) { return ls != ls ? ls : ls == -INFINITY ? 0.f : __expf(ls - mx); };
+    for (int k0 = 0; k0 < nsplit; k0 += 2 * kBatch) {
+      float ls[2 * kBatch];
+#pragma unroll
+      for (int k = 0; k < 2 * kBatch; ++k) ls[k] = k0 + k < nsplit ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 2 * kBatch; ++k) sum += weight(ls[k]);
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    for (int k = 0; k < nsplit; ++k) weight[k][lane] *= inv;
-    float* lp = p.lse + ((size_t)(item / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
-    if (q0 == 0 && live && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err))
-      *lp = sum != 0.f ? mx + logf(sum) : -INFINITY;
-  }
-  __syncthreads();
-  if (!live) return;
-  // four column quads (32 bytes of a bf16 row) a thread, four splits' loads in flight
-  const int q = q0 + 4 * warp;
-  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((size_t)(c_first + item) * 128 + q) * p.TQ + r;
-  const size_t slot_stride = (size_t)128 * p.TQ;
-  float4 acc[4] = {};
-  for (int k0 = 0; k0 < nsplit; k0 += 4) {
-    float4 x[4][4];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((size_t)(c_first + item) * 128 + q) * p.TQ + r;
+    const size_t slot_stride = (size_t)128 * p.TQ;
+    float4 acc[2] = {};
+    for (int k0 = 0; k0 < nsplit; k0 += kBatch) {
+      float4 x[kBatch][2];
+      float ls[kBatch];
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
+      for (int k = 0; k < kBatch; ++k) {
+        const bool in = k0 + k < nsplit;
+        ls[k] = in ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[kk][j] = k0 + kk < nsplit ? ptx::ld_l2(src + (k0 + kk) * slot_stride + (size_t)j * p.TQ)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 2; ++j)
+          x[k][j] = in ? ptx::ld_l2(src + (k0 + k) * slot_stride + (size_t)j * p.TQ) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const float w = k0 + kk < nsplit ? weight[k0 + kk][lane] : 0.f;
+      for (int k = 0; k < kBatch; ++k) {
+        const float wk = weight(ls[k]) * inv;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[j].x = fmaf(w, x[kk][j].x, acc[j].x);
-        acc[j].y = fmaf(w, x[kk][j].y, acc[j].y);
-        acc[j].z = fmaf(w, x[kk][j].z, acc[j].z);
-        acc[j].w = fmaf(w, x[kk][j].w, acc[j].w);
+        for (int j = 0; j < 2; ++j) {
+          acc[j].x = fmaf(wk, x[k][j].x, acc[j].x);
+          acc[j].y = fmaf(wk, x[k][j].y, acc[j].y);
+          acc[j].z = fmaf(wk, x[k][j].z, acc[j].z);
+          acc[j].w = fmaf(wk, x[k][j].w, acc[j].w);
+        }
       }
     }
+    uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)(item / p.NQT) * p.T * p.H + gr) * kDl + q * 4);
+    if (MLA_STORE_OK(o, p.out, p.out_bytes, p.err))
+      *o = make_uint4(ptx::pack_bf16x2(acc[0].x, acc[0].y), ptx::pack_bf16x2(acc[0].z, acc[0].w),
+                      ptx::pack_bf16x2(acc[1].x, acc[1].y), ptx::pack_bf16x2(acc[1].z, acc[1].w));
+    float* lp = p.lse + ((size_t)(item / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
+    if (q == 0 && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = sum != 0.f ? mx + logf(sum) : -INFINITY;
   }
-  uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)(item / p.NQT) * p.T * p.H + gr) * kDl + q * 4);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (MLA_STORE_OK(o + j, p.out, p.out_bytes, p.err))
-      o[j] = make_uint4(ptx::pack_bf16x2(acc[2 * j].x, acc[2 * j].y), ptx::pack_bf16x2(acc[2 * j].z, acc[2 * j].w),
-                        ptx::pack_bf16x2(acc[2 * j + 1].x, acc[2 * j + 1].y),
-                        ptx::pack_bf16x2(acc[2 * j + 1].z, acc[2 * j + 1].w));
 }
 
 // Zeroes the split counters of a decode call; the split kernel is launched behind it as a
 // programmatic dependent and waits for it only where it first touches a counter.
 __global__ void __launch_bounds__(256) zero_counters_kernel(int* __restrict__ c, int n,
-                                                               int2* __restrict__ deferred, int units) {
+                                                               int4* __restrict__ deferred) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0 && threadIdx.x < units) deferred[threadIdx.x] = make_int2(0, 0);
+  if (deferred && blockIdx.x == 0 && threadIdx.x == 0) deferred[0] = make_int4(0, 0, 0, 0);
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) c[i] = 0;
 }
 
@@ -1567,7 +1588,8 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
       &tm, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_cache,
       dims, strides, box, /*swizzle128=*/!fp8 || f8);
   if (e != cudaSuccess) return e;
-  if (tree_mask && G > kMaxSplits) return cudaErrorNotSupported;  // the merge kernel's tables
+  // the list of deferred items in a slot of one row (2048 bytes)
+  if (tree_mask && (G + 1) * sizeof(int4) > kDl * sizeof(float)) return cudaErrorNotSupported;
   // The same bytes as a 3-D tensor (64 columns of a chunk, row, chunk of 64 columns): a box
   // of 64 x 64 x n is n consecutive 64-column chunks of a page, landing chunk-major exactly as
   // n 2-D boxes do (one TMA instruction instead of n): fp8 pages take one box of nine chunks,
@@ -1635,12 +1657,13 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   p.mask_stride = mask_stride;
   p.mask_words = (T + 31) / 32;
   p.new_lens = new_lens;
-  p.deferred = reinterpret_cast<int2*>(part_o + (size_t)(p.n_slots - 1) * TQ * kDl);
+  p.deferred = reinterpret_cast<int4*>(part_o + (size_t)(p.n_slots - 1) * TQ * kDl);
   p.page_box = page_box ? 1 : 0;
   // one flat page charged per work item (its Q load, epilogue and merge; measured against
   // 0, 2 and 4 on uniform and ragged batches: the same time for 64 sequences of 4096 keys,
   // up to 7 % less where sequences split over several units or end mid-unit)
-  p.item_cost = 1;
+  if (tree_mask) p.item_cost = fp8 ? kF8ItemCost : kTreeItemCost;  // at most, the plan adapts them
+  else p.item_cost = 1;
   const size_t out_full = (size_t)B * T * H * kDl * 2;
   p.out_bytes = out_full - std::min(out_full, testing_out_shrink());
   p.lse_bytes = (size_t)B * H * T * sizeof(float);
@@ -1660,7 +1683,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     __atomic_store_n(&carveout_set, 1, __ATOMIC_RELEASE);
   }
   const int zero_blocks = (int)std::min<long long>((n_cnt + 2047) / 2048, 1024);
-  zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt, p.deferred, tree_mask ? G : 0);
+  zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt, tree_mask ? p.deferred : nullptr);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto go = [&](auto kern) -> cudaError_t {
     static unsigned long long smem_set[4] = {0, 0, 0, 0};
@@ -1694,7 +1717,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     }
     if ((e = fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(G, (kRows / kMergeRows) * (128 / kMergeQuads));
+    cfg.gridDim = dim3(kMergeBlocks);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
