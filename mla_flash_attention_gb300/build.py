@@ -59,7 +59,7 @@ def _build_marshal():
     _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
           *[x for i in inc for x in ("-isystem", i)], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
-          "-L", lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"])
+          "-L", lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])
     os.replace(tmp, MARSHAL)
     return MARSHAL
 

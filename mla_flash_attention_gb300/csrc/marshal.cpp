@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -102,7 +103,7 @@ int64_t row_stride(const Tensor& t, const char* name) {
 }
 
 Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, const at::Device& dev) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+  return at::detail::empty_cuda(shape, dtype, dev, std::nullopt);
 }
 
 void* stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
