@@ -9,9 +9,10 @@
 // partial result of unit c for item v goes to slot c + v, which is unique because consecutive
 // units never move backwards through the items; there are at most G + (items) - 1 slots.
 // A parameter struct passed to make_plan / Segments::init provides cache_lens, B, NQT
-// (query tiles per sequence), max_pages, G and item_cost (flat pages charged per item).  An
-// adaptive plan charges at most a unit's even share of the real pages, so that with few pages
-// whole units are not spent on flat pages without keys; Plan::item_cost is what it charges.
+// (query tiles per sequence), max_pages, G and item_cost (flat pages charged per item).  The plan
+// of drafted trees (kTree) leaves out query tiles that hold only padding (new_lens, T and H of the
+// struct tell), and charges an item at most a unit's even share of the real pages, so that with
+// few pages whole units are not spent on flat pages without keys; Plan::item_cost is what it charges.
 #pragma once
 
 #include "common.cuh"
@@ -35,6 +36,21 @@ __device__ __forceinline__ int clamp_len(int L, int max_pages) {
   return min(max(L, 0), max_pages * kPage);
 }
 
+// Drafted tokens of sequence b (tree); its rows of later tokens are padding.
+template <typename Prm>
+__device__ __forceinline__ int drafted_of(const Prm& prm, int b) {
+  return prm.new_lens ? min(max(__ldg(prm.new_lens + b), 0), prm.T) : prm.T;
+}
+
+// Keys that item v (sequence v / NQT, query tile v % NQT) works on: its sequence's, or none.
+template <bool kTree, typename Prm>
+__device__ __forceinline__ int item_len(const Prm& prm, int v) {
+  const int L = clamp_len(__ldg(prm.cache_lens + v / prm.NQT), prm.max_pages);
+  if constexpr (kTree)
+    if (prm.new_lens && (v % prm.NQT) * 128 >= drafted_of(prm, v / prm.NQT) * prm.H) return 0;
+  return L;
+}
+
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -43,14 +59,14 @@ __device__ __forceinline__ int warp_sum(int v) {
 
 // The Plan of work unit `unit`, computed by one warp with coalesced loads of the lengths
 // (256 at a time) and warp scans.
-template <bool kAdaptive = false, typename Prm>
+template <bool kTree = false, typename Prm>
 __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
   const int lane = threadIdx.x & 31;
   const int B = prm.B * prm.NQT;  // work is planned per (sequence, query tile)
   auto len_at = [&](int bb) {
-    return bb < B ? clamp_len(__ldg(prm.cache_lens + bb / prm.NQT), prm.max_pages) : 0;
+    return bb < B ? item_len<kTree>(prm, bb) : 0;
   };
-  int cost = kAdaptive ? 0 : prm.item_cost;
+  int cost = kTree ? 0 : prm.item_cost;
   auto flat_of = [&](int Lb) {
     const int n = pages_of(Lb, kPage);
     return n > 0 ? n + cost : 0;
@@ -68,12 +84,12 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += flat_of(l[i]);
     total += warp_sum(sum);
-    if (kAdaptive) {
+    if (kTree) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) items += __popc(__ballot_sync(0xffffffffu, l[i] > 0));
     }
   }
-  if (kAdaptive) {
+  if (kTree) {
     cost = max(1, min(prm.item_cost, total / prm.G));
     total += items * cost;
   }
@@ -122,12 +138,20 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
 
 // Walks the (sequence, page range) segments of this CTA's work unit in order; every
 // role runs its own copy and sees the same sequence.
-struct Segments {
-  const int* lens;
+template <bool kTree>
+struct SegmentsOf {
+  const int* cache_lens;
+  const int* new_lens;  // tree
+  int T, H;             // tree
   int B, NQT, max_pages, item_cost, start, end, b, pb;
   template <typename Prm>
   __device__ void init(const Prm& prm, const Plan& plan) {
-    lens = prm.cache_lens;
+    cache_lens = prm.cache_lens;
+    if constexpr (kTree) {
+      new_lens = prm.new_lens;
+      T = prm.T;
+      H = prm.H;
+    }
     NQT = prm.NQT;
     B = prm.B * prm.NQT;
     max_pages = prm.max_pages;
@@ -164,11 +188,11 @@ struct Segments {
     while (b < B && pb < end) {
       int Ls[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) Ls[i] = b + i < B ? __ldg(lens + (b + i) / NQT) : 0;
+      for (int i = 0; i < 8; ++i) Ls[i] = b + i < B ? item_len<kTree>(*this, b + i) : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (b >= B || pb >= end) return false;
-        const int Lb = clamp_len(Ls[i], max_pages);
+        const int Lb = Ls[i];
         const int n = pages_of(Lb, kPage);
         const int nv = n > 0 ? n + item_cost : 0;  // flat pages of the item
         const int l0 = max(start, pb) - pb, h0 = min(min(end, pb + nv) - pb, n);
@@ -188,6 +212,7 @@ struct Segments {
     return false;
   }
 };
+using Segments = SegmentsOf<false>;
 
 
 }  // namespace decode_plan

@@ -55,7 +55,7 @@ namespace mla {
 namespace sm103_decode {
 
 using decode_plan::Plan;
-using decode_plan::Segments;
+using decode_plan::SegmentsOf;
 using decode_plan::clamp_len;
 using decode_plan::make_plan;
 constexpr int kPage = decode_plan::kPage;
@@ -180,9 +180,7 @@ struct Bars {
 static_assert(sizeof(Bars<true, true>) <= 3072, "static shared memory of the fp8 tree");
 
 // Drafted tokens of virtual sequence v: the newest n keys; rows of tokens n .. T - 1 are padding.
-__device__ __forceinline__ int drafted(const Params& p, int vseq) {
-  return p.new_lens ? min(max(__ldg(p.new_lens + vseq / p.NQT), 0), p.T) : p.T;
-}
+__device__ __forceinline__ int drafted(const Params& p, int vseq) { return decode_plan::drafted_of(p, vseq / p.NQT); }
 
 // Bits j .. j + 63 of a row's tree mask, 0 past its words (j >= 0).
 __device__ __forceinline__ unsigned long long mask_bits(const uint32_t* row, int words, int j) {
@@ -246,7 +244,7 @@ __device__ __forceinline__ float q_factor(int k) {
 // bf16 become 128 of hi and 128 of lo).  A row's power of two needs all its columns, so the second
 // part is loaded twice, first for its largest value.
 template <bool kQ, typename B>
-__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, Segments segs, unsigned char* sm, int TH,
+__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int TH,
                                            const CUtensorMap& tm_qlat, const CUtensorMap& tm_qrope) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pw = kQ ? warp - 6 : warp - 2;  // 0 .. kF8PrepWarps - 1
@@ -479,6 +477,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort_flag;
+  using Segments = SegmentsOf<kTree>;
   Segments segs;
   segs.init(p, bars.plan);
   int seq, L, lo, hi;
@@ -964,15 +963,18 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int g = 0, n_epi = 0, n_part = 0, n_bulk = 0, n_bulk_issued = 0;
     bool ok = true;
-    // a sequence with no cached key is in no work unit's range: unit u writes O = 0 and
-    // LSE = -inf for the empty sequences u, u + G, u + 2G, ...
+    // an item with no keys (an empty sequence; tree: a query tile of padding) is in no work unit's
+    // range: unit u writes O = 0 and LSE = -inf for such sequences (tree: items) u, u + G, u + 2G, ...
     if (half == 0) {
-      for (int b = unit; b < p.B; b += p.G) {
-        if (clamp_len(__ldg(p.cache_lens + b), p.max_pages) > 0) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * TH * kDl);
-        for (int i = r; i < TH * (kDl / 8); i += 32 * n_soft)
+      const int per = kTree ? p.NQT : 1;  // items a sequence
+      for (int v = unit; v < p.B * per; v += p.G) {
+        const int b = v / per, row0 = (v % per) * kRows;
+        if ((kTree ? decode_plan::item_len<kTree>(p, v) : clamp_len(__ldg(p.cache_lens + b), p.max_pages)) > 0) continue;
+        const int rows = kTree ? min(kRows, TH - row0) : TH;
+        uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)b * TH + row0) * kDl);
+        for (int i = r; i < rows * (kDl / 8); i += 32 * n_soft)
           if (MLA_STORE_OK(o + i, p.out, p.out_bytes, p.err)) o[i] = make_uint4(0, 0, 0, 0);
-        for (int i = r; i < TH; i += 32 * n_soft) {
+        for (int i = row0 + r; i < row0 + rows; i += 32 * n_soft) {
           float* lp = p.lse + ((size_t)b * p.H + i % p.H) * p.T + i / p.H;
           if (MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = -INFINITY;
         }

@@ -60,6 +60,8 @@ class Problem:
     (16, 13, [13, 500, 64, 0, 77], [13, 0, 7, 5, 13]),    # no drafted token, an empty sequence
     (3, 64, [64, 63, 200], [64, 64, 50]),                 # 64 nodes: a whole page of drafted keys
     (2, 150, [140, 600], [150, 131]),                     # five mask words over three pages
+    (128, 5, [300, 65, 0, 700, 9, 64], [1, 5, 3, 0, 3, 2]),  # whole tiles of query rows that are padding
+    (48, 7, [2000, 130], [3, 6]),                         # tiles that end in padding, or within a token's heads
 ])
 def test_trees(lib, H, T, lens, new, fp8):
     p = Problem(H, T, lens, fp8, seed=H * 100 + T, new=new)
