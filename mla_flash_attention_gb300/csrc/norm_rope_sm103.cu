@@ -10,14 +10,16 @@
 // One pass over memory bounds it: 2 bytes in and out an element (forward), 6 (gradient), about
 // ten operations each.  The work is a list of warp tasks of four kinds, walked in a grid stride:
 // four (row, head) pairs of q's nope part, the same of k_nope (16 lanes a pair, 16 bytes a lane),
-// the rope parts of eight of q's heads in one row (8 lanes a head), one row's rope key.  One kind at a time keeps few values live, so that the SM holds enough warps
-// to cover memory's latency: 16384 tokens of 128 heads, q and keys, 424 us (6.3 TB/s, 93 % of the
-// measured copy rate); the gradient of 4096 tokens of 64 heads 90 us (5.6 TB/s, 82 %).  With q and
-// k_nope of four heads in one task the registers (104 and 152 a thread) left too few warps: 520 and
-// 175 us.  A task's loads issued while the one before is worked on cost more in registers than they
-// gave (429 and 91 us at 64 and 80 registers).  The sums are shuffles inside the 16 or 8 lanes; each lane makes the cos and sin of one of
-// the 32 frequencies and the others fetch it by shuffle.  Everything between load and store is
-// fp32, rounded once.
+// the rope parts of eight of q's heads in one row (8 lanes a head), one row's rope key.  One kind
+// at a time keeps few values live, so that the SM holds enough warps to cover memory's latency:
+// 16384 tokens of 128 heads, q and keys, 424 us (6.3 TB/s, 93 % of the measured copy rate); the
+// gradient of 4096 tokens of 64 heads 90 us (5.6 TB/s, 82 %).  With q and k_nope of four heads in
+// one task the registers (104 and 152 a thread) left too few warps: 520 and 175 us.  A task's
+// loads issued while the one before is worked on cost more in registers than they gave (429 and
+// 91 us at 64 and 80 registers).
+// The sums are shuffles inside the 16 or 8 lanes; each lane makes the cos and sin of one of the 32
+// frequencies and the others fetch it by shuffle.  Everything between load and store is fp32,
+// rounded once.
 // The gradient's weight sums stay in registers while a warp's tasks are of one kind, then go to
 // the warp's own row in shared memory; a block writes its warps' sum as one partial row of 384, and
 // a second kernel adds the partial rows in a fixed order, so the result does not depend on the run.
@@ -298,14 +300,15 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) norm_rope_grad_kernel(c
 
 // dw[col] = sum of the blocks' partial rows.  A block takes 32 columns, its 32 warps every 32nd
 // row each, joined in warp order.
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restrict__ partial, int rows,
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partial, int rows,
                                                            float* dw_qn, float* dw_qr, float* dw_kn, float* dw_kr) {
   __shared__ float joined[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are written
 #pragma unroll 4
-  for (int r = warp; r < rows; r += 32) v += __ldg(partial + (size_t)r * kDw + col);
+  for (int r = warp; r < rows; r += 32) v += ptx::ld_l2(partial + (size_t)r * kDw + col);
   joined[warp][lane] = v;
   __syncthreads();
   if (warp > 0) return;
@@ -437,8 +440,18 @@ cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const 
     norm_rope_grad_kernel<false><<<grid, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
-  weight_grad_kernel<<<kDw / 32, 1024, 0, stream>>>(workspace, grid, dw_qn, dw_qr, dw_kn, dw_kr);
-  return cudaGetLastError();
+  // a programmatic dependent: it is set up while the last blocks finish
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kDw / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_grad_kernel, static_cast<const float*>(workspace), grid, dw_qn, dw_qr, dw_kn,
+                            dw_kr);
 }
 
 }  // namespace mla
