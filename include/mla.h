@@ -1,7 +1,7 @@
 /*
  * mla.h -- C ABI of the GB300 (sm_103a) fused multi-head latent attention library.
  *
- * Two operations, both exact attention in flash form (scores S = Q K', online
+ * Three operations, all exact attention in flash form (scores S = Q K', online
  * softmax, O += P V -- Modular API docs, "KVPipelineGeneric" (nn/attention/gpu/
  * nvidia/sm100/mla_decode_utils), struct description and Parameters):
  *
@@ -14,6 +14,12 @@
  *                shared latent head (d_latent + d_rope columns per token) kept in a
  *                paged cache; V is the first d_latent columns of the same rows.
  *                Split over the key axis across CTAs, then merged by log-sum-exp.
+ *   mla_decode_tree  the same for a tree of drafted tokens: which of the newest keys a new
+ *                token sees comes from a bit mask.
+ *
+ * and the steps around them: cache appends (mla_cache_append, mla_rope_append), norms and
+ * rotation of queries and keys with their gradient (mla_qk_norm_rope), the absorption products
+ * (mla_absorb) and the prefill's backward pass.
  *
  * Conventions shared by every entry point
  *   - All tensor arguments are DEVICE pointers, contiguous, innermost dimension
@@ -237,8 +243,8 @@ mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm
  * name.  A row that sees no key gets O = 0 and LSE = -inf.  A drafted key whose cached row (or
  * scale) is not finite makes the rows that see it NaN and leaves the others alone.
  * Everything else -- layouts, cache types, lengths, bad pages, out, lse, the workspace
- * (mla_decode_workspace_size) and the limits -- is as for mla_decode, with num_pages * page_size
- * and B * q_len * H below 2^31.
+ * (mla_decode_workspace_size; calls that overlap on the GPU need one each) and the limits -- is as
+ * for mla_decode, with num_pages * page_size and B * q_len * H below 2^31.
  */
 mla_status mla_decode_tree(const void* q_latent, const void* q_rope, const void* kv_cache,
                            const float* kv_scale, const int* page_table, const int* cache_lens,

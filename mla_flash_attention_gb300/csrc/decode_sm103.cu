@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           float2 k2 = make_float2(key < L ? ks_next.x : 0.f, key + 1 < L ? ks_next.y : 0.f);
           // log2 of the scale, floored (a scale of 0 gives weights of 0); NaN flags a drafted key whose
           // scale is not finite
-          float2 l2 = make_float2(fmaxf(__log2f(k2.x), -100.f), fmaxf(__log2f(k2.y), -100.f));
+          float2 l2 = make_float2(fmaxf(__log2f(fabsf(k2.x)), -100.f), fmaxf(__log2f(fabsf(k2.y)), -100.f));
           if (tree_page && !(fabsf(k2.x) < INFINITY)) k2.x = 0.f, l2.x = __int_as_float(0x7fc00000);
           if (tree_page && !(fabsf(k2.y) < INFINITY)) k2.y = 0.f, l2.y = __int_as_float(0x7fc00000);
           __syncwarp();  // the warp has read the page before's

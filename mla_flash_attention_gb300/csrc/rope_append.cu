@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Para
     rp = __ldg(reinterpret_cast<const uint2*>(src + kDl) + l);
   }
   const ulonglong2 turns = *(reinterpret_cast<const ulonglong2*>(p.turns) + l);
-  const int place = static_cast<int>(min((long long)L - n + t, 0x7fffffffLL));
+  const int place = static_cast<int>(max(min((long long)L - n + t, 0x7fffffffLL), -1LL));
   // rows t >= n are padding; of a sequence with fewer cached tokens than new ones the first have
   // no place; more new tokens than rows are refused
   bool write = t < n && (place >= 0 || n > p.T);

@@ -6,18 +6,16 @@ import os
 import pytest
 import torch
 
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P, I, L, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
 
 @pytest.fixture(scope="module")
 def clib():
-    path = os.path.join(ROOT, "mla_flash_attention_gb300", "libmla_gb300.so")
-    if not os.path.exists(path):
-        from mla_flash_attention_gb300 import build
+    from mla_flash_attention_gb300 import build
 
+    if not (os.path.exists(build.LIB) and os.path.exists(build.MARSHAL)):
         build.build()
-    lib = ctypes.CDLL(path)
+    lib = ctypes.CDLL(build.LIB)
     lib.mla_last_error.restype = ctypes.c_char_p
     return lib
 

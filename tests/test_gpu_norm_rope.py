@@ -4,8 +4,8 @@ Tolerances, element by element, from the arithmetic (fp32 inside, one rounding a
   - bf16 outputs are rounded once: 2^-8 |y|.
   - a norm's sum of squares has at most 7 + 4 fp32 additions in a chain, then rsqrt (2 ulp), two
     products: below 2^-19 relative.  An angle is off by 2^-24 of half a turn (its fraction of a turn
-    in fp32) plus sincospif's 2 ulp: below 2^-20; so a rotated value is off by less than
-    2^-18 (|a| + |b|) of its pair (a, b).
+    in fp32) and the fast sine and cosine of an angle in [-pi, pi] by 2^-21: together below 2^-19; so a
+    rotated value is off by less than 2^-18 (|a| + |b|) of its pair (a, b).
   - dx = r (w g - x r^2 mean(x w g)): every factor to 2^-19, so 2^-17 r (|w g| + |x| r^2 mean |x w g|),
     with g, where it was turned back, off by 2^-18 (|g_a| + |g_b|) itself.
   - dw: a lane adds at most a few tens of terms in a row before the joins over lanes, warps and

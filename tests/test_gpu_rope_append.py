@@ -1,8 +1,8 @@
 """GPU parity of mla_rope_append (through the C ABI) against the fp64 oracle.
 
 Tolerances: bf16 rows 2^-8 |y| for the rounding plus 2^-17 (|y|, or |a| + |b| of a rotated pair)
-for the fp32 arithmetic (a 512-term sum in chains of 16 + 5 additions, rsqrt, two products; angles to
-2^-20).  e4m3 rows: scale = amax / 448 to 2^-17, codes 2^-4 |y| relative or half the smallest step,
+for the fp32 arithmetic (a 512-term sum in chains of 16 + 5 additions, rsqrt, two products; sines and
+cosines to 2^-19).  e4m3 rows: scale = amax / 448 to 2^-17, codes 2^-4 |y| relative or half the smallest step,
 2^-10 scale, plus the same fp32 part.
 """
 import numpy as np
@@ -100,6 +100,22 @@ def test_ragged_new_tokens(lib, fp8):
     p.run(lib, False)
     lib.check_device_error()
     p.check(False)
+
+
+def test_lengths_of_no_meaning_write_nothing(lib):
+    p = Problem([70, 70, 90], 2, True, seed=50)
+    keep = p.lens.clone()
+    p.lens[0], p.lens[1] = -2 ** 31, -5
+    p.run(lib, True)
+    lib.check_device_error()
+    p.check(True)  # places below 0: not written, not reported
+    p.lens.copy_(keep)
+    p.lens[1] = 2 ** 31 - 1
+    p.run(lib, True)
+    with pytest.raises(lib.MLAError, match="DEVICE_CHECK"):
+        lib.check_device_error()  # past the page table: reported, not written
+    p.lens[1] = 0
+    p.check(True)
 
 
 def test_negative_and_oversized_counts(lib):

@@ -161,10 +161,9 @@ def test_padding_and_unseen_drafts_do_not_matter():
 def binding():
     import os
 
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    if not os.path.exists(os.path.join(root, "mla_flash_attention_gb300", "libmla_gb300.so")):
-        from mla_flash_attention_gb300 import build
+    from mla_flash_attention_gb300 import build
 
+    if not (os.path.exists(build.LIB) and os.path.exists(build.MARSHAL)):
         build.build()
     from mla_flash_attention_gb300 import binding
 
