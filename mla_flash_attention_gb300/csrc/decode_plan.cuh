@@ -169,11 +169,34 @@ struct SegmentsOf {
   // L, lo, hi (page indices within the sequence); flat0 = the sequence's first flat page.
   // A unit whose range reaches only into an item's key-less flat pages gets no segment of it.
   // Lengths are fetched eight at a time so that skipping to this unit's first sequence
-  // costs one load latency per eight sequences rather than one per sequence.
+  // costs one load latency per eight sequences rather than one per sequence.  (Trees: the other
+  // query tiles of a sequence already met are walked without loads.)
   int flat0 = 0;
   int seg_ok, seg_L, seg_lo, seg_hi;  // the first segment, from the plan
+  int tile = -1, tile_L, tile_live;   // tree: the last item's query tile, its sequence's keys and tiles with keys
+  __device__ void met(int item, int keys) {
+    tile = item % NQT;
+    tile_L = keys;
+    tile_live = new_lens ? (drafted_of(*this, item / NQT) * H + 127) / 128 : NQT;
+  }
   __device__ bool next(int& seq, int& L, int& lo, int& hi) {
+    if constexpr (kTree) {
+      while (!seg_ok && tile >= 0 && tile + 1 < NQT && pb < end) {
+        const int n = ++tile < tile_live ? pages_of(tile_L, kPage) : 0;
+        const int nv = n > 0 ? n + item_cost : 0;
+        const int l0 = max(start, pb) - pb, h0 = min(min(end, pb + nv) - pb, n);
+        flat0 = pb;
+        seq = b;
+        L = tile_L;
+        lo = l0;
+        hi = h0;
+        pb += nv;
+        ++b;
+        if (l0 < h0) return true;
+      }
+    }
     if (seg_ok) {
+      if constexpr (kTree) met(b, seg_L);
       seg_ok = 0;
       flat0 = pb;
       seq = b;
@@ -200,6 +223,7 @@ struct SegmentsOf {
         pb += nv;
         ++b;
         if (l0 < h0) {
+          if constexpr (kTree) met(cur, Lb);
           flat0 = cur_pb;
           seq = cur;
           L = Lb;

@@ -867,35 +867,47 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero & 1, abort_flag, p.err));
             if (!ok) break;
             if constexpr (kTree) {
-              // drafted keys first .. valid - 1 of the page: non-finite granules are zeroed and the
-              // key flagged; a warp scans a whole row (72 granules), the two warps every other row
-              const int first = max(clean - pg * kPage, 0);
-              if (tid < kPage && (tid < first || tid >= valid)) bars.key_nan[g & 1][tid] = 0;
-              for (int rw = first + (tid >> 5); rw < valid; rw += n_prep / 32) {
-                bool bad_row = false;
+              // rows of drafted keys first .. valid - 1: non-finite granules are zeroed and the key flagged;
+              // rows past the end are zeroed.  A warp takes a whole row (72 granules), four at a time.
+              const int first = max(clean - pg * kPage, 0), lane = tid & 31;
+              unsigned char* flags = bars.key_nan[g & 1];
+              if (tid < first) flags[tid] = 0;
+              constexpr int kRowsAtOnce = 4;
+              for (int base = first + (tid >> 5); base < kPage; base += kRowsAtOnce * (n_prep / 32)) {
+                uint4* gr[kRowsAtOnce][3];
+                bool hit[kRowsAtOnce][3];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                  const int e = (tid & 31) + 32 * i, c = e >> 3;
-                  if (e >= 72) continue;
-                  unsigned char* base = sm + (c < 5 ? kOffSPart + c * kPageChunk
-                                                    : kOffVPart + (g % kVSlots) * kVPartBytes + (c - 5) * kPageChunk);
-                  uint4* gr = reinterpret_cast<uint4*>(base + rw * 128 + (e & 7) * 16);
-                  if (granule_nonfinite<false>(*gr)) {
-                    *gr = make_uint4(0, 0, 0, 0);
-                    bad_row = true;
+                for (int i = 0; i < kRowsAtOnce; ++i) {
+                  const int rw = base + i * (n_prep / 32);
+#pragma unroll
+                  for (int x = 0; x < 3; ++x) {
+                    const int e = lane + 32 * x, c = e >> 3;
+                    gr[i][x] = reinterpret_cast<uint4*>(
+                        sm + (c < 5 ? kOffSPart + c * kPageChunk
+                                    : kOffVPart + (g % kVSlots) * kVPartBytes + (c - 5) * kPageChunk) +
+                        rw * 128 + (e & 7) * 16);
+                    hit[i][x] = e < 72 && rw < kPage && (rw >= valid || granule_nonfinite<false>(*gr[i][x]));
                   }
                 }
-                bad_row = __any_sync(0xffffffffu, bad_row);
-                if ((tid & 31) == 0) bars.key_nan[g & 1][rw] = bad_row;
+#pragma unroll
+                for (int i = 0; i < kRowsAtOnce; ++i) {
+                  const int rw = base + i * (n_prep / 32);
+                  const bool any = __any_sync(0xffffffffu, hit[i][0] || hit[i][1] || hit[i][2]);
+#pragma unroll
+                  for (int x = 0; x < 3; ++x)
+                    if (hit[i][x]) *gr[i][x] = make_uint4(0, 0, 0, 0);
+                  if (lane == 0 && rw < kPage) flags[rw] = any && rw < valid;
+                }
               }
-            }
-            const int nrow = kPage - valid;
-            for (int part = 0; part < 2; ++part) {
-              const int nch = part == 0 ? 5 : 4;
-              unsigned char* base = sm + (part == 0 ? kOffSPart : kOffVPart + (g % kVSlots) * kVPartBytes);
-              for (int e = tid; e < nrow * nch * 8; e += n_prep) {
-                const int rw = valid + e / (nch * 8), rem = e % (nch * 8), c = rem >> 3, gr = rem & 7;
-                *reinterpret_cast<uint4*>(base + c * kPageChunk + rw * 128 + gr * 16) = make_uint4(0, 0, 0, 0);
+            } else {
+              const int nrow = kPage - valid;
+              for (int part = 0; part < 2; ++part) {
+                const int nch = part == 0 ? 5 : 4;
+                unsigned char* base = sm + (part == 0 ? kOffSPart : kOffVPart + (g % kVSlots) * kVPartBytes);
+                for (int e = tid; e < nrow * nch * 8; e += n_prep) {
+                  const int rw = valid + e / (nch * 8), rem = e % (nch * 8), c = rem >> 3, gr = rem & 7;
+                  *reinterpret_cast<uint4*>(base + c * kPageChunk + rw * 128 + gr * 16) = make_uint4(0, 0, 0, 0);
+                }
               }
             }
             ptx::fence_proxy_async();
@@ -961,7 +973,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     if constexpr (kF8) ptx::regs_inc<kF8RegsHigh>();
     const int r = threadIdx.x - 128;  // query row == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int g = 0, n_epi = 0, n_part = 0, n_bulk = 0, n_bulk_issued = 0;
+    int g = 0, n_epi = 0, n_dec = 0, n_part = 0, n_bulk = 0, n_bulk_issued = 0;
     bool ok = true;
     // an item with no keys (an empty sequence; tree: a query tile of padding) is in no work unit's
     // range: unit u writes O = 0 and LSE = -inf for such sequences (tree: items) u, u + G, u + 2G, ...
@@ -1023,15 +1035,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           if (L - pg * kPage < kPage) vis &= (1ull << (L - pg * kPage)) - 1;
         }
         int page8 = -1;
+        uint32_t nan_keys[2] = {0, 0};
         if constexpr (kF8) {
           page8 = tab[0];
           const int key = pg * kPage + 2 * (r & 31);
           float2 k2 = make_float2(key < L ? ks_next.x : 0.f, key + 1 < L ? ks_next.y : 0.f);
-          // log2 of the scale, floored (a scale of 0 gives weights of 0); NaN flags a drafted key whose
-          // scale is not finite
+          // log2 of the scale, floored (a scale of 0 gives weights of 0); a drafted key whose scale is
+          // not finite is flagged
           float2 l2 = make_float2(fmaxf(__log2f(fabsf(k2.x)), -100.f), fmaxf(__log2f(fabsf(k2.y)), -100.f));
-          if (tree_page && !(fabsf(k2.x) < INFINITY)) k2.x = 0.f, l2.x = __int_as_float(0x7fc00000);
-          if (tree_page && !(fabsf(k2.y) < INFINITY)) k2.y = 0.f, l2.y = __int_as_float(0x7fc00000);
+          if (tree_page) {
+            const bool bad0 = !(fabsf(k2.x) < INFINITY), bad1 = !(fabsf(k2.y) < INFINITY);
+            if (bad0) k2.x = l2.x = 0.f;
+            if (bad1) k2.y = l2.y = 0.f;
+            const uint32_t even = __ballot_sync(0xffffffffu, bad0), odd = __ballot_sync(0xffffffffu, bad1);
+            nan_keys[0] = nan_keys[1] = 0;
+            if (even | odd) {  // keys 2 lane, 2 lane + 1 of each lane, as bits of the keys
+              for (int x = 0; x < 32; ++x) nan_keys[x >> 4] |= ((even >> x & 1) | (odd >> x & 1) << 1) << (2 * x & 31);
+            }
+          }
           __syncwarp();  // the warp has read the page before's
           *reinterpret_cast<float2*>(&bars.f8.ks[warp - 4][2 * (r & 31)]) = k2;
           *reinterpret_cast<float2*>(&bars.f8.lk[warp - 4][2 * (r & 31)]) = l2;
@@ -1077,19 +1098,26 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kTree) {
           if (bad) vis = 0;
           if (tree_page || bad) {
-            const unsigned char* kn = bars.key_nan[g & 1];
-            const float nan = __int_as_float(0x7fc00000);
+            if (tree_page && !bad) {
+              // keys whose row (or scale) is not finite, hardly ever any: NaN for who sees them
+              const unsigned char* kn = bars.key_nan[g & 1];
+              const uint32_t f0 = __ballot_sync(0xffffffffu, kn[r & 31] != 0) | nan_keys[0];
+              const uint32_t f1 = __ballot_sync(0xffffffffu, kn[32 + (r & 31)] != 0) | nan_keys[1];
+              if (f0 | f1) {
+                const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                  const uint32_t f = x < 16 ? f0 >> (2 * x) : f1 >> (2 * x - 32);
+                  s2[x] = ptx::f2(f & 1 ? nan : ptx::f2_lo(s2[x]), f & 2 ? nan : ptx::f2_hi(s2[x]));
+                }
+              }
+            }
+            const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const uint32_t two = static_cast<uint32_t>(vis >> (2 * x));
-              float a = ptx::f2_lo(s2[x]), b = ptx::f2_hi(s2[x]);
-              if (tree_page && kn[2 * x]) a = nan;
-              if (tree_page && kn[2 * x + 1]) b = nan;
-              if constexpr (kF8) {  // 0, or NaN where the scale was flagged
-                a += bars.f8.lk[warp - 4][2 * x] - bars.f8.lk[warp - 4][2 * x];
-                b += bars.f8.lk[warp - 4][2 * x + 1] - bars.f8.lk[warp - 4][2 * x + 1];
-              }
-              s2[x] = ptx::f2(two & 1 ? a : -INFINITY, two & 2 ? b : -INFINITY);
+              const uint32_t v = x < 16 ? v0 : v1;
+              s2[x] = ptx::f2(v & (1u << (2 * x & 31)) ? ptx::f2_lo(s2[x]) : -INFINITY,
+                              v & (2u << (2 * x & 31)) ? ptx::f2_hi(s2[x]) : -INFINITY);
             }
           }
         } else if (key0 + kPage - 1 > lim) {  // a partial page (or a bad one): mask invisible keys
@@ -1199,6 +1227,13 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       // arrive while PV(g-2) is still pending and one parity bit cannot tell that phase from
       // the one after PV(g-1).  seg_done of the next segment needs this warp's P, so it is
       // never more than one phase ahead.
+      bool last_seg;
+      auto look_ahead = [&]() {
+        Segments nx = segs;
+        int s2, L2, lo2, hi2;
+        last_seg = !nx.next(s2, L2, lo2, hi2);
+      };
+      if constexpr (kTree) look_ahead();  // while the last PV product is on its way
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.seg_done, n_epi & 1, abort_flag, p.err));
       if (!ok) break;
       ptx::tc_fence_after();
@@ -1229,13 +1264,10 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       // area takes the staged bf16 output rows, the page stages a bulk copy of the other
       // split's partial when the sequence has exactly two (one TMA transfer instead of
       // rounds of dependent L2 loads per thread).
-      bool last_seg;
-      {
-        Segments nx = segs;
-        int s2, L2, lo2, hi2;
-        last_seg = !nx.next(s2, L2, lo2, hi2);
-      }
-      if (r == 0) {
+      if constexpr (!kTree) look_ahead();
+      // (a tree's item in one split needs no decision: it merges)
+      const bool decide = !kTree || nsplit > 1;
+      if (r == 0 && decide) {
         int fast = 1, bulk = 0;
         if (deferred) {
           fast = 0;
@@ -1261,13 +1293,13 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         bars.merge_bulk = bulk;
         ptx::mbar_arrive(&bars.dec_go);
       }
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.dec_go, n_epi & 1, abort_flag, p.err));
+      if (decide) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.dec_go, n_dec++ & 1, abort_flag, p.err));
       ++n_epi;
       if (!ok) break;
       // The accumulator is intact until the next segment's first PV product, which waits for
       // this epilogue: a split that merges always takes its own share from it.
-      bool own_in_tmem = *reinterpret_cast<volatile int*>(&bars.merge_fast) != 0;
-      bool bulk = *reinterpret_cast<volatile int*>(&bars.merge_bulk) != 0;
+      bool own_in_tmem = !decide || *reinterpret_cast<volatile int*>(&bars.merge_fast) != 0;
+      bool bulk = decide && *reinterpret_cast<volatile int*>(&bars.merge_bulk) != 0;
       bool merge = own_in_tmem;
       if (!own_in_tmem) {
         // partial layout [slot][column quad (128)][row (T*H)][4]: the 32 rows of a warp store
