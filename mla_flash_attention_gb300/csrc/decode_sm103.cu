@@ -221,13 +221,17 @@ __device__ __forceinline__ int page_row(const Params& p, int vseq, int pg) {
 // Sixteen bf16 (times alpha) as their hi and lo e4m3 terms, 16 bytes each.
 __device__ __forceinline__ void split16(const uint4& w0, const uint4& w1, float alpha, uint4& hi, uint4& lo) {
   const uint32_t in[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  uint32_t h[8], l[8];
+  const uint64_t a2 = ptx::f2(alpha, alpha);
+  uint32_t v[8], h[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    ptx::split_e4m3x2(ptx::pack_f16x2(__uint_as_float(in[i] << 16) * alpha, __uint_as_float(in[i] & 0xffff0000u) * alpha),
-                      h[i], l[i]);
-  hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-  lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t x = ptx::mul2(ptx::f2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), a2);
+    v[i] = ptx::pack_f16x2(ptx::f2_lo(x), ptx::f2_hi(x));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ptx::split_e4m3x4(v[2 * i], v[2 * i + 1], h[i], l[i]);
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 constexpr int kQNonFinite = 127;  // q_exp of a row with a NaN or an infinity: all its terms are NaN
@@ -1181,17 +1185,16 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kF8) {
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {  // four keys: one word of hi codes, one of lo codes
-            uint32_t h[2], lo8[2];
+            uint32_t w16[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint64_t a2 = ptx::add2(s2[x + y], nm2);
               const uint64_t pp = ptx::f2(ptx::ex2(ptx::f2_lo(a2)), ptx::ex2(ptx::f2_hi(a2)));
               ps2[y] = ptx::add2(ps2[y], pp);
               const uint64_t ab = ptx::mul2(pp, *reinterpret_cast<const uint64_t*>(ks + 2 * (x + y)));
-              ptx::split_e4m3x2(ptx::pack_f16x2(ptx::f2_lo(ab), ptx::f2_hi(ab)), h[y], lo8[y]);
+              w16[y] = ptx::pack_f16x2(ptx::f2_lo(ab), ptx::f2_hi(ab));
             }
-            pk[x / 2] = h[0] | h[1] << 16;
-            pk[16 + x / 2] = lo8[0] | lo8[1] << 16;
+            ptx::split_e4m3x4(w16[0], w16[1], pk[x / 2], pk[16 + x / 2]);
           }
         }
 #pragma unroll

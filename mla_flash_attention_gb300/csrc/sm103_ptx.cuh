@@ -487,18 +487,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// A packed f16 pair as a sum of two e4m3 pairs: hi = e4m3(v), lo = e4m3(v - hi), the difference exact
-// in f16.  16 bits each, first value low.  v within +-448; a NaN gives NaN codes.
-__device__ __forceinline__ void split_e4m3x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
-  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, r;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
-      "sub.rn.f16x2 r, %2, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n\t"
-      "cvt.u32.u16 %0, h;\n\t"
-      "cvt.u32.u16 %1, l;\n\t}"
-      : "=r"(hi), "=r"(lo)
-      : "r"(v));
+// Four f16 values as sums of two e4m3 terms: hi = e4m3(v), lo = e4m3(v - hi), the difference exact in
+// f16.  A word of hi codes and one of lo codes, first value lowest.  v within +-448; a NaN gives NaN
+// codes.
+__device__ __forceinline__ void split_e4m3x4(uint32_t v01, uint32_t v23, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t.reg .b32 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, %3;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, b;\n\t"
+      "sub.rn.f16x2 x, %2, x;\n\t"
+      "sub.rn.f16x2 y, %3, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 d, y;\n\t"
+      "mov.b32 %0, {a, b};\n\t"
+      "mov.b32 %1, {c, d};\n\t}"
+      : "=&r"(hi), "=r"(lo)
+      : "r"(v01), "r"(v23));
 }
 
 // max of three (one instruction)
