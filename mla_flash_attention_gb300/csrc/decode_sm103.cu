@@ -39,7 +39,12 @@
 // [128, 256) at its row's largest value, is hi + lo exactly (8 significant bits, 4 + 4) down to 2^-10
 // of that value, and a weight P'' = p ks is hi + lo to 2^-8.  Twice the k-steps at twice the rate: the
 // tensor work is bf16's, pages take half the bytes, and four fit instead of two; each page is its
-// own stage, released by its PV product.  The preparation warps make the query terms.
+// own stage, released by its PV product.  The preparation warps make the query terms.  64 ragged
+// sequences of up to 16384 keys, 1 to 13 tokens of 16 heads: 613 us with the pages widened to bf16, 433
+// with e4m3 operands (an item's query terms then took 20 us), 344 with the terms made in place from
+// TMA loads and items charged in the split plan, 255 with tiles of padding left out.  A page takes
+// 1.2 us, 2,300 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key half each, were no faster,
+// nor was splitting into terms with integer instructions.)
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
 #include <cuda.h>
@@ -93,8 +98,8 @@ constexpr int kF8Stages = 4;
 static_assert(kF8Stages * kF8Page <= kStages * kStageBytes, "fp8 tree pages fit the stages");
 // Flat pages the tree's split plan charges for an item's start and end (its queries, the epilogue, and
 // for fp8 the query terms), at most: a page of keys takes 1.4 us (bf16) and 1.2 us (fp8).  64 ragged
-// sequences of up to 16384 keys, fp8: 404, 384, 364, 354, 345 and 346 us for 1, 4, 8, 12, 16 and 19; 16
-// sequences of 4096 keys and 16 x 128 rows, bf16: 371, 372, 368 and 367 us for 1, 3, 5 and 8.
+// sequences of up to 16384 keys, fp8: 278, 280, 271 and 263 us for 6, 9, 12 and 16 (16 and 19 alike before);
+// 16 sequences of 4096 keys and 16 x 128 rows, bf16: 366, 365, 360 and 360 us for 2, 4, 6 and 8.
 constexpr int kF8ItemCost = 16, kTreeItemCost = 6;
 constexpr int kF8PrepWarps = 6;                 // warps 2-3 and 8-11
 // registers a thread: 384 threads launched at kF8RegsLaunch, then traded between the warpgroups
@@ -1508,6 +1513,70 @@ constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeQuads = 16;  // two qu
 constexpr int kMergeSlices = (kRows / kMergeRows) * (128 / kMergeQuads);
 constexpr int kMergeBlocks = 304;
 
+// One thread's part of a slice: row r of the item (gr of its sequence's), column quads q and q + 1, of
+// nsplit splits from the item's first on, eight of them in flight; the first eight log-sum-exps stay
+// in registers.
+__device__ __forceinline__ void merge_row(const Params& p, int item, int c_first, int nsplit, int r, int gr, int q) {
+  constexpr int kBatch = 8;
+  const float* lsp = p.part_lse + ((size_t)(q / 64) * p.n_slots + c_first + item) * p.TQ + r;
+  float first[kBatch], mx = -INFINITY, sum = 0.f;
+  auto lse_of = [&](int k) { return k < nsplit ? ptx::ld_l2(lsp + (size_t)k * p.TQ) : -INFINITY; };
+  auto weight = [&](float ls) { return ls != ls ? ls : ls == -INFINITY ? 0.f : __expf(ls - mx); };
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) first[k] = lse_of(k);
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, first[k]);
+  for (int k0 = kBatch; k0 < nsplit; k0 += kBatch) {
+    float ls[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) ls[k] = lse_of(k0 + k);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mx = fmaxf(mx, ls[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) sum += weight(first[k]);
+  for (int k0 = kBatch; k0 < nsplit; k0 += kBatch) {
+    float ls[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) ls[k] = lse_of(k0 + k);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) sum += weight(ls[k]);
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((size_t)(c_first + item) * 128 + q) * p.TQ + r;
+  const size_t slot_stride = (size_t)128 * p.TQ;
+  float4 acc[2] = {};
+  for (int k0 = 0; k0 < nsplit; k0 += kBatch) {
+    float4 x[kBatch][2];
+    float ls[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      ls[k] = k0 == 0 ? first[k] : lse_of(k0 + k);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        x[k][j] = k0 + k < nsplit ? ptx::ld_l2(src + (k0 + k) * slot_stride + (size_t)j * p.TQ)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = weight(ls[k]) * inv;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        acc[j].x = fmaf(w, x[k][j].x, acc[j].x);
+        acc[j].y = fmaf(w, x[k][j].y, acc[j].y);
+        acc[j].z = fmaf(w, x[k][j].z, acc[j].z);
+        acc[j].w = fmaf(w, x[k][j].w, acc[j].w);
+      }
+    }
+  }
+  uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)(item / p.NQT) * p.T * p.H + gr) * kDl + q * 4);
+  if (MLA_STORE_OK(o, p.out, p.out_bytes, p.err))
+    *o = make_uint4(ptx::pack_bf16x2(acc[0].x, acc[0].y), ptx::pack_bf16x2(acc[0].z, acc[0].w),
+                    ptx::pack_bf16x2(acc[1].x, acc[1].y), ptx::pack_bf16x2(acc[1].z, acc[1].w));
+  float* lp = p.lse + ((size_t)(item / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
+  if (q == 0 && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = sum != 0.f ? mx + logf(sum) : -INFINITY;
+}
+
 __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel is done
@@ -1516,60 +1585,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Para
     const int4 d = __ldcg(reinterpret_cast<const int4*>(p.deferred + 1) + w / kMergeSlices);
     const int item = d.x, c_first = d.y, nsplit = d.z, slice = w % kMergeSlices;
     const int r = (slice & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
-    const bool live = r < p.TQ && gr < p.T * p.H;
-    const int q = (slice >> 2) * kMergeQuads + 2 * warp, half = q / 64;
-    if (!live) continue;  // (no warp-collective step below)
-    const float* lsp = p.part_lse + ((size_t)half * p.n_slots + c_first + item) * p.TQ + r;
-    constexpr int kBatch = 8;  // splits in flight
-    float mx = -INFINITY, sum = 0.f;
-    for (int k0 = 0; k0 < nsplit; k0 += 2 * kBatch) {
-      float ls[2 * kBatch];
-#pragma unroll
-      for (int k = 0; k < 2 * kBatch; ++k) ls[k] = k0 + k < nsplit ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 2 * kBatch; ++k) mx = fmaxf(mx, ls[k]);
-    }
-    auto weight = [&](float ls) { return ls != ls ? ls : ls == -INFINITY ? 0.f : __expf(ls - mx); };
-    for (int k0 = 0; k0 < nsplit; k0 += 2 * kBatch) {
-      float ls[2 * kBatch];
-#pragma unroll
-      for (int k = 0; k < 2 * kBatch; ++k) ls[k] = k0 + k < nsplit ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 2 * kBatch; ++k) sum += weight(ls[k]);
-    }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((size_t)(c_first + item) * 128 + q) * p.TQ + r;
-    const size_t slot_stride = (size_t)128 * p.TQ;
-    float4 acc[2] = {};
-    for (int k0 = 0; k0 < nsplit; k0 += kBatch) {
-      float4 x[kBatch][2];
-      float ls[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const bool in = k0 + k < nsplit;
-        ls[k] = in ? ptx::ld_l2(lsp + (size_t)(k0 + k) * p.TQ) : -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          x[k][j] = in ? ptx::ld_l2(src + (k0 + k) * slot_stride + (size_t)j * p.TQ) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float wk = weight(ls[k]) * inv;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[j].x = fmaf(wk, x[k][j].x, acc[j].x);
-          acc[j].y = fmaf(wk, x[k][j].y, acc[j].y);
-          acc[j].z = fmaf(wk, x[k][j].z, acc[j].z);
-          acc[j].w = fmaf(wk, x[k][j].w, acc[j].w);
-        }
-      }
-    }
-    uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)(item / p.NQT) * p.T * p.H + gr) * kDl + q * 4);
-    if (MLA_STORE_OK(o, p.out, p.out_bytes, p.err))
-      *o = make_uint4(ptx::pack_bf16x2(acc[0].x, acc[0].y), ptx::pack_bf16x2(acc[0].z, acc[0].w),
-                      ptx::pack_bf16x2(acc[1].x, acc[1].y), ptx::pack_bf16x2(acc[1].z, acc[1].w));
-    float* lp = p.lse + ((size_t)(item / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
-    if (q == 0 && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = sum != 0.f ? mx + logf(sum) : -INFINITY;
+    if (r >= p.TQ || gr >= p.T * p.H) continue;
+    const int q = (slice >> 2) * kMergeQuads + 2 * warp;
+    merge_row(p, item, c_first, nsplit, r, gr, q);
   }
 }
 
