@@ -293,6 +293,12 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
     done(&bars.f8.q_sync);
     return wait(&bars.f8.q_sync, n_sync++);
   };
+  // raw rows landed; a copy that was given up lands before its issuer leaves
+  auto landed = [&](int phase) {
+    if (wait(&bars.f8.q_raw, phase)) return true;
+    if (threadIdx.x == 8 * 32) ptx::mbar_wait_drain(&bars.f8.q_raw, phase & 1);
+    return false;
+  };
   uint32_t mx = 0;  // the largest magnitude's bits of the row, as integers
   auto largest = [&](int chunk) {
 #pragma unroll
@@ -314,13 +320,13 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
         if (col) ptx::tma_load_2d(qa + 4 * kQChunk, &tm_qrope, &bars.f8.q_raw, 0, r0);
       };
       load(256);
-      if (!wait(&bars.f8.q_raw, 3 * nseg)) return;
+      if (!landed(3 * nseg)) return;
       mx = 0;
 #pragma unroll 1
       for (int c = 0; c < 5; ++c) largest(c);
       if (!sync()) return;
       load(0);
-      if (!wait(&bars.f8.q_raw, 3 * nseg + 1)) return;
+      if (!landed(3 * nseg + 1)) return;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) largest(c);
       const uint32_t bits = max(mx & 0xffffu, mx >> 16);
@@ -333,7 +339,7 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
       done(&bars.q_lo_full);
       if (!wait(&bars.q_cp_done, nseg)) return;
       load(256);
-      if (!wait(&bars.f8.q_raw, 3 * nseg + 2)) return;
+      if (!landed(3 * nseg + 2)) return;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) turn(c, f, live);
       {  // rope: 64 columns, hi and lo in one chunk
@@ -501,6 +507,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     // value part, which goes out about a page earlier, never waits behind a score-only part.
     if ((threadIdx.x & 31) == 0) {
       int g = 0, nseg = 0;
+      int n_v = 0, n_s = 0;  // value and score-only parts issued (bf16)
       bool ok = true;
       while (ok && segs.next(seq, L, lo, hi)) {
         // the first page's table entry is read before Q is issued, so its latency overlaps
@@ -584,6 +591,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
               for (int c = 0; c < 4; ++c)
                 ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, &bars.vpart_full[v], (4 * half + c) * 64, y);
             }
+            ++n_v;
             // then the score-only chunks (chunk_idx order: half 0 takes 4..8, half 1 0..3 and
             // 8), once the previous page's score k-steps over them are done
             if (!(ok = ptx::mbar_wait(&bars.spart_empty, (g & 1) ^ 1, abort_flag, p.err))) break;
@@ -599,6 +607,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                 ptx::tma_load_2d(dst + i * kPageChunk, &tm_cache, &bars.spart_full,
                                  (half == 0 ? 4 + i : (i < 4 ? i : 8)) * 64, y);
             }
+            ++n_s;
           }
           if (pg == lo) warm_next_q();
           // warm L2 with the pages ahead (after this page's own load has been issued)
@@ -610,6 +619,18 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             constexpr uint32_t kPageBytes = kPage * kDc * (kFp8 ? 1 : 2);
             ptx::bulk_prefetch(p.cache_bytes + (size_t)ya * (kDc * (kFp8 ? 1 : 2)), kPageBytes);
           }
+        }
+      }
+      if (kTree && !ok) {  // after an abort: copies that nobody may wait for land before the CTA leaves
+        if constexpr (kF8) {
+          for (int v = max(0, g - kF8Stages); v < g; ++v)
+            ptx::mbar_wait_drain(&bars.f8.full[v % kF8Stages], (v / kF8Stages) & 1);
+        } else {
+          for (int v = max(0, n_v - kVSlots); v < n_v; ++v)
+            ptx::mbar_wait_drain(&bars.vpart_full[v % kVSlots], (v / kVSlots) & 1);
+          if (n_s > 0) ptx::mbar_wait_drain(&bars.spart_full, (n_s - 1) & 1);
+          if (nseg > 0) ptx::mbar_wait_drain(&bars.q_lo_full, (nseg - 1) & 1);
+          if (nseg == 1) ptx::mbar_wait_drain(&bars.q_hi_full, 0);
         }
       }
     }
@@ -751,7 +772,10 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             ptx::tma_load_2d(sm + kOffQhi + c * kQChunk, &tm_qlat, &bars.q_hi_full, 256 + c * 64, q_row0(seq));
           ptx::tma_load_2d(sm + kOffQhi + 4 * kQChunk, &tm_qrope, &bars.q_hi_full, 0, q_row0(seq));
         }
-        if (!(ok = ptx::mbar_wait(&bars.q_hi_full, nseg & 1, abort_flag, p.err))) break;
+        if (!(ok = ptx::mbar_wait(&bars.q_hi_full, nseg & 1, abort_flag, p.err))) {
+          if (kTree && !kF8) ptx::mbar_wait_drain(&bars.q_hi_full, nseg & 1);  // issued above
+          break;
+        }
         ptx::tc_fence_after();
         const int g_end = g + (hi - lo), g_first = g;
         const int clean = clean_keys(seq, L);
@@ -840,6 +864,10 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if (ok) ptx::mma_commit(&bars.seg_done);  // the segment's last PV product is complete
         g = g_end;
         ++nseg;
+      }
+      if (kTree && !ok) {  // after an abort: every MMA issued completes before the CTA frees its TMEM
+        ptx::mma_commit(&bars.stage_empty[0]);  // (a barrier that only the widening kernel uses)
+        ptx::mbar_wait_drain(&bars.stage_empty[0], 0);
       }
     }
    } else if constexpr (kF8) {
