@@ -69,4 +69,23 @@ inline cudaError_t smem_attr_once(Kernel kernel, int bytes, unsigned long long* 
   return e;
 }
 
+// Launch `kernel` as a programmatic dependent of the work ahead of it in the stream: it is set up
+// while that finishes, and griddepcontrol.wait in it waits until that is complete and visible.
+template <typename... Prm, typename... Arg>
+inline cudaError_t launch_dependent(void (*kernel)(Prm...), int grid, int block, cudaStream_t stream, Arg... arg) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+
+// In a kernel launched so, before its first access to memory.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace mla

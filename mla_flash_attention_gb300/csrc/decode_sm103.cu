@@ -1607,7 +1607,7 @@ __device__ __forceinline__ void merge_row(const Params& p, int item, int c_first
 
 __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel is done
+  wait_for_stream();  // the split kernel is done
   const int work = __ldcg(&p.deferred[0].x) * kMergeSlices;
   for (int w = blockIdx.x; w < work; w += gridDim.x) {
     const int4 d = __ldcg(reinterpret_cast<const int4*>(p.deferred + 1) + w / kMergeSlices);
@@ -1623,6 +1623,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Para
 // programmatic dependent and waits for it only where it first touches a counter.
 __global__ void __launch_bounds__(256) zero_counters_kernel(int* __restrict__ c, int n,
                                                                int4* __restrict__ deferred) {
+  // (A tree's zeroing is itself a programmatic dependent.  It lets the split kernel, which reads its
+  // inputs without waiting, start only once the work ahead is complete.)
+  if (deferred) wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (deferred && blockIdx.x == 0 && threadIdx.x == 0) deferred[0] = make_int4(0, 0, 0, 0);
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) c[i] = 0;
@@ -1766,8 +1769,13 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     __atomic_store_n(&carveout_set, 1, __ATOMIC_RELEASE);
   }
   const int zero_blocks = (int)std::min<long long>((n_cnt + 2047) / 2048, 1024);
-  zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt, tree_mask ? p.deferred : nullptr);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (tree_mask) {
+    if ((e = launch_dependent(zero_counters_kernel, zero_blocks, 256, stream, counters, (int)n_cnt, p.deferred)) != cudaSuccess)
+      return e;
+  } else {
+    zero_counters_kernel<<<zero_blocks, 256, 0, stream>>>(counters, (int)n_cnt, nullptr);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   auto go = [&](auto kern) -> cudaError_t {
     static unsigned long long smem_set[4] = {0, 0, 0, 0};
     const int smem = f8 ? kSmemBytes : kSmemAlloc;
@@ -1799,16 +1807,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
       if (regs < kF8RegsLaunch) return cudaErrorInvalidDeviceFunction;
     }
     if ((e = fp8 ? go(decode_split_kernel<true, true>) : go(decode_split_kernel<false, true>)) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMergeBlocks);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p);
+    return launch_dependent(tree_merge_kernel, kMergeBlocks, kMergeThreads, stream, p);
   }
   return fp8 ? go(decode_split_kernel<true, false>) : go(decode_split_kernel<false, false>);
 }

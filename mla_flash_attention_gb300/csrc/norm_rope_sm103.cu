@@ -272,12 +272,14 @@ __device__ __forceinline__ void all_tasks(const Params& p, unsigned u, unsigned 
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_rope_kernel(const Params p) {
   const unsigned step = gridDim.x * kWarps;
+  wait_for_stream();
   all_tasks<false, kPairs>(p, blockIdx.x * kWarps + (threadIdx.x >> 5), step, nullptr);
 }
 
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, kGradBlocks) norm_rope_grad_kernel(const Params p) {
   __shared__ float joined[kWarps][kDw];
+  wait_for_stream();
   const int warp = threadIdx.x >> 5;
   const unsigned step = gridDim.x * kWarps;
   float* mine = nullptr;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partial,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are written
+  wait_for_stream();  // the partial rows are written
 #pragma unroll 4
   for (int r = warp; r < rows; r += 32) v += ptx::ld_l2(partial + (size_t)r * kDw + col);
   joined[warp][lane] = v;
@@ -401,11 +403,7 @@ cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_h
   p.kn_bytes = (size_t)rows * H * kDn * 2;
   p.kr_bytes = (size_t)rows * kDr * 2;
   const int grid = blocks_for(task_count(p), kForwardBlocks, sms);
-  if (pairs)
-    norm_rope_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    norm_rope_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(pairs ? norm_rope_kernel<true> : norm_rope_kernel<false>, grid, kThreads, stream, p);
 }
 
 cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const float* dkr,
@@ -434,24 +432,11 @@ cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const 
   const bool weights = dw_qn || dw_qr || dw_kn || dw_kr;
   p.partial = weights ? workspace : nullptr;
   p.partial_bytes = (size_t)grid * kDw * sizeof(float);
-  if (pairs)
-    norm_rope_grad_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    norm_rope_grad_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(pairs ? norm_rope_grad_kernel<true> : norm_rope_grad_kernel<false>, grid,
+                                         kThreads, stream, p);
   if (e != cudaSuccess || !weights) return e;
-  // a programmatic dependent: it is set up while the last blocks finish
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kDw / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weight_grad_kernel, static_cast<const float*>(workspace), grid, dw_qn, dw_qr, dw_kn,
-                            dw_kr);
+  return launch_dependent(weight_grad_kernel, kDw / 32, 1024, stream, static_cast<const float*>(workspace), grid, dw_qn,
+                          dw_qr, dw_kn, dw_kr);
 }
 
 }  // namespace mla

@@ -65,6 +65,7 @@ __device__ __forceinline__ float row_max(float v) {
 
 template <bool kFp8, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Params p) {
+  wait_for_stream();
   const int lane = threadIdx.x & 31, l = lane & 15;
   const int id = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * 2 + (lane >> 4);
   // a half-warp without a row to write stays for the other one's shuffles
@@ -227,15 +228,11 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
   p.num_pages = num_pages;
   p.err = err;
   const int grid = (p.rows + 2 * kWarps - 1) / (2 * kWarps);
-  if (fp8 && pairs)
-    rope_append_kernel<true, true><<<grid, kWarps * 32, 0, stream>>>(p);
-  else if (fp8)
-    rope_append_kernel<true, false><<<grid, kWarps * 32, 0, stream>>>(p);
-  else if (pairs)
-    rope_append_kernel<false, true><<<grid, kWarps * 32, 0, stream>>>(p);
-  else
-    rope_append_kernel<false, false><<<grid, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  auto kernel = fp8 ? (pairs ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
+                    : (pairs ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+  // (a programmatic dependent: calls of 128 x 7 rows in a row take 3.3 instead of 6.2 us, of 65536 rows
+  // 26.2 instead of 28.7)
+  return launch_dependent(kernel, grid, kWarps * 32, stream, p);
 }
 
 }  // namespace mla
