@@ -97,10 +97,10 @@ constexpr int kF8Page = 4 * kPageChunk + kPage * 64;  // 36 KB
 constexpr int kF8Stages = 4;
 static_assert(kF8Stages * kF8Page <= kStages * kStageBytes, "fp8 tree pages fit the stages");
 // Flat pages the tree's split plan charges for an item's start and end (its queries, the epilogue, and
-// for fp8 the query terms), at most: a page of keys takes 1.4 us (bf16) and 1.2 us (fp8).  64 ragged
-// sequences of up to 16384 keys, fp8: 278, 280, 271 and 263 us for 6, 9, 12 and 16 (16 and 19 alike before);
-// 16 sequences of 4096 keys and 16 x 128 rows, bf16: 366, 365, 360 and 360 us for 2, 4, 6 and 8.
-constexpr int kF8ItemCost = 16, kTreeItemCost = 6;
+// for fp8 the query terms), at most: a page of keys takes 1.4 us (bf16) and 1.3 us (fp8).  64 ragged
+// sequences of up to 16384 keys, fp8: 256, 257, 254 and 261 us for 10, 12, 13 and 16; 16 of up to 8000
+// keys and 8 x 128 rows, bf16: 158, 159, 151 and 150 us for 4, 5, 6 and 8.
+constexpr int kF8ItemCost = 13, kTreeItemCost = 8;
 constexpr int kF8PrepWarps = 6;                 // warps 2-3 and 8-11
 // registers a thread: 384 threads launched at kF8RegsLaunch, then traded between the warpgroups
 constexpr int kF8RegsLaunch = 168, kF8RegsHigh = 232, kF8RegsLow = 136;
@@ -147,7 +147,8 @@ struct Params {
 
 struct F8Bars {
   uint64_t full[kF8Stages], empty[kF8Stages];
-  uint64_t q_raw, q_sync;                   // raw query rows landed; warpgroup 2 has read them
+  uint64_t q_lo_raw, q_raw;                 // a segment's raw rows landed in the ring and in the query area
+  uint64_t q0_sync;                         // first segment: both warpgroups have read their raw rows
   signed char q_exp[2][kRows];              // the power of two a query row was scaled by, by segment parity
   float ks[kRows / 32][kPage], lk[kRows / 32][kPage];  // a page's key scales and their log2, a copy a softmax warp
 };
@@ -182,7 +183,7 @@ struct Bars {
 };
 
 // with 224 KB of dynamic shared memory and no slack, what the fp8 tree's block has left
-static_assert(sizeof(Bars<true, true>) <= 3072, "static shared memory of the fp8 tree");
+static_assert(kSmemBytes + sizeof(Bars<true, true>) <= 227 * 1024, "static shared memory of the fp8 tree");
 
 // Drafted tokens of virtual sequence v: the newest n keys; rows of tokens n .. T - 1 are padding.
 __device__ __forceinline__ int drafted(const Params& p, int vseq) { return decode_plan::drafted_of(p, vseq / p.NQT); }
@@ -246,15 +247,126 @@ __device__ __forceinline__ float q_factor(int k) {
   return k == kQNonFinite ? __int_as_float(0x7fc00000) : __int_as_float((k + 127) << 23);
 }
 
+// Granule i of row r in a chunk of the query area (128 rows of 128 bytes, 128B-swizzled).
+__device__ __forceinline__ uint4* q_granule(unsigned char* base, int r, int chunk, int i) {
+  return reinterpret_cast<uint4*>(base + chunk * kQChunk + r * 128 + ((i ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t larger(uint32_t mx, const uint4& w) {  // magnitudes as integers, two a word
+  return __vmaxu2(__vmaxu2(__vmaxu2(mx, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu),
+                  __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+
+// The largest exponent field (0 .. 255) of row r's bf16 values in chunks 0 .. n - 1.
+__device__ __forceinline__ int q_field(unsigned char* base, int r, int n) {
+  uint32_t mx = 0;
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = larger(mx, *q_granule(base, r, c, i));
+  }
+  return static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7);
+}
+
+// The same over whole query rows row0 + lane (lane < rows), read from memory by one warp, eight rows at a
+// time: the next segment's, while this one's pages are under way.
+__device__ __forceinline__ int q_field_ahead(const Params& p, size_t row0, int rows) {
+  const int lane = threadIdx.x & 31;
+  int field = 0;
+#pragma unroll 1
+  for (int b = 0; b < rows; b += 8) {
+    uint4 w[8][2], rope[2];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q_latent + (row0 + b + i) * kDl) + lane;
+      w[i][0] = b + i < rows ? __ldg(src) : zero;
+      w[i][1] = b + i < rows ? __ldg(src + 32) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // rope: a row's 128 bytes in eight lanes
+      const int at = b + 4 * i + (lane >> 3);
+      rope[i] = at < rows ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + (row0 + at) * 64) + (lane & 7)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t mx = larger(larger(0, w[i][0]), w[i][1]);
+      if ((lane >> 3) == (i & 3)) mx = larger(mx, rope[i >> 2]);
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      if (lane == b + i) field = static_cast<int>(mx >> 7);
+    }
+  }
+  return field;
+}
+
+// The power of two that a row with this largest field is scaled by (field 255: NaN or infinity).
+__device__ __forceinline__ int q_exponent(int field) {
+  return field == 255 ? kQNonFinite : min(max(134 - field, -120), 120);
+}
+
+// Row r's raw chunks 0 and 1 (64 columns of bf16 each) at p0, then those at p1, become a hi and a lo
+// chunk; 0 where the row is not live.
+__device__ __forceinline__ void q_turn(unsigned char* p0, unsigned char* p1, int r, float f, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    unsigned char* base = c ? p1 : p0;
+    uint4 raw[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) raw[i] = live ? *q_granule(base, r, i >> 3, i & 7) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 h, l;
+      split16(raw[2 * i], raw[2 * i + 1], f, h, l);
+      *q_granule(base, r, 0, i) = h;
+      *q_granule(base, r, 1, i) = l;
+    }
+  }
+}
+
+// The same for the rope chunk: 64 columns, hi and lo in one chunk.
+__device__ __forceinline__ void q_turn_rope(unsigned char* base, int r, float f, bool live) {
+  uint4 raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) raw[i] = live ? *q_granule(base, r, 4, i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 h, l;
+    split16(raw[2 * i], raw[2 * i + 1], f, h, l);
+    *q_granule(base, r, 4, i) = h;
+    *q_granule(base, r, 4, 4 + i) = l;
+  }
+}
+
+// Tree: an item without keys (a query tile of padding, an empty sequence) is in no work unit's range.
+// Unit u writes O = 0 and LSE = -inf for the items u, u + G, u + 2G, ... that are empty, each half its
+// columns, by its warps 2 and 3, which have the least to do.
+__device__ __forceinline__ void empty_items(const Params& p, int unit, int half, int TH) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
+  for (int v = unit; v < p.B * p.NQT; v += p.G) {
+    if (decode_plan::item_len<true>(p, v) > 0) continue;
+    const int b = v / p.NQT, row0 = (v % p.NQT) * kRows, rows = min(kRows, TH - row0);
+    uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)b * TH + row0) * kDl + half * 256) + lane;
+    for (int i = w; i < rows; i += 2)
+      if (MLA_STORE_OK(o + i * (kDl / 8), p.out, p.out_bytes, p.err)) o[i * (kDl / 8)] = make_uint4(0, 0, 0, 0);
+    if (half) continue;
+    for (int i = row0 + w * 32 + lane; i < row0 + rows; i += 64) {
+      float* lp = p.lse + ((size_t)b * p.H + i % p.H) * p.T + i / p.H;
+      if (MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = -INFINITY;
+    }
+  }
+}
+
 // The preparation warps of the tree over an fp8 cache.  All six prepare the pages that end a sequence
-// or hold drafted keys; warpgroup 2 (kQ) makes the query terms of every segment, in two steps through
-// the same shared memory (latent 0..255, copied on to TMEM by the MMA thread; then the rest, which
-// stays): raw rows by TMA, turned in place into terms by one thread a row (128 columns: 256 bytes of
-// bf16 become 128 of hi and 128 of lo).  A row's power of two needs all its columns, so the second
-// part is loaded twice, first for its largest value.
+// or hold drafted keys; warpgroup 2 (kQ) makes the query terms of every segment: raw rows by TMA,
+// turned in place into terms by one thread a row (128 columns: 256 bytes of bf16 become 128 of hi and
+// 128 of lo).  Latent 0..255 comes through two entries of the page ring ahead of the segment's pages
+// and is copied on to TMEM by the MMA thread, the rest stays in the query area, which is free when the
+// previous segment has its last scores.  A row's power of two needs all its columns: it is found ahead,
+// from memory, while the previous segment's pages are under way.  Only the first segment, which no
+// other work covers, finds it from both parts in shared memory, and warpgroup 1, which has no scores
+// yet, turns its latent 0..255.
 template <bool kQ, typename B>
-__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int TH,
-                                           const CUtensorMap& tm_qlat, const CUtensorMap& tm_qrope) {
+__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int TH) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pw = kQ ? warp - 6 : warp - 2;  // 0 .. kF8PrepWarps - 1
   volatile int* abort_flag = &bars.abort_flag;
@@ -268,93 +380,41 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
   };
-  auto first_row = [&](int v) { return (size_t)(v / p.NQT) * TH + (v % p.NQT) * kRows; };
-  auto live_rows = [&](int v) { return min(p.TQ, TH - (v % p.NQT) * kRows); };
-  // row r's raw chunks 2 c, 2 c + 1 (64 columns of bf16 each) become its hi and its lo chunk
+  auto rows_of = [&](int v) { return min(p.TQ, TH - (v % p.NQT) * kRows); };
   const int r = (warp & 3) * 32 + lane;
-  auto granule = [&](int chunk, int i) {
-    return reinterpret_cast<uint4*>(qa + chunk * kQChunk + r * 128 + ((i ^ (r & 7)) << 4));
-  };
-  auto turn = [&](int c, float f, bool live) {
-    uint4 raw[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) raw[i] = live ? *granule(2 * c + (i >> 3), i & 7) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint4 h, l;
-      split16(raw[2 * i], raw[2 * i + 1], f, h, l);
-      *granule(2 * c, i) = h;
-      *granule(2 * c + 1, i) = l;
-    }
-  };
-  // all of warpgroup 2 is done with what is in the query area
-  int n_sync = 0;
-  auto sync = [&]() {
-    done(&bars.f8.q_sync);
-    return wait(&bars.f8.q_sync, n_sync++);
-  };
-  // raw rows landed; a copy that was given up lands before its issuer leaves
-  auto landed = [&](int phase) {
-    if (wait(&bars.f8.q_raw, phase)) return true;
-    if (threadIdx.x == 8 * 32) ptx::mbar_wait_drain(&bars.f8.q_raw, phase & 1);
-    return false;
-  };
-  uint32_t mx = 0;  // the largest magnitude's bits of the row, as integers
-  auto largest = [&](int chunk) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 w = *granule(chunk, i);
-      mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu),
-                    __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-    }
-  };
+  int field = 0;  // of this thread's row in the segment at hand
   while (segs.next(seq, L, lo, hi)) {
     if constexpr (kQ) {
-      if (nseg > 0 && !wait(&bars.q_free, nseg - 1)) return;
-      const int r0 = (seq / p.NQT) * TH + (seq % p.NQT) * kRows;
-      const bool live = r < min(p.TQ, TH - (seq % p.NQT) * kRows);
-      auto load = [&](int col) {  // latent col .. col + 255, and the rope columns with the second half
-        if (threadIdx.x != 8 * 32) return;
-        ptx::mbar_arrive_expect_tx(&bars.f8.q_raw, (col ? 5 : 4) * p.TQ * 128);
-        for (int c = 0; c < 4; ++c) ptx::tma_load_2d(qa + c * kQChunk, &tm_qlat, &bars.f8.q_raw, col + c * 64, r0);
-        if (col) ptx::tma_load_2d(qa + 4 * kQChunk, &tm_qrope, &bars.f8.q_raw, 0, r0);
-      };
-      load(256);
-      if (!landed(3 * nseg)) return;
-      mx = 0;
-#pragma unroll 1
-      for (int c = 0; c < 5; ++c) largest(c);
-      if (!sync()) return;
-      load(0);
-      if (!landed(3 * nseg + 1)) return;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) largest(c);
-      const uint32_t bits = max(mx & 0xffffu, mx >> 16);
-      const int field = bits >> 7;  // exponent + 127; 255: NaN or infinity
-      const int k = field == 255 ? kQNonFinite : bits == 0 ? 0 : min(max(134 - field, -120), 120);
-      bars.f8.q_exp[nseg & 1][r] = static_cast<signed char>(k);
-      const float f = q_factor(k);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) turn(c, f, live);
-      done(&bars.q_lo_full);
-      if (!wait(&bars.q_cp_done, nseg)) return;
-      load(256);
-      if (!landed(3 * nseg + 2)) return;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) turn(c, f, live);
-      {  // rope: 64 columns, hi and lo in one chunk
-        uint4 raw[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) raw[i] = live ? *granule(4, i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 h, l;
-          split16(raw[2 * i], raw[2 * i + 1], f, h, l);
-          *granule(4, i) = h;
-          *granule(4, 4 + i) = l;
-        }
+      const bool live = r < rows_of(seq);
+      if (nseg == 0) {
+        if (!wait(&bars.f8.q_raw, 0)) return;
+        if (live) field = q_field(qa, r, 5);
+        bars.f8.q_exp[0][r] = static_cast<signed char>(field);
+        done(&bars.f8.q0_sync);
+        if (!wait(&bars.f8.q0_sync, 0)) return;
+        field = max(field, static_cast<int>(static_cast<unsigned char>(bars.f8.q_exp[1][r])));
       }
+      const int k = q_exponent(field);
+      const float f = q_factor(k);
+      if (nseg > 0) {
+        const int e = g + 2 * nseg;  // ring entries of latent 0..127 and (e + 1) 128..255
+        unsigned char *e0 = sm + kOffStage + (e % kF8Stages) * kF8Page,
+                      *e1 = sm + kOffStage + ((e + 1) % kF8Stages) * kF8Page;
+        if (!wait(&bars.f8.q_lo_raw, nseg)) return;
+        q_turn(e0, e1, r, f, live);
+        done(&bars.q_lo_full);
+        if (!wait(&bars.f8.q_raw, nseg)) return;
+        bars.f8.q_exp[nseg & 1][r] = static_cast<signed char>(k);
+      }
+      q_turn(qa, qa + 2 * kQChunk, r, f, live);
+      q_turn_rope(qa, r, f, live);
       done(&bars.q_hi_full);
+      SegmentsOf<true> nx = segs;
+      int s2, L2, lo2, hi2;
+      if (nx.next(s2, L2, lo2, hi2)) {
+        const size_t row0 = (size_t)(s2 / p.NQT) * TH + (s2 % p.NQT) * kRows + (warp & 3) * 32;
+        field = q_field_ahead(p, row0, min(32, rows_of(s2) - (warp & 3) * 32));
+      }
     }
     ++nseg;
     // pages past the clean keys: granules of drafted keys that hold a NaN are zeroed and the key
@@ -363,7 +423,7 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
     for (int pg = max(lo, clean / kPage); pg < hi; ++pg) {
       if (!wait(&bars.zero_go, n_zero++)) return;
       const int gg = g + pg - lo, first = max(clean - pg * kPage, 0), valid = min(kPage, L - pg * kPage);
-      unsigned char* st = sm + kOffStage + (gg % kF8Stages) * kF8Page;
+      unsigned char* st = sm + kOffStage + ((gg + 2 * nseg) % kF8Stages) * kF8Page;
       unsigned char* flags = bars.key_nan[gg & 1];
       for (int rw = pw; rw < kPage; rw += kF8PrepWarps) {
         uint4* g0 = reinterpret_cast<uint4*>(st + (lane >> 3) * kPageChunk + rw * 128 + (lane & 7) * 16);
@@ -440,8 +500,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         ptx::mbar_init(&bars.f8.full[s], 1);
         ptx::mbar_init(&bars.f8.empty[s], 1);
       }
+      ptx::mbar_init(&bars.f8.q_lo_raw, 1);
       ptx::mbar_init(&bars.f8.q_raw, 1);
-      ptx::mbar_init(&bars.f8.q_sync, 4);
+      ptx::mbar_init(&bars.f8.q0_sync, 8);
     }
     if (!kFp8 && p.page_box) {
       ptx::prefetch_tensormap(&tm_c4);
@@ -469,7 +530,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::mbar_init(&bars.o_done, 1);
     ptx::mbar_init(&bars.seg_done, 1);
     ptx::mbar_init(&bars.q_free, 1);
-    ptx::mbar_init(&bars.q_lo_full, kF8 ? 4 : 1);  // kF8: the warps of warpgroup 2
+    ptx::mbar_init(&bars.q_lo_full, kF8 ? 4 : 1);  // kF8: a warpgroup's warps (first segment: 1, later ones: 2)
     ptx::mbar_init(&bars.q_cp_done, 1);
     ptx::mbar_init(&bars.q_hi_full, kF8 ? 4 : 1);
     ptx::mbar_init(&bars.q0_copied, 1);
@@ -508,12 +569,34 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     if ((threadIdx.x & 31) == 0) {
       int g = 0, nseg = 0;
       int n_v = 0, n_s = 0;  // value and score-only parts issued (bf16)
+      int n_f8 = 0, n_q = 0;  // ring entries, and segments' queries in them, issued (tree over fp8)
       bool ok = true;
       while (ok && segs.next(seq, L, lo, hi)) {
         // the first page's table entry is read before Q is issued, so its latency overlaps
         // the Q copies instead of delaying the page's own
         const int page_first = page_of(p, seq, lo);
-        if constexpr (!kF8) {  // (kF8: the preparation warps bring Q)
+        if constexpr (kF8) {
+          // Q latent 0..255 as two entries of the page ring, the rest into the Q area once the
+          // previous segment's last scores are done
+          // (after one page the ring may have room while that segment's are still on their way)
+          if (n_q > 0 && !(ok = ptx::mbar_wait(&bars.f8.q_lo_raw, (n_q - 1) & 1, abort_flag, p.err))) break;
+          for (int e = 0; e < 2; ++e, ++n_f8) {
+            const int t = n_f8 % kF8Stages;
+            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((n_f8 / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
+            ptx::mbar_arrive(&bars.f8.full[t]);  // nobody waits for this phase
+            if (e == 0) ptx::mbar_arrive_expect_tx(&bars.f8.q_lo_raw, 4 * TQ * 128), ++n_q;
+            for (int c = 0; c < 2; ++c)
+              ptx::tma_load_2d(sm + kOffStage + t * kF8Page + c * kQChunk, &tm_qlat, &bars.f8.q_lo_raw, e * 128 + c * 64,
+                               q_row0(seq));
+          }
+          if (!ok) break;
+          if (nseg > 0 && !(ok = ptx::mbar_wait(&bars.q_free, (nseg - 1) & 1, abort_flag, p.err))) break;
+          ptx::mbar_arrive_expect_tx(&bars.f8.q_raw, 5 * TQ * 128);
+          for (int c = 0; c < 4; ++c)
+            ptx::tma_load_2d(sm + kOffQhi + c * kQChunk, &tm_qlat, &bars.f8.q_raw, 256 + c * 64, q_row0(seq));
+          ptx::tma_load_2d(sm + kOffQhi + 4 * kQChunk, &tm_qrope, &bars.f8.q_raw, 0, q_row0(seq));
+          ++nseg;
+        } else {
           if (nseg == 0) {
             // first sequence: Q latent 0..255 staged in the (still unused) second page
             // stage, the rest of Q straight into the Q area, all at once
@@ -554,8 +637,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           if (kWiden && g == 1 && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
           const int y = pg == lo ? row_of_page(p, page_first) : page_row(p, seq, pg);
           if constexpr (kF8) {
-            const int t = g % kF8Stages;
-            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((g / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
+            const int t = n_f8 % kF8Stages;
+            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((n_f8 / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
+            ++n_f8;
             unsigned char* dst = sm + kOffStage + t * kF8Page;
             ptx::mbar_arrive_expect_tx(&bars.f8.full[t], kF8Page);
             if (p.page_box) {
@@ -621,10 +705,12 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           }
         }
       }
-      if (kTree && !ok) {  // after an abort: copies that nobody may wait for land before the CTA leaves
+      if (kTree && (kF8 || !ok)) {  // copies that after an abort nobody may wait for land before the CTA leaves
         if constexpr (kF8) {
-          for (int v = max(0, g - kF8Stages); v < g; ++v)
+          for (int v = max(0, n_f8 - kF8Stages); v < n_f8; ++v)
             ptx::mbar_wait_drain(&bars.f8.full[v % kF8Stages], (v / kF8Stages) & 1);
+          if (n_q > 0) ptx::mbar_wait_drain(&bars.f8.q_lo_raw, (n_q - 1) & 1);
+          if (nseg > 0) ptx::mbar_wait_drain(&bars.f8.q_raw, (nseg - 1) & 1);
         } else {
           for (int v = max(0, n_v - kVSlots); v < n_v; ++v)
             ptx::mbar_wait_drain(&bars.vpart_full[v % kVSlots], (v / kVSlots) & 1);
@@ -656,6 +742,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const uint64_t b2 = ptx::sw128_desc(smb + kOffVPart + kVPartBytes, 16, 1024);
       const uint64_t b3 = ptx::sw128_desc(smb + kOffVPart + 2 * kVPartBytes, 16, 1024);
       const uint64_t qd = ptx::sw128_desc(qhi, 16, 1024);
+      // kF8: the ring entry of this segment's page gg (two entries of Q precede a segment's pages)
+      auto f8_entry = [&](int gg) { return gg + 2 * (nseg + 1); };
       // k-step k (a compile-time constant at every call) of S into d, B from chunk base bc
       auto mma_k = [&](uint32_t d, uint64_t bc, int k, bool acc) {
         const uint64_t db = bc + 2 * (k & 3);
@@ -672,9 +760,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kF8) {
           // 18 k-steps of 32 columns, the query's hi term and its lo term
           constexpr uint32_t kIdS8 = ptx::make_idesc(0, kRows, kPage, 0, 0);
-          const uint64_t st = b0 + (gg % kF8Stages) * (kF8Page / 16);
-          const uint64_t rp = ptx::smem_desc(smb + kOffStage + (gg % kF8Stages) * kF8Page + 4 * kPageChunk, 16, 512,
-                                             ptx::kSwz64);
+          const uint64_t st = b0 + f8_entry(gg) % kF8Stages * (kF8Page / 16);
+          const uint64_t rp = ptx::smem_desc(smb + kOffStage + f8_entry(gg) % kF8Stages * kF8Page + 4 * kPageChunk, 16,
+                                             512, ptx::kSwz64);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // latent 0..255: A from TMEM
             const uint64_t db = st + 512 * (j >> 2) + 2 * (j & 3);
@@ -734,7 +822,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kF8) {
           // two 128-column chunks 8 KB apart, 32 keys per k-step; P'' hi in 16 TMEM columns, lo in 16 more
           constexpr uint32_t kIdPV8 = ptx::make_idesc(0, kRows, 256, 0, 1);
-          const uint64_t vd8 = ptx::sw128_desc(smb + kOffStage + (gg % kF8Stages) * kF8Page + 2 * half * kPageChunk,
+          const uint64_t vd8 = ptx::sw128_desc(smb + kOffStage + f8_entry(gg) % kF8Stages * kF8Page + 2 * half * kPageChunk,
                                                kPageChunk, 1024);
           const uint32_t pa8 = tmem + 128 + (gg & 1) * 64;
 #pragma unroll
@@ -757,14 +845,22 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         // 0..127 (lane = query row); then latent 256..511 + rope over the staging copy
         if (!(ok = ptx::mbar_wait(&bars.q_lo_full, nseg & 1, abort_flag, p.err))) break;
         ptx::tc_fence_after();
-        // the first sequence's Q latent 0..255 was staged in the second page stage
+        // the first sequence's Q latent 0..255 was staged in the second page stage; kF8: every one's
+        // in two ring entries, which the copies free
+        const int e0 = f8_entry(g) - 2;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const uint32_t qc = !kF8 && nseg == 0 ? smb + q_stage_off(k >> 2) : qhi + (k >> 2) * kQChunk;
+          const uint32_t qc = kF8 ? smb + kOffStage + (e0 + (k >> 3)) % kF8Stages * kF8Page + ((k >> 2) & 1) * kQChunk
+                            : nseg == 0 ? smb + q_stage_off(k >> 2) : qhi + (k >> 2) * kQChunk;
           ptx::tmem_cp_128x256b(tmem + k * 8, ptx::sw128_desc(qc + (k & 3) * 32, 16, 1024));
         }
-        ptx::mma_commit(&bars.q_cp_done);
-        if (nseg == 0) ptx::mma_commit(&bars.q0_copied);
+        if constexpr (kF8) {
+          ptx::mma_commit(&bars.f8.empty[e0 % kF8Stages]);
+          ptx::mma_commit(&bars.f8.empty[(e0 + 1) % kF8Stages]);
+        } else {
+          ptx::mma_commit(&bars.q_cp_done);
+          if (nseg == 0) ptx::mma_commit(&bars.q0_copied);
+        }
         if (!kF8 && nseg > 0) {  // the rest of Q over the staging copy (the producer loaded the first)
           if (!(ok = ptx::mbar_wait(&bars.q_cp_done, nseg & 1, abort_flag, p.err))) break;
           ptx::mbar_arrive_expect_tx(&bars.q_hi_full, 5 * TQ * 128);
@@ -792,7 +888,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             ptx::mma_commit(&bars.o_done);
             // fp8: the whole stage; bf16: the value part (the score-only part was released
             // after the scores)
-            if constexpr (kF8) ptx::mma_commit(&bars.f8.empty[gp % kF8Stages]);
+            if constexpr (kF8) ptx::mma_commit(&bars.f8.empty[f8_entry(gp) % kF8Stages]);
             else ptx::mma_commit(kFp8 ? &bars.stage_empty[gp % kStages] : &bars.vpart_empty[gp % kVSlots]);
             ++gp;
             progress = true;
@@ -804,7 +900,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           bool can = false;
           if (gs < g_end && gs <= gp + 1) {
             if constexpr (kF8) {
-              if (!zero_asked && ptx::mbar_test_wait(&bars.f8.full[gs % kF8Stages], (gs / kF8Stages) & 1)) {
+              if (!zero_asked && ptx::mbar_test_wait(&bars.f8.full[f8_entry(gs) % kF8Stages], (f8_entry(gs) / kF8Stages) & 1)) {
                 can = (lo + (gs - g_first) + 1) * kPage <= clean;
                 if (!can) {
                   ptx::mbar_arrive(&bars.zero_go);
@@ -871,14 +967,18 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       }
     }
    } else if constexpr (kF8) {
-    if (warp < 4) prepare_f8<false>(p, bars, segs, sm, TH, tm_qlat, tm_qrope);
-    else prepare_f8<true>(p, bars, segs, sm, TH, tm_qlat, tm_qrope);
+    if (warp < 4) {
+      empty_items(p, unit, half, TH);
+      prepare_f8<false>(p, bars, segs, sm, TH);
+    }
+    else prepare_f8<true>(p, bars, segs, sm, TH);
    } else {
     // -------------------------------------------------------------- stage preparation
     // 0 .. n_prep - 1: warps 2-3, then 8-11, then the softmax warps that joined
     const int tid = warp < 4 ? threadIdx.x - 64
                   : warp >= 8 ? threadIdx.x - 192
                               : kPrepOf<kFp8> + threadIdx.x - 32 * (4 + n_soft);
+    if constexpr (kTree) empty_items(p, unit, half, TH);
     const int row = tid & (kPage - 1);  // the page row whose scale (fp8) this thread stages
     int g = 0, n_zero = 0;
     bool ok = true;
@@ -1012,20 +1112,44 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int g = 0, n_epi = 0, n_dec = 0, n_part = 0, n_bulk = 0, n_bulk_issued = 0;
     bool ok = true;
-    // an item with no keys (an empty sequence; tree: a query tile of padding) is in no work unit's
-    // range: unit u writes O = 0 and LSE = -inf for such sequences (tree: items) u, u + G, u + 2G, ...
-    if (half == 0) {
-      const int per = kTree ? p.NQT : 1;  // items a sequence
-      for (int v = unit; v < p.B * per; v += p.G) {
-        const int b = v / per, row0 = (v % per) * kRows;
-        if ((kTree ? decode_plan::item_len<kTree>(p, v) : clamp_len(__ldg(p.cache_lens + b), p.max_pages)) > 0) continue;
-        const int rows = kTree ? min(kRows, TH - row0) : TH;
-        uint4* o = reinterpret_cast<uint4*>(p.out + ((size_t)b * TH + row0) * kDl);
-        for (int i = r; i < rows * (kDl / 8); i += 32 * n_soft)
+    // a sequence with no keys is in no work unit's range: unit u writes O = 0 and LSE = -inf for
+    // such sequences u, u + G, u + 2G, ...  (tree: empty_items)
+    if (!kTree && half == 0) {
+      for (int b = unit; b < p.B; b += p.G) {
+        if (clamp_len(__ldg(p.cache_lens + b), p.max_pages) > 0) continue;
+        uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * TH * kDl);
+        for (int i = r; i < TH * (kDl / 8); i += 32 * n_soft)
           if (MLA_STORE_OK(o + i, p.out, p.out_bytes, p.err)) o[i] = make_uint4(0, 0, 0, 0);
-        for (int i = row0 + r; i < row0 + rows; i += 32 * n_soft) {
+        for (int i = r; i < TH; i += 32 * n_soft) {
           float* lp = p.lse + ((size_t)b * p.H + i % p.H) * p.T + i / p.H;
           if (MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = -INFINITY;
+        }
+      }
+    }
+    if constexpr (kF8) {
+      // The first segment's query terms of latent 0..255 (warpgroup 2 makes the others).  A row's two
+      // largest fields change hands through q_exp, whose first entry then holds the row's power of two.
+      Segments first = segs;
+      if (first.next(seq, L, lo, hi)) {
+        unsigned char *e0 = sm + kOffStage, *e1 = e0 + kF8Page;
+        const bool live = r < min(p.TQ, TH - (seq % p.NQT) * kRows);
+        int mine = 0;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.f8.q_lo_raw, 0, abort_flag, p.err));
+        if (ok) {
+          if (live) mine = max(q_field(e0, r, 2), q_field(e1, r, 2));
+          bars.f8.q_exp[1][r] = static_cast<signed char>(mine);
+          ptx::fence_proxy_async();
+          __syncwarp();
+          if ((r & 31) == 0) ptx::mbar_arrive(&bars.f8.q0_sync);
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.f8.q0_sync, 0, abort_flag, p.err));
+        }
+        if (ok) {
+          const int k = q_exponent(max(mine, static_cast<int>(static_cast<unsigned char>(bars.f8.q_exp[0][r]))));
+          bars.f8.q_exp[0][r] = static_cast<signed char>(k);
+          q_turn(e0, e1, r, q_factor(k), live);
+          ptx::fence_proxy_async();
+          __syncwarp();
+          if ((r & 31) == 0) ptx::mbar_arrive(&bars.q_lo_full);
         }
       }
     }
@@ -1283,6 +1407,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         return kTree && lr == 0.f ? 0.f : o;
       };
       const bool row_live = r < TQ && gr < TH;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // tree: rows in whole sectors
       // The work units that cover this virtual sequence write their partials of this column
       // half into slots c + seq, c_first <= c <= c_first + nsplit - 1; this one is k_own.
       const int n_pages = pages_of(L, kPage);
@@ -1399,7 +1524,36 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         bulk = *reinterpret_cast<volatile int*>(&bars.merge_bulk) != 0;
         own_in_tmem = merge;
       }
-      if (merge) {
+      if (kTree && !decide) {
+        // One split: the rows go out from the accumulator.  A thread stores its own row, whole 32-byte
+        // sectors at a time: half sectors took 1.2 us a round of 64 columns, most of an epilogue of 8 us.
+        uint4* orow = reinterpret_cast<uint4*>(p.out + ((size_t)(seq / p.NQT) * TH + gr) * kDl + half * 256);
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 64) {
+          uint32_t v[2][32];
+          ptx::tmem_ld32(o_addr + c, v[0]);
+          ptx::tmem_ld32(o_addr + c + 32, v[1]);
+          ptx::tmem_ld_wait();
+          if (!row_live) continue;
+#pragma unroll
+          for (int j = 0; j < 64; j += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = ptx::pack_bf16x2(own_o(v[j >> 5][(j & 31) + 2 * i]), own_o(v[j >> 5][(j & 31) + 2 * i + 1]));
+            uint4* at = orow + (c + j) / 8;
+            if (!MLA_STORE_OK(at + 1, p.out, p.out_bytes, p.err)) continue;  // (the later of the two)
+            if (wide) {
+              ptx::st_v8(at, w);
+            } else {
+              at[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              at[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+        float* lp = p.lse + ((size_t)(seq / p.NQT) * p.H + gr % p.H) * p.T + gr / p.H;
+        if (half == 0 && row_live && MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = lse_own;
+      } else if (merge) {
         // Every lane of a warp runs this block (the accumulator loads are warp-collective:
         // a lane that skipped them would stall its warp for good); global memory is touched
         // for the live rows only.  This thread's row: weights of the splits from their LSEs
@@ -1491,15 +1645,26 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             }
           }
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const uint4 w = make_uint4(ptx::pack_bf16x2(acc[j].x, acc[j].y), ptx::pack_bf16x2(acc[j].z, acc[j].w),
-                                       ptx::pack_bf16x2(acc[j + 1].x, acc[j + 1].y),
-                                       ptx::pack_bf16x2(acc[j + 1].z, acc[j + 1].w));
-            const int ch = (q + j) >> 1;  // 16-byte chunk of the row's 512 bytes
-            if (staged)
-              *reinterpret_cast<uint4*>(stage_out + r * 512 + ((ch ^ (r & 31)) << 4)) = w;
-            else if (row_live && MLA_STORE_OK(orow + ch, p.out, p.out_bytes, p.err))
-              orow[ch] = w;
+          for (int j = 0; j < 16; j += 4) {
+            uint32_t w[8];  // 16 columns: 16-byte chunks ch and ch + 1 of the row's 512 bytes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[2 * i] = ptx::pack_bf16x2(acc[j + i].x, acc[j + i].y);
+              w[2 * i + 1] = ptx::pack_bf16x2(acc[j + i].z, acc[j + i].w);
+            }
+            const int ch = (q + j) >> 1;
+            if (kTree && wide && !staged) {
+              if (row_live && MLA_STORE_OK(orow + ch + 1, p.out, p.out_bytes, p.err)) ptx::st_v8(orow + ch, w);
+              continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 x = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              if (staged)
+                *reinterpret_cast<uint4*>(stage_out + r * 512 + (((ch + i) ^ (r & 31)) << 4)) = x;
+              else if (row_live && MLA_STORE_OK(orow + ch + i, p.out, p.out_bytes, p.err))
+                orow[ch + i] = x;
+            }
           }
         }
         if (staged) {

@@ -230,6 +230,17 @@ def test_many_short_sequences(lib):
     p.check(out, lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("long", [0, 900])
+def test_many_query_tiles_of_one_page(lib, fp8, long):
+    # each work unit takes several items, most of one page: an item's queries and its only page are
+    # asked for while the item before is still loading its own
+    lens = [long if long and b % 7 == 3 else 4 + b % 60 for b in range(160)]
+    p = Problem(128, 4, lens, fp8, seed=29)
+    p.check(*p.run(lib))
+    lib.check_device_error()
+
+
 def test_bad_page_is_reported(lib):
     p = Problem(4, 3, [100, 100], False, seed=13)
     p.args[3][1, 1] = p.inp.num_pages + 5
@@ -253,6 +264,20 @@ def test_writes_only_out_lse_and_workspace(lib, fp8):
     assert out.intact() and lse.intact() and ws.intact()
     assert torch.equal(p.args[2].view(torch.uint8), before)
     p.check(out.t, lse.t)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_an_output_aligned_to_16_bytes_only(lib, fp8):
+    # items in one split, in two and in more; rows that end a tile
+    p = Problem(40, 5, [5, 130, 9000, 20, 40, 60], fp8, seed=15, new=[5, 2, 4, 0, 1, 5])
+    ref, ref_lse = p.run(lib)
+    flat = torch.full((ref.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:8 + ref.numel()].view(ref.shape)
+    assert out.data_ptr() % 32 == 16
+    _, lse = p.run(lib, out=out)
+    lib.check_device_error()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    assert (flat[:8] == 7).all() and (flat[-8:] == 7).all()
 
 
 def test_captured_and_replayed_with_new_lengths_and_masks(lib):
