@@ -31,19 +31,19 @@
 //               the bf16 output and the LSE
 // Two further instances serve a tree of drafted tokens (kTree): which of the n newest keys a row
 // sees comes from a bit mask a token instead of the diagonal, and the pages that hold drafted keys
-// pass through the preparation warps, which take non-finite values out of them (a zero weight
-// times such a value would reach rows that do not see the key) and flag their keys, so that the
-// rows that see them, and no others, come out as NaN.
+// pass through warps 2 and 3, which take non-finite values out of them (a zero weight times such a
+// value would reach rows that do not see the key) and flag their keys, so that the rows that see
+// them, and no others, come out as NaN.  They also write the rows of items without keys.
 // The tree over an fp8 cache (kF8) widens nothing: the e4m3 page is the MMA's operand as it lies.
 // Its other operands are sums of two e4m3 terms: a bf16 query, scaled by a power of two into
 // [128, 256) at its row's largest value, is hi + lo exactly (8 significant bits, 4 + 4) down to 2^-10
 // of that value, and a weight P'' = p ks is hi + lo to 2^-8.  Twice the k-steps at twice the rate: the
 // tensor work is bf16's, pages take half the bytes, and four fit instead of two; each page is its
-// own stage, released by its PV product.  The preparation warps make the query terms.  64 ragged
+// own stage, released by its PV product.  Warps 8-11 make the query terms.  64 ragged
 // sequences of up to 16384 keys, 1 to 13 tokens of 16 heads: 613 us with the pages widened to bf16, 433
 // with e4m3 operands (an item's query terms then took 20 us), 344 with the terms made in place from
-// TMA loads and items charged in the split plan, 255 with tiles of padding left out.  A page takes
-// 1.2 us, 2,300 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key half each, were no faster,
+// TMA loads and items charged in the split plan, 255 with tiles of padding left out, 248 with the ends of
+// items shortened.  A page takes 1.3 us, 2,500 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key half each, were no faster,
 // nor was splitting into terms with integer instructions.)
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
@@ -101,7 +101,6 @@ static_assert(kF8Stages * kF8Page <= kStages * kStageBytes, "fp8 tree pages fit 
 // sequences of up to 16384 keys, fp8: 256, 257, 254 and 261 us for 10, 12, 13 and 16; 16 of up to 8000
 // keys and 8 x 128 rows, bf16: 158, 159, 151 and 150 us for 4, 5, 6 and 8.
 constexpr int kF8ItemCost = 13, kTreeItemCost = 8;
-constexpr int kF8PrepWarps = 6;                 // warps 2-3 and 8-11
 // registers a thread: 384 threads launched at kF8RegsLaunch, then traded between the warpgroups
 constexpr int kF8RegsLaunch = 168, kF8RegsHigh = 232, kF8RegsLow = 136;
 static_assert(128 * kF8RegsHigh + 256 * kF8RegsLow <= 384 * kF8RegsLaunch, "register split");
@@ -356,8 +355,71 @@ __device__ __forceinline__ void empty_items(const Params& p, int unit, int half,
   }
 }
 
-// The preparation warps of the tree over an fp8 cache.  All six prepare the pages that end a sequence
-// or hold drafted keys; warpgroup 2 (kQ) makes the query terms of every segment: raw rows by TMA,
+// Tree: warps 2 and 3 take non-finite values out of the pages that hold drafted keys, and what lies
+// behind a sequence's end out of its last page: a weight of zero times such a value would reach every
+// row.  Scores need no such care, a key's are its own column, so only the value columns of this half
+// are zeroed, and for fp8 the MMA thread issues the scores meanwhile (it tells nobody of them before
+// `zeroed`; what they read of a row that is being zeroed is a column that nobody uses).
+// A drafted key's flag, on the other hand, stands for its whole row.  It is found ahead of the page's
+// copy, from memory: after the copy, an item's last page took 4 us longer than its others (bf16; 32
+// sequences of 300 keys and 32 x 128 rows: 247 us against 195).
+template <bool kFp8, typename B>
+__device__ __forceinline__ void prepare_pages(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int half) {
+  constexpr int kGranules = kDc * (kFp8 ? 1 : 2) / 16;  // of a row
+  constexpr int kLoads = 8 * kGranules / 32;            // eight rows (contiguous) by a warp
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
+  // a warp has the rows 16 j + 8 w .. + 7 of a page; bit and lane 8 j + i: row 16 j + 8 w + i
+  const int mine = (lane >> 3) * 16 + w * 8 + (lane & 7);
+  int seq, L, lo, hi, g = 0, nseg = 0, n_zero = 0;
+  while (segs.next(seq, L, lo, hi)) {
+    ++nseg;
+    const int clean = max(L - drafted(p, seq), 0);
+    if constexpr (!kFp8) {
+      for (int pg = lo + (int)threadIdx.x - 64; pg < hi && seq % p.NQT == 0; pg += 64) {
+        const int page = page_of(p, seq, pg);
+        if (page < 0 || page >= p.num_pages) latch_error(p.err, kErrBadPage);
+      }
+    }
+    for (int pg = max(lo, clean / kPage); pg < hi; ++pg) {
+      const int gg = g + pg - lo, first = max(clean - pg * kPage, 0), valid = min(kPage, L - pg * kPage);
+      const int page = page_of(p, seq, pg);
+      uint32_t flagged = 0;
+      if (page >= 0 && page < p.num_pages) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const int r0 = 16 * j + 8 * w;
+          if (r0 + 8 <= first || r0 >= valid) continue;
+          const uint4* src = reinterpret_cast<const uint4*>(p.cache_bytes) + ((size_t)page * kPage + r0) * kGranules;
+          uint4 v[kLoads];
+          uint32_t rows = 0;
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) v[x] = __ldcg(src + lane + 32 * x);
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x)
+            if (granule_nonfinite<kFp8>(v[x])) rows |= 1u << ((lane + 32 * x) / kGranules);
+          flagged |= __reduce_or_sync(0xffffffffu, rows) << (8 * j);
+        }
+      }
+      flagged &= __ballot_sync(0xffffffffu, mine >= first && mine < valid);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero++ & 1, &bars.abort_flag, p.err))) return;
+      bars.key_nan[gg & 1][mine] = flagged >> lane & 1;
+      const uint32_t zero = flagged | __ballot_sync(0xffffffffu, mine >= valid);
+      // (whole rows of a chunk, so the swizzle is immaterial)
+      unsigned char* values = kFp8 ? sm + kOffStage + (gg + 2 * nseg) % kF8Stages * kF8Page + 2 * half * kPageChunk
+                                   : sm + kOffVPart + gg % kVSlots * kVPartBytes;
+      for (int i = 0; i < 32; ++i)
+        if ((zero >> i & 1) && lane < (kFp8 ? 16 : 32))
+          *reinterpret_cast<uint4*>(values + (lane >> 3) * kPageChunk + ((i >> 3) * 16 + w * 8 + (i & 7)) * 128 +
+                                    (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars.zeroed);
+    }
+    g += hi - lo;
+  }
+}
+
+// Warpgroup 2 of the tree over an fp8 cache makes the query terms of every segment: raw rows by TMA,
 // turned in place into terms by one thread a row (128 columns: 256 bytes of bf16 become 128 of hi and
 // 128 of lo).  Latent 0..255 comes through two entries of the page ring ahead of the segment's pages
 // and is copied on to TMEM by the MMA thread, the rest stays in the query area, which is free when the
@@ -365,13 +427,12 @@ __device__ __forceinline__ void empty_items(const Params& p, int unit, int half,
 // from memory, while the previous segment's pages are under way.  Only the first segment, which no
 // other work covers, finds it from both parts in shared memory, and warpgroup 1, which has no scores
 // yet, turns its latent 0..255.
-template <bool kQ, typename B>
-__device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int TH) {
+template <typename B>
+__device__ __forceinline__ void prepare_queries(const Params& p, B& bars, SegmentsOf<true> segs, unsigned char* sm, int TH) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pw = kQ ? warp - 6 : warp - 2;  // 0 .. kF8PrepWarps - 1
   volatile int* abort_flag = &bars.abort_flag;
   unsigned char* qa = sm + kOffQhi;
-  int seq, L, lo, hi, g = 0, nseg = 0, n_zero = 0;
+  int seq, L, lo, hi, g = 0, nseg = 0;
   auto wait = [&](uint64_t* bar, int phase) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, abort_flag, p.err)) != 0;
   };
@@ -384,65 +445,38 @@ __device__ __forceinline__ void prepare_f8(const Params& p, B& bars, SegmentsOf<
   const int r = (warp & 3) * 32 + lane;
   int field = 0;  // of this thread's row in the segment at hand
   while (segs.next(seq, L, lo, hi)) {
-    if constexpr (kQ) {
-      const bool live = r < rows_of(seq);
-      if (nseg == 0) {
-        if (!wait(&bars.f8.q_raw, 0)) return;
-        if (live) field = q_field(qa, r, 5);
-        bars.f8.q_exp[0][r] = static_cast<signed char>(field);
-        done(&bars.f8.q0_sync);
-        if (!wait(&bars.f8.q0_sync, 0)) return;
-        field = max(field, static_cast<int>(static_cast<unsigned char>(bars.f8.q_exp[1][r])));
-      }
-      const int k = q_exponent(field);
-      const float f = q_factor(k);
-      if (nseg > 0) {
-        const int e = g + 2 * nseg;  // ring entries of latent 0..127 and (e + 1) 128..255
-        unsigned char *e0 = sm + kOffStage + (e % kF8Stages) * kF8Page,
-                      *e1 = sm + kOffStage + ((e + 1) % kF8Stages) * kF8Page;
-        if (!wait(&bars.f8.q_lo_raw, nseg)) return;
-        q_turn(e0, e1, r, f, live);
-        done(&bars.q_lo_full);
-        if (!wait(&bars.f8.q_raw, nseg)) return;
-        bars.f8.q_exp[nseg & 1][r] = static_cast<signed char>(k);
-      }
-      q_turn(qa, qa + 2 * kQChunk, r, f, live);
-      q_turn_rope(qa, r, f, live);
-      done(&bars.q_hi_full);
-      SegmentsOf<true> nx = segs;
-      int s2, L2, lo2, hi2;
-      if (nx.next(s2, L2, lo2, hi2)) {
-        const size_t row0 = (size_t)(s2 / p.NQT) * TH + (s2 % p.NQT) * kRows + (warp & 3) * 32;
-        field = q_field_ahead(p, row0, min(32, rows_of(s2) - (warp & 3) * 32));
-      }
+    const bool live = r < rows_of(seq);
+    if (nseg == 0) {
+      if (!wait(&bars.f8.q_raw, 0)) return;
+      if (live) field = q_field(qa, r, 5);
+      bars.f8.q_exp[0][r] = static_cast<signed char>(field);
+      done(&bars.f8.q0_sync);
+      if (!wait(&bars.f8.q0_sync, 0)) return;
+      field = max(field, static_cast<int>(static_cast<unsigned char>(bars.f8.q_exp[1][r])));
     }
+    const int k = q_exponent(field);
+    const float f = q_factor(k);
+    if (nseg > 0) {
+      const int e = g + 2 * nseg;  // ring entries of latent 0..127 and (e + 1) 128..255
+      unsigned char *e0 = sm + kOffStage + (e % kF8Stages) * kF8Page,
+                    *e1 = sm + kOffStage + ((e + 1) % kF8Stages) * kF8Page;
+      if (!wait(&bars.f8.q_lo_raw, nseg)) return;
+      q_turn(e0, e1, r, f, live);
+      done(&bars.q_lo_full);
+      if (!wait(&bars.f8.q_raw, nseg)) return;
+      bars.f8.q_exp[nseg & 1][r] = static_cast<signed char>(k);
+    }
+    q_turn(qa, qa + 2 * kQChunk, r, f, live);
+    q_turn_rope(qa, r, f, live);
+    done(&bars.q_hi_full);
     ++nseg;
-    // pages past the clean keys: granules of drafted keys that hold a NaN are zeroed and the key
-    // flagged, the rows past the sequence's end are zeroed (whole rows, so the swizzles are immaterial)
-    const int clean = max(L - drafted(p, seq), 0);
-    for (int pg = max(lo, clean / kPage); pg < hi; ++pg) {
-      if (!wait(&bars.zero_go, n_zero++)) return;
-      const int gg = g + pg - lo, first = max(clean - pg * kPage, 0), valid = min(kPage, L - pg * kPage);
-      unsigned char* st = sm + kOffStage + ((gg + 2 * nseg) % kF8Stages) * kF8Page;
-      unsigned char* flags = bars.key_nan[gg & 1];
-      for (int rw = pw; rw < kPage; rw += kF8PrepWarps) {
-        uint4* g0 = reinterpret_cast<uint4*>(st + (lane >> 3) * kPageChunk + rw * 128 + (lane & 7) * 16);
-        uint4* g1 = reinterpret_cast<uint4*>(st + 4 * kPageChunk + rw * 64 + (lane & 3) * 16);
-        bool hit0 = rw >= valid, hit1 = hit0;
-        if (rw >= first && rw < valid) {
-          hit0 = granule_nonfinite<true>(*g0);
-          hit1 = lane < 4 && granule_nonfinite<true>(*g1);
-          const bool any = __any_sync(0xffffffffu, hit0 || hit1);
-          if (lane == 0) flags[rw] = any;
-        } else if (lane == 0) {
-          flags[rw] = 0;
-        }
-        if (hit0) *g0 = make_uint4(0, 0, 0, 0);
-        if (hit1 && lane < 4) *g1 = make_uint4(0, 0, 0, 0);
-      }
-      done(&bars.zeroed);
-    }
     g += hi - lo;
+    SegmentsOf<true> nx = segs;
+    int s2, L2, lo2, hi2;
+    if (nx.next(s2, L2, lo2, hi2)) {
+      const size_t row0 = (size_t)(s2 / p.NQT) * TH + (s2 % p.NQT) * kRows + (warp & 3) * 32;
+      field = q_field_ahead(p, row0, min(32, rows_of(s2) - (warp & 3) * 32));
+    }
   }
 }
 
@@ -522,7 +556,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       ptx::mbar_init(&bars.vpart_empty[v], 1);
     }
     ptx::mbar_init(&bars.zero_go, 1);
-    ptx::mbar_init(&bars.zeroed, n_prep / 32);
+    ptx::mbar_init(&bars.zeroed, kTree ? 2 : n_prep / 32);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars.s_full[i], 1);
       ptx::mbar_init(&bars.p_full[i], n_soft);  // one arrival per softmax warp
@@ -879,6 +913,12 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         int sp = 0;          // next part of S(gs)
         bool zero_asked = false;  // bf16: the partial page gs was handed to the preparation warps
         long long t0 = clock64();
+        bool s_held = false;      // kF8: S(gs) is issued, its page not prepared yet
+        auto s_issued = [&](int& page) {
+          ptx::mma_commit(&bars.s_full[page & 1]);
+          ++page;
+          if (page == g_end) ptx::mma_commit(&bars.q_free);  // Q no longer read
+        };
         while (gp < g_end) {
           bool progress = false;
           // PV first: it releases the page stage for the next load
@@ -896,26 +936,41 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           // S(gs) may run at most one page ahead of the oldest unissued PV (two S buffers).
           // A full bf16 page needs no preparation: its parts are ready when they land.  A page
           // that ends its sequence part-way goes to the preparation warps once both parts have
-          // landed and comes back with the rows past the end zeroed.
+          // landed (tree: the value part, which the scores' second part then waits for; fp8: the
+          // page, with the scores issued meanwhile) and comes back with the rows past the end zeroed.
           bool can = false;
           if (gs < g_end && gs <= gp + 1) {
+            const bool whole = (lo + (gs - g_first) + 1) * kPage <= clean;
             if constexpr (kF8) {
-              if (!zero_asked && ptx::mbar_test_wait(&bars.f8.full[f8_entry(gs) % kF8Stages], (f8_entry(gs) / kF8Stages) & 1)) {
-                can = (lo + (gs - g_first) + 1) * kPage <= clean;
-                if (!can) {
-                  ptx::mbar_arrive(&bars.zero_go);
-                  zero_asked = progress = true;
+              if (s_held) {
+                // the scores of a page that is prepared are out; their readers may go on once it is
+                if (ptx::mbar_test_wait(&bars.zeroed, n_zeroed & 1)) {
+                  ++n_zeroed;
+                  s_held = false;
+                  s_issued(gs);
+                  progress = true;
                 }
-              } else if (zero_asked && ptx::mbar_test_wait(&bars.zeroed, n_zeroed & 1)) {
-                can = true;
-                zero_asked = false;
-                ++n_zeroed;
+              } else {
+                can = ptx::mbar_test_wait(&bars.f8.full[f8_entry(gs) % kF8Stages], (f8_entry(gs) / kF8Stages) & 1);
+                if (can && !whole) ptx::mbar_arrive(&bars.zero_go);
               }
             } else if constexpr (kFp8) {
               can = ptx::mbar_test_wait(&bars.stage_ready[gs % kStages][sp], (gs / kStages) & 1);
-            } else if ((lo + (gs - g_first) + 1) * kPage <= clean) {
+            } else if (whole) {
               can = sp == 0 ? ptx::mbar_test_wait(&bars.spart_full, gs & 1)
                             : ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1);
+            } else if (kTree) {
+              // prepared from its value part on, which lands about a page ahead of the score-only part
+              if (!zero_asked && ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1)) {
+                ptx::mbar_arrive(&bars.zero_go);
+                zero_asked = progress = true;
+              }
+              can = sp == 0 ? ptx::mbar_test_wait(&bars.spart_full, gs & 1)
+                            : zero_asked && ptx::mbar_test_wait(&bars.zeroed, n_zeroed & 1);
+              if (can && sp == 1) {
+                zero_asked = false;
+                ++n_zeroed;
+              }
             } else if (sp == 1) {
               can = true;  // zeroed before its part 0
             } else if (!zero_asked) {
@@ -937,11 +992,11 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             if (!kFp8 && sp == 0) ptx::mma_commit(&bars.spart_empty);
             if (sp + 1 < kParts) {
               ++sp;
+            } else if (kF8 && (lo + (gs - g_first) + 1) * kPage > clean) {
+              s_held = true;
             } else {
               sp = 0;
-              ptx::mma_commit(&bars.s_full[gs & 1]);
-              ++gs;
-              if (gs == g_end) ptx::mma_commit(&bars.q_free);  // Q no longer read
+              s_issued(gs);
             }
             progress = true;
           }
@@ -969,16 +1024,19 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
    } else if constexpr (kF8) {
     if (warp < 4) {
       empty_items(p, unit, half, TH);
-      prepare_f8<false>(p, bars, segs, sm, TH);
+      prepare_pages<true>(p, bars, segs, sm, half);
+    } else {
+      prepare_queries(p, bars, segs, sm, TH);
     }
-    else prepare_f8<true>(p, bars, segs, sm, TH);
+   } else if constexpr (kTree) {
+    empty_items(p, unit, half, TH);
+    prepare_pages<false>(p, bars, segs, sm, half);
    } else {
     // -------------------------------------------------------------- stage preparation
     // 0 .. n_prep - 1: warps 2-3, then 8-11, then the softmax warps that joined
     const int tid = warp < 4 ? threadIdx.x - 64
                   : warp >= 8 ? threadIdx.x - 192
                               : kPrepOf<kFp8> + threadIdx.x - 32 * (4 + n_soft);
-    if constexpr (kTree) empty_items(p, unit, half, TH);
     const int row = tid & (kPage - 1);  // the page row whose scale (fp8) this thread stages
     int g = 0, n_zero = 0;
     bool ok = true;
@@ -1003,48 +1061,13 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           if ((pg + 1) * kPage > clean) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero & 1, abort_flag, p.err));
             if (!ok) break;
-            if constexpr (kTree) {
-              // rows of drafted keys first .. valid - 1: non-finite granules are zeroed and the key flagged;
-              // rows past the end are zeroed.  A warp takes a whole row (72 granules), four at a time.
-              const int first = max(clean - pg * kPage, 0), lane = tid & 31;
-              unsigned char* flags = bars.key_nan[g & 1];
-              if (tid < first) flags[tid] = 0;
-              constexpr int kRowsAtOnce = 4;
-              for (int base = first + (tid >> 5); base < kPage; base += kRowsAtOnce * (n_prep / 32)) {
-                uint4* gr[kRowsAtOnce][3];
-                bool hit[kRowsAtOnce][3];
-#pragma unroll
-                for (int i = 0; i < kRowsAtOnce; ++i) {
-                  const int rw = base + i * (n_prep / 32);
-#pragma unroll
-                  for (int x = 0; x < 3; ++x) {
-                    const int e = lane + 32 * x, c = e >> 3;
-                    gr[i][x] = reinterpret_cast<uint4*>(
-                        sm + (c < 5 ? kOffSPart + c * kPageChunk
-                                    : kOffVPart + (g % kVSlots) * kVPartBytes + (c - 5) * kPageChunk) +
-                        rw * 128 + (e & 7) * 16);
-                    hit[i][x] = e < 72 && rw < kPage && (rw >= valid || granule_nonfinite<false>(*gr[i][x]));
-                  }
-                }
-#pragma unroll
-                for (int i = 0; i < kRowsAtOnce; ++i) {
-                  const int rw = base + i * (n_prep / 32);
-                  const bool any = __any_sync(0xffffffffu, hit[i][0] || hit[i][1] || hit[i][2]);
-#pragma unroll
-                  for (int x = 0; x < 3; ++x)
-                    if (hit[i][x]) *gr[i][x] = make_uint4(0, 0, 0, 0);
-                  if (lane == 0 && rw < kPage) flags[rw] = any && rw < valid;
-                }
-              }
-            } else {
-              const int nrow = kPage - valid;
-              for (int part = 0; part < 2; ++part) {
-                const int nch = part == 0 ? 5 : 4;
-                unsigned char* base = sm + (part == 0 ? kOffSPart : kOffVPart + (g % kVSlots) * kVPartBytes);
-                for (int e = tid; e < nrow * nch * 8; e += n_prep) {
-                  const int rw = valid + e / (nch * 8), rem = e % (nch * 8), c = rem >> 3, gr = rem & 7;
-                  *reinterpret_cast<uint4*>(base + c * kPageChunk + rw * 128 + gr * 16) = make_uint4(0, 0, 0, 0);
-                }
+            const int nrow = kPage - valid;
+            for (int part = 0; part < 2; ++part) {
+              const int nch = part == 0 ? 5 : 4;
+              unsigned char* base = sm + (part == 0 ? kOffSPart : kOffVPart + (g % kVSlots) * kVPartBytes);
+              for (int e = tid; e < nrow * nch * 8; e += n_prep) {
+                const int rw = valid + e / (nch * 8), rem = e % (nch * 8), c = rem >> 3, gr = rem & 7;
+                *reinterpret_cast<uint4*>(base + c * kPageChunk + rw * 128 + gr * 16) = make_uint4(0, 0, 0, 0);
               }
             }
             ptx::fence_proxy_async();

@@ -192,6 +192,28 @@ def test_non_finite_drafted_keys_reach_only_rows_that_see_them(lib, fp8, value, 
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("node,column", [(0, 0), (99, 575), (37, 255), (36, 256), (63, 511), (64, 512), (27, 128), (28, 447)])
+def test_a_non_finite_value_anywhere_in_a_tree_over_three_pages(lib, fp8, node, column):
+    # 36 + 64 keys drafted up to a page's end, 28 + 64 + 8 otherwise: each page's first, last and other rows
+    T, lens = 100, [64 * 3, 64 * 2 + 8, 100]
+    p = Problem(4, T, lens, fp8, seed=31, shared=True)
+    clean_out, clean_lse = p.run(lib)
+    for b, L in enumerate(lens):
+        place = L - T + node
+        page, row = int(p.inp.page_table[b, place // 64]), place % 64
+        if fp8:
+            p.args[2].view(torch.uint8)[page, row, column] = 0x7F
+        else:
+            p.args[2][page, row, column] = float("-inf")
+    out, lse = p.run(lib)
+    lib.check_device_error()
+    hit = torch.from_numpy(p.sees[0, :, node].copy()).cuda()
+    assert bool(hit.any())
+    assert bool(torch.isnan(out[:, hit]).all()) and bool(torch.isnan(lse[:, :, hit]).all())
+    assert torch.equal(out[:, ~hit], clean_out[:, ~hit]) and torch.equal(lse[:, :, ~hit], clean_lse[:, :, ~hit])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_padding_rows_are_zero_whatever_the_prefix_holds(lib, fp8):
     p = Problem(8, 5, [200], fp8, seed=9, new=[2])
     page = int(p.inp.page_table[0, 0])
