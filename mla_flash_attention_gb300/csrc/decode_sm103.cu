@@ -406,7 +406,7 @@ __device__ __forceinline__ void prepare_pages(const Params& p, B& bars, Segments
       const uint32_t zero = flagged | __ballot_sync(0xffffffffu, mine >= valid);
       // (whole rows of a chunk, so the swizzle is immaterial)
       unsigned char* values = kFp8 ? sm + kOffStage + (gg + 2 * nseg) % kF8Stages * kF8Page + 2 * half * kPageChunk
-                                   : sm + kOffVPart + gg % kVSlots * kVPartBytes;
+                                   : sm + kOffVPart + (gg + 2 * nseg) % kVSlots * kVPartBytes;
       for (int i = 0; i < 32; ++i)
         if ((zero >> i & 1) && lane < (kFp8 ? 16 : 32))
           *reinterpret_cast<uint4*>(values + (lane >> 3) * kPageChunk + ((i >> 3) * 16 + w * 8 + (i & 7)) * 128 +
@@ -513,6 +513,20 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     if constexpr (kFp8) return kOffStage + kStageBytes + c * kQChunk;
     return kOffVPart + (1 + (c >> 1)) * kVPartBytes + (c & 1) * kQChunk;
   };
+  // Tree: every sequence's Q latent 0..255 takes two entries of a ring ahead of its pages (fp8: whole
+  // pages; bf16: value parts), so that it is there when the sequence before has its last scores
+  constexpr int kRing = kF8 ? kF8Stages : kVSlots;
+  auto ring_full = [&](int entry) -> uint64_t* {
+    if constexpr (kF8) return &bars.f8.full[entry % kRing];
+    else return &bars.vpart_full[entry % kRing];
+  };
+  auto ring_empty = [&](int entry) -> uint64_t* {
+    if constexpr (kF8) return &bars.f8.empty[entry % kRing];
+    else return &bars.vpart_empty[entry % kRing];
+  };
+  auto ring_off = [&](int entry) {
+    return kF8 ? kOffStage + entry % kRing * kF8Page : kOffVPart + entry % kRing * kVPartBytes;
+  };
   const int warp = threadIdx.x >> 5;
   const int unit = blockIdx.x >> 1, half = blockIdx.x & 1;
   const int TH = p.T * p.H, TQ = p.TQ;
@@ -602,33 +616,35 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     // value part, which goes out about a page earlier, never waits behind a score-only part.
     if ((threadIdx.x & 31) == 0) {
       int g = 0, nseg = 0;
-      int n_v = 0, n_s = 0;  // value and score-only parts issued (bf16)
-      int n_f8 = 0, n_q = 0;  // ring entries, and segments' queries in them, issued (tree over fp8)
+      [[maybe_unused]] int n_ring = 0, n_q = 0, n_s = 0;  // tree: ring entries, queries in them, score-only parts issued
       bool ok = true;
       while (ok && segs.next(seq, L, lo, hi)) {
         // the first page's table entry is read before Q is issued, so its latency overlaps
         // the Q copies instead of delaying the page's own
         const int page_first = page_of(p, seq, lo);
-        if constexpr (kF8) {
-          // Q latent 0..255 as two entries of the page ring, the rest into the Q area once the
-          // previous segment's last scores are done
+        if constexpr (kTree) {
+          // Q latent 0..255 as two ring entries, the rest into the Q area once the previous segment's
+          // last scores are done (fp8: raw rows, which warps 8-11 turn into terms)
+          uint64_t *lo_bar = &bars.q_lo_full, *hi_bar = &bars.q_hi_full;
+          if constexpr (kF8) {
+            lo_bar = &bars.f8.q_lo_raw;
+            hi_bar = &bars.f8.q_raw;
+          }
           // (after one page the ring may have room while that segment's are still on their way)
-          if (n_q > 0 && !(ok = ptx::mbar_wait(&bars.f8.q_lo_raw, (n_q - 1) & 1, abort_flag, p.err))) break;
-          for (int e = 0; e < 2; ++e, ++n_f8) {
-            const int t = n_f8 % kF8Stages;
-            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((n_f8 / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
-            ptx::mbar_arrive(&bars.f8.full[t]);  // nobody waits for this phase
-            if (e == 0) ptx::mbar_arrive_expect_tx(&bars.f8.q_lo_raw, 4 * TQ * 128), ++n_q;
+          if (n_q > 0 && !(ok = ptx::mbar_wait(lo_bar, (n_q - 1) & 1, abort_flag, p.err))) break;
+          for (int e = 0; e < 2; ++e, ++n_ring) {
+            if (!(ok = ptx::mbar_wait(ring_empty(n_ring), ((n_ring / kRing) & 1) ^ 1, abort_flag, p.err))) break;
+            ptx::mbar_arrive(ring_full(n_ring));  // nobody waits for this phase
+            if (e == 0) ptx::mbar_arrive_expect_tx(lo_bar, 4 * TQ * 128), ++n_q;
             for (int c = 0; c < 2; ++c)
-              ptx::tma_load_2d(sm + kOffStage + t * kF8Page + c * kQChunk, &tm_qlat, &bars.f8.q_lo_raw, e * 128 + c * 64,
-                               q_row0(seq));
+              ptx::tma_load_2d(sm + ring_off(n_ring) + c * kQChunk, &tm_qlat, lo_bar, e * 128 + c * 64, q_row0(seq));
           }
           if (!ok) break;
           if (nseg > 0 && !(ok = ptx::mbar_wait(&bars.q_free, (nseg - 1) & 1, abort_flag, p.err))) break;
-          ptx::mbar_arrive_expect_tx(&bars.f8.q_raw, 5 * TQ * 128);
+          ptx::mbar_arrive_expect_tx(hi_bar, 5 * TQ * 128);
           for (int c = 0; c < 4; ++c)
-            ptx::tma_load_2d(sm + kOffQhi + c * kQChunk, &tm_qlat, &bars.f8.q_raw, 256 + c * 64, q_row0(seq));
-          ptx::tma_load_2d(sm + kOffQhi + 4 * kQChunk, &tm_qrope, &bars.f8.q_raw, 0, q_row0(seq));
+            ptx::tma_load_2d(sm + kOffQhi + c * kQChunk, &tm_qlat, hi_bar, 256 + c * 64, q_row0(seq));
+          ptx::tma_load_2d(sm + kOffQhi + 4 * kQChunk, &tm_qrope, hi_bar, 0, q_row0(seq));
           ++nseg;
         } else {
           if (nseg == 0) {
@@ -671,18 +687,17 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           if (kWiden && g == 1 && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
           const int y = pg == lo ? row_of_page(p, page_first) : page_row(p, seq, pg);
           if constexpr (kF8) {
-            const int t = n_f8 % kF8Stages;
-            if (!(ok = ptx::mbar_wait(&bars.f8.empty[t], ((n_f8 / kF8Stages) & 1) ^ 1, abort_flag, p.err))) break;
-            ++n_f8;
-            unsigned char* dst = sm + kOffStage + t * kF8Page;
-            ptx::mbar_arrive_expect_tx(&bars.f8.full[t], kF8Page);
+            if (!(ok = ptx::mbar_wait(ring_empty(n_ring), ((n_ring / kRing) & 1) ^ 1, abort_flag, p.err))) break;
+            unsigned char* dst = sm + ring_off(n_ring);
+            uint64_t* full = ring_full(n_ring++);
+            ptx::mbar_arrive_expect_tx(full, kF8Page);
             if (p.page_box) {
-              ptx::tma_load_3d(dst, &tm_page, &bars.f8.full[t], 0, y, 0);
+              ptx::tma_load_3d(dst, &tm_page, full, 0, y, 0);
             } else {
               for (int c = 0; c < 4; ++c)
-                ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, &bars.f8.full[t], c * 128, y);
+                ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, full, c * 128, y);
             }
-            ptx::tma_load_2d(dst + 4 * kPageChunk, &tm_c4, &bars.f8.full[t], 512, y);
+            ptx::tma_load_2d(dst + 4 * kPageChunk, &tm_c4, full, 512, y);
           } else if constexpr (kFp8) {
             unsigned char* dst = sm + kOffStage + s * kStageBytes + kRawOffset;
             ptx::mbar_arrive_expect_tx(&bars.stage_full[s], 9 * kRawChunk);
@@ -698,18 +713,19 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             // score k-steps reach it, instead of queueing behind this page's score-only part.
             // Own latent chunks 4 half .. 4 half + 3 (value slots 1 and 2 first hold the first
             // sequence's staged Q).
-            const int v = g % kVSlots;
-            if (!(ok = ptx::mbar_wait(&bars.vpart_empty[v], ((g / kVSlots) & 1) ^ 1, abort_flag, p.err))) break;
-            if ((g == 1 || g == 2) && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
-            unsigned char* dst = sm + kOffVPart + v * kVPartBytes;
-            ptx::mbar_arrive_expect_tx(&bars.vpart_full[v], kVPartBytes);
+            const int v = kTree ? n_ring : g;
+            if (!(ok = ptx::mbar_wait(ring_empty(v), ((v / kVSlots) & 1) ^ 1, abort_flag, p.err))) break;
+            if (!kTree && (g == 1 || g == 2) && !(ok = ptx::mbar_wait(&bars.q0_copied, 0, abort_flag, p.err))) break;
+            unsigned char* dst = sm + ring_off(v);
+            uint64_t* full = ring_full(v);
+            ptx::mbar_arrive_expect_tx(full, kVPartBytes);
             if (p.page_box) {
-              ptx::tma_load_3d(dst, &tm_c4, &bars.vpart_full[v], 0, y, 4 * half);
+              ptx::tma_load_3d(dst, &tm_c4, full, 0, y, 4 * half);
             } else {
               for (int c = 0; c < 4; ++c)
-                ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, &bars.vpart_full[v], (4 * half + c) * 64, y);
+                ptx::tma_load_2d(dst + c * kPageChunk, &tm_cache, full, (4 * half + c) * 64, y);
             }
-            ++n_v;
+            ++n_ring;
             // then the score-only chunks (chunk_idx order: half 0 takes 4..8, half 1 0..3 and
             // 8), once the previous page's score k-steps over them are done
             if (!(ok = ptx::mbar_wait(&bars.spart_empty, (g & 1) ^ 1, abort_flag, p.err))) break;
@@ -739,19 +755,16 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           }
         }
       }
-      if (kTree && (kF8 || !ok)) {  // copies that after an abort nobody may wait for land before the CTA leaves
+      if (kTree) {  // copies that after an abort nobody may wait for land before the CTA leaves
+        for (int v = max(0, n_ring - kRing); v < n_ring; ++v) ptx::mbar_wait_drain(ring_full(v), (v / kRing) & 1);
+        if (!kF8 && n_s > 0) ptx::mbar_wait_drain(&bars.spart_full, (n_s - 1) & 1);
+        uint64_t *lo_bar = &bars.q_lo_full, *hi_bar = &bars.q_hi_full;
         if constexpr (kF8) {
-          for (int v = max(0, n_f8 - kF8Stages); v < n_f8; ++v)
-            ptx::mbar_wait_drain(&bars.f8.full[v % kF8Stages], (v / kF8Stages) & 1);
-          if (n_q > 0) ptx::mbar_wait_drain(&bars.f8.q_lo_raw, (n_q - 1) & 1);
-          if (nseg > 0) ptx::mbar_wait_drain(&bars.f8.q_raw, (nseg - 1) & 1);
-        } else {
-          for (int v = max(0, n_v - kVSlots); v < n_v; ++v)
-            ptx::mbar_wait_drain(&bars.vpart_full[v % kVSlots], (v / kVSlots) & 1);
-          if (n_s > 0) ptx::mbar_wait_drain(&bars.spart_full, (n_s - 1) & 1);
-          if (nseg > 0) ptx::mbar_wait_drain(&bars.q_lo_full, (nseg - 1) & 1);
-          if (nseg == 1) ptx::mbar_wait_drain(&bars.q_hi_full, 0);
+          lo_bar = &bars.f8.q_lo_raw;
+          hi_bar = &bars.f8.q_raw;
         }
+        if (n_q > 0) ptx::mbar_wait_drain(lo_bar, (n_q - 1) & 1);
+        if (nseg > 0) ptx::mbar_wait_drain(hi_bar, (nseg - 1) & 1);
       }
     }
    } else if (warp == 1) {
@@ -776,8 +789,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const uint64_t b2 = ptx::sw128_desc(smb + kOffVPart + kVPartBytes, 16, 1024);
       const uint64_t b3 = ptx::sw128_desc(smb + kOffVPart + 2 * kVPartBytes, 16, 1024);
       const uint64_t qd = ptx::sw128_desc(qhi, 16, 1024);
-      // kF8: the ring entry of this segment's page gg (two entries of Q precede a segment's pages)
-      auto f8_entry = [&](int gg) { return gg + 2 * (nseg + 1); };
+      // the ring entry of this segment's page gg (tree: two entries of Q precede a segment's pages)
+      auto entry = [&](int gg) { return kTree ? gg + 2 * (nseg + 1) : gg; };
       // k-step k (a compile-time constant at every call) of S into d, B from chunk base bc
       auto mma_k = [&](uint32_t d, uint64_t bc, int k, bool acc) {
         const uint64_t db = bc + 2 * (k & 3);
@@ -794,9 +807,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kF8) {
           // 18 k-steps of 32 columns, the query's hi term and its lo term
           constexpr uint32_t kIdS8 = ptx::make_idesc(0, kRows, kPage, 0, 0);
-          const uint64_t st = b0 + f8_entry(gg) % kF8Stages * (kF8Page / 16);
-          const uint64_t rp = ptx::smem_desc(smb + kOffStage + f8_entry(gg) % kF8Stages * kF8Page + 4 * kPageChunk, 16,
-                                             512, ptx::kSwz64);
+          const uint64_t st = b0 + entry(gg) % kF8Stages * (kF8Page / 16);
+          const uint64_t rp = ptx::smem_desc(smb + ring_off(entry(gg)) + 4 * kPageChunk, 16, 512, ptx::kSwz64);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // latent 0..255: A from TMEM
             const uint64_t db = st + 512 * (j >> 2) + 2 * (j & 3);
@@ -839,7 +851,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             for (int k = 32; k < 36; ++k) mma_k(d, b0 + 512 * chunk_idx(k >> 2, 1), k, true);
           }
         } else {
-          const int v = gg % kVSlots;
+          const int v = entry(gg) % kVSlots;
           const uint64_t vb = v == 0 ? b1 : v == 1 ? b2 : b3;
           if (half == 0) {
 #pragma unroll
@@ -856,8 +868,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if constexpr (kF8) {
           // two 128-column chunks 8 KB apart, 32 keys per k-step; P'' hi in 16 TMEM columns, lo in 16 more
           constexpr uint32_t kIdPV8 = ptx::make_idesc(0, kRows, 256, 0, 1);
-          const uint64_t vd8 = ptx::sw128_desc(smb + kOffStage + f8_entry(gg) % kF8Stages * kF8Page + 2 * half * kPageChunk,
-                                               kPageChunk, 1024);
+          const uint64_t vd8 = ptx::sw128_desc(smb + ring_off(entry(gg)) + 2 * half * kPageChunk, kPageChunk, 1024);
           const uint32_t pa8 = tmem + 128 + (gg & 1) * 64;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -867,7 +878,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           return;
         }
         if constexpr (kFp8) st = kOffStage + (gg % kStages) * kStageBytes + 4 * half * kPageChunk;
-        else st = kOffVPart + (gg % kVSlots) * kVPartBytes;
+        else st = ring_off(entry(gg));
         const uint64_t vd = ptx::sw128_desc(smb + st, kPageChunk, 1024);
         const uint32_t pa = tmem + 128 + (gg & 1) * 64;
 #pragma unroll
@@ -879,33 +890,30 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         // 0..127 (lane = query row); then latent 256..511 + rope over the staging copy
         if (!(ok = ptx::mbar_wait(&bars.q_lo_full, nseg & 1, abort_flag, p.err))) break;
         ptx::tc_fence_after();
-        // the first sequence's Q latent 0..255 was staged in the second page stage; kF8: every one's
+        // the first sequence's Q latent 0..255 was staged in the second page stage; tree: every one's
         // in two ring entries, which the copies free
-        const int e0 = f8_entry(g) - 2;
+        const int e0 = entry(g) - 2;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const uint32_t qc = kF8 ? smb + kOffStage + (e0 + (k >> 3)) % kF8Stages * kF8Page + ((k >> 2) & 1) * kQChunk
+          const uint32_t qc = kTree ? smb + ring_off(e0 + (k >> 3)) + ((k >> 2) & 1) * kQChunk
                             : nseg == 0 ? smb + q_stage_off(k >> 2) : qhi + (k >> 2) * kQChunk;
           ptx::tmem_cp_128x256b(tmem + k * 8, ptx::sw128_desc(qc + (k & 3) * 32, 16, 1024));
         }
-        if constexpr (kF8) {
-          ptx::mma_commit(&bars.f8.empty[e0 % kF8Stages]);
-          ptx::mma_commit(&bars.f8.empty[(e0 + 1) % kF8Stages]);
+        if constexpr (kTree) {
+          ptx::mma_commit(ring_empty(e0));
+          ptx::mma_commit(ring_empty(e0 + 1));
         } else {
           ptx::mma_commit(&bars.q_cp_done);
           if (nseg == 0) ptx::mma_commit(&bars.q0_copied);
         }
-        if (!kF8 && nseg > 0) {  // the rest of Q over the staging copy (the producer loaded the first)
+        if (!kTree && nseg > 0) {  // the rest of Q over the staging copy (the producer loaded the first)
           if (!(ok = ptx::mbar_wait(&bars.q_cp_done, nseg & 1, abort_flag, p.err))) break;
           ptx::mbar_arrive_expect_tx(&bars.q_hi_full, 5 * TQ * 128);
           for (int c = 0; c < 4; ++c)
             ptx::tma_load_2d(sm + kOffQhi + c * kQChunk, &tm_qlat, &bars.q_hi_full, 256 + c * 64, q_row0(seq));
           ptx::tma_load_2d(sm + kOffQhi + 4 * kQChunk, &tm_qrope, &bars.q_hi_full, 0, q_row0(seq));
         }
-        if (!(ok = ptx::mbar_wait(&bars.q_hi_full, nseg & 1, abort_flag, p.err))) {
-          if (kTree && !kF8) ptx::mbar_wait_drain(&bars.q_hi_full, nseg & 1);  // issued above
-          break;
-        }
+        if (!(ok = ptx::mbar_wait(&bars.q_hi_full, nseg & 1, abort_flag, p.err))) break;
         ptx::tc_fence_after();
         const int g_end = g + (hi - lo), g_first = g;
         const int clean = clean_keys(seq, L);
@@ -928,8 +936,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             ptx::mma_commit(&bars.o_done);
             // fp8: the whole stage; bf16: the value part (the score-only part was released
             // after the scores)
-            if constexpr (kF8) ptx::mma_commit(&bars.f8.empty[f8_entry(gp) % kF8Stages]);
-            else ptx::mma_commit(kFp8 ? &bars.stage_empty[gp % kStages] : &bars.vpart_empty[gp % kVSlots]);
+            ptx::mma_commit(kWiden ? &bars.stage_empty[gp % kStages] : ring_empty(entry(gp)));
             ++gp;
             progress = true;
           }
@@ -951,17 +958,17 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
                   progress = true;
                 }
               } else {
-                can = ptx::mbar_test_wait(&bars.f8.full[f8_entry(gs) % kF8Stages], (f8_entry(gs) / kF8Stages) & 1);
+                can = ptx::mbar_test_wait(ring_full(entry(gs)), (entry(gs) / kRing) & 1);
                 if (can && !whole) ptx::mbar_arrive(&bars.zero_go);
               }
             } else if constexpr (kFp8) {
               can = ptx::mbar_test_wait(&bars.stage_ready[gs % kStages][sp], (gs / kStages) & 1);
             } else if (whole) {
               can = sp == 0 ? ptx::mbar_test_wait(&bars.spart_full, gs & 1)
-                            : ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1);
+                            : ptx::mbar_test_wait(ring_full(entry(gs)), (entry(gs) / kVSlots) & 1);
             } else if (kTree) {
               // prepared from its value part on, which lands about a page ahead of the score-only part
-              if (!zero_asked && ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1)) {
+              if (!zero_asked && ptx::mbar_test_wait(ring_full(entry(gs)), (entry(gs) / kVSlots) & 1)) {
                 ptx::mbar_arrive(&bars.zero_go);
                 zero_asked = progress = true;
               }
@@ -975,7 +982,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
               can = true;  // zeroed before its part 0
             } else if (!zero_asked) {
               if (ptx::mbar_test_wait(&bars.spart_full, gs & 1) &&
-                  ptx::mbar_test_wait(&bars.vpart_full[gs % kVSlots], (gs / kVSlots) & 1)) {
+                  ptx::mbar_test_wait(ring_full(entry(gs)), (entry(gs) / kVSlots) & 1)) {
                 ptx::mbar_arrive(&bars.zero_go);
                 zero_asked = true;
                 progress = true;
