@@ -107,8 +107,10 @@ static_assert(128 * kF8RegsHigh + 256 * kF8RegsLow <= 384 * kF8RegsLaunch, "regi
 // bf16: 8 warps; fp8: 12 (four more preparation warps)
 template <bool kFp8> constexpr int kThreadsOf = kFp8 ? 384 : 256;
 template <bool kFp8> constexpr int kPrepOf = kFp8 ? 192 : 64;
-// a tree's item in at most this many splits is merged by the split that finishes last, from its
-// accumulator and one bulk copy
+// A tree's item in at most this many splits is merged by the split that finishes last, from its
+// accumulator and one bulk copy, if there are more items than half the units.  With fewer the merge
+// kernel is done sooner than that split, whose unit has nothing else to do meanwhile: 6 ragged
+// sequences of up to 1432 keys, 8 x 16 rows, 31 -> 22 us; 160 items of up to 2000 keys, 84 -> 91 us.
 constexpr int kFusedSplits = 2;
 constexpr int kPrefetchAhead = 4;             // pages warmed in L2 ahead of their load
 
@@ -1444,8 +1446,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const int c_first = segs.flat0 / bars.plan.chunk;
       const int nsplit = (segs.flat0 + n_pages - 1) / bars.plan.chunk - c_first + 1;
       const int k_own = unit - c_first;
-      // a tree's item in more splits than that is merged by the kernel behind this one
-      const bool deferred = kTree && nsplit > kFusedSplits;
+      // (a tree's other items are merged by the kernel behind this one)
+      const bool deferred = kTree && nsplit > (2 * p.B * p.NQT > p.G ? kFusedSplits : 1);
       // Merge path.  A split that finds every other split of this (sequence, column half)
       // counted in (always so for a sequence with one split) merges at once, its own share
       // read from the accumulator.  Otherwise it writes its partial (O_half / l, LSE), makes
@@ -1727,7 +1729,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   }
 }
 
-// Merges the tree items that went into more than kFusedSplits splits, all over the GPU: the split
+// Merges the tree items that no split merges (see kFusedSplits), all over the GPU: the split
 // kernel lists them (Params::deferred), the blocks here share the list's slices of 32 rows and 16
 // column quads.  Left to the split that finishes last, the merge reads every partial through one SM,
 // about 4 us a split: one sequence of 1000 keys and 128 rows, in 16 splits, took 68 us, 50 of them

@@ -263,6 +263,17 @@ def test_many_query_tiles_of_one_page(lib, fp8, long):
     lib.check_device_error()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,H,T,L", [(1, 16, 4, 700), (3, 64, 5, 333), (20, 16, 2, 190), (36, 8, 3, 500), (40, 16, 2, 260),
+                                     (58, 16, 2, 224), (76, 8, 2, 70), (77, 8, 2, 70)])
+def test_sequences_of_one_length_on_whole_units(lib, fp8, B, H, T, L):
+    # items cut evenly, uncut, cut anywhere; in two splits merged by either kernel; some a page shorter, some empty
+    for lens in ([L] * B, [L - 64 * (b % 3 == 1) if b % 5 else 0 for b in range(B)]):
+        p = Problem(H, T, lens, fp8, seed=37)
+        p.check(*p.run(lib))
+    lib.check_device_error()
+
+
 def test_bad_page_is_reported(lib):
     p = Problem(4, 3, [100, 100], False, seed=13)
     p.args[3][1, 1] = p.inp.num_pages + 5
