@@ -225,18 +225,21 @@ __device__ __forceinline__ int page_row(const Params& p, int vseq, int pg) {
   return row_of_page(p, page_of(p, vseq, pg));
 }
 
-// Sixteen bf16 (times alpha) as their hi and lo e4m3 terms, 16 bytes each.
+// Sixteen bf16 (times alpha, a power of two) as their hi and lo e4m3 terms, 16 bytes each.  Cut in two
+// rather than hi rounded and the rest taken from its code: two conversions a pair instead of four, 253
+// against 262 us for 32 sequences of 300 keys and 32 x 128 rows.  Values too small for two exact terms
+// come out to 2^-9, 2^-16 of their row's largest.
 __device__ __forceinline__ void split16(const uint4& w0, const uint4& w1, float alpha, uint4& hi, uint4& lo) {
   const uint32_t in[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
   const uint64_t a2 = ptx::f2(alpha, alpha);
-  uint32_t v[8], h[4], l[4];
+  uint32_t h[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t x = ptx::mul2(ptx::f2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), a2);
-    v[i] = ptx::pack_f16x2(ptx::f2_lo(x), ptx::f2_hi(x));
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = ptx::mul2(ptx::f2(__uint_as_float(in[2 * i] << 16), __uint_as_float(in[2 * i] & 0xffff0000u)), a2);
+    const uint64_t y =
+        ptx::mul2(ptx::f2(__uint_as_float(in[2 * i + 1] << 16), __uint_as_float(in[2 * i + 1] & 0xffff0000u)), a2);
+    ptx::cut_e4m3x4(x, y, h[i], l[i]);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) ptx::split_e4m3x4(v[2 * i], v[2 * i + 1], h[i], l[i]);
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }

@@ -513,6 +513,25 @@ __device__ __forceinline__ void split_e4m3x4(uint32_t v01, uint32_t v23, uint32_
       : "r"(v01), "r"(v23));
 }
 
+// Four fp32 values of at most eight significant bits as sums of two e4m3 terms: hi is the value cut
+// to four bits, lo the rest.  A word of hi codes and one of lo codes, first value lowest.
+__device__ __forceinline__ void cut_e4m3x4(uint64_t v01, uint64_t v23, uint32_t& hi, uint32_t& lo) {
+  constexpr uint64_t kCut = 0xfff00000fff00000ull;
+  const uint64_t h01 = v01 & kCut, h23 = v23 & kCut, l01 = sub2(v01, h01), l23 = sub2(v23, h23);
+  auto codes = [](uint64_t a, uint64_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(f2_lo(a)), "f"(f2_hi(a)), "f"(f2_lo(b)), "f"(f2_hi(b)));
+    return r;
+  };
+  hi = codes(h01, h23);
+  lo = codes(l01, l23);
+}
+
 // max of three (one instruction)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
