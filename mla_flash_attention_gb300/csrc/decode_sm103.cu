@@ -108,7 +108,7 @@ static_assert(128 * kF8RegsHigh + 256 * kF8RegsLow <= 384 * kF8RegsLaunch, "regi
 template <bool kFp8> constexpr int kThreadsOf = kFp8 ? 384 : 256;
 template <bool kFp8> constexpr int kPrepOf = kFp8 ? 192 : 64;
 // A tree's item in at most this many splits is merged by the split that finishes last, from its
-// accumulator and one bulk copy, if there are more items than half the units.  With fewer the merge
+// accumulator and one bulk copy, if there are more items than half the units.  With fewer (few) the merge
 // kernel is done sooner than that split, whose unit has nothing else to do meanwhile: 6 ragged
 // sequences of up to 1432 keys, 8 x 16 rows, 31 -> 22 us; 160 items of up to 2000 keys, 84 -> 91 us.
 constexpr int kFusedSplits = 2;
@@ -127,6 +127,10 @@ struct Params {
   // {item, first unit, splits} of each, at most one a unit.  They lie in the last of the n_slots
   // slots of part_o, which no split uses (unit c and item v share slot c + v <= G - 1 + B * NQT - 1).
   int4* deferred;
+  // tree: at most half as many items as units.  Every item in several splits is left to the merge
+  // kernel, and entry 1 + v is item v's, whatever its splits (0: no keys), so that nothing has to be
+  // zeroed before this launch; the split kernel is then itself the one that waits for the work ahead.
+  int few;
   int* counters;     // [B * NQT][2]: finished splits per (virtual sequence, half), zeroed per call
   uint16_t* out;     // [B, T, H, 512] bf16
   float* lse;        // [B, H, T]
@@ -353,6 +357,7 @@ __device__ __forceinline__ void empty_items(const Params& p, int unit, int half,
     for (int i = w; i < rows; i += 2)
       if (MLA_STORE_OK(o + i * (kDl / 8), p.out, p.out_bytes, p.err)) o[i * (kDl / 8)] = make_uint4(0, 0, 0, 0);
     if (half) continue;
+    if (p.few && threadIdx.x == 64) p.deferred[1 + v] = make_int4(v, 0, 0, 0);
     for (int i = row0 + w * 32 + lane; i < row0 + rows; i += 64) {
       float* lp = p.lse + ((size_t)b * p.H + i % p.H) * p.T + i / p.H;
       if (MLA_STORE_OK(lp, p.lse, p.lse_bytes, p.err)) *lp = -INFINITY;
@@ -594,6 +599,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     ptx::mbar_init(&bars.merge_full, 1);
     ptx::fence_barrier_init();
   }
+  if (kTree && p.few) wait_for_stream();
   // the plan's length loads go out first; the other warps set up meanwhile
   if (warp == 3) make_plan<kTree>(p, unit, &bars.plan);
   // Q rows T*H..127 are never loaded: keep them zero (finite scores in the padded rows)
@@ -1450,7 +1456,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       const int nsplit = (segs.flat0 + n_pages - 1) / bars.plan.chunk - c_first + 1;
       const int k_own = unit - c_first;
       // (a tree's other items are merged by the kernel behind this one)
-      const bool deferred = kTree && nsplit > (2 * p.B * p.NQT > p.G ? kFusedSplits : 1);
+      const bool deferred = kTree && nsplit > (p.few ? 1 : kFusedSplits);
+      if (kTree && p.few && half == 0 && k_own == 0 && r == 0) p.deferred[1 + seq] = make_int4(seq, c_first, nsplit, 0);
       // Merge path.  A split that finds every other split of this (sequence, column half)
       // counted in (always so for a sequence with one split) merges at once, its own share
       // read from the accumulator.  Otherwise it writes its partial (O_half / l, LSE), makes
@@ -1467,7 +1474,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         int fast = 1, bulk = 0;
         if (deferred) {
           fast = 0;
-          if (half == 0 && k_own == 1) {
+          if (!p.few && half == 0 && k_own == 1) {
             asm volatile("griddepcontrol.wait;" ::: "memory");  // zeroed before
             p.deferred[1 + atomicAdd(&p.deferred[0].x, 1)] = make_int4(seq, c_first, nsplit, 0);
           }
@@ -1808,10 +1815,12 @@ __device__ __forceinline__ void merge_row(const Params& p, int item, int c_first
 __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_stream();  // the split kernel is done
-  const int work = __ldcg(&p.deferred[0].x) * kMergeSlices;
+  const int work = (p.few ? p.B * p.NQT : __ldcg(&p.deferred[0].x)) * kMergeSlices;
   for (int w = blockIdx.x; w < work; w += gridDim.x) {
     const int4 d = __ldcg(reinterpret_cast<const int4*>(p.deferred + 1) + w / kMergeSlices);
     const int item = d.x, c_first = d.y, nsplit = d.z, slice = w % kMergeSlices;
+    // (an entry that a split kernel that gave up left unwritten may hold anything)
+    if (p.few && (item != w / kMergeSlices || nsplit < 2 || nsplit > p.G || c_first < 0 || c_first > p.G - nsplit)) continue;
     const int r = (slice & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
     if (r >= p.TQ || gr >= p.T * p.H) continue;
     const int q = (slice >> 2) * kMergeQuads + 2 * warp;
@@ -1944,6 +1953,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
   p.mask_words = (T + 31) / 32;
   p.new_lens = new_lens;
   p.deferred = reinterpret_cast<int4*>(part_o + (size_t)(p.n_slots - 1) * TQ * kDl);
+  p.few = tree_mask && 2 * B * p.NQT <= G && B * p.NQT < 2048 / 16;  // the entries fit any slot
   p.page_box = page_box ? 1 : 0;
   // one flat page charged per work item (its Q load, epilogue and merge; measured against
   // 0, 2 and 4 on uniform and ragged batches: the same time for 64 sequences of 4096 keys,
@@ -1969,7 +1979,9 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     __atomic_store_n(&carveout_set, 1, __ATOMIC_RELEASE);
   }
   const int zero_blocks = (int)std::min<long long>((n_cnt + 2047) / 2048, 1024);
-  if (tree_mask) {
+  if (p.few) {
+    // no counter is used
+  } else if (tree_mask) {
     if ((e = launch_dependent(zero_counters_kernel, zero_blocks, 256, stream, counters, (int)n_cnt, p.deferred)) != cudaSuccess)
       return e;
   } else {
@@ -1982,7 +1994,7 @@ cudaError_t launch_decode_sm103(const void* q_latent, const void* q_rope, const 
     const cudaError_t e2 = smem_attr_once(kern, smem, &smem_set[(fp8 ? 1 : 0) + (tree_mask ? 2 : 0)]);
     if (e2 != cudaSuccess) return e2;
     // programmatic dependent of the zeroing kernel: the prologue (barriers, TMEM, plan, first
-    // loads) overlaps it
+    // loads) overlaps it (Params::few: of the work ahead)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * G);
     cfg.blockDim = dim3(fp8 ? kThreadsOf<true> : kThreadsOf<false>);
