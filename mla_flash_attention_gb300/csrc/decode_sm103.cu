@@ -42,9 +42,9 @@
 // own stage, released by its PV product.  Warps 8-11 make the query terms.  64 ragged
 // sequences of up to 16384 keys, 1 to 13 tokens of 16 heads: 613 us with the pages widened to bf16, 433
 // with e4m3 operands (an item's query terms then took 20 us), 344 with the terms made in place from
-// TMA loads and items charged in the split plan, 255 with tiles of padding left out, 248 with the ends of
-// items shortened.  A page takes 1.3 us, 2,500 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key half each, were no faster,
-// nor was splitting into terms with integer instructions.)
+// TMA loads and items charged in the split plan, 255 with tiles of padding left out, 250 with the ends of
+// items shortened.  A page takes 1.3 us, 2,500 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key
+// half each, were no faster, nor was splitting into terms with integer instructions.)
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
 #include <cuda.h>
@@ -1349,7 +1349,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         if (pg == lo) {
           m_use = mx;
         } else {
-          const bool grow = mx > m + (8.0f - kTop);
+          // (a tree's rows past the last token hold whatever lay in the ring: they ask for nothing)
+          const bool grow = (!kTree || (r < TQ && gr < TH)) && mx > m + (8.0f - kTop);
           if (__any_sync(0xffffffffu, grow)) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.o_done, (g - 1) & 1, abort_flag, p.err));
             if (!ok) break;
