@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
   constexpr bool kWiden = kFp8 && !kTree;   // e4m3 pages widened to bf16
   if (kF8 && sm != smem_raw) {  // allocated without the slack of the others (never taken: it is 1024-aligned)
     if (threadIdx.x == 0) latch_error(p.err, kErrBounds);
+    wait_for_stream();  // (as at the end)
     return;
   }
   constexpr int kThreads = kThreadsOf<kFp8>;
@@ -1732,6 +1733,9 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
     // after an abort: a bulk copy issued but never waited for lands before the CTA exits
     if (r == 0 && n_bulk_issued > n_bulk) ptx::mbar_wait_drain(&bars.merge_full, n_bulk & 1);
   }
+  // Kernels behind this one may be its programmatic dependents, which wait for this one alone: it ends
+  // after the zeroing kernel has, also where no item was split and so nobody waited for that above.
+  if (threadIdx.x == 0) wait_for_stream();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 2) {
@@ -1815,13 +1819,15 @@ __device__ __forceinline__ void merge_row(const Params& p, int item, int c_first
 
 __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_for_stream();  // the split kernel is done
-  const int work = (p.few ? p.B * p.NQT : __ldcg(&p.deferred[0].x)) * kMergeSlices;
+  wait_for_stream();  // the split kernel is done, and with it the zeroing
+  const int listed = p.few ? p.B * p.NQT : min(__ldcg(&p.deferred[0].x), p.G);
+  const int work = listed * kMergeSlices;
   for (int w = blockIdx.x; w < work; w += gridDim.x) {
     const int4 d = __ldcg(reinterpret_cast<const int4*>(p.deferred + 1) + w / kMergeSlices);
     const int item = d.x, c_first = d.y, nsplit = d.z, slice = w % kMergeSlices;
     // (an entry that a split kernel that gave up left unwritten may hold anything)
-    if (p.few && (item != w / kMergeSlices || nsplit < 2 || nsplit > p.G || c_first < 0 || c_first > p.G - nsplit)) continue;
+    if (nsplit < 2 || nsplit > p.G || c_first < 0 || c_first > p.G - nsplit) continue;
+    if (item < 0 || item >= p.B * p.NQT || (p.few && item != w / kMergeSlices)) continue;
     const int r = (slice & 3) * kMergeRows + lane, gr = (item % p.NQT) * kRows + r;
     if (r >= p.TQ || gr >= p.T * p.H) continue;
     const int q = (slice >> 2) * kMergeQuads + 2 * warp;

@@ -940,6 +940,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  // kernels behind this one may be its programmatic dependents, which wait for this one alone: it
+  // ends after the zeroing kernel has, also where no sequence was split and nobody waited for that
+  if (threadIdx.x == 0) wait_for_stream();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
