@@ -35,15 +35,17 @@
 // value would reach rows that do not see the key) and flag their keys, so that the rows that see
 // them, and no others, come out as NaN.  They also write the rows of items without keys.
 // The tree over an fp8 cache (kF8) widens nothing: the e4m3 page is the MMA's operand as it lies.
-// Its other operands are sums of two e4m3 terms: a bf16 query, scaled by a power of two into
-// [128, 256) at its row's largest value, is hi + lo exactly (8 significant bits, 4 + 4) down to 2^-10
-// of that value, and a weight P'' = p ks is hi + lo to 2^-8.  Twice the k-steps at twice the rate: the
-// tensor work is bf16's, pages take half the bytes, and four fit instead of two; each page is its
+// Its other operands are sums of two 8-bit terms: a bf16 query, scaled by a power of two into
+// [128, 256) at its row's largest value, is two e4m3 terms exactly (8 significant bits, 4 + 4) down to 2^-10
+// of that value (2^-17 of it is lost at most); a weight P'' = p ks is hi (e4m3) + lo (e5m2) to 2^-8 of
+// itself, as a bf16 weight is (and see kF8StepsPerMass for small weights).  Twice the k-steps at twice the
+// rate: the tensor work is bf16's, pages take half the bytes, and four fit instead of two; each page is its
 // own stage, released by its PV product.  Warps 8-11 make the query terms.  64 ragged
 // sequences of up to 16384 keys, 1 to 13 tokens of 16 heads: 613 us with the pages widened to bf16, 433
 // with e4m3 operands (an item's query terms then took 20 us), 344 with the terms made in place from
 // TMA loads and items charged in the split plan, 255 with tiles of padding left out, 250 with the ends of
-// items shortened.  A page takes 1.3 us, 2,500 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key
+// items shortened, 255 with the range of the weights above (two e4m3 terms before, which lost small
+// weights).  A page takes 1.3 us, 2,500 clocks for 2,240 of MMAs.  (Two softmax warpgroups, a key
 // half each, were no faster, nor was splitting into terms with integer instructions.)
 // TMEM columns: [0,128) Q latent 0..255 (bf16 pairs), [128,256) two S / P buffers of 64,
 // [256,512) O half.
@@ -247,6 +249,21 @@ __device__ __forceinline__ void split16(const uint4& w0, const uint4& w1, float 
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
+
+// Two terms hold a weight P'' to 2^-8 of itself down to 2^-6, and to 2^-14 below (split_e4m3_e5m2x4): the 64
+// keys of a page lose at most 2^-8 more, and at most 2^-3 of 64 times the page's largest P''.  That is
+// nothing beside a largest weight of 2^5, but thousands of keys far below a dominating one would lose
+// much of what they hold together.  So each row counts its pages by what they may lose (f8_steps, in
+// units of 2^-8) and sums the pages' largest weights (f8_mass, in units of 2^5), both relative to its
+// reference m.  Once there are more than kF8StepsPerMass of the one to the other, m falls to kF8FallTo above the
+// maximum of the next page that lies low (the accumulator, in fp32, is scaled up), and the count starts
+// again: between two falls at most 2^-9 of the sum of the pages' largest weights is lost.  m falls by 16
+// bits at most at a time, and then only a mass as much larger lets it fall again, so O stays below
+// 2^90; and it does not fall where the sum of p = P'' / ks is huge because the key scales are tiny.
+// A fall costs what a rise does, about a third of a page.  With kF8FallTo of 4 the scores of normal
+// queries and keys cause none (64 ragged sequences of up to 16384 keys 255 us, as without falls; 261 us with 0, as
+// many rises follow), with scores of four times the spread 280 us instead of 265.
+constexpr float kF8StepsPerMass = 16.f, kF8FallTo = 4.f;
 
 constexpr int kQNonFinite = 127;  // q_exp of a row with a NaN or an infinity: all its terms are NaN
 
@@ -878,14 +895,16 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       auto issue_pv = [&](int gg, bool first) {
         uint32_t st;
         if constexpr (kF8) {
-          // two 128-column chunks 8 KB apart, 32 keys per k-step; P'' hi in 16 TMEM columns, lo in 16 more
+          // two 128-column chunks 8 KB apart, 32 keys per k-step; P'' hi (e4m3) in 16 TMEM columns, lo
+          // (e5m2) in 16 more
           constexpr uint32_t kIdPV8 = ptx::make_idesc(0, kRows, 256, 0, 1);
+          constexpr uint32_t kIdPV8Lo = ptx::make_idesc2(1, 0, kRows, 256, 0, 1);
           const uint64_t vd8 = ptx::sw128_desc(smb + ring_off(entry(gg)) + 2 * half * kPageChunk, kPageChunk, 1024);
           const uint32_t pa8 = tmem + 128 + (gg & 1) * 64;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             ptx::mma_f8_ts(o_tm, pa8 + k * 8, vd8 + 256 * k, kIdPV8, (!first || k > 0) ? 1u : 0u);
-            ptx::mma_f8_ts(o_tm, pa8 + 16 + k * 8, vd8 + 256 * k, kIdPV8, 1u);
+            ptx::mma_f8_ts(o_tm, pa8 + 16 + k * 8, vd8 + 256 * k, kIdPV8Lo, 1u);
           }
           return;
         }
@@ -1209,6 +1228,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
       // kF8: each lane has the scales of keys 2 lane and 2 lane + 1 of the next page on their way, and
       // the page-table entry of the one after
       float f8_scale = 0.f;  // softmax scale in the exponent over the row's power of two
+      float f8_mass = 0.f, f8_steps = 0.f;  // see kF8StepsPerMass
       int tab[2] = {-1, -1};
       float2 ks_next = make_float2(0.f, 0.f);
       auto entry = [&](int pg) {
@@ -1329,8 +1349,8 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
             s2[x] = ptx::f2(key0 + 2 * x <= lim ? ptx::f2_lo(s2[x]) : -INFINITY,
                             key0 + 2 * x + 1 <= lim ? ptx::f2_hi(s2[x]) : -INFINITY);
         }
-        // kF8: the weights P'' = p ks are what has to fit e4m3, so the maximum is that of their exponents,
-        // and it is mapped to 2^5: they lie in (0, 2^8], their lo terms' steps 2^-15 of the row's largest
+        // kF8: the weights P'' = p ks are what has to fit the two terms, so the maximum is that of their
+        // exponents, and it is mapped to 2^5: they lie in (0, 2^8]
         auto exponents = [&](int x) {
           if constexpr (kF8) return ptx::add2(s2[x], *reinterpret_cast<const uint64_t*>(&bars.f8.lk[warp - 4][2 * x]));
           else return s2[x];
@@ -1349,15 +1369,24 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         float m_use = m;
         if (pg == lo) {
           m_use = mx;
+          if constexpr (kF8) f8_mass = f8_steps = 0.f;
         } else {
           // (a tree's rows past the last token hold whatever lay in the ring: they ask for nothing)
-          const bool grow = (!kTree || (r < TQ && gr < TH)) && mx > m + (8.0f - kTop);
-          if (__any_sync(0xffffffffu, grow)) {
+          const bool asks = !kTree || (r < TQ && gr < TH);
+          const bool grow = asks && mx > m + (8.0f - kTop);
+          const bool fall = kF8 && asks && mx < m - (kF8FallTo + 3.f) && mx > m - 20.f && l < 0x1p80f &&
+                            f8_steps > kF8StepsPerMass * f8_mass;
+          if (__any_sync(0xffffffffu, grow || fall)) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.o_done, (g - 1) & 1, abort_flag, p.err));
             if (!ok) break;
             ptx::tc_fence_after();
-            const float alpha = grow ? ptx::ex2(m - mx) : 1.f;  // m = -inf gives 0
             if (grow) m_use = mx;
+            if (fall) m_use = mx + kF8FallTo;
+            const float alpha = grow || fall ? ptx::ex2(m - m_use) : 1.f;  // m = -inf gives 0
+            if constexpr (kF8) {
+              f8_mass *= alpha;
+              f8_steps = fall ? 0.f : f8_steps * alpha;
+            }
             uint32_t v[2][32];
 #pragma unroll 1
             for (int c = 0; c < 8; c += 2) {
@@ -1394,7 +1423,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
               const uint64_t ab = ptx::mul2(pp, *reinterpret_cast<const uint64_t*>(ks + 2 * (x + y)));
               w16[y] = ptx::pack_f16x2(ptx::f2_lo(ab), ptx::f2_hi(ab));
             }
-            ptx::split_e4m3x4(w16[0], w16[1], pk[x / 2], pk[16 + x / 2]);
+            ptx::split_e4m3_e5m2x4(w16[0], w16[1], pk[x / 2], pk[16 + x / 2]);
           }
         }
 #pragma unroll
@@ -1422,6 +1451,11 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&bars.p_full[g & 1]);
+        if constexpr (kF8) {
+          const float w = mx == -INFINITY ? 0.f : ptx::ex2(mx - m);
+          f8_mass += w;
+          f8_steps += fminf(1.f, 65536.f * w);
+        }
       }
       if (!ok) break;
       // epilogue of the segment: partial (O_half / l, LSE) into slot unit + seq, once the

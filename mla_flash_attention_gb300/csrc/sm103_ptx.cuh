@@ -263,14 +263,17 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
 }
 
 // Instruction descriptor for dense MMAs with fp32 accumulation.
-//   ab_fmt: kind::f16 -> 0 f16, 1 bf16; kind::f8f6f4 -> 0 e4m3, 1 e5m2.
+//   a_fmt, b_fmt: kind::f16 -> 0 f16, 1 bf16, the same for both; kind::f8f6f4 -> 0 e4m3, 1 e5m2.
 //   a_mn / b_mn: 1 when the operand is stored MN-major (M or N contiguous).
-__host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_fmt, int M, int N, uint32_t a_mn,
-                                                  uint32_t b_mn) {
+__host__ __device__ constexpr uint32_t make_idesc2(uint32_t a_fmt, uint32_t b_fmt, int M, int N, uint32_t a_mn,
+                                                   uint32_t b_mn) {
   return (1u << 4)                       // D format: f32
-         | (ab_fmt << 7) | (ab_fmt << 10)  // A, B formats
+         | (a_fmt << 7) | (b_fmt << 10)
          | (a_mn << 15) | (b_mn << 16)     // major-ness
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_fmt, int M, int N, uint32_t a_mn, uint32_t b_mn) {
+  return make_idesc2(ab_fmt, ab_fmt, M, N, a_mn, b_mn);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]
@@ -494,10 +497,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Four f16 values as sums of two e4m3 terms: hi = e4m3(v), lo = e4m3(v - hi), the difference exact in
-// f16.  A word of hi codes and one of lo codes, first value lowest.  v within +-448; a NaN gives NaN
-// codes.
-__device__ __forceinline__ void split_e4m3x4(uint32_t v01, uint32_t v23, uint32_t& hi, uint32_t& lo) {
+// Four f16 values as sums of an e4m3 and an e5m2 term: hi = e4m3(v), lo = e5m2(v - hi), the difference
+// exact in f16.  A word of hi codes and one of lo codes, first value lowest.  v within +-448; a NaN
+// gives NaN codes.  hi + lo is v to 2^-8 of itself down to 2^-6 (hi's half step is 2^-4 of v at most,
+// and lo has three bits of that), then to 2^-14, and below 2^-14 to half of e5m2's least step, 2^-17.
+__device__ __forceinline__ void split_e4m3_e5m2x4(uint32_t v01, uint32_t v23, uint32_t& hi, uint32_t& lo) {
   asm("{\n\t.reg .b16 a, b, c, d;\n\t.reg .b32 x, y;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 b, %3;\n\t"
@@ -505,8 +509,8 @@ __device__ __forceinline__ void split_e4m3x4(uint32_t v01, uint32_t v23, uint32_
       "cvt.rn.f16x2.e4m3x2 y, b;\n\t"
       "sub.rn.f16x2 x, %2, x;\n\t"
       "sub.rn.f16x2 y, %3, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 c, x;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 d, y;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 c, x;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 d, y;\n\t"
       "mov.b32 %0, {a, b};\n\t"
       "mov.b32 %1, {c, d};\n\t}"
       : "=&r"(hi), "=r"(lo)
