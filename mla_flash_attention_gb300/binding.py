@@ -428,23 +428,24 @@ def tree_mask_from_parents(parents):
     the last accepted token.  Returns (mask int32 [..., q_len, ceil(q_len / 32)] with the bits of
     every token's ancestors and itself, depth int32 [..., q_len], 0 for a child of the last
     accepted token).  Reads ``parents`` on the host."""
-    par = torch.as_tensor(parents)
+    par = parents if isinstance(parents, torch.Tensor) else torch.as_tensor(parents)
     if par.dim() not in (1, 2) or par.shape[-1] == 0 or par.dtype.is_floating_point or par.dtype == torch.bool:
         raise ValueError("parents must be integers of shape [q_len] or [B, q_len]")
     dev, par = par.device, par.cpu().to(torch.int64)
-    T = par.shape[-1]
-    if bool(((par >= torch.arange(T)) | (par < -1)).any()):
-        raise ValueError("a parent must be -1 or the index of an earlier token")
-    sees = torch.zeros(*par.shape, T + 1)  # column T stands for the last accepted token
-    sees.scatter_(-1, torch.where(par < 0, T, par)[..., None], 1.0)
-    sees = sees[..., :T] + torch.eye(T)
-    for _ in range(max(1, T.bit_length())):  # ancestors up to 2, 4, 8, ... generations back
-        sees = ((sees @ sees) > 0).float()
-    W = (T + 31) // 32
-    bits = torch.zeros(*par.shape, W * 32, dtype=torch.int64)
-    bits[..., :T] = sees.to(torch.int64)
-    words = (bits.unflatten(-1, (W, 32)) << torch.arange(32)).sum(-1)
-    words = torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
+    with torch.device("cpu"):  # whatever the program's default device
+        T = par.shape[-1]
+        if bool(((par >= torch.arange(T)) | (par < -1)).any()):
+            raise ValueError("a parent must be -1 or the index of an earlier token")
+        sees = torch.zeros(*par.shape, T + 1)  # column T stands for the last accepted token
+        sees.scatter_(-1, torch.where(par < 0, T, par)[..., None], 1.0)
+        sees = sees[..., :T] + torch.eye(T)
+        for _ in range(max(1, T.bit_length())):  # ancestors up to 2, 4, 8, ... generations back
+            sees = ((sees @ sees) > 0).float()
+        W = (T + 31) // 32
+        bits = torch.zeros(*par.shape, W * 32, dtype=torch.int64)
+        bits[..., :T] = sees.to(torch.int64)
+        words = (bits.unflatten(-1, (W, 32)) << torch.arange(32)).sum(-1)
+        words = torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
     return words.to(dev), (sees.sum(-1).to(torch.int32) - 1).to(dev)
 
 
