@@ -1,10 +1,12 @@
-"""Thin ctypes binding of the C ABI (include/mla.h).
+"""Thin binding of the C ABI (include/mla.h).
 
 Argument marshalling only: torch tensors are checked for device, dtype, shape and
 contiguity, then their device pointers and the current CUDA stream are passed to
-the library.  Every step of the attention runs inside the library's CUDA kernels;
-there is no fallback of any kind: if the shared library is missing, importing this
-module raises.
+the library, through ctypes or, for the calls around the attention (norms, rotated
+append, drafted trees), through the compiled module ``_marshal``.  Every step of the
+attention runs inside the library's CUDA kernels; there is no fallback of any kind:
+if the shared library is missing, importing this module raises, and if ``_marshal``
+is missing or does not fit the installed torch, the calls that it marshals raise.
 """
 from __future__ import annotations
 
@@ -15,11 +17,23 @@ from typing import Optional
 
 import torch
 
+
+
+class _NoMarshal:
+    """Stands in for ``_marshal`` where that does not load: the calls it marshals raise."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the marshalling module is not built (%s); run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`" % self._why)
+
+
 try:
     from . import _marshal
 except ImportError as e:
-    raise ImportError("the marshalling module is not built (%s); run "
-                      "`python -c 'import __graft_entry__ as g; g.build()'`" % e) from e
+    _marshal = _NoMarshal(e)
 
 # MLA_GB300_LIB selects another build of the same library, e.g. the bounds-checked
 # libmla_gb300_debug.so (mla_flash_attention_gb300.build.build(debug=True))
@@ -394,9 +408,10 @@ def _address(f) -> int:
     return ctypes.cast(f, ctypes.c_void_p).value
 
 
-_marshal.connect(_address(_lib.mla_qk_norm_rope), _address(_lib.mla_qk_norm_rope_backward),
-                 _address(_lib.mla_qk_norm_rope_backward_workspace_size), _address(_lib.mla_rope_append),
-                 _address(_lib.mla_decode_tree), _address(_lib.mla_decode_workspace_size), _check)
+if not isinstance(_marshal, _NoMarshal):
+    _marshal.connect(_address(_lib.mla_qk_norm_rope), _address(_lib.mla_qk_norm_rope_backward),
+                     _address(_lib.mla_qk_norm_rope_backward_workspace_size), _address(_lib.mla_rope_append),
+                     _address(_lib.mla_decode_tree), _address(_lib.mla_decode_workspace_size), _check)
 
 
 def _call(stream, tensor, f, *args):
