@@ -12,7 +12,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <array>
+#include <limits>
 #include <optional>
 #include <string>
 #include <vector>
@@ -105,6 +107,9 @@ int64_t row_stride(const Tensor& t, const char* name) {
 Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, const at::Device& dev) {
   return at::detail::empty_cuda(shape, dtype, dev, std::nullopt);
 }
+
+// A size as the C entry points take it.  One past an int's range is one that they refuse, not its low bits.
+int size_arg(int64_t v) { return static_cast<int>(std::min<int64_t>(v, std::numeric_limits<int>::max())); }
 
 void* stream_of(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
@@ -231,8 +236,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check(unlocked([&] {
     return f_norm(ptr(o.q), o.q_row, o.q_head, ptr(o.kn), o.kn_row, o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]),
                   ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]), static_cast<const int*>(ptr(o.pos)), ptr(o.turns), eps, il,
-                  ptr(out[0]), ptr(out[1]), ptr(out[2]), ptr(out[3]), o.B * o.S, static_cast<int>(o.H),
-                  static_cast<int>(o.dn), static_cast<int>(o.dr), st);
+                  ptr(out[0]), ptr(out[1]), ptr(out[2]), ptr(out[3]), o.B * o.S, size_arg(o.H),
+                  size_arg(o.dn), size_arg(o.dr), st);
   }));
   return wrap_all(out, 4);
   END_HANDLE_TH_ERRORS
@@ -279,7 +284,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor ws = optional(a[16], "workspace");
   if (ws.defined()) scratch(ws, o.dev);
   else if (weights)
-    ws = empty({std::max<int64_t>(static_cast<int64_t>(f_grad_ws(o.B * o.S, static_cast<int>(o.H))), 16)}, at::kByte, o.dev);
+    ws = empty({std::max<int64_t>(static_cast<int64_t>(f_grad_ws(o.B * o.S, size_arg(o.H))), 16)}, at::kByte, o.dev);
   const size_t ws_bytes = ws.defined() ? ws.nbytes() : 0;
   const float eps = static_cast<float>(number(a[9]));
   const int il = truth(a[10]);
@@ -289,8 +294,8 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return f_grad(ptr(up[0]), ptr(up[1]), ptr(up[2]), f32(up[3]), ptr(o.q), o.q_row, o.q_head, ptr(o.kn), o.kn_row,
                   o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]), ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]),
                   static_cast<const int*>(ptr(o.pos)), ptr(o.turns), eps, il, ptr(g[0]), ptr(g[1]), ptr(g[2]),
-                  f32(g[3]), f32(g[4]), f32(g[5]), f32(g[6]), o.B * o.S, static_cast<int>(o.H),
-                  static_cast<int>(o.dn), static_cast<int>(o.dr), ptr(ws), ws_bytes, st);
+                  f32(g[3]), f32(g[4]), f32(g[5]), f32(g[6]), o.B * o.S, size_arg(o.H),
+                  size_arg(o.dn), size_arg(o.dr), ptr(ws), ws_bytes, st);
   }));
   return wrap_all(g, 7);
   END_HANDLE_TH_ERRORS
@@ -351,9 +356,9 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* st = stream_of(dev);
   check(unlocked([&] {
     return f_append(ptr(c), stride, ptr(w), eps, ints(pos), ptr(turns), il, ptr(k.kv), static_cast<float*>(ptr(k.scale)),
-                    ints(k.table), ints(k.lens), ints(k.fresh), static_cast<int>(B), static_cast<int>(T),
-                    static_cast<int>(D - dr), static_cast<int>(dr), static_cast<int>(k.page_size),
-                    static_cast<int>(k.max_pages), static_cast<int>(k.pages), k.type(), st);
+                    ints(k.table), ints(k.lens), ints(k.fresh), size_arg(B), size_arg(T),
+                    size_arg(D - dr), size_arg(dr), size_arg(k.page_size),
+                    size_arg(k.max_pages), size_arg(k.pages), k.type(), st);
   }));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
@@ -383,16 +388,16 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   else lse = empty({B, H, T}, at::kFloat, dev);
   if (ws.defined()) scratch(ws, dev);
   else
-    ws = empty({std::max<int64_t>(static_cast<int64_t>(f_tree_ws(static_cast<int>(B), static_cast<int>(H),
-                                                                 static_cast<int>(T), static_cast<int>(dl))), 16)},
+    ws = empty({std::max<int64_t>(static_cast<int64_t>(f_tree_ws(size_arg(B), size_arg(H),
+                                                                 size_arg(T), size_arg(dl))), 16)},
                at::kByte, dev);
   void* st = stream_of(dev);
   check(unlocked([&] {
     return f_tree(ptr(ql), ptr(qr), ptr(k.kv), static_cast<const float*>(ptr(k.scale)), ints(k.table), ints(k.lens),
                   ptr(mask), shared ? 0 : T * words, ints(k.fresh), ptr(out), static_cast<float*>(ptr(lse)),
-                  static_cast<int>(B), static_cast<int>(H), static_cast<int>(T), static_cast<int>(dl),
-                  static_cast<int>(dr), static_cast<int>(k.page_size), static_cast<int>(k.max_pages),
-                  static_cast<int>(k.pages), scale, k.type(), ptr(ws), ws.nbytes(), st);
+                  size_arg(B), size_arg(H), size_arg(T), size_arg(dl),
+                  size_arg(dr), size_arg(k.page_size), size_arg(k.max_pages),
+                  size_arg(k.pages), scale, k.type(), ptr(ws), ws.nbytes(), st);
   }));
   const Tensor res[2] = {out, lse};
   return wrap_all(res, 2);
