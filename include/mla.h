@@ -242,9 +242,10 @@ mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm
  * Token t < n_b sees every key of the prefix, 0 .. L_b - n_b - 1, and the drafted keys its bits
  * name.  A row that sees no key gets O = 0 and LSE = -inf.  A drafted key whose cached row (or
  * scale) is not finite makes the rows that see it NaN and leaves the others alone.
- * Precision: softmax weights enter the product with V with eight significant bits, as in mla_decode,
- * and what rounds away of weights far below a row's largest stays below 2^-8 of the row's sum.  Over
- * an e4m3 cache, query values below 2^-10 of their row's largest are rounded to steps of 2^-17 of it.
+ * Precision: softmax weights enter the product with V with eight significant bits.  Over an e4m3
+ * cache those far below a row's largest have fewer, so that what they lose together stays about 2^-8
+ * of the row's sum at most, and query values below 2^-10 of their row's largest are rounded to steps
+ * of 2^-17 of it.
  * Everything else -- layouts, cache types, lengths, bad pages, out, lse, the workspace
  * (mla_decode_workspace_size; calls that overlap on the GPU need one each) and the limits -- is as
  * for mla_decode, with num_pages * page_size and B * q_len * H below 2^31.

@@ -470,8 +470,8 @@ def mla_qk_norm_rope(q=None, k_nope=None, k_rope=None, *, positions, rope_turns,
     """RMS norms of queries and keys for each head, with the position rotation in the same pass
     (before mla_prefill; queries alone before mla_absorb and the decode calls).
 
-    q [B,S,H,dn+dr], k_nope [B,S,H,dn], k_rope [B,S,dr] bf16, strided views with a contiguous
-    last dimension allowed, each optional; weights bf16 (None: that part is not normalised);
+    q [B,S,H,dn+dr], k_nope [B,S,H,dn], k_rope [B,S,dr] bf16, each optional, strided views allowed
+    whose last dimension is contiguous and whose B and S dimensions have one stride; weights bf16 (None: that part is not normalised);
     positions [B,S] int32; rope_turns from ``rope_turns()``.  Returns (q_nope [B,S,H,dn],
     q_rope [B,S,H,dr], k_nope, k_rope), contiguous bf16, None for operands not given; ``out``
     may pass those four preallocated."""
@@ -502,8 +502,8 @@ def mla_qk_norm_rope_backward(dq_nope, dq_rope, dk_nope, dk_rope, q=None, k_nope
 
 def mla_rope_append(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, rope_turns, norm_weight=None,
                     eps: float = 1e-6, positions=None, new_lens=None, interleaved: bool = True, stream=None):
-    """mla_cache_append of raw rows c_new [B, q_len, dl+dr] (bf16, strided views with a
-    contiguous last dimension allowed): the latent's RMS norm (norm_weight bf16 [dl], None: none)
+    """mla_cache_append of raw rows c_new [B, q_len, dl+dr] (bf16, strided views allowed
+    as for mla_qk_norm_rope): the latent's RMS norm (norm_weight bf16 [dl], None: none)
     and the rope part's rotation are applied on the way.  positions int32 [B, q_len] (None: the
     token's place in its sequence); new_lens int32 [B] (None: q_len): the tokens of each
     sequence that are real, its rows behind them padding.  Modifies kv_cache (and kv_scale) in

@@ -260,9 +260,9 @@ __device__ __forceinline__ void split16(const uint4& w0, const uint4& w1, float 
 // again: between two falls at most 2^-9 of the sum of the pages' largest weights is lost.  m falls by 16
 // bits at most at a time, and then only a mass as much larger lets it fall again, so O stays below
 // 2^90; and it does not fall where the sum of p = P'' / ks is huge because the key scales are tiny.
-// A fall costs what a rise does, about a third of a page.  With kF8FallTo of 4 the scores of normal
-// queries and keys cause none (64 ragged sequences of up to 16384 keys 255 us, as without falls; 261 us with 0, as
-// many rises follow), with scores of four times the spread 280 us instead of 265.
+// A fall costs what a rise does.  With kF8FallTo of 4 the scores of normal queries and keys hardly ever
+// cause one (64 ragged sequences of up to 16384 keys: 255 us, as without falls; 261 with 0, as many rises
+// follow); with scores of four times the spread 275 to 280 us instead of 265.
 constexpr float kF8StepsPerMass = 16.f, kF8FallTo = 4.f;
 
 constexpr int kQNonFinite = 127;  // q_exp of a row with a NaN or an infinity: all its terms are NaN
@@ -1870,7 +1870,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) tree_merge_kernel(const Para
 }
 
 // Zeroes the split counters of a decode call; the split kernel is launched behind it as a
-// programmatic dependent and waits for it only where it first touches a counter.
+// programmatic dependent and waits for it where it first touches a counter, or else before it ends.
 __global__ void __launch_bounds__(256) zero_counters_kernel(int* __restrict__ c, int n,
                                                                int4* __restrict__ deferred) {
   // (A tree's zeroing is itself a programmatic dependent.  It lets the split kernel, which reads its

@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Zeroes the per-sequence split counters of a call; the decode kernel is launched behind it as
-// a programmatic dependent and waits for it only where it first touches a counter.
+// a programmatic dependent and waits for it where it first touches a counter, or else before it ends.
 __global__ void __launch_bounds__(256) zero_counters_t_kernel(int* __restrict__ c, int n) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) c[i] = 0;

@@ -10,7 +10,7 @@
 // latent columns 8 l + 128 i (16-byte loads, 8- or 16-byte stores) and rope columns 4 l .. 4 l + 3;
 // all the row's loads are issued at once, and the page-table entry, which waits for the length,
 // is fetched while the row is computed.  65536 rows into an e4m3 cache: 26.2 us (4.3 TB/s of rows in
-// and out), its instructions and the latency of a row's two reductions and scale in about equal
+// and out; into a bf16 cache 24.0 us, 6.3 TB/s), its instructions and the latency of a row's two reductions and scale in about equal
 // parts.  With a whole warp a row, scalar arithmetic, a division for every code and the table entry
 // awaited first it was 36 us.  (Blocks of two warps at 64 registers: with four 27.0, at 56
 // registers 29.5.)
