@@ -121,7 +121,9 @@ size_t mla_decode_workspace_size(int B, int H, int q_len, int d_latent);
  * 128 are processed in tiles of 128 rows: q_len > 1 new tokens over a cached prefix is
  * chunked prefill in absorbed form, after mla_cache_append has written the chunk's rows),
  * B <= 65535, B * ceil(q_len * H / 128) <= 2^24, max_pages_per_seq * page_size < 2^31.
- * Larger sizes return MLA_ERR_UNSUPPORTED.
+ * Larger sizes return MLA_ERR_UNSUPPORTED.  The sequences' pages, each times its sequence's
+ * ceil(q_len * H / 128), may be 1.9e9 in sum; more is reported through MLA_ERR_DEVICE_CHECK, and
+ * out and lse are then not written in full.
  */
 mla_status mla_decode(const void* q_latent, const void* q_rope, const void* kv_cache,
                       const float* kv_scale, const int* page_table, const int* cache_lens,

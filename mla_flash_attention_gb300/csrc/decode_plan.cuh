@@ -23,6 +23,7 @@ namespace mla {
 namespace decode_plan {
 
 constexpr int kPage = 64;
+constexpr float kMostPages = 1.9e9f;  // 2^31 less 13 flat pages for each of 2^24 items
 
 // The work unit's page range [start, end) of the flat page numbering and the first
 // sequence that reaches into it (b0, whose pages start at flat page pb0).
@@ -80,6 +81,7 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
     return flat_pages<kTree>(n, cost);
   };
   int total = 0, items = 0, longest = 0;
+  float pages_sum = 0.f;  // of this lane
   int l0s[8];  // the first 256 items' lengths, kept for the second pass
   for (int base = 0; base < B; base += 256) {
     int l[8], sum = 0;
@@ -92,6 +94,7 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += flat_of(l[i]);
     total += warp_sum(sum);
+    pages_sum += static_cast<float>(sum);
     if (kTree) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -99,6 +102,16 @@ __device__ void make_plan(const Prm& prm, int unit, Plan* out) {
         longest = max(longest, l[i]);
       }
     }
+  }
+  // more flat pages than an int can number (with what items are charged): nothing is done, and reported
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) pages_sum += __shfl_xor_sync(0xffffffffu, pages_sum, off);
+  if (pages_sum > kMostPages) {
+    if (lane == 0) {
+      if (unit == 0) latch_error(prm.err, kErrBadPage);
+      *out = Plan{0, 0, B, 0, 1, 0, 0, 0, 0, 1};
+    }
+    return;
   }
   int chunk = 0;
   if (kTree) {
