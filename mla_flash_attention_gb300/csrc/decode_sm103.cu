@@ -115,6 +115,10 @@ template <bool kFp8> constexpr int kPrepOf = kFp8 ? 192 : 64;
 // sequences of up to 1432 keys, 8 x 16 rows, 31 -> 22 us; 160 items of up to 2000 keys, 84 -> 91 us.
 constexpr int kFusedSplits = 2;
 constexpr int kPrefetchAhead = 4;             // pages warmed in L2 ahead of their load
+// Limit of the waits of a role that has nothing to do between an item's start and its last pages, in SM
+// clocks: an item of 2^25 pages takes 50 s.  The others wait for a page at a time, each half a second at
+// most, and what makes one of them give up ends these waits too (the abort flag).
+constexpr long long kItemWait = 200000000000LL;
 
 struct Params {
   const uint16_t* q_latent;  // [B, T, H, 512]
@@ -428,7 +432,7 @@ __device__ __forceinline__ void prepare_pages(const Params& p, B& bars, Segments
         }
       }
       flagged &= __ballot_sync(0xffffffffu, mine >= first && mine < valid);
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero++ & 1, &bars.abort_flag, p.err))) return;
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero++ & 1, &bars.abort_flag, p.err, kItemWait))) return;
       bars.key_nan[gg & 1][mine] = flagged >> lane & 1;
       const uint32_t zero = flagged | __ballot_sync(0xffffffffu, mine >= valid);
       // (whole rows of a chunk, so the swizzle is immaterial)
@@ -461,7 +465,7 @@ __device__ __forceinline__ void prepare_queries(const Params& p, B& bars, Segmen
   unsigned char* qa = sm + kOffQhi;
   int seq, L, lo, hi, g = 0, nseg = 0;
   auto wait = [&](uint64_t* bar, int phase) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, abort_flag, p.err)) != 0;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, abort_flag, p.err, kItemWait)) != 0;
   };
   auto done = [&](uint64_t* bar) {
     ptx::fence_proxy_async();
@@ -1097,7 +1101,7 @@ __global__ void __launch_bounds__(kThreadsOf<kFp8>, 1)
           // are zeroed (16-byte granules; whole rows, so the swizzle is immaterial) and handed
           // back (zeroed).  Full pages go straight from the copy to the MMA.
           if ((pg + 1) * kPage > clean) {
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero & 1, abort_flag, p.err));
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.zero_go, n_zero & 1, abort_flag, p.err, kItemWait));
             if (!ok) break;
             const int nrow = kPage - valid;
             for (int part = 0; part < 2; ++part) {

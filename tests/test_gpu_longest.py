@@ -31,3 +31,24 @@ def test_more_pages_than_can_be_numbered(lib, fp8, tree):
     run()
     with pytest.raises(lib.MLAError, match="DEVICE_CHECK"):
         lib.check_device_error()
+
+
+@pytest.mark.parametrize("fp8,tree", [(False, True), (True, True), (False, False)])
+def test_items_that_take_longer_than_a_wait_for_a_page(lib, fp8, tree):
+    # 450000 pages an item, 0.6 s, in which some roles wait for its last page or for the next item's
+    # queries: one query tile for each work unit (two SMs), for fp8 two
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pages = 450000
+    run, q, keys = inputs(lib, 128, sms // 2 * (2 if fp8 else 1), pages, fp8, tree)
+    out, lse = run()
+    lib.check_device_error()
+    s = 0.05 * q @ keys.T
+    w = torch.softmax(s, -1)
+    # every fp32 sum of a page's share: half a step of 2^-24 at most on the row's sums, one of 2^-23 in each of the
+    # four or less additions to the accumulator; 2^-8 twice for the weights and the output
+    drift = pages * 2.0 ** -24
+    err = (out[0].double() - w @ keys[:, :512]).abs()
+    size = w @ keys[:, :512].abs()
+    assert bool((err <= size * (2.0 ** -7 + 9 * drift)).all())
+    want = torch.logsumexp(s, -1) + torch.tensor(float(pages)).double().log()
+    assert float((lse[0].T.double() - want).abs().max()) <= 1e-3 + drift
