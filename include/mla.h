@@ -19,7 +19,9 @@
  *
  * and the steps around them: cache appends (mla_cache_append, mla_rope_append), norms and
  * rotation of queries and keys with their gradient (mla_qk_norm_rope), the absorption products
- * (mla_absorb) and the prefill's backward pass.
+ * (mla_absorb), the prefill's backward pass, and cross attention to an encoder's states of another
+ * length with its gradient (mla_cross_attention).  Where tokens have positions on several axes
+ * (time, height, width), the norm and append calls have a form of that (.._axes).
  *
  * Conventions shared by every entry point
  *   - All tensor arguments are DEVICE pointers, contiguous, innermost dimension
@@ -198,6 +200,12 @@ mla_status mla_cache_append(const void* c_new, void* kv_cache, float* kv_scale,
  * columns (2i, 2i + 1); otherwise (i, i + d_rope / 2).  (x, y) becomes
  * (x cos - y sin, y cos + x sin).
  *
+ * Several axes: the .._axes entry points take `axes` (1 to 4) positions a token, `positions`
+ * [.., axes] int32, and a table rope_turns [axes][d_rope / 2]: pair i is turned by the sum over the
+ * axes a of position_a * rope_turns[a][i] * 2^-64 turns, exactly mod 1.  A pair that one axis turns has
+ * zeros in the other rows, so sections one after another, axes in turn and planes of two axes are all
+ * tables.  They take positions always (a token's place says nothing of its row and column).
+ *
  * RMS norm, where an entry point takes a norm weight w: y = w x / sqrt(mean(x^2) + eps).  Sums,
  * norms and rotations are computed in fp32 and rounded once to the stored type.
  */
@@ -228,6 +236,17 @@ mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm
                            const int* cache_lens, const int* new_lens, int B, int q_len,
                            int d_latent, int d_rope, int page_size, int max_pages_per_seq,
                            int num_pages, mla_dtype kv_dtype, void* stream);
+
+/*
+ * mla_rope_append_axes -- mla_rope_append with positions on several axes ([B, q_len, axes] int32, not
+ * NULL; rope_turns [axes][d_rope / 2]).
+ */
+mla_status mla_rope_append_axes(const void* c_new, int64_t c_stride, const void* norm_weight, float eps,
+                                const int* positions, const void* rope_turns, int axes, int interleaved,
+                                void* kv_cache, float* kv_scale, const int* page_table,
+                                const int* cache_lens, const int* new_lens, int B, int q_len,
+                                int d_latent, int d_rope, int page_size, int max_pages_per_seq,
+                                int num_pages, mla_dtype kv_dtype, void* stream);
 
 /*
  * mla_decode_tree -- mla_decode for a tree of drafted tokens: the q_len new tokens of a sequence
@@ -322,6 +341,38 @@ mla_status mla_qk_norm_rope_backward(
     size_t workspace_bytes, void* stream);
 
 /*
+ * mla_qk_norm_rope_axes -- mla_qk_norm_rope with positions on several axes ([rows, axes] int32;
+ * rope_turns [axes][d_rope / 2]).
+ */
+mla_status mla_qk_norm_rope_axes(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                 const void* k_nope, int64_t k_nope_row_stride,
+                                 int64_t k_nope_head_stride, const void* k_rope,
+                                 int64_t k_rope_row_stride, const void* q_nope_weight,
+                                 const void* q_rope_weight, const void* k_nope_weight,
+                                 const void* k_rope_weight, const int* positions,
+                                 const void* rope_turns, int axes, float eps, int interleaved,
+                                 void* q_nope_out, void* q_rope_out, void* k_nope_out,
+                                 void* k_rope_out, int64_t rows, int H, int d_nope, int d_rope,
+                                 void* stream);
+
+/*
+ * mla_qk_norm_rope_axes_backward -- gradients of mla_qk_norm_rope_axes.  dk_rope, the upstream
+ * gradient of the rope key, is fp32 (as mla_prefill_backward gives it) or bf16 (as
+ * mla_cross_attention_backward does), by dk_rope_dtype; the rest, the workspace included, is as for
+ * mla_qk_norm_rope_backward.
+ */
+mla_status mla_qk_norm_rope_axes_backward(
+    const void* dq_nope, const void* dq_rope, const void* dk_nope, const void* dk_rope,
+    mla_dtype dk_rope_dtype, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+    const void* k_nope, int64_t k_nope_row_stride, int64_t k_nope_head_stride, const void* k_rope,
+    int64_t k_rope_row_stride, const void* q_nope_weight, const void* q_rope_weight,
+    const void* k_nope_weight, const void* k_rope_weight, const int* positions,
+    const void* rope_turns, int axes, float eps, int interleaved, void* dq, void* dk_nope_in,
+    void* dk_rope_in, float* dq_nope_weight, float* dq_rope_weight, float* dk_nope_weight,
+    float* dk_rope_weight, int64_t rows, int H, int d_nope, int d_rope, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * mla_absorb -- the per-head absorption product either side of absorbed decode:
  *     y[r, h, :] = x[r, h, :] @ w[h]      (fp32 accumulation, bf16 round-to-nearest-even out)
  *   x [R, H, K] bf16, w [H, K, N] bf16, y [R, H, N] bf16 (all contiguous, 16-byte aligned).
@@ -366,6 +417,37 @@ mla_status mla_prefill_backward(const void* q_nope, const void* q_rope, const vo
                                 int H, int S, int d_nope, int d_rope, int d_v,
                                 float softmax_scale, int causal, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/*
+ * mla_cross_attention_workspace_size -- bytes of device workspace mla_cross_attention needs (0 where the
+ * keys of a call of these sizes are not split).  Independent of the key lengths.
+ */
+size_t mla_cross_attention_workspace_size(int B, int H, int Sq, int Sk);
+
+/*
+ * mla_cross_attention -- attention of Sq queries a sequence to Sk keys and values of another source (an
+ * encoder's states; the earlier part of a prompt), in the split nope + rope form of mla_prefill, with
+ * no mask but each sequence's number of keys.
+ *
+ *   q_nope  [B, Sq, H, d_nope]  q_rope [B, Sq, H, d_rope]
+ *   k_nope  [B, Sk, H, d_nope]  k_rope [B, Sk, d_rope] (shared by the heads)  v [B, Sk, H, d_v]
+ *           all bf16
+ *   key_lens [B] int32, or NULL (Sk for every sequence) -- n_b, clamped to 0 .. Sk: the queries of
+ *           sequence b see keys 0 .. n_b - 1.  The rows behind them may hold anything (even NaN).
+ *   out     [B, Sq, H, d_v] bf16,  lse [B, H, Sq] fp32.  A sequence without keys: O = 0, LSE = -inf.
+ *   workspace  at least mla_cross_attention_workspace_size() bytes (NULL where that is 0); calls that
+ *           overlap on the GPU need one each
+ * Queries that share their keys (beams of one sequence) are rows of one sequence: Sq counts them all.
+ * Attention to two sources, or to a prefix and then causally to the rest, joins by the two LSEs.
+ * Softmax weights enter the product with V as bf16, as in mla_prefill.
+ * Supported: d_nope = 128, d_rope = 64, d_v = 128; B, H <= 65535; B * H * ceil(Sq / 256) <= 2^30,
+ * B * H * Sq <= 8e9 and Sq * H, Sk * H below 2^32.
+ */
+mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const void* k_nope,
+                               const void* k_rope, const void* v, const int* key_lens, void* out,
+                               float* lse, int B, int H, int Sq, int Sk, int d_nope, int d_rope,
+                               int d_v, float softmax_scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /*
  * mla_check_device_error -- synchronise `stream`, then read and clear the device

@@ -85,6 +85,20 @@ _lib.mla_qk_norm_rope_backward.restype = _i
 _lib.mla_qk_norm_rope_backward.argtypes = [_vp, _vp, _vp, _fp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _vp, _vp,
                                            _vp, _ip, _vp, _f, _i, _vp, _vp, _vp, _fp, _fp, _fp, _fp, _ll, _i, _i, _i,
                                            _vp, _sz, _vp]
+_lib.mla_rope_append_axes.restype = _i
+_lib.mla_rope_append_axes.argtypes = [_vp, _ll, _vp, _f, _ip, _vp, _i, _i, _vp, _fp, _ip, _ip, _ip, _i, _i, _i, _i, _i,
+                                      _i, _i, _i, _vp]
+_lib.mla_qk_norm_rope_axes.restype = _i
+_lib.mla_qk_norm_rope_axes.argtypes = [_vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ip, _vp, _i, _f, _i,
+                                       _vp, _vp, _vp, _vp, _ll, _i, _i, _i, _vp]
+_lib.mla_qk_norm_rope_axes_backward.restype = _i
+_lib.mla_qk_norm_rope_axes_backward.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _vp,
+                                                _vp, _vp, _ip, _vp, _i, _f, _i, _vp, _vp, _vp, _fp, _fp, _fp, _fp, _ll,
+                                                _i, _i, _i, _vp, _sz, _vp]
+_lib.mla_cross_attention_workspace_size.restype = _sz
+_lib.mla_cross_attention_workspace_size.argtypes = [_i, _i, _i, _i]
+_lib.mla_cross_attention.restype = _i
+_lib.mla_cross_attention.argtypes = [_vp, _vp, _vp, _vp, _vp, _ip, _vp, _fp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]
 _lib.mla_prefill_backward_workspace_size.restype = _sz
 _lib.mla_prefill_backward_workspace_size.argtypes = [_i, _i, _i]
 _lib.mla_prefill_backward.restype = _i
@@ -108,6 +122,8 @@ EXPORTED = ("mla_prefill", "mla_decode_workspace_size", "mla_decode", "mla_decod
             "mla_prefill_backward_workspace_size", "mla_prefill_backward",
             "mla_rope_append", "mla_decode_tree", "mla_qk_norm_rope",
             "mla_qk_norm_rope_backward_workspace_size", "mla_qk_norm_rope_backward",
+            "mla_rope_append_axes", "mla_qk_norm_rope_axes", "mla_qk_norm_rope_axes_backward",
+            "mla_cross_attention_workspace_size", "mla_cross_attention",
             "mla_check_device_error",
             "mla_last_error", "mla_version", "mla_testing_decode_stall", "mla_testing_bounds_checked",
             "mla_testing_bounds_shrink")
@@ -409,9 +425,11 @@ def _address(f) -> int:
 
 
 if not isinstance(_marshal, _NoMarshal):
-    _marshal.connect(_address(_lib.mla_qk_norm_rope), _address(_lib.mla_qk_norm_rope_backward),
-                     _address(_lib.mla_qk_norm_rope_backward_workspace_size), _address(_lib.mla_rope_append),
-                     _address(_lib.mla_decode_tree), _address(_lib.mla_decode_workspace_size), _check)
+    _marshal.connect(tuple(_address(f) for f in (
+        _lib.mla_qk_norm_rope, _lib.mla_qk_norm_rope_axes, _lib.mla_qk_norm_rope_backward,
+        _lib.mla_qk_norm_rope_axes_backward, _lib.mla_qk_norm_rope_backward_workspace_size, _lib.mla_rope_append,
+        _lib.mla_rope_append_axes, _lib.mla_decode_tree, _lib.mla_decode_workspace_size, _lib.mla_cross_attention,
+        _lib.mla_cross_attention_workspace_size)), _check)
 
 
 def _call(stream, tensor, f, *args):
@@ -435,6 +453,21 @@ def rope_turns(inv_freq, device=None) -> torch.Tensor:
         raise ValueError("inv_freq must be finite")
     turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) % 2 ** 64 for f in freqs]
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def rope_turns_axes(inv_freq, pair_axes, device=None) -> torch.Tensor:
+    """rope_turns for positions on several axes (time, height, width): a table int64 [axes, d_rope / 2] for the
+    entry points that end in ``_axes``.  ``inv_freq`` [d_rope / 2] as for ``rope_turns``; ``pair_axes``
+    [d_rope / 2] names the axis whose position turns each pair (0, 1, ..), in any order: sections one
+    after another ([0] * 8 + [1] * 12 + [2] * 12), axes in turn, halves for rows and columns."""
+    freqs = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else list(inv_freq)
+    axis = pair_axes.tolist() if isinstance(pair_axes, torch.Tensor) else list(pair_axes)
+    if len(freqs) != len(axis) or not axis:
+        raise ValueError("pair_axes must name an axis for each of the %d pairs (got %d)" % (len(freqs), len(axis)))
+    if not all(isinstance(a, int) and not isinstance(a, bool) and 0 <= a < 4 for a in axis):
+        raise ValueError("pair_axes must be integers from 0 to 3")
+    return torch.stack([rope_turns([f if a == row else 0.0 for f, a in zip(freqs, axis)], device)
+                        for row in range(max(axis) + 1)])
 
 
 def tree_mask_from_parents(parents):
@@ -500,6 +533,29 @@ def mla_qk_norm_rope_backward(dq_nope, dq_rope, dk_nope, dk_rope, q=None, k_nope
                  grads, workspace)
 
 
+def mla_qk_norm_rope_axes(q=None, k_nope=None, k_rope=None, *, positions, rope_turns, q_nope_weight=None,
+                          q_rope_weight=None, k_nope_weight=None, k_rope_weight=None, eps: float = 1e-6,
+                          interleaved: bool = True, out=None, stream=None):
+    """mla_qk_norm_rope with positions on several axes (images, video): positions int32 [B,S,axes],
+    rope_turns [axes, dr/2] from ``rope_turns_axes()``; a pair is turned by the sum over the axes of
+    position times turns.  Everything else is as for mla_qk_norm_rope."""
+    return _call(stream, q if q is not None else k_nope if k_nope is not None else k_rope, _marshal.qk_norm_rope_axes,
+                 q, k_nope, k_rope, positions, rope_turns, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+                 eps, interleaved, out)
+
+
+def mla_qk_norm_rope_axes_backward(dq_nope, dq_rope, dk_nope, dk_rope, q=None, k_nope=None, k_rope=None, *, positions,
+                                   rope_turns, q_nope_weight=None, q_rope_weight=None, k_nope_weight=None,
+                                   k_rope_weight=None, eps: float = 1e-6, interleaved: bool = True, grads=None,
+                                   workspace=None, stream=None):
+    """Gradients of mla_qk_norm_rope_axes.  dk_rope is fp32 (from mla_prefill_backward) or bf16 (from
+    mla_cross_attention_backward); everything else is as for mla_qk_norm_rope_backward."""
+    return _call(stream, q if q is not None else k_nope if k_nope is not None else k_rope,
+                 _marshal.qk_norm_rope_axes_backward, q, k_nope, k_rope, positions, rope_turns, q_nope_weight,
+                 q_rope_weight, k_nope_weight, k_rope_weight, eps, interleaved, dq_nope, dq_rope, dk_nope, dk_rope,
+                 grads, workspace)
+
+
 def mla_rope_append(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, rope_turns, norm_weight=None,
                     eps: float = 1e-6, positions=None, new_lens=None, interleaved: bool = True, stream=None):
     """mla_cache_append of raw rows c_new [B, q_len, dl+dr] (bf16, strided views allowed
@@ -513,6 +569,15 @@ def mla_rope_append(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, r
     return kv_cache, kv_scale
 
 
+def mla_rope_append_axes(c_new, kv_cache, page_table, cache_lens, kv_scale=None, *, rope_turns, positions,
+                         norm_weight=None, eps: float = 1e-6, new_lens=None, interleaved: bool = True, stream=None):
+    """mla_rope_append with positions on several axes: positions int32 [B, q_len, axes], rope_turns
+    [axes, dr/2] from ``rope_turns_axes()``.  Everything else is as for mla_rope_append."""
+    _call(stream, c_new, _marshal.rope_append_axes, c_new, kv_cache, kv_scale, page_table, cache_lens, new_lens,
+          rope_turns, norm_weight, eps, positions, interleaved)
+    return kv_cache, kv_scale
+
+
 def mla_decode_tree(q_latent, q_rope, kv_cache, page_table, cache_lens, tree_mask, kv_scale=None, *, new_lens=None,
                     softmax_scale: float, out=None, lse=None, workspace=None, stream=None):
     """mla_decode for a tree of drafted tokens.  tree_mask int32 words [B, q_len, ceil(q_len/32)],
@@ -522,3 +587,23 @@ def mla_decode_tree(q_latent, q_rope, kv_cache, page_table, cache_lens, tree_mas
     them are padding (O = 0, LSE = -inf).  The rest is as for mla_decode."""
     return _call(stream, q_latent, _marshal.decode_tree, q_latent, q_rope, kv_cache, kv_scale, page_table, cache_lens,
                  new_lens, tree_mask, softmax_scale, out, lse, workspace)
+
+
+# ------------------------------------------------- cross attention
+
+def cross_attention_workspace_size(B: int, H: int, Sq: int, Sk: int) -> int:
+    return int(_lib.mla_cross_attention_workspace_size(B, H, Sq, Sk))
+
+
+def mla_cross_attention(q_nope, q_rope, k_nope, k_rope, v, key_lens=None, *, softmax_scale: float, out=None, lse=None,
+                        workspace=None, stream=None):
+    """Attention to an encoder's states, or any keys of another length.  Returns (out [B,Sq,H,d_v] bf16,
+    lse [B,H,Sq] fp32).
+
+    q_nope [B,Sq,H,dn], q_rope [B,Sq,H,dr]; k_nope [B,Sk,H,dn], k_rope [B,Sk,dr], v [B,Sk,H,d_v], all bf16;
+    key_lens int32 [B] (None: Sk): the keys of each sequence that exist, what stands behind them does
+    not matter; a sequence without keys gives O = 0 and LSE = -inf.  One query a sequence (a decode step)
+    and few queries over long keys are cut along the keys.  ``workspace`` may pass
+    cross_attention_workspace_size() bytes that the program keeps."""
+    return _call(stream, q_nope, _marshal.cross_attention, q_nope, q_rope, k_nope, k_rope, v, key_lens, softmax_scale,
+                 out, lse, workspace)

@@ -72,10 +72,12 @@ inline cudaError_t smem_attr_once(Kernel kernel, int bytes, unsigned long long* 
 // Launch `kernel` as a programmatic dependent of the work ahead of it in the stream: it is set up
 // while that finishes, and griddepcontrol.wait in it waits until that is complete and visible.
 template <typename... Prm, typename... Arg>
-inline cudaError_t launch_dependent(void (*kernel)(Prm...), int grid, int block, cudaStream_t stream, Arg... arg) {
+inline cudaError_t launch_dependent_smem(void (*kernel)(Prm...), int grid, int block, int smem, cudaStream_t stream,
+                                         const Arg&... arg) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -83,6 +85,10 @@ inline cudaError_t launch_dependent(void (*kernel)(Prm...), int grid, int block,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+template <typename... Prm, typename... Arg>
+inline cudaError_t launch_dependent(void (*kernel)(Prm...), int grid, int block, cudaStream_t stream, const Arg&... arg) {
+  return launch_dependent_smem(kernel, grid, block, 0, stream, arg...);
 }
 
 // In a kernel launched so, before its first access to memory.

@@ -17,6 +17,7 @@
 #include <limits>
 #include <optional>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/mla.h"
@@ -28,11 +29,16 @@ using Shape = std::vector<int64_t>;
 
 // The C entry points of the loaded library and the Python function that raises for a status.
 decltype(&mla_qk_norm_rope) f_norm = nullptr;
+decltype(&mla_qk_norm_rope_axes) f_norm_axes = nullptr;
 decltype(&mla_qk_norm_rope_backward) f_grad = nullptr;
+decltype(&mla_qk_norm_rope_axes_backward) f_grad_axes = nullptr;
 decltype(&mla_qk_norm_rope_backward_workspace_size) f_grad_ws = nullptr;
 decltype(&mla_rope_append) f_append = nullptr;
+decltype(&mla_rope_append_axes) f_append_axes = nullptr;
 decltype(&mla_decode_tree) f_tree = nullptr;
 decltype(&mla_decode_workspace_size) f_tree_ws = nullptr;
+decltype(&mla_cross_attention) f_cross = nullptr;
+decltype(&mla_cross_attention_workspace_size) f_cross_ws = nullptr;
 PyObject* raise_status = nullptr;
 
 [[noreturn]] void fail(PyObject* type, const std::string& msg) {
@@ -166,9 +172,18 @@ PyObject* member(PyObject* seq, const char* name, Py_ssize_t n, Py_ssize_t i) {
 
 const char* const kWeightNames[4] = {"q_nope_weight", "q_rope_weight", "k_nope_weight", "k_rope_weight"};
 
+// rope_turns: [pairs], or [axes, pairs] where positions have several axes.
+struct Turns {
+  const Tensor& t;
+  int64_t axes, dr;
+  Turns(PyObject* o, bool several)
+      : t(tensor(o, "rope_turns", several ? 2 : 1)), axes(several ? t.size(0) : 1), dr(2 * t.size(several ? 1 : 0)) {}
+  void check_on(const at::Device& dev) const { need(t, "rope_turns", at::kLong, t.sizes(), dev); }
+};
+
 struct Operands {
   Tensor q, kn, kr, pos, turns, w[4];
-  int64_t B = 0, S = 0, H = 1, dn = 128, dr = 64;
+  int64_t B = 0, S = 0, H = 1, dn = 128, dr = 64, axes = 1;
   int64_t q_row = 0, q_head = 0, kn_row = 0, kn_head = 0, kr_row = 0;
   at::Device dev{at::kCPU};
   Shape q_shape() const { return {B, S, H, dn + dr}; }
@@ -176,19 +191,21 @@ struct Operands {
   Shape rope_shape() const { return {B, S, H, dr}; }
   Shape key_shape() const { return {B, S, dr}; }
 
-  // q, k_nope, k_rope, positions, rope_turns, four weights
-  explicit Operands(PyObject* const* a) {
+  // q, k_nope, k_rope, positions, rope_turns, four weights; several: positions on several axes
+  Operands(PyObject* const* a, bool several) {
     if (a[0] == Py_None && a[1] == Py_None && a[2] == Py_None)
       fail(PyExc_ValueError, "one of q, k_nope, k_rope must be given");
     q = optional(a[0], "q", 4);
     kn = optional(a[1], "k_nope", 4);
     kr = optional(a[2], "k_rope", 3);
-    turns = tensor(a[4], "rope_turns", 1);
+    const Turns table(a[4], several);
+    turns = table.t;
+    axes = table.axes;
     const Tensor& some = q.defined() ? q : kn.defined() ? kn : kr;
     B = some.size(0);
     S = some.size(1);
     if (some.dim() == 4) H = some.size(2);
-    dr = 2 * turns.size(0);
+    dr = table.dr;
     if (q.defined()) dn = q.size(3) - dr;
     else if (kn.defined()) dn = kn.size(3);
     dev = some.device();
@@ -202,8 +219,8 @@ struct Operands {
     stride(kn, "k_nope", nope_shape(), kn_row, &kn_head);
     stride(kr, "k_rope", key_shape(), kr_row, nullptr);
     pos = tensor(a[3], "positions");
-    need(pos, "positions", at::kInt, {B, S}, dev);
-    need(turns, "rope_turns", at::kLong, {dr / 2}, dev);
+    need(pos, "positions", at::kInt, several ? Shape{B, S, axes} : Shape{B, S}, dev);
+    table.check_on(dev);
     for (int i = 0; i < 4; ++i) {
       w[i] = optional(a[5 + i], kWeightNames[i]);
       if (w[i].defined()) need(w[i], kWeightNames[i], at::kBFloat16, {i % 2 ? dr : dn}, dev);
@@ -212,10 +229,11 @@ struct Operands {
 };
 
 // (q, k_nope, k_rope, positions, rope_turns, 4 weights, eps, interleaved, out or None)
+template <bool kAxes>
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 12) fail(PyExc_TypeError, "qk_norm_rope takes 12 arguments");
-  const Operands o(a);
+  const Operands o(a, kAxes);
   const c10::cuda::CUDAGuard guard(o.dev);
   const bool given[4] = {o.q.defined(), o.q.defined(), o.kn.defined(), o.kr.defined()};
   const Shape shapes[4] = {o.nope_shape(), o.rope_shape(), o.nope_shape(), o.key_shape()};
@@ -234,6 +252,11 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int il = truth(a[10]);
   void* st = stream_of(o.dev);
   check(unlocked([&] {
+    if constexpr (kAxes)
+      return f_norm_axes(ptr(o.q), o.q_row, o.q_head, ptr(o.kn), o.kn_row, o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]),
+                         ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]), static_cast<const int*>(ptr(o.pos)), ptr(o.turns),
+                         size_arg(o.axes), eps, il, ptr(out[0]), ptr(out[1]), ptr(out[2]), ptr(out[3]), o.B * o.S,
+                         size_arg(o.H), size_arg(o.dn), size_arg(o.dr), st);
     return f_norm(ptr(o.q), o.q_row, o.q_head, ptr(o.kn), o.kn_row, o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]),
                   ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]), static_cast<const int*>(ptr(o.pos)), ptr(o.turns), eps, il,
                   ptr(out[0]), ptr(out[1]), ptr(out[2]), ptr(out[3]), o.B * o.S, size_arg(o.H),
@@ -245,10 +268,11 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // (q, k_nope, k_rope, positions, rope_turns, 4 weights, eps, interleaved, dq_nope, dq_rope, dk_nope,
 //  dk_rope, grads or None, workspace or None)
+template <bool kAxes>
 PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 17) fail(PyExc_TypeError, "qk_norm_rope_backward takes 17 arguments");
-  const Operands o(a);
+  const Operands o(a, kAxes);
   const c10::cuda::CUDAGuard guard(o.dev);
   const bool has_up[4] = {o.q.defined(), o.q.defined(), o.kn.defined(), o.kr.defined()};
   const Shape up_shapes[4] = {o.nope_shape(), o.rope_shape(), o.nope_shape(), o.key_shape()};
@@ -257,7 +281,8 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   for (int i = 0; i < 4; ++i) {
     if (!has_up[i]) continue;
     up[i] = tensor(a[11 + i], up_names[i]);
-    need(up[i], up_names[i], i == 3 ? at::kFloat : at::kBFloat16, up_shapes[i], o.dev);
+    const bool f32 = i == 3 && (!kAxes || up[i].scalar_type() != at::kBFloat16);
+    need(up[i], up_names[i], f32 ? at::kFloat : at::kBFloat16, up_shapes[i], o.dev);
   }
   const Tensor* given[7] = {&o.q, &o.kn, &o.kr, &o.w[0], &o.w[1], &o.w[2], &o.w[3]};
   const char* const names[7] = {"grads[0]", "grads[1]", "grads[2]", "grads[3]", "grads[4]", "grads[5]", "grads[6]"};
@@ -291,6 +316,13 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* st = stream_of(o.dev);
   const auto f32 = [](const Tensor& t) { return static_cast<float*>(ptr(t)); };
   check(unlocked([&] {
+    if constexpr (kAxes)
+      return f_grad_axes(ptr(up[0]), ptr(up[1]), ptr(up[2]), ptr(up[3]),
+                         up[3].defined() && up[3].scalar_type() == at::kBFloat16 ? MLA_BF16 : MLA_FP32, ptr(o.q),
+                         o.q_row, o.q_head, ptr(o.kn), o.kn_row, o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]),
+                         ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]), static_cast<const int*>(ptr(o.pos)), ptr(o.turns),
+                         size_arg(o.axes), eps, il, ptr(g[0]), ptr(g[1]), ptr(g[2]), f32(g[3]), f32(g[4]), f32(g[5]),
+                         f32(g[6]), o.B * o.S, size_arg(o.H), size_arg(o.dn), size_arg(o.dr), ptr(ws), ws_bytes, st);
     return f_grad(ptr(up[0]), ptr(up[1]), ptr(up[2]), f32(up[3]), ptr(o.q), o.q_row, o.q_head, ptr(o.kn), o.kn_row,
                   o.kn_head, ptr(o.kr), o.kr_row, ptr(o.w[0]), ptr(o.w[1]), ptr(o.w[2]), ptr(o.w[3]),
                   static_cast<const int*>(ptr(o.pos)), ptr(o.turns), eps, il, ptr(g[0]), ptr(g[1]), ptr(g[2]),
@@ -335,6 +367,7 @@ const int* ints(const Tensor& t) { return static_cast<const int*>(ptr(t)); }
 
 // (c_new, kv_cache, kv_scale, page_table, cache_lens, new_lens, rope_turns, norm_weight, eps,
 //  positions, interleaved)
+template <bool kAxes>
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 11) fail(PyExc_TypeError, "rope_append takes 11 arguments");
@@ -343,19 +376,25 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need(c, "c_new", at::kBFloat16, {B, T, D}, std::nullopt, true);
   const at::Device dev = c.device();
   const Cache k(a + 1, B, D, dev);
-  const Tensor& turns = tensor(a[6], "rope_turns", 1);
-  const int64_t dr = 2 * turns.size(0);
-  need(turns, "rope_turns", at::kLong, {dr / 2}, dev);
-  const Tensor w = optional(a[7], "norm_weight"), pos = optional(a[9], "positions");
+  const Turns turns(a[6], kAxes);
+  const int64_t dr = turns.dr;
+  turns.check_on(dev);
+  const Tensor w = optional(a[7], "norm_weight");
+  const Tensor pos = kAxes ? tensor(a[9], "positions") : optional(a[9], "positions");
   if (w.defined()) need(w, "norm_weight", at::kBFloat16, {D - dr}, dev);
-  if (pos.defined()) need(pos, "positions", at::kInt, {B, T}, dev);
+  if (pos.defined()) need(pos, "positions", at::kInt, kAxes ? Shape{B, T, turns.axes} : Shape{B, T}, dev);
   const c10::cuda::CUDAGuard guard(dev);
   const int64_t stride = row_stride(c, "c_new");
   const float eps = static_cast<float>(number(a[8]));
   const int il = truth(a[10]);
   void* st = stream_of(dev);
   check(unlocked([&] {
-    return f_append(ptr(c), stride, ptr(w), eps, ints(pos), ptr(turns), il, ptr(k.kv), static_cast<float*>(ptr(k.scale)),
+    if constexpr (kAxes)
+      return f_append_axes(ptr(c), stride, ptr(w), eps, ints(pos), ptr(turns.t), size_arg(turns.axes), il, ptr(k.kv),
+                           static_cast<float*>(ptr(k.scale)), ints(k.table), ints(k.lens), ints(k.fresh), size_arg(B),
+                           size_arg(T), size_arg(D - dr), size_arg(dr), size_arg(k.page_size), size_arg(k.max_pages),
+                           size_arg(k.pages), k.type(), st);
+    return f_append(ptr(c), stride, ptr(w), eps, ints(pos), ptr(turns.t), il, ptr(k.kv), static_cast<float*>(ptr(k.scale)),
                     ints(k.table), ints(k.lens), ints(k.fresh), size_arg(B), size_arg(T),
                     size_arg(D - dr), size_arg(dr), size_arg(k.page_size),
                     size_arg(k.max_pages), size_arg(k.pages), k.type(), st);
@@ -404,17 +443,91 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// connect(addresses of the six C functions, the function that raises for a status)
+// ------------------------------------------------------------------------- cross attention
+
+struct CrossOperands {
+  Tensor qn, qr, kn, kr, v, lens;
+  int64_t B, H, Sq, Sk, dn, dr, dv;
+  at::Device dev{at::kCPU};
+  // q_nope, q_rope, k_nope, k_rope, v, key_lens
+  explicit CrossOperands(PyObject* const* a) {
+    qn = tensor(a[0], "q_nope", 4);
+    qr = tensor(a[1], "q_rope", 4);
+    kn = tensor(a[2], "k_nope", 4);
+    kr = tensor(a[3], "k_rope", 3);
+    v = tensor(a[4], "v", 4);
+    lens = optional(a[5], "key_lens");
+    B = qn.size(0);
+    Sq = qn.size(1);
+    H = qn.size(2);
+    dn = qn.size(3);
+    dr = qr.size(3);
+    Sk = kn.size(1);
+    dv = v.size(3);
+    need(qn, "q_nope", at::kBFloat16, {B, Sq, H, dn}, std::nullopt);
+    dev = qn.device();
+    need(qr, "q_rope", at::kBFloat16, {B, Sq, H, dr}, dev);
+    need(kn, "k_nope", at::kBFloat16, {B, Sk, H, dn}, dev);
+    need(kr, "k_rope", at::kBFloat16, {B, Sk, dr}, dev);
+    need(v, "v", at::kBFloat16, {B, Sk, H, dv}, dev);
+    if (lens.defined()) need(lens, "key_lens", at::kInt, {B}, dev);
+  }
+};
+
+// A workspace of `bytes`: the one passed in, or a new one.
+Tensor workspace_of(PyObject* o, size_t bytes, const at::Device& dev) {
+  Tensor ws = optional(o, "workspace");
+  if (ws.defined()) scratch(ws, dev);
+  else if (bytes > 0) ws = empty({static_cast<int64_t>(bytes)}, at::kByte, dev);
+  return ws;
+}
+
+// (q_nope, q_rope, k_nope, k_rope, v, key_lens, softmax_scale, out, lse, workspace)
+PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) fail(PyExc_TypeError, "cross_attention takes 10 arguments");
+  const CrossOperands o(a);
+  const float scale = static_cast<float>(number(a[6]));
+  const c10::cuda::CUDAGuard guard(o.dev);
+  Tensor out = optional(a[7], "out"), lse = optional(a[8], "lse");
+  if (out.defined()) need(out, "out", at::kBFloat16, {o.B, o.Sq, o.H, o.dv}, o.dev);
+  else out = empty({o.B, o.Sq, o.H, o.dv}, at::kBFloat16, o.dev);
+  if (lse.defined()) need(lse, "lse", at::kFloat, {o.B, o.H, o.Sq}, o.dev);
+  else lse = empty({o.B, o.H, o.Sq}, at::kFloat, o.dev);
+  const int B = size_arg(o.B), H = size_arg(o.H), Sq = size_arg(o.Sq), Sk = size_arg(o.Sk);
+  const Tensor ws = workspace_of(a[9], a[9] == Py_None ? f_cross_ws(B, H, Sq, Sk) : 0, o.dev);
+  const size_t ws_bytes = ws.defined() ? ws.nbytes() : 0;
+  void* st = stream_of(o.dev);
+  check(unlocked([&] {
+    return f_cross(ptr(o.qn), ptr(o.qr), ptr(o.kn), ptr(o.kr), ptr(o.v), ints(o.lens), ptr(out),
+                   static_cast<float*>(ptr(lse)), B, H, Sq, Sk, size_arg(o.dn), size_arg(o.dr), size_arg(o.dv), scale,
+                   ptr(ws), ws_bytes, st);
+  }));
+  const Tensor res[2] = {out, lse};
+  return wrap_all(res, 2);
+  END_HANDLE_TH_ERRORS
+}
+
+// connect(addresses of the C functions in the order below, the function that raises for a status)
 PyObject* connect(PyObject*, PyObject* args) {
-  unsigned long long f[6];
+  unsigned long long f[11];
   PyObject* raise;
-  if (!PyArg_ParseTuple(args, "KKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &raise)) return nullptr;
-  f_norm = reinterpret_cast<decltype(f_norm)>(f[0]);
-  f_grad = reinterpret_cast<decltype(f_grad)>(f[1]);
-  f_grad_ws = reinterpret_cast<decltype(f_grad_ws)>(f[2]);
-  f_append = reinterpret_cast<decltype(f_append)>(f[3]);
-  f_tree = reinterpret_cast<decltype(f_tree)>(f[4]);
-  f_tree_ws = reinterpret_cast<decltype(f_tree_ws)>(f[5]);
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                        &f[10], &raise))
+    return nullptr;
+  const unsigned long long* next = f;
+  const auto take = [&](auto& fn) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(*next++); };
+  take(f_norm);
+  take(f_norm_axes);
+  take(f_grad);
+  take(f_grad_axes);
+  take(f_grad_ws);
+  take(f_append);
+  take(f_append_axes);
+  take(f_tree);
+  take(f_tree_ws);
+  take(f_cross);
+  take(f_cross_ws);
   Py_INCREF(raise);
   Py_XSETREF(raise_status, raise);
   Py_RETURN_NONE;
@@ -426,9 +539,13 @@ PyCFunction fast() {
 }
 
 PyMethodDef methods[] = {{"connect", connect, METH_VARARGS, nullptr},
-                         {"qk_norm_rope", fast<qk_norm_rope>(), METH_FASTCALL, nullptr},
-                         {"qk_norm_rope_backward", fast<qk_norm_rope_backward>(), METH_FASTCALL, nullptr},
-                         {"rope_append", fast<rope_append>(), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope", fast<qk_norm_rope<false>>(), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope_axes", fast<qk_norm_rope<true>>(), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope_backward", fast<qk_norm_rope_backward<false>>(), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope_axes_backward", fast<qk_norm_rope_backward<true>>(), METH_FASTCALL, nullptr},
+                         {"rope_append", fast<rope_append<false>>(), METH_FASTCALL, nullptr},
+                         {"rope_append_axes", fast<rope_append<true>>(), METH_FASTCALL, nullptr},
+                         {"cross_attention", fast<cross_attention>(), METH_FASTCALL, nullptr},
                          {"decode_tree", fast<decode_tree>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

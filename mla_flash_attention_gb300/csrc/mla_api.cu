@@ -52,22 +52,28 @@ cudaError_t launch_cache_append(const void* c_new, void* cache, float* kv_scale,
                                 int max_pages, int num_pages, bool fp8, unsigned int* err,
                                 cudaStream_t stream);
 cudaError_t launch_rope_append(const void* c_new, long long row_stride, const void* w, float eps,
-                               const int* positions, const void* turns, bool pairs, void* cache, float* kv_scale,
+                               const int* positions, const void* turns, int axes, bool pairs, void* cache,
+                               float* kv_scale,
                                const int* page_table, const int* cache_lens, const int* new_lens, int B, int T,
                                int max_pages, int num_pages, bool fp8, unsigned int* err, cudaStream_t stream);
+bool cross_fits(int B, int H, int Sq);
+size_t cross_workspace_bytes(int B, int H, int Sq, int Sk, int sms);
+cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
+                               const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
+                               float softmax_scale, void* workspace, int sms, unsigned int* err, cudaStream_t stream);
 size_t norm_rope_grad_workspace_bytes(long long rows, int H, int sms);
 cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_head, const void* kn,
                                    long long kn_row, long long kn_head, const void* kr, long long kr_row,
                                    const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                                   const int* pos, const void* turns, float eps, bool pairs, long long rows,
-                                   int H, void* qn_out, void* qr_out, void* kn_out, void* kr_out, int sms,
+                                   const int* pos, const void* turns, int axes, float eps, bool pairs,
+                                   long long rows, int H, void* qn_out, void* qr_out, void* kn_out, void* kr_out, int sms,
                                    unsigned int* err, cudaStream_t stream);
-cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const float* dkr,
-                                        const void* q, long long q_row, long long q_head, const void* kn,
+cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const void* dkr,
+                                        bool dkr_bf16, const void* q, long long q_row, long long q_head, const void* kn,
                                         long long kn_row, long long kn_head, const void* kr, long long kr_row,
                                         const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                                        const int* pos, const void* turns, float eps, bool pairs, long long rows,
-                                        int H, void* dq, void* dk_nope, void* dk_rope, float* dw_qn, float* dw_qr,
+                                        const int* pos, const void* turns, int axes, float eps, bool pairs,
+                                        long long rows, int H, void* dq, void* dk_nope, void* dk_rope, float* dw_qn, float* dw_qr,
                                         float* dw_kn, float* dw_kr, float* workspace, int sms, unsigned int* err,
                                         cudaStream_t stream);
 }  // namespace mla
@@ -177,12 +183,19 @@ DecodeWorkspace decode_workspace_layout_t(void* base, int B, int TH, int d_laten
   return w;
 }
 
+// The axes of a position rotation.
+mla_status check_axes(const char* fn, int axes) {
+  if (axes <= 0) return fail(MLA_ERR_INVALID_ARG, "%s: axes must be positive (got %d)", fn, axes);
+  if (axes > 4) return fail(MLA_ERR_UNSUPPORTED, "%s: positions have at most 4 axes (got %d)", fn, axes);
+  return MLA_OK;
+}
+
 // What mla_qk_norm_rope and its backward share: the operands present and their strides.
 mla_status check_qk_norm_rope(const char* fn, const void* q, long long q_row, long long q_head, const void* k_nope,
                               long long kn_row, long long kn_head, const void* k_rope, long long kr_row,
                               const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                              const int* positions, const void* rope_turns, float eps, long long rows, int H,
-                              int d_nope, int d_rope) {
+                              const int* positions, const void* rope_turns, int axes, float eps, long long rows,
+                              int H, int d_nope, int d_rope) {
   if (!q && !k_nope && !k_rope) return fail(MLA_ERR_INVALID_ARG, "%s: q, k_nope and k_rope are all NULL", fn);
   if (!positions || !rope_turns) return fail(MLA_ERR_INVALID_ARG, "%s: positions and rope_turns must not be NULL", fn);
   if ((!q && (w_qn || w_qr)) || (!k_nope && w_kn) || (!k_rope && w_kr))
@@ -193,6 +206,7 @@ mla_status check_qk_norm_rope(const char* fn, const void* q, long long q_row, lo
   // the kernels number (row, head) pairs in 32 bits
   if (H > 65535 || rows > 0x70000000LL / H)
     return fail(MLA_ERR_UNSUPPORTED, "%s: H must be at most 65535 and rows * H at most 0x70000000", fn);
+  if (const mla_status st = check_axes(fn, axes)) return st;
   if (!std::isfinite(eps) || eps < 0.f) return fail(MLA_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
   const void* ptrs[] = {q, k_nope, k_rope, w_qn, w_qr, w_kn, w_kr, rope_turns};
   for (const void* p : ptrs)
@@ -206,6 +220,149 @@ mla_status check_qk_norm_rope(const char* fn, const void* q, long long q_row, lo
       return fail(MLA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements and not negative (got %lld)", fn, s);
   if ((double)rows * ((double)strides[0] + strides[2] + strides[4]) + (double)H * ((double)strides[1] + strides[3]) >= 4.0e18)
     return fail(MLA_ERR_UNSUPPORTED, "%s: strides too large", fn);
+  return MLA_OK;
+}
+
+// What mla_cross_attention and its backward share: sizes.
+mla_status check_cross(const char* fn, int B, int H, int Sq, int Sk, int d_nope, int d_rope, int d_v, float softmax_scale) {
+  if (B <= 0 || H <= 0 || Sq <= 0 || Sk <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "%s: B, H, Sq, Sk must be positive (got %d, %d, %d, %d)", fn, B, H, Sq, Sk);
+  if (d_nope != 128 || d_rope != 64 || d_v != 128)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: only d_nope=128, d_rope=64, d_v=128 are built (got %d, %d, %d)", fn, d_nope,
+                d_rope, d_v);
+  if (B > 65535 || H > 65535) return fail(MLA_ERR_UNSUPPORTED, "%s: B and H must be at most 65535", fn);
+  // (a sequence's bytes have to fit a tensor map's stride of 40 bits)
+  if (!mla::cross_fits(B, H, Sq) || (long long)Sq * H >= (1LL << 32) || (long long)Sk * H >= (1LL << 32))
+    return fail(MLA_ERR_UNSUPPORTED, "%s: problem too large", fn);
+  if (!std::isfinite(softmax_scale) || softmax_scale <= 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "%s: softmax_scale must be finite and positive", fn);
+  return MLA_OK;
+}
+
+// One body for each pair of entry points, with one axis of positions and with several.
+mla_status rope_append(const char* fn, const void* c_new, int64_t c_stride, const void* norm_weight, float eps,
+                       const int* positions, const void* rope_turns, int axes, int interleaved, void* kv_cache,
+                       float* kv_scale, const int* page_table, const int* cache_lens, const int* new_lens, int B,
+                       int q_len, int d_latent, int d_rope, int page_size, int max_pages_per_seq, int num_pages,
+                       mla_dtype kv_dtype, void* stream) {
+  if (!c_new || !rope_turns || !kv_cache || !page_table || !cache_lens)
+    return fail(MLA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (B <= 0 || q_len <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "%s: B, q_len, max_pages_per_seq, num_pages must be positive", fn);
+  if (d_latent != 512 || d_rope != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: only d_latent=512, d_rope=64 are built (got %d, %d)", fn, d_latent, d_rope);
+  if (page_size != 64)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: only page_size=64 is built (got %d)", fn, page_size);
+  if ((long long)B * q_len > 0x7fffffffLL / 4)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: B*q_len too large", fn);
+  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: max_pages_per_seq*page_size overflows int32", fn);
+  if (c_stride < d_latent + d_rope || c_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "%s: c_stride must be a multiple of 8 and at least %d (got %lld)", fn,
+                d_latent + d_rope, (long long)c_stride);
+  if (!std::isfinite(eps) || eps < 0.f)
+    return fail(MLA_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  if (const mla_status st = check_axes(fn, axes)) return st;
+  const bool fp8 = kv_dtype == MLA_FP8_E4M3;
+  if (kv_dtype != MLA_BF16 && !fp8)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: kv_dtype must be MLA_BF16 or MLA_FP8_E4M3", fn);
+  if (fp8 != (kv_scale != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "%s: kv_scale is required for fp8 and must be NULL for bf16", fn);
+  const void* ptrs[] = {c_new, norm_weight, kv_cache, rope_turns};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const void* words[] = {kv_scale, positions, page_table, cache_lens, new_lens};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3)
+      return fail(MLA_ERR_INVALID_ARG, "%s: scales and integer tensors must be 4-byte aligned", fn);
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
+  cudaError_t e = mla::launch_rope_append(c_new, c_stride, norm_weight, eps, positions, rope_turns, axes,
+                                          interleaved != 0, kv_cache, kv_scale, page_table, cache_lens, new_lens, B, q_len,
+                                          max_pages_per_seq, num_pages, fp8, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return MLA_OK;
+}
+
+mla_status qk_norm_rope(const char* fn, const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
+                        int64_t k_nope_row_stride, int64_t k_nope_head_stride, const void* k_rope,
+                        int64_t k_rope_row_stride, const void* q_nope_weight, const void* q_rope_weight,
+                        const void* k_nope_weight, const void* k_rope_weight, const int* positions,
+                        const void* rope_turns, int axes, float eps, int interleaved, void* q_nope_out,
+                        void* q_rope_out, void* k_nope_out, void* k_rope_out, int64_t rows, int H, int d_nope,
+                        int d_rope, void* stream) {
+  const mla_status st = check_qk_norm_rope(fn, q, q_row_stride, q_head_stride, k_nope,
+                                           k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
+                                           q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions,
+                                           rope_turns, axes, eps, rows, H, d_nope, d_rope);
+  if (st != MLA_OK) return st;
+  if ((q && (!q_nope_out || !q_rope_out)) || (k_nope && !k_nope_out) || (k_rope && !k_rope_out))
+    return fail(MLA_ERR_INVALID_ARG, "%s: an output of a given operand is NULL", fn);
+  const void* outs[] = {q_nope_out, q_rope_out, k_nope_out, k_rope_out};
+  for (const void* p : outs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const int sms = num_sms_current();
+  unsigned int* err = device_error_word();
+  if (!err || sms <= 0) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
+  cudaError_t e = mla::launch_norm_rope_sm103(
+      q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
+      q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, axes, eps, interleaved != 0, rows,
+      H, q_nope_out, q_rope_out, k_nope_out, k_rope_out, sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return MLA_OK;
+}
+
+mla_status qk_norm_rope_backward(const char* fn, const void* dq_nope, const void* dq_rope, const void* dk_nope,
+                             const void* dk_rope, mla_dtype dk_rope_dtype, const void* q, int64_t q_row_stride,
+                             int64_t q_head_stride, const void* k_nope, int64_t k_nope_row_stride,
+                             int64_t k_nope_head_stride, const void* k_rope, int64_t k_rope_row_stride,
+                             const void* q_nope_weight, const void* q_rope_weight, const void* k_nope_weight,
+                             const void* k_rope_weight, const int* positions, const void* rope_turns, int axes,
+                             float eps, int interleaved, void* dq, void* dk_nope_in, void* dk_rope_in,
+                             float* dq_nope_weight, float* dq_rope_weight, float* dk_nope_weight,
+                             float* dk_rope_weight, int64_t rows, int H, int d_nope, int d_rope, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const mla_status st = check_qk_norm_rope(fn, q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
+                                           k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight,
+                                           q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, axes, eps,
+                                           rows, H, d_nope, d_rope);
+  if (st != MLA_OK) return st;
+  if ((q && (!dq_nope || !dq_rope || !dq)) || (k_nope && (!dk_nope || !dk_nope_in)) || (k_rope && (!dk_rope || !dk_rope_in)))
+    return fail(MLA_ERR_INVALID_ARG, "%s: a gradient of a given operand is NULL", fn);
+  if ((q_nope_weight != nullptr) != (dq_nope_weight != nullptr) || (q_rope_weight != nullptr) != (dq_rope_weight != nullptr) ||
+      (k_nope_weight != nullptr) != (dk_nope_weight != nullptr) || (k_rope_weight != nullptr) != (dk_rope_weight != nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "%s: a weight's gradient must be given exactly where the weight is", fn);
+  if (dk_rope_dtype != MLA_FP32 && dk_rope_dtype != MLA_BF16)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: dk_rope_dtype must be MLA_FP32 or MLA_BF16", fn);
+  const void* ptrs[] = {dq_nope, dq_rope, dk_nope, dk_rope, dq, dk_nope_in, dk_rope_in, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const void* dws[] = {dq_nope_weight, dq_rope_weight, dk_nope_weight, dk_rope_weight};
+  for (const void* p : dws)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(MLA_ERR_INVALID_ARG, "%s: weight gradients must be 4-byte aligned", fn);
+  // gradients share their operand's strides: every element needs a place of its own
+  auto overlaps = [&](int64_t row, int64_t head, int d) {
+    return (H > 1 && head < d) || (rows > 1 && row < d) ||
+           (rows > 1 && H > 1 && row < (int64_t)(H - 1) * head + d && head < (rows - 1) * row + d);
+  };
+  if ((q && overlaps(q_row_stride, q_head_stride, d_nope + d_rope)) ||
+      (k_nope && overlaps(k_nope_row_stride, k_nope_head_stride, d_nope)) ||
+      (k_rope && rows > 1 && k_rope_row_stride < d_rope))
+    return fail(MLA_ERR_INVALID_ARG, "%s: an operand's strides make its elements overlap, so its gradient has no such layout", fn);
+  const bool weights = dq_nope_weight || dq_rope_weight || dk_nope_weight || dk_rope_weight;
+  const int sms = num_sms_current();
+  if (sms <= 0) return fail(MLA_ERR_CUDA, "%s: cannot query the SM count", fn);
+  const size_t need = weights ? mla::norm_rope_grad_workspace_bytes(rows, H, sms) : 0;
+  if (weights && (!workspace || workspace_bytes < need))
+    return fail(MLA_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", fn, workspace_bytes, need);
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
+  cudaError_t e = mla::launch_norm_rope_grad_sm103(
+      dq_nope, dq_rope, dk_nope, dk_rope, dk_rope_dtype == MLA_BF16, q, q_row_stride, q_head_stride, k_nope,
+      k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+      positions, rope_turns, axes, eps, interleaved != 0, rows, H, dq, dk_nope_in, dk_rope_in, dq_nope_weight,
+      dq_rope_weight, dk_nope_weight, dk_rope_weight, static_cast<float*>(workspace), sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
   return MLA_OK;
 }
 
@@ -482,42 +639,20 @@ mla_status mla_rope_append(const void* c_new, int64_t c_stride, const void* norm
                            float* kv_scale, const int* page_table, const int* cache_lens, const int* new_lens, int B,
                            int q_len, int d_latent, int d_rope, int page_size, int max_pages_per_seq, int num_pages,
                            mla_dtype kv_dtype, void* stream) {
-  if (!c_new || !rope_turns || !kv_cache || !page_table || !cache_lens)
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: null tensor pointer");
-  if (B <= 0 || q_len <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: B, q_len, max_pages_per_seq, num_pages must be positive");
-  if (d_latent != 512 || d_rope != 64)
-    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: only d_latent=512, d_rope=64 are built (got %d, %d)", d_latent, d_rope);
-  if (page_size != 64)
-    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: only page_size=64 is built (got %d)", page_size);
-  if ((long long)B * q_len > 0x7fffffffLL / 4)
-    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: B*q_len too large");
-  if ((long long)max_pages_per_seq * page_size > 0x7fffffffLL)
-    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: max_pages_per_seq*page_size overflows int32");
-  if (c_stride < d_latent + d_rope || c_stride % 8 != 0)
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: c_stride must be a multiple of 8 and at least %d (got %lld)",
-                d_latent + d_rope, (long long)c_stride);
-  if (!std::isfinite(eps) || eps < 0.f)
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: eps must be finite and not negative");
-  const bool fp8 = kv_dtype == MLA_FP8_E4M3;
-  if (kv_dtype != MLA_BF16 && !fp8)
-    return fail(MLA_ERR_UNSUPPORTED, "mla_rope_append: kv_dtype must be MLA_BF16 or MLA_FP8_E4M3");
-  if (fp8 != (kv_scale != nullptr))
-    return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: kv_scale is required for fp8 and must be NULL for bf16");
-  const void* ptrs[] = {c_new, norm_weight, kv_cache, rope_turns};
-  for (const void* p : ptrs)
-    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: tensors must be 16-byte aligned");
-  const void* words[] = {kv_scale, positions, page_table, cache_lens, new_lens};
-  for (const void* p : words)
-    if (reinterpret_cast<uintptr_t>(p) & 3)
-      return fail(MLA_ERR_INVALID_ARG, "mla_rope_append: scales and integer tensors must be 4-byte aligned");
-  unsigned int* err = device_error_word();
-  if (!err) return fail(MLA_ERR_CUDA, "mla_rope_append: device error word not reachable");
-  cudaError_t e = mla::launch_rope_append(c_new, c_stride, norm_weight, eps, positions, rope_turns, interleaved != 0,
-                                          kv_cache, kv_scale, page_table, cache_lens, new_lens, B, q_len,
-                                          max_pages_per_seq, num_pages, fp8, err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "mla_rope_append launch");
-  return MLA_OK;
+  return rope_append("mla_rope_append", c_new, c_stride, norm_weight, eps, positions, rope_turns, 1, interleaved,
+                     kv_cache, kv_scale, page_table, cache_lens, new_lens, B, q_len, d_latent, d_rope, page_size,
+                     max_pages_per_seq, num_pages, kv_dtype, stream);
+}
+
+mla_status mla_rope_append_axes(const void* c_new, int64_t c_stride, const void* norm_weight, float eps,
+                       const int* positions, const void* rope_turns, int axes, int interleaved, void* kv_cache,
+                       float* kv_scale, const int* page_table, const int* cache_lens, const int* new_lens, int B,
+                       int q_len, int d_latent, int d_rope, int page_size, int max_pages_per_seq, int num_pages,
+                       mla_dtype kv_dtype, void* stream) {
+  if (!positions) return fail(MLA_ERR_INVALID_ARG, "mla_rope_append_axes: positions must not be NULL");
+  return rope_append("mla_rope_append_axes", c_new, c_stride, norm_weight, eps, positions, rope_turns, axes,
+                     interleaved, kv_cache, kv_scale, page_table, cache_lens, new_lens, B, q_len, d_latent, d_rope,
+                     page_size, max_pages_per_seq, num_pages, kv_dtype, stream);
 }
 
 mla_status mla_decode_tree(const void* q_latent, const void* q_rope, const void* kv_cache, const float* kv_scale,
@@ -584,25 +719,23 @@ mla_status mla_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_
                             const void* rope_turns, float eps, int interleaved, void* q_nope_out, void* q_rope_out,
                             void* k_nope_out, void* k_rope_out, int64_t rows, int H, int d_nope, int d_rope,
                             void* stream) {
-  const mla_status st = check_qk_norm_rope("mla_qk_norm_rope", q, q_row_stride, q_head_stride, k_nope,
-                                           k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
-                                           q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions,
-                                           rope_turns, eps, rows, H, d_nope, d_rope);
-  if (st != MLA_OK) return st;
-  if ((q && (!q_nope_out || !q_rope_out)) || (k_nope && !k_nope_out) || (k_rope && !k_rope_out))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qk_norm_rope: an output of a given operand is NULL");
-  const void* outs[] = {q_nope_out, q_rope_out, k_nope_out, k_rope_out};
-  for (const void* p : outs)
-    if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "mla_qk_norm_rope: tensors must be 16-byte aligned");
-  const int sms = num_sms_current();
-  unsigned int* err = device_error_word();
-  if (!err || sms <= 0) return fail(MLA_ERR_CUDA, "mla_qk_norm_rope: device error word not reachable");
-  cudaError_t e = mla::launch_norm_rope_sm103(
-      q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride, k_nope_head_stride, k_rope, k_rope_row_stride,
-      q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, eps, interleaved != 0, rows, H,
-      q_nope_out, q_rope_out, k_nope_out, k_rope_out, sms, err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "mla_qk_norm_rope launch");
-  return MLA_OK;
+  return qk_norm_rope("mla_qk_norm_rope", q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
+                      k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight,
+                      k_rope_weight, positions, rope_turns, 1, eps, interleaved, q_nope_out, q_rope_out, k_nope_out,
+                      k_rope_out, rows, H, d_nope, d_rope, stream);
+}
+
+mla_status mla_qk_norm_rope_axes(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
+                        int64_t k_nope_row_stride, int64_t k_nope_head_stride, const void* k_rope,
+                        int64_t k_rope_row_stride, const void* q_nope_weight, const void* q_rope_weight,
+                        const void* k_nope_weight, const void* k_rope_weight, const int* positions,
+                        const void* rope_turns, int axes, float eps, int interleaved, void* q_nope_out,
+                        void* q_rope_out, void* k_nope_out, void* k_rope_out, int64_t rows, int H, int d_nope,
+                        int d_rope, void* stream) {
+  return qk_norm_rope("mla_qk_norm_rope_axes", q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
+                      k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight,
+                      k_rope_weight, positions, rope_turns, axes, eps, interleaved, q_nope_out, q_rope_out,
+                      k_nope_out, k_rope_out, rows, H, d_nope, d_rope, stream);
 }
 
 size_t mla_qk_norm_rope_backward_workspace_size(int64_t rows, int H) {
@@ -621,46 +754,61 @@ mla_status mla_qk_norm_rope_backward(const void* dq_nope, const void* dq_rope, c
                                      float* dq_rope_weight, float* dk_nope_weight, float* dk_rope_weight,
                                      int64_t rows, int H, int d_nope, int d_rope, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-  const char* fn = "mla_qk_norm_rope_backward";
-  const mla_status st = check_qk_norm_rope(fn, q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
-                                           k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight,
-                                           q_rope_weight, k_nope_weight, k_rope_weight, positions, rope_turns, eps,
-                                           rows, H, d_nope, d_rope);
-  if (st != MLA_OK) return st;
-  if ((q && (!dq_nope || !dq_rope || !dq)) || (k_nope && (!dk_nope || !dk_nope_in)) || (k_rope && (!dk_rope || !dk_rope_in)))
-    return fail(MLA_ERR_INVALID_ARG, "%s: a gradient of a given operand is NULL", fn);
-  if ((q_nope_weight != nullptr) != (dq_nope_weight != nullptr) || (q_rope_weight != nullptr) != (dq_rope_weight != nullptr) ||
-      (k_nope_weight != nullptr) != (dk_nope_weight != nullptr) || (k_rope_weight != nullptr) != (dk_rope_weight != nullptr))
-    return fail(MLA_ERR_INVALID_ARG, "%s: a weight's gradient must be given exactly where the weight is", fn);
-  const void* ptrs[] = {dq_nope, dq_rope, dk_nope, dk_rope, dq, dk_nope_in, dk_rope_in, workspace};
+  return qk_norm_rope_backward("mla_qk_norm_rope_backward", dq_nope, dq_rope, dk_nope, dk_rope, MLA_FP32, q,
+                               q_row_stride, q_head_stride, k_nope, k_nope_row_stride, k_nope_head_stride, k_rope,
+                               k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+                               positions, rope_turns, 1, eps, interleaved, dq, dk_nope_in, dk_rope_in, dq_nope_weight,
+                               dq_rope_weight, dk_nope_weight, dk_rope_weight, rows, H, d_nope, d_rope, workspace,
+                               workspace_bytes, stream);
+}
+
+mla_status mla_qk_norm_rope_axes_backward(const void* dq_nope, const void* dq_rope, const void* dk_nope,
+                             const void* dk_rope, mla_dtype dk_rope_dtype, const void* q, int64_t q_row_stride,
+                             int64_t q_head_stride, const void* k_nope, int64_t k_nope_row_stride,
+                             int64_t k_nope_head_stride, const void* k_rope, int64_t k_rope_row_stride,
+                             const void* q_nope_weight, const void* q_rope_weight, const void* k_nope_weight,
+                             const void* k_rope_weight, const int* positions, const void* rope_turns, int axes,
+                             float eps, int interleaved, void* dq, void* dk_nope_in, void* dk_rope_in,
+                             float* dq_nope_weight, float* dq_rope_weight, float* dk_nope_weight,
+                             float* dk_rope_weight, int64_t rows, int H, int d_nope, int d_rope, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return qk_norm_rope_backward("mla_qk_norm_rope_axes_backward", dq_nope, dq_rope, dk_nope, dk_rope, dk_rope_dtype, q,
+                               q_row_stride, q_head_stride, k_nope, k_nope_row_stride, k_nope_head_stride, k_rope,
+                               k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
+                               positions, rope_turns, axes, eps, interleaved, dq, dk_nope_in, dk_rope_in,
+                               dq_nope_weight, dq_rope_weight, dk_nope_weight, dk_rope_weight, rows, H, d_nope,
+                               d_rope, workspace, workspace_bytes, stream);
+}
+
+size_t mla_cross_attention_workspace_size(int B, int H, int Sq, int Sk) {
+  if (check_cross("mla_cross_attention_workspace_size", B, H, Sq, Sk, 128, 64, 128, 1.f) != MLA_OK) return 0;
+  const int sms = num_sms_current();
+  return sms > 0 ? mla::cross_workspace_bytes(B, H, Sq, Sk, sms) : 0;
+}
+
+mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
+                               const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
+                               int d_nope, int d_rope, int d_v, float softmax_scale, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const char* fn = "mla_cross_attention";
+  if (!q_nope || !q_rope || !k_nope || !k_rope || !v || !out || !lse)
+    return fail(MLA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (const mla_status st = check_cross(fn, B, H, Sq, Sk, d_nope, d_rope, d_v, softmax_scale)) return st;
+  const void* ptrs[] = {q_nope, q_rope, k_nope, k_rope, v, out, lse, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
-  const void* dws[] = {dq_nope_weight, dq_rope_weight, dk_nope_weight, dk_rope_weight};
-  for (const void* p : dws)
-    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(MLA_ERR_INVALID_ARG, "%s: weight gradients must be 4-byte aligned", fn);
-  // gradients share their operand's strides: every element needs a place of its own
-  auto overlaps = [&](int64_t row, int64_t head, int d) {
-    return (H > 1 && head < d) || (rows > 1 && row < d) ||
-           (rows > 1 && H > 1 && row < (int64_t)(H - 1) * head + d && head < (rows - 1) * row + d);
-  };
-  if ((q && overlaps(q_row_stride, q_head_stride, d_nope + d_rope)) ||
-      (k_nope && overlaps(k_nope_row_stride, k_nope_head_stride, d_nope)) ||
-      (k_rope && rows > 1 && k_rope_row_stride < d_rope))
-    return fail(MLA_ERR_INVALID_ARG, "%s: an operand's strides make its elements overlap, so its gradient has no such layout", fn);
-  const bool weights = dq_nope_weight || dq_rope_weight || dk_nope_weight || dk_rope_weight;
+  if (reinterpret_cast<uintptr_t>(key_lens) & 3)
+    return fail(MLA_ERR_INVALID_ARG, "%s: key_lens must be 4-byte aligned", fn);
   const int sms = num_sms_current();
   if (sms <= 0) return fail(MLA_ERR_CUDA, "%s: cannot query the SM count", fn);
-  const size_t need = weights ? mla::norm_rope_grad_workspace_bytes(rows, H, sms) : 0;
-  if (weights && (!workspace || workspace_bytes < need))
+  const size_t need = mla::cross_workspace_bytes(B, H, Sq, Sk, sms);
+  if (need && (!workspace || workspace_bytes < need))
     return fail(MLA_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", fn, workspace_bytes, need);
   unsigned int* err = device_error_word();
   if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
-  cudaError_t e = mla::launch_norm_rope_grad_sm103(
-      dq_nope, dq_rope, dk_nope, dk_rope, q, q_row_stride, q_head_stride, k_nope, k_nope_row_stride,
-      k_nope_head_stride, k_rope, k_rope_row_stride, q_nope_weight, q_rope_weight, k_nope_weight, k_rope_weight,
-      positions, rope_turns, eps, interleaved != 0, rows, H, dq, dk_nope_in, dk_rope_in, dq_nope_weight, dq_rope_weight,
-      dk_nope_weight, dk_rope_weight, static_cast<float*>(workspace), sms, err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "mla_qk_norm_rope_backward launch");
+  const cudaError_t e = mla::launch_cross_sm103(q_nope, q_rope, k_nope, k_rope, v, key_lens, out, lse, B, H, Sq, Sk,
+                                                softmax_scale, workspace, sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
   return MLA_OK;
 }
 

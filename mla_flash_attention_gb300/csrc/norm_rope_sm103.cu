@@ -50,7 +50,8 @@ struct Params {
   long long q_row, q_head, kn_row, kn_head, kr_row;
   const uint16_t *w_qn, *w_qr, *w_kn, *w_kr;  // null: the part is not normalised
   const int* pos;
-  const unsigned long long* turns;
+  const unsigned long long* turns;  // [axes][32]; pos is [rows][axes]
+  int axes;
   float eps;
   int H;
   unsigned pairs;        // rows * H
@@ -62,7 +63,8 @@ struct Params {
   uint16_t *qn_out, *qr_out, *kn_out, *kr_out;
   // gradient: contiguous upstream gradients
   const uint16_t *dqn, *dqr, *dkn;
-  const float* dkr;
+  const void* dkr;  // fp32, or bf16 where dkr_bf16
+  int dkr_bf16;
   float* partial;  // [blocks][384]
   unsigned int* err;
   size_t qn_bytes, qr_bytes, kn_bytes, kr_bytes, partial_bytes;  // for the store checks
@@ -183,8 +185,9 @@ __device__ __forceinline__ unsigned nope_tasks(const Params& p, unsigned u, unsi
 }
 
 // The rope tasks u, u + step, ... < n: of q (eight heads of a row, groups tasks a row) or of the
-// rope key (kKey: one "head" a row, and its upstream gradient in fp32).
-template <bool kGrad, bool kPairs, bool kKey>
+// rope key (kKey: one "head" a row, and its upstream gradient in fp32 or bf16).  kAxes: positions on
+// one axis, its frequency kept in a register, or on up to kMaxAxes, the table read from L1 for each row.
+template <bool kGrad, bool kPairs, bool kKey, bool kAxes>
 __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsigned n, unsigned step,
                                                const uint16_t* x, long long row_stride, long long head_stride,
                                                int heads, unsigned groups, const uint16_t* w, const void* dy,
@@ -192,7 +195,7 @@ __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsi
   if (u >= n) return u;
   const int lane = threadIdx.x & 31, c8 = lane & 7;
   const uint4 w8 = weights8(w, c8), zero = make_uint4(0, 0, 0, 0);
-  const unsigned long long turns = __ldg(p.turns + lane);
+  const unsigned long long turns = kAxes ? 0 : __ldg(p.turns + lane);
   constexpr int kLoads = kKey ? 1 : 2;
   float dw[8] = {};
   for (; u < n; u += step) {
@@ -208,8 +211,10 @@ __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsi
       const bool live = mine && h < heads;
       in[i] = live ? load16(x + row * row_stride + h * head_stride + 8 * c8) : zero;
       if constexpr (kGrad && kKey) {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(dy) + row * kDr + 8 * c8);
-        if (live) {
+        if (p.dkr_bf16) {
+          up[i] = live ? load16(static_cast<const uint16_t*>(dy) + row * kDr + 8 * c8) : zero;
+        } else if (live) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(dy) + row * kDr + 8 * c8);
           uk[0] = __ldg(src);
           uk[1] = __ldg(src + 1);
         }
@@ -217,8 +222,17 @@ __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsi
         up[i] = live ? load16(static_cast<const uint16_t*>(dy) + (row * heads + h) * kDr + 8 * c8) : zero;
       }
     }
+    unsigned long long phase;
+    if constexpr (kAxes) {
+      phase = 0;
+#pragma unroll
+      for (int a = 0; a < rope::kMaxAxes; ++a)
+        if (a < p.axes) phase += rope::phase(__ldg(p.pos + row * p.axes + a), __ldg(p.turns + a * rope::kFreqs + lane));
+    } else {
+      phase = rope::phase(__ldg(p.pos + row), turns);
+    }
     float c, s;
-    rope::cos_sin(__ldg(p.pos + row), turns, c, s);
+    rope::cos_sin(phase, c, s);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int h = h0 + 4 * i;
@@ -228,7 +242,7 @@ __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsi
       rope::unpack8(in[i], v);
       uint4* dst;
       if constexpr (kGrad) {
-        if constexpr (kKey) {
+        if (kKey && !p.dkr_bf16) {
           d[0] = uk[0].x; d[1] = uk[0].y; d[2] = uk[0].z; d[3] = uk[0].w;
           d[4] = uk[1].x; d[5] = uk[1].y; d[6] = uk[1].z; d[7] = uk[1].w;
         } else {
@@ -257,7 +271,7 @@ __device__ __forceinline__ unsigned rope_tasks(const Params& p, unsigned u, unsi
 }
 
 // The four kinds of tasks of warp `u` of `step`.
-template <bool kGrad, bool kPairs>
+template <bool kGrad, bool kPairs, bool kAxes>
 __device__ __forceinline__ void all_tasks(const Params& p, unsigned u, unsigned step, float* dw_row) {
   auto at = [&](int off) { return dw_row ? dw_row + off : nullptr; };
   u = nope_tasks<kGrad>(p, u, p.n_qn, step, p.q, p.q_row, p.q_head, p.q_linear, p.w_qn, p.dqn, p.qn_out, p.qn_bytes,
@@ -265,21 +279,21 @@ __device__ __forceinline__ void all_tasks(const Params& p, unsigned u, unsigned 
   u = nope_tasks<kGrad>(p, u, p.n_kn, step, p.kn, p.kn_row, p.kn_head, p.kn_linear, p.w_kn, p.dkn, p.kn_out,
                         p.kn_bytes, at(kOffKn)) - p.n_kn;
   // (the gradient of q's rope part lies behind its nope part, as in q)
-  u = rope_tasks<kGrad, kPairs, false>(p, u, p.n_qr, step, p.q + kDn, p.q_row, p.q_head, p.H, p.rope_groups, p.w_qr,
+  u = rope_tasks<kGrad, kPairs, false, kAxes>(p, u, p.n_qr, step, p.q + kDn, p.q_row, p.q_head, p.H, p.rope_groups, p.w_qr,
                                        p.dqr, kGrad ? p.qn_out + kDn : p.qr_out,
                                        kGrad ? p.qn_bytes - 2 * kDn : p.qr_bytes, at(kOffQr)) - p.n_qr;
-  rope_tasks<kGrad, kPairs, true>(p, u, p.n_kr, step, p.kr, p.kr_row, 0, 1, 1, p.w_kr, p.dkr, p.kr_out, p.kr_bytes,
+  rope_tasks<kGrad, kPairs, true, kAxes>(p, u, p.n_kr, step, p.kr, p.kr_row, 0, 1, 1, p.w_kr, p.dkr, p.kr_out, p.kr_bytes,
                                   at(kOffKr));
 }
 
-template <bool kPairs>
+template <bool kPairs, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_rope_kernel(const Params p) {
   const unsigned step = gridDim.x * kWarps;
   wait_for_stream();
-  all_tasks<false, kPairs>(p, blockIdx.x * kWarps + (threadIdx.x >> 5), step, nullptr);
+  all_tasks<false, kPairs, kAxes>(p, blockIdx.x * kWarps + (threadIdx.x >> 5), step, nullptr);
 }
 
-template <bool kPairs>
+template <bool kPairs, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kGradBlocks) norm_rope_grad_kernel(const Params p) {
   __shared__ float joined[kWarps][kDw];
   wait_for_stream();
@@ -291,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) norm_rope_grad_kernel(c
     for (int i = threadIdx.x & 31; i < kDw; i += 32) mine[i] = 0.f;
     __syncwarp();
   }
-  all_tasks<true, kPairs>(p, blockIdx.x * kWarps + warp, step, mine);
+  all_tasks<true, kPairs, kAxes>(p, blockIdx.x * kWarps + warp, step, mine);
   if (!p.partial) return;
   __syncthreads();
   for (int col = threadIdx.x; col < kDw; col += kThreads) {
@@ -354,7 +368,7 @@ namespace {
 norm_rope::Params shared_params(const void* q, long long q_row, long long q_head, const void* kn,
                                 long long kn_row, long long kn_head, const void* kr, long long kr_row,
                                 const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                                const int* pos, const void* turns, float eps, long long rows, int H,
+                                const int* pos, const void* turns, int axes, float eps, long long rows, int H,
                                 unsigned int* err) {
   norm_rope::Params p = {};
   p.q = static_cast<const uint16_t*>(q);
@@ -371,6 +385,7 @@ norm_rope::Params shared_params(const void* q, long long q_row, long long q_head
   p.w_kr = static_cast<const uint16_t*>(w_kr);
   p.pos = pos;
   p.turns = static_cast<const unsigned long long*>(turns);
+  p.axes = axes;
   p.eps = eps;
   p.H = H;
   p.pairs = static_cast<unsigned>(rows * H);  // the caller keeps rows * H at most 0x70000000
@@ -390,12 +405,12 @@ norm_rope::Params shared_params(const void* q, long long q_row, long long q_head
 cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_head, const void* kn,
                                    long long kn_row, long long kn_head, const void* kr, long long kr_row,
                                    const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                                   const int* pos, const void* turns, float eps, bool pairs, long long rows,
+                                   const int* pos, const void* turns, int axes, float eps, bool pairs, long long rows,
                                    int H, void* qn_out, void* qr_out, void* kn_out, void* kr_out, int sms,
                                    unsigned int* err, cudaStream_t stream) {
   using namespace norm_rope;
   Params p = shared_params(q, q_row, q_head, kn, kn_row, kn_head, kr, kr_row, w_qn, w_qr, w_kn, w_kr, pos, turns,
-                           eps, rows, H, err);
+                           axes, eps, rows, H, err);
   p.qn_out = static_cast<uint16_t*>(qn_out);
   p.qr_out = static_cast<uint16_t*>(qr_out);
   p.kn_out = static_cast<uint16_t*>(kn_out);
@@ -406,24 +421,27 @@ cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_h
   p.kn_bytes = (size_t)rows * H * kDn * 2;
   p.kr_bytes = (size_t)rows * kDr * 2;
   const int grid = blocks_for(task_count(p), kForwardBlocks, sms);
-  return launch_dependent(pairs ? norm_rope_kernel<true> : norm_rope_kernel<false>, grid, kThreads, stream, p);
+  auto kernel = axes > 1 ? (pairs ? norm_rope_kernel<true, true> : norm_rope_kernel<false, true>)
+                         : (pairs ? norm_rope_kernel<true, false> : norm_rope_kernel<false, false>);
+  return launch_dependent(kernel, grid, kThreads, stream, p);
 }
 
-cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const float* dkr,
-                                        const void* q, long long q_row, long long q_head, const void* kn,
+cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const void* dkn, const void* dkr,
+                                        bool dkr_bf16, const void* q, long long q_row, long long q_head, const void* kn,
                                         long long kn_row, long long kn_head, const void* kr, long long kr_row,
                                         const void* w_qn, const void* w_qr, const void* w_kn, const void* w_kr,
-                                        const int* pos, const void* turns, float eps, bool pairs, long long rows,
+                                        const int* pos, const void* turns, int axes, float eps, bool pairs, long long rows,
                                         int H, void* dq, void* dk_nope, void* dk_rope, float* dw_qn, float* dw_qr,
                                         float* dw_kn, float* dw_kr, float* workspace, int sms, unsigned int* err,
                                         cudaStream_t stream) {
   using namespace norm_rope;
   Params p = shared_params(q, q_row, q_head, kn, kn_row, kn_head, kr, kr_row, w_qn, w_qr, w_kn, w_kr, pos, turns,
-                           eps, rows, H, err);
+                           axes, eps, rows, H, err);
   p.dqn = static_cast<const uint16_t*>(dqn);
   p.dqr = static_cast<const uint16_t*>(dqr);
   p.dkn = static_cast<const uint16_t*>(dkn);
   p.dkr = dkr;
+  p.dkr_bf16 = dkr_bf16;
   p.qn_out = static_cast<uint16_t*>(dq);
   p.kn_out = static_cast<uint16_t*>(dk_nope);
   p.kr_out = static_cast<uint16_t*>(dk_rope);
@@ -435,8 +453,9 @@ cudaError_t launch_norm_rope_grad_sm103(const void* dqn, const void* dqr, const 
   const bool weights = dw_qn || dw_qr || dw_kn || dw_kr;
   p.partial = weights ? workspace : nullptr;
   p.partial_bytes = (size_t)grid * kDw * sizeof(float);
-  const cudaError_t e = launch_dependent(pairs ? norm_rope_grad_kernel<true> : norm_rope_grad_kernel<false>, grid,
-                                         kThreads, stream, p);
+  auto kernel = axes > 1 ? (pairs ? norm_rope_grad_kernel<true, true> : norm_rope_grad_kernel<false, true>)
+                         : (pairs ? norm_rope_grad_kernel<true, false> : norm_rope_grad_kernel<false, false>);
+  const cudaError_t e = launch_dependent(kernel, grid, kThreads, stream, p);
   if (e != cudaSuccess || !weights) return e;
   return launch_dependent(weight_grad_kernel, kDw / 32, 1024, stream, static_cast<const float*>(workspace), grid, dw_qn,
                           dw_qr, dw_kn, dw_kr);

@@ -5,6 +5,10 @@
 // turns fall off the top exactly, so the angle of a far position is as good as that of a near
 // one (a product p * inv_freq in fp32 is off by up to 2^-25 p radians).  The phase error is
 // p * 2^-65 turns from the rounding of turns[i] and 2^-32 turns from the 32 bits kept here.
+// With several axes (time, height, width) a token has a position on each and turns is a table
+// [axes][32]; the phase is the sum over the axes, as exact mod 2^64 as each term.  A pair that one
+// axis turns has zeros in the other rows, so any assignment of pairs to axes is a table, and no index
+// of an axis has to be read or checked.
 #pragma once
 
 #include "common.cuh"
@@ -14,13 +18,17 @@ namespace mla {
 namespace rope {
 
 constexpr int kDr = 64, kFreqs = kDr / 2;
+constexpr int kMaxAxes = 4;
 
-// cos and sin of frequency `turns` at position `pos` (any int32, negative ones included).  The
-// angle lies in [-pi, pi), where the fast sine and cosine are within 2^-21 of the true ones: results
-// are rounded to 8 bits or fewer, and the accurate functions took a quarter of the append's
-// instructions.
-__device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float& c, float& s) {
-  const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
+// The phase of position `pos` (any int32, negative ones included) on one axis.
+__device__ __forceinline__ unsigned long long phase(int pos, unsigned long long turns) {
+  return static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
+}
+
+// cos and sin of a phase.  The angle lies in [-pi, pi), where the fast sine and cosine are within
+// 2^-21 of the true ones: results are rounded to 8 bits or fewer, and the accurate functions took a
+// quarter of the append's instructions.
+__device__ __forceinline__ void cos_sin(unsigned long long phase, float& c, float& s) {
   // the top 32 bits, as a signed fraction of a turn in [-1/2, 1/2): times 2 pi 2^-32
   const float angle = static_cast<float>(static_cast<int>(phase >> 32)) * 1.4629180792671596e-9f;
   s = __sinf(angle);

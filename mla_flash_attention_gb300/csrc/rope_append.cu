@@ -30,8 +30,9 @@ struct Params {
   long long row_stride;
   const uint16_t* w;  // [512] or null
   float eps;
-  const int* positions;  // [B, T] or null: a token's place in its sequence
-  const unsigned long long* turns;
+  const int* positions;  // [B, T, axes], or null with one axis: a token's place in its sequence
+  const unsigned long long* turns;  // [axes][32]
+  int axes;
   void* cache;
   float* kv_scale;
   const int *page_table, *cache_lens, *new_lens;
@@ -63,7 +64,7 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
-template <bool kFp8, bool kPairs>
+template <bool kFp8, bool kPairs, bool kAxes>
 __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Params p) {
   wait_for_stream();
   const int lane = threadIdx.x & 31, l = lane & 15;
@@ -77,13 +78,27 @@ __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Para
   if (in_range) {
     L = __ldg(p.cache_lens + b);
     n = p.new_lens ? __ldg(p.new_lens + b) : p.T;
-    if (p.positions) pos = __ldg(p.positions + id);
+    if (!kAxes && p.positions) pos = __ldg(p.positions + id);
     const uint16_t* src = p.c_new + (long long)id * p.row_stride;
 #pragma unroll
     for (int i = 0; i < 4; ++i) lat[i] = __ldg(reinterpret_cast<const uint4*>(src) + l + 16 * i);
     rp = __ldg(reinterpret_cast<const uint2*>(src + kDl) + l);
   }
-  const ulonglong2 turns = *(reinterpret_cast<const ulonglong2*>(p.turns) + l);
+  // lane l makes cos and sin of frequencies 2l and 2l + 1
+  const ulonglong2* turns_l = reinterpret_cast<const ulonglong2*>(p.turns) + l;
+  ulonglong2 turns = make_ulonglong2(0, 0);  // several axes: the phases themselves
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int a = 0; a < rope::kMaxAxes; ++a) {
+      if (!in_range || a >= p.axes) break;
+      const ulonglong2 of = __ldg(turns_l + a * (rope::kFreqs / 2));
+      const int at = __ldg(p.positions + (long long)id * p.axes + a);
+      turns.x += rope::phase(at, of.x);
+      turns.y += rope::phase(at, of.y);
+    }
+  } else {
+    turns = *turns_l;
+  }
   const int place = static_cast<int>(max(min((long long)L - n + t, 0x7fffffffLL), -1LL));
   // rows t >= n are padding; of a sequence with fewer cached tokens than new ones the first have
   // no place; more new tokens than rows are refused
@@ -120,11 +135,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Para
     }
   }
   // Rope columns 4l .. 4l + 3: two pairs, or the same half of four pairs (lanes 0..7 the first, lanes
-  // 8..15 the second).  Lane l makes cos and sin of frequencies 2l and 2l + 1.
-  if (!p.positions) pos = place;
+  // 8..15 the second).
+  if (!kAxes && !p.positions) pos = place;
   float c[2], s[2];
-  rope::cos_sin(pos, turns.x, c[0], s[0]);
-  rope::cos_sin(pos, turns.y, c[1], s[1]);
+  rope::cos_sin(kAxes ? turns.x : rope::phase(pos, turns.x), c[0], s[0]);
+  rope::cos_sin(kAxes ? turns.y : rope::phase(pos, turns.y), c[1], s[1]);
   const float a[4] = {__uint_as_float(rp.x << 16), __uint_as_float(rp.x & 0xffff0000u), __uint_as_float(rp.y << 16),
                       __uint_as_float(rp.y & 0xffff0000u)};
   float y[4];
@@ -206,7 +221,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Para
 }  // namespace rope_append
 
 cudaError_t launch_rope_append(const void* c_new, long long row_stride, const void* w, float eps,
-                               const int* positions, const void* turns, bool pairs, void* cache, float* kv_scale,
+                               const int* positions, const void* turns, int axes, bool pairs, void* cache, float* kv_scale,
                                const int* page_table, const int* cache_lens, const int* new_lens, int B, int T,
                                int max_pages, int num_pages, bool fp8, unsigned int* err, cudaStream_t stream) {
   using namespace rope_append;
@@ -216,6 +231,7 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
   p.w = static_cast<const uint16_t*>(w);
   p.eps = eps;
   p.positions = positions;
+  p.axes = axes;
   p.turns = static_cast<const unsigned long long*>(turns);
   p.cache = cache;
   p.kv_scale = kv_scale;
@@ -228,11 +244,13 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
   p.num_pages = num_pages;
   p.err = err;
   const int grid = (p.rows + 2 * kWarps - 1) / (2 * kWarps);
-  auto kernel = fp8 ? (pairs ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
-                    : (pairs ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+  auto one = fp8 ? (pairs ? rope_append_kernel<true, true, false> : rope_append_kernel<true, false, false>)
+                 : (pairs ? rope_append_kernel<false, true, false> : rope_append_kernel<false, false, false>);
+  auto more = fp8 ? (pairs ? rope_append_kernel<true, true, true> : rope_append_kernel<true, false, true>)
+                  : (pairs ? rope_append_kernel<false, true, true> : rope_append_kernel<false, false, true>);
   // (a programmatic dependent: calls of 128 x 7 rows in a row take 3.3 instead of 6.2 us, of 65536 rows
   // 26.2 instead of 28.7)
-  return launch_dependent(kernel, grid, kWarps * 32, stream, p);
+  return launch_dependent(axes > 1 ? more : one, grid, kWarps * 32, stream, p);
 }
 
 }  // namespace mla

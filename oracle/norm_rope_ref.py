@@ -4,7 +4,8 @@ Plain definitions in float64:
 
 * ``rms(x, w, eps)``: w x / sqrt(mean(x^2) + eps) over the last axis; x itself where w is None.
 * ``rotate(x, pos, inv_freq, interleaved)``: pair i of the last axis -- columns (2i, 2i+1), or
-  (i, i + n/2) -- turned by pos * inv_freq[i] radians.
+  (i, i + n/2) -- turned by pos * inv_freq[i] radians.  With inv_freq [axes, n/2] and pos [.., axes],
+  positions on several axes: by the sum over the axes of pos[a] * inv_freq[a, i].
 * ``qk_norm_rope``: queries and keys, the nope and the rope part of each head normalised on
   their own, the rope part then rotated.
 * ``qk_norm_rope_backward``: the chain rule of that, written out: with g the upstream gradient
@@ -37,7 +38,8 @@ def rms_backward(x, w, eps, g):
 def rotate(x, pos, inv_freq, interleaved):
     """x [..., n]; pos broadcastable to x's leading axes."""
     x = np.asarray(x, dtype=np.float64)
-    ang = np.asarray(pos, dtype=np.float64)[..., None] * np.asarray(inv_freq, dtype=np.float64)
+    freq, pos = np.asarray(inv_freq, dtype=np.float64), np.asarray(pos, dtype=np.float64)
+    ang = pos[..., None] * freq if freq.ndim == 1 else (pos[..., None] * freq).sum(axis=-2)
     c, s = np.cos(ang), np.sin(ang)
     n = x.shape[-1]
     first, second = (slice(0, n, 2), slice(1, n, 2)) if interleaved else (slice(0, n // 2), slice(n // 2, n))
@@ -47,16 +49,21 @@ def rotate(x, pos, inv_freq, interleaved):
     return y
 
 
+def for_heads(pos, inv_freq):
+    """Positions with an axis of one for the heads."""
+    return np.expand_dims(np.asarray(pos), -1 if np.ndim(inv_freq) == 1 else -2)
+
+
 def qk_norm_rope(q, k_nope, k_rope, pos, inv_freq, weights, eps, interleaved):
     """q [B,S,H,dn+dr], k_nope [B,S,H,dn], k_rope [B,S,dr] (each may be None), pos [B,S], weights
     (q_nope, q_rope, k_nope, k_rope).  Returns the four outputs (None where not given)."""
     w_qn, w_qr, w_kn, w_kr = weights
-    pos = np.asarray(pos)
-    dr = 2 * len(inv_freq)
+    pos, each = np.asarray(pos), for_heads(pos, inv_freq)
+    dr = 2 * np.shape(inv_freq)[-1]
     qn = qr = kn = kr = None
     if q is not None:
         qn = rms(q[..., :-dr], w_qn, eps)
-        qr = rotate(rms(q[..., -dr:], w_qr, eps), pos[..., None], inv_freq, interleaved)
+        qr = rotate(rms(q[..., -dr:], w_qr, eps), each, inv_freq, interleaved)
     if k_nope is not None:
         kn = rms(k_nope, w_kn, eps)
     if k_rope is not None:
@@ -67,12 +74,12 @@ def qk_norm_rope(q, k_nope, k_rope, pos, inv_freq, weights, eps, interleaved):
 def qk_norm_rope_backward(dqn, dqr, dkn, dkr, q, k_nope, k_rope, pos, inv_freq, weights, eps, interleaved):
     """(dq, dk_nope, dk_rope, dw_qn, dw_qr, dw_kn, dw_kr); None where not given."""
     w_qn, w_qr, w_kn, w_kr = weights
-    pos = np.asarray(pos)
-    dr = 2 * len(inv_freq)
+    pos, each = np.asarray(pos), for_heads(pos, inv_freq)
+    dr = 2 * np.shape(inv_freq)[-1]
     res = [None] * 7
     if q is not None:
         a, res[3] = rms_backward(q[..., :-dr], w_qn, eps, dqn)
-        b, res[4] = rms_backward(q[..., -dr:], w_qr, eps, rotate(dqr, -pos[..., None], inv_freq, interleaved))
+        b, res[4] = rms_backward(q[..., -dr:], w_qr, eps, rotate(dqr, -each, inv_freq, interleaved))
         res[0] = np.concatenate([a, b], axis=-1)
     if k_nope is not None:
         res[1], res[5] = rms_backward(k_nope, w_kn, eps, dkn)
@@ -91,6 +98,6 @@ def append_places(lens, new_lens, T):
 
 def rope_append_rows(c_new, pos, inv_freq, w, eps, interleaved):
     """Finished rows [B, T, dl + dr] (float64, not rounded) of the raw rows c_new."""
-    dr = 2 * len(inv_freq)
+    dr = 2 * np.shape(inv_freq)[-1]
     return np.concatenate([rms(c_new[..., :-dr], w, eps), rotate(c_new[..., -dr:], pos, inv_freq, interleaved)],
                           axis=-1)
