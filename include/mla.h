@@ -450,6 +450,35 @@ mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const voi
                                size_t workspace_bytes, void* stream);
 
 /*
+ * mla_cross_attention_backward_workspace_size -- bytes of device workspace
+ * mla_cross_attention_backward needs (0 for sizes it refuses).
+ */
+size_t mla_cross_attention_backward_workspace_size(int B, int H, int Sq, int Sk);
+
+/*
+ * mla_cross_attention_backward -- gradients of mla_cross_attention for an upstream gradient d_out,
+ * from the forward's out and lse: P = exp(s - lse), dV = P' dO, dP = dO V', D_i = sum_d dO_id O_id,
+ * dS = P * (dP - D), dQ = softmax_scale dS [Kn|Kr], dK = softmax_scale dS' [Qn|Qr]; dk_rope is the sum
+ * over the heads.
+ *
+ *   q_nope .. key_lens   the forward's inputs;  out, lse its outputs;  d_out [B, Sq, H, d_v] bf16
+ *   dq_nope [B, Sq, H, d_nope], dq_rope [B, Sq, H, d_rope], dk_nope [B, Sk, H, d_nope],
+ *   dk_rope [B, Sk, d_rope], dv [B, Sk, H, d_v]   bf16, written in full: zeros for keys behind a
+ *           sequence's last and for queries that see no key
+ *   workspace  at least mla_cross_attention_backward_workspace_size() bytes
+ * All gradients are accumulated in fp32 in an order that does not depend on the run, and rounded once;
+ * P and dS enter the products as bf16.  Supported sizes as for mla_cross_attention, with
+ * B * H * (ceil(Sq / 128) + ceil(Sk / 128)) <= 2^30.
+ */
+mla_status mla_cross_attention_backward(const void* q_nope, const void* q_rope, const void* k_nope,
+                                        const void* k_rope, const void* v, const int* key_lens,
+                                        const void* out, const float* lse, const void* d_out,
+                                        void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
+                                        void* dv, int B, int H, int Sq, int Sk, int d_nope, int d_rope,
+                                        int d_v, float softmax_scale, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
  * mla_check_device_error -- synchronise `stream`, then read and clear the device
  * error word latched by earlier kernels of this library on the current device.
  * Returns MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_DEVICE_CHECK (or MLA_ERR_CUDA if the

@@ -99,6 +99,11 @@ _lib.mla_cross_attention_workspace_size.restype = _sz
 _lib.mla_cross_attention_workspace_size.argtypes = [_i, _i, _i, _i]
 _lib.mla_cross_attention.restype = _i
 _lib.mla_cross_attention.argtypes = [_vp, _vp, _vp, _vp, _vp, _ip, _vp, _fp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]
+_lib.mla_cross_attention_backward_workspace_size.restype = _sz
+_lib.mla_cross_attention_backward_workspace_size.argtypes = [_i, _i, _i, _i]
+_lib.mla_cross_attention_backward.restype = _i
+_lib.mla_cross_attention_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _ip, _vp, _fp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                                              _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]
 _lib.mla_prefill_backward_workspace_size.restype = _sz
 _lib.mla_prefill_backward_workspace_size.argtypes = [_i, _i, _i]
 _lib.mla_prefill_backward.restype = _i
@@ -124,6 +129,7 @@ EXPORTED = ("mla_prefill", "mla_decode_workspace_size", "mla_decode", "mla_decod
             "mla_qk_norm_rope_backward_workspace_size", "mla_qk_norm_rope_backward",
             "mla_rope_append_axes", "mla_qk_norm_rope_axes", "mla_qk_norm_rope_axes_backward",
             "mla_cross_attention_workspace_size", "mla_cross_attention",
+            "mla_cross_attention_backward_workspace_size", "mla_cross_attention_backward",
             "mla_check_device_error",
             "mla_last_error", "mla_version", "mla_testing_decode_stall", "mla_testing_bounds_checked",
             "mla_testing_bounds_shrink")
@@ -429,7 +435,8 @@ if not isinstance(_marshal, _NoMarshal):
         _lib.mla_qk_norm_rope, _lib.mla_qk_norm_rope_axes, _lib.mla_qk_norm_rope_backward,
         _lib.mla_qk_norm_rope_axes_backward, _lib.mla_qk_norm_rope_backward_workspace_size, _lib.mla_rope_append,
         _lib.mla_rope_append_axes, _lib.mla_decode_tree, _lib.mla_decode_workspace_size, _lib.mla_cross_attention,
-        _lib.mla_cross_attention_workspace_size)), _check)
+        _lib.mla_cross_attention_workspace_size, _lib.mla_cross_attention_backward,
+        _lib.mla_cross_attention_backward_workspace_size)), _check)
 
 
 def _call(stream, tensor, f, *args):
@@ -607,3 +614,18 @@ def mla_cross_attention(q_nope, q_rope, k_nope, k_rope, v, key_lens=None, *, sof
     cross_attention_workspace_size() bytes that the program keeps."""
     return _call(stream, q_nope, _marshal.cross_attention, q_nope, q_rope, k_nope, k_rope, v, key_lens, softmax_scale,
                  out, lse, workspace)
+
+
+def cross_attention_backward_workspace_size(B: int, H: int, Sq: int, Sk: int) -> int:
+    return int(_lib.mla_cross_attention_backward_workspace_size(B, H, Sq, Sk))
+
+
+def mla_cross_attention_backward(q_nope, q_rope, k_nope, k_rope, v, out, lse, d_out, key_lens=None, *,
+                                 softmax_scale: float, grads=None, workspace=None, stream=None):
+    """Gradients of mla_cross_attention.  Returns (dq_nope, dq_rope, dk_nope, dk_rope, dv), bf16 in the layouts
+    of their operands (dk_rope summed over the heads in fp32), zeros for keys behind a sequence's last.
+
+    out/lse are the forward's results, d_out the upstream gradient [B,Sq,H,d_v] bf16.  ``grads`` may pass
+    those five tensors preallocated."""
+    return _call(stream, q_nope, _marshal.cross_attention_backward, q_nope, q_rope, k_nope, k_rope, v, key_lens, out,
+                 lse, d_out, softmax_scale, grads, workspace)

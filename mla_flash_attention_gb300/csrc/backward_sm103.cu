@@ -1,4 +1,4 @@
-// MLA prefill backward on tcgen05 / TMEM / TMA, bf16 operands.
+// Backward pass of the MLA prefill and of cross attention on tcgen05 / TMEM / TMA, bf16 operands.
 //
 // For one (batch, head), with s = scale * [Qn|Qr][Kn|Kr]' and P = exp(s - LSE) (the forward's
 // log-sum-exp reused, so no row statistics are recomputed):
@@ -19,6 +19,12 @@
 // Shared memory (both roles): fixed 3-chunk tile (K | Q) + fixed 2-chunk tile (V | dO), a
 // 2-stage ring of streamed 3-chunk tiles (Q | K), one streamed 2-chunk tile (dO | V), and
 // the streamed query tiles' -LSE*log2(e) and D vectors (key-tile role).
+// Cross attention (kCross) has queries and keys of unlike counts, each sequence its own number of keys, no
+// causal mask.  In the key role the keys are TMEM lanes, so what stands behind a sequence's last key stays in
+// lanes that are stored as zeros; in the query role those keys' weights and dP are masked and their K rows
+// zeroed in shared memory (0 * NaN is NaN).  The tiles that a CTA streams are cut in shares where few tiles
+// of the one kind meet many of the other, and the rope key's gradient is summed over the heads from fp32
+// partial results by a kernel of its own, in a fixed order: gradients do not depend on the run.
 // Warps: 0 TMA producer, 1 MMA issuer, 2-9 elementwise (TMEM lane quarter = warp % 4,
 // column half = (warp - 2) / 4; each half owns 64 score columns and 32 packed columns of Y).
 #include <cuda.h>
@@ -43,7 +49,7 @@ constexpr int kThreads = 320;
 constexpr uint32_t kColX = 0, kColDP = 128, kColDV = 128, kColAcc = 256, kColY = 448;
 
 struct Params {
-  const float* nlse2;  // [B*H, S_pad]: -LSE * log2(e); +padding rows hold -inf
+  const float* nlse2;  // [B*H, S_pad]: -LSE * log2(e); +padding rows hold -inf  (S_pad: of the queries)
   const float* dvec;   // [B*H, S_pad]: D = rowsum(dO * O); padding rows hold 0
   uint16_t* dq_nope;   // [B, S, H, 128]
   uint16_t* dq_rope;   // [B, S, H, 64]
@@ -53,7 +59,23 @@ struct Params {
   unsigned int* err;
   int B, H, S, S_pad, nt, causal, n_key_ctas;
   float scale, scale_log2;
+  // cross attention: S is Sq, nt the query tiles
+  int Sk, nkt;             // keys, key tiles of Sk
+  int n_qs, n_ks;          // shares of the query tiles (key role) and of the key tiles (query role)
+  const int* key_lens;     // or null
+  float *part_rope;        // [B*H][n_qs][Sk][64]: dk_rope of one head and share
+  float *part_kv;          // n_qs > 1: [key role's CTAs][128][dV 128 | dK nope 128]
+  float *part_q;           // n_ks > 1: [query role's CTAs][128][192]
+  uint16_t* dk_rope_out;   // [B, Sk, 64]
 };
+
+__device__ __forceinline__ int key_len(const Params& p, int b) {
+  return p.key_lens ? min(max(__ldg(p.key_lens + b), 0), p.Sk) : p.Sk;
+}
+// first tile of share s
+__device__ __forceinline__ int share_begin(int tiles, int s, int n) {
+  return static_cast<int>(static_cast<long long>(tiles) * s / n);
+}
 
 struct Bars {
   // one full barrier per 16 KB chunk of a streamed tile, so the MMAs over its first chunk can
@@ -68,13 +90,16 @@ struct Bars {
 // One warp per (b, h, 32 consecutive queries): each 256-byte row of dO and O is read by the
 // whole warp (8 bytes a lane), the 32 per-lane partial sums are reduced across lanes by a
 // transposing butterfly (16 + 8 + 4 + 2 + 1 exchanges) that leaves row i0 + lane's sum in
-// lane `lane`, so the D and LSE accesses are 128-byte coalesced.
+// lane `lane`, so the D and LSE accesses are 128-byte coalesced.  kCross: a row that saw no key (LSE = -inf)
+// gets -inf like the padding, so its weights are 0.
+template <bool kCross>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restrict__ out,
                                                        const uint16_t* __restrict__ d_out,
                                                        const float* __restrict__ lse,
                                                        float* __restrict__ nlse2,
                                                        float* __restrict__ dvec, int B, int H,
                                                        int S, int S_pad) {
+  if (kCross) wait_for_stream();
   const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int groups = S_pad / 32;
@@ -117,7 +142,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restric
   const size_t vo = (size_t)bh * S_pad + i;
   if (i < S) {
     dvec[vo] = part[0];
-    nlse2[vo] = -lse[(size_t)bh * S + i] * 1.4426950408889634f;
+    const float of = lse[(size_t)bh * S + i];
+    nlse2[vo] = kCross && of == -INFINITY ? -INFINITY : -of * 1.4426950408889634f;
   } else {
     dvec[vo] = 0.f;
     nlse2[vo] = -INFINITY;
@@ -145,22 +171,56 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t (&u)
   }
 }
 
+// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst
+__device__ __forceinline__ void store_f32x32(float* dst, const uint32_t (&u)[32], float mul) {
+  float4* d = reinterpret_cast<float4*>(dst);
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    d[x] = make_float4(__uint_as_float(u[4 * x]) * mul, __uint_as_float(u[4 * x + 1]) * mul,
+                       __uint_as_float(u[4 * x + 2]) * mul, __uint_as_float(u[4 * x + 3]) * mul);
+}
+
 struct Maps {
   const CUtensorMap *qn, *qr, *kn, *kr, *v, *dout;
 };
 
 // kKeyRole: this CTA owns key tile `tile` and streams query tiles (dK, dV); otherwise it
-// owns query tile `tile` and streams key tiles (dQ).
-template <bool kKeyRole>
+// owns query tile `tile` and streams key tiles (dQ).  kCross: share `share` of them; `cta` numbers the
+// role's CTAs.
+template <bool kKeyRole, bool kCross>
 __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigned char* sm,
-                                         Bars& bars, int b, int h, int tile) {
+                                         Bars& bars, int b, int h, int tile, int share, int cta) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t_begin = kKeyRole ? (p.causal ? tile : 0) : 0;
-  const int t_end = kKeyRole ? p.nt : (p.causal ? tile + 1 : p.nt);
+  const int len = kCross ? key_len(p, b) : p.S;  // keys
+  int t_begin, t_end;
+  if constexpr (kCross) {
+    const int of = kKeyRole ? (tile * BT < len ? p.nt : 0) : (len + BT - 1) / BT, n = kKeyRole ? p.n_qs : p.n_ks;
+    t_begin = share_begin(of, share, n);
+    t_end = share_begin(of, share + 1, n);
+  } else {
+    t_begin = kKeyRole ? (p.causal ? tile : 0) : 0;
+    t_end = kKeyRole ? p.nt : (p.causal ? tile + 1 : p.nt);
+  }
   const int nsteps = t_end - t_begin;
+  const int rows = kCross && kKeyRole ? p.Sk : p.S;  // of the owned operand and its gradients
   const int bh = b * p.H + h;
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort_flag;
+
+  if (kCross && nsteps == 0) {
+    // queries without a key, keys behind their sequence's last: zeros (shares are joined without them)
+    const int r = (warp & 3) * 32 + lane, hf = (warp - 2) >> 2, row_idx = tile * BT + r;
+    if (warp >= 2 && row_idx < rows && (kKeyRole ? p.n_qs : p.n_ks) == 1) {
+      const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4* wide = reinterpret_cast<uint4*>((kKeyRole ? (hf == 0 ? p.dv : p.dk_nope) : p.dq_nope) + ro * 128);
+      for (int x = 0; x < 16; ++x)
+        if (kKeyRole || x / 8 == hf) wide[x] = zero;
+      if (!kKeyRole && hf == 0)
+        for (int x = 0; x < 8; ++x) reinterpret_cast<uint4*>(p.dq_rope + ro * 64)[x] = zero;
+    }
+    return;
+  }
 
   if (warp == 0) {
     if (ptx::elect_one()) {
@@ -205,6 +265,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       };
       for (int n = 0; n < kAhead && n < nsteps; ++n) warm(n);
+      int n_ring = 0, n_one = 0;  // tiles under way
       for (int n = 0; n < nsteps; ++n) {
         if (n + kAhead < nsteps) warm(n + kAhead);
         const int r0 = (t_begin + n) * BT, s = n & 1;
@@ -227,6 +288,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tma_load_4d(dst + kChunk, m.kn, &bars.ring_full[s][1], 64, h, r0, b);
           ptx::tma_load_3d(dst + 2 * kChunk, m.kr, &bars.ring_full[s][2], 0, r0, b);
         }
+        n_ring = n + 1;
         if (!ptx::mbar_wait(&bars.one_empty, (n & 1) ^ 1, abort_flag, p.err)) break;
         unsigned char* one = sm + kOffOne;
         const CUtensorMap* tm = kKeyRole ? m.dout : m.v;
@@ -234,6 +296,13 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         ptx::mbar_arrive_expect_tx(&bars.one_full[1], kChunk);
         ptx::tma_load_4d(one, tm, &bars.one_full[0], 0, h, r0, b);
         ptx::tma_load_4d(one + kChunk, tm, &bars.one_full[1], 64, h, r0, b);
+        n_one = n + 1;
+      }
+      if constexpr (kCross) {  // copies that after an abort nobody may wait for land before the CTA leaves
+        ptx::mbar_wait_drain(&bars.fix_full, 0);
+        for (int v = n_ring > 2 ? n_ring - 2 : 0; v < n_ring; ++v)
+          for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
+        for (int c = 0; c < 2 && n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (n_one - 1) & 1);
       }
     }
     __syncwarp();
@@ -326,7 +395,9 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           }
         }
       }
-      if (ok) ptx::mma_commit(&bars.acc_done);
+      if (ok || kCross) ptx::mma_commit(&bars.acc_done);
+      // after an abort: every MMA issued completes before the CTA frees its TMEM
+      if (kCross && !ok) ptx::mbar_wait_drain(&bars.acc_done, 0);
     }
     __syncwarp();
   } else {
@@ -381,7 +452,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
           pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
         }
-        if (p.causal && t == tile) {  // diagonal tile: a query before the key sees nothing
+        if (!kCross && p.causal && t == tile) {  // diagonal tile: a query before the key sees nothing
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (hf * 64 + x < r) pr[x] = 0.f;
@@ -395,12 +466,12 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
           pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
         }
-        if (p.causal && t == tile) {  // diagonal tile: keys after the query are masked
+        if (!kCross && p.causal && t == tile) {  // diagonal tile: keys after the query are masked
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (hf * 64 + x > r) pr[x] = 0.f;
-        } else if (!p.causal && (t + 1) * BT > p.S) {  // keys past the sequence end
-          const int lim = p.S - t * BT - hf * 64;
+        } else if ((kCross || !p.causal) && (t + 1) * BT > len) {  // keys past the sequence end
+          const int lim = len - t * BT - hf * 64;
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (x >= lim) pr[x] = 0.f;
@@ -421,6 +492,24 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       ptx::tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
       ptx::tmem_ld_wait();
       arrive(&bars.dp_read);
+      if constexpr (kCross && !kKeyRole) {
+        if ((t + 1) * BT > len && len < p.Sk) {
+          // what stands behind the last key may be NaN: out of dP, and out of the product with K
+          const int lim = len - t * BT;
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (hf * 64 + x >= lim) u[x] = 0u;
+          for (int c = 0; c < 3 && ok; ++c) ok = wait(&bars.ring_full[s][c], (n >> 1) & 1);
+          if (!ok) break;
+          if (r >= lim) {
+            for (int c = hf; c < 3; c += 2) {
+              uint4* row = reinterpret_cast<uint4*>(sm + kOffRing + (s * 3 + c) * kChunk + r * 128);
+              for (int x = 0; x < 8; ++x) row[x] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          ptx::fence_proxy_async();
+        }
+      }
       // dS = P * (dP - D) as bf16 pairs
       if (kKeyRole) {
         const float2* dd = reinterpret_cast<const float2*>(vec + BT) + hf * 32;  // per query
@@ -456,8 +545,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.acc_done, 0, abort_flag, p.err));
     if (ok) {
       ptx::tc_fence_after();
-      const bool store = row_idx < p.S;
-      const size_t ro = ((size_t)b * p.S + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
+      const bool store = row_idx < rows;
+      const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
       if (kKeyRole) {
         // half 0: dV (4 chunks) and rope columns 0..31 of dK; half 1: dK nope (4 chunks) and
         // rope columns 32..63
@@ -469,6 +558,24 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tmem_ld32(tmem + lane_off + col, w);
           ptx::tmem_ld_wait();
           if (!store) continue;
+          if constexpr (kCross) {
+            if (row_idx >= len) {  // lanes of no key
+              if (c < 4 && p.n_qs == 1) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) w[x] = 0u;
+                store_bf16x32((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, 1.f);
+              }
+              continue;
+            }
+            const float mul = c < 4 && hf == 0 ? 1.f : p.scale;
+            if (c == 4)
+              store_f32x32(p.part_rope + (((size_t)bh * p.n_qs + share) * p.Sk + row_idx) * 64 + 32 * hf, w, mul);
+            else if (p.n_qs > 1)
+              store_f32x32(p.part_kv + ((size_t)cta * BT + r) * 256 + hf * 128 + 32 * c, w, mul);
+            else
+              store_bf16x32((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, mul);
+            continue;
+          }
           if (c < 4) {
             if (hf == 0)
               store_bf16x32(p.dv + ro * 128 + 32 * c, w, 1.f);
@@ -493,7 +600,9 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tmem_ld32(tmem + lane_off + kColAcc + 32 * cc, w);
           ptx::tmem_ld_wait();
           if (!store) continue;
-          if (cc < 4)
+          if (kCross && p.n_ks > 1)
+            store_f32x32(p.part_q + ((size_t)cta * BT + r) * 192 + 32 * cc, w, p.scale);
+          else if (cc < 4)
             store_bf16x32(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
           else
             store_bf16x32(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
@@ -503,6 +612,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
   }
 }
 
+template <bool kCross>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_bwd_kernel(const __grid_constant__ CUtensorMap tm_qn,
                        const __grid_constant__ CUtensorMap tm_qr,
@@ -519,9 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // consecutive (most work first), so CTAs that run together stream the same (b, h)'s tiles
   // and find them in L2
   const bool key_role = static_cast<int>(blockIdx.x) < p.n_key_ctas;
-  const int idx = key_role ? blockIdx.x : blockIdx.x - p.n_key_ctas;
-  const int bh = idx / p.nt;
-  const int tile = key_role ? idx % p.nt : p.nt - 1 - idx % p.nt;
+  const int cta = key_role ? blockIdx.x : blockIdx.x - p.n_key_ctas;
+  const int shares = !kCross ? 1 : key_role ? p.n_qs : p.n_ks, idx = cta / shares, share = cta % shares;
+  const int tiles = kCross && key_role ? p.nkt : p.nt;
+  const int bh = idx / tiles;
+  const int tile = key_role || kCross ? idx % tiles : tiles - 1 - idx % tiles;
   const int b = bh / p.H, h = bh % p.H;
 
   if (threadIdx.x == 0) {
@@ -549,17 +661,88 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (kCross) wait_for_stream();
   const Maps m{&tm_qn, &tm_qr, &tm_kn, &tm_kr, &tm_v, &tm_do};
   if (key_role)
-    bwd_body<true>(m, p, sm, bars, b, h, tile);
+    bwd_body<true, kCross>(m, p, sm, bars, b, h, tile, share, cta);
   else
-    bwd_body<false>(m, p, sm, bars, b, h, tile);
+    bwd_body<false, kCross>(m, p, sm, bars, b, h, tile, share, cta);
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(bars.tmem_base, 512);
   }
+}
+
+// Cross attention: joins what the CTAs left in fp32, one thread for four columns of a row: the rope key's
+// gradient over heads and shares, and the shares' gradients of K and V, and of Q, where those were cut.
+__global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
+  wait_for_stream();
+  const long long n_rope = (long long)p.B * p.Sk * 16;
+  const long long n_kv = p.n_qs > 1 ? (long long)p.B * p.Sk * p.H * 64 : 0;
+  const long long n_q = p.n_ks > 1 ? (long long)p.B * p.S * p.H * 48 : 0;
+  auto add = [](float4& a, const float4& v) { a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
+  auto put = [](uint16_t* dst, const float4& a) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
+  };
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_rope + n_kv + n_q;
+       i += (long long)gridDim.x * blockDim.x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n_rope) {
+      const long long row = i >> 4;
+      const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk), c = (i & 15) * 4;
+      if (key < key_len(p, b)) {
+        const float* src = p.part_rope + ((size_t)b * p.H * p.n_qs * p.Sk + key) * 64 + c;
+#pragma unroll 8
+        for (int k = 0; k < p.H * p.n_qs; ++k) add(a, ptx::ld_l2(reinterpret_cast<const float4*>(src + (size_t)k * p.Sk * 64)));
+      }
+      put(p.dk_rope_out + row * 64 + c, a);
+    } else if (i < n_rope + n_kv) {
+      const long long at = i - n_rope, bkh = at >> 6;  // (b, key, h)
+      const int c = (at & 63) * 4, h = static_cast<int>(bkh % p.H);
+      const long long bk = bkh / p.H;
+      const int b = static_cast<int>(bk / p.Sk), key = static_cast<int>(bk - (long long)b * p.Sk);
+      if (key < key_len(p, b)) {
+        const size_t cta = (((size_t)b * p.H + h) * p.nkt + key / BT) * p.n_qs;
+        for (int s = 0; s < p.n_qs; ++s)
+          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_kv + ((cta + s) * BT + key % BT) * 256 + c)));
+      }
+      put((c < 128 ? p.dv : p.dk_nope) + bkh * 128 + (c & 127), a);
+    } else {
+      const long long at = i - n_rope - n_kv, bqh = at / 48;  // (b, query, h)
+      const int c = static_cast<int>(at - bqh * 48) * 4, h = static_cast<int>(bqh % p.H);
+      const long long bq = bqh / p.H;
+      const int b = static_cast<int>(bq / p.S), q = static_cast<int>(bq - (long long)b * p.S);
+      const int tiles = (key_len(p, b) + BT - 1) / BT;
+      const size_t cta = (((size_t)b * p.H + h) * p.nt + q / BT) * p.n_ks;
+      for (int s = 0; s < p.n_ks; ++s)
+        if (share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
+          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((cta + s) * BT + q % BT) * 192 + c)));
+      put(c < 128 ? p.dq_nope + bqh * 128 + c : p.dq_rope + bqh * 64 + (c - 128), a);
+    }
+  }
+}
+
+// How a cross attention's backward is cut: the tiles that one CTA streams go in shares where their
+// steps would last longer than half of what an SM has to do in all.
+struct Cut {
+  int nqt, nkt, n_qs, n_ks;
+  long long key_ctas, query_ctas;
+};
+constexpr int kLeastSteps = 4;
+
+inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
+  Cut c;
+  c.nqt = (Sq + BT - 1) / BT;
+  c.nkt = (Sk + BT - 1) / BT;
+  const double each = (double)B * H * c.nqt * c.nkt / sms;  // half of both roles' steps, an SM
+  const double most = each > kLeastSteps ? each : kLeastSteps;
+  c.n_qs = c.nqt > most ? (int)(c.nqt / most + 0.999) : 1;
+  c.n_ks = c.nkt > most ? (int)(c.nkt / most + 0.999) : 1;
+  c.key_ctas = (long long)B * H * c.nkt * c.n_qs;
+  c.query_ctas = (long long)B * H * c.nqt * c.n_ks;
+  return c;
 }
 
 }  // namespace sm103_bwd
@@ -601,7 +784,7 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
   const long long tasks = (long long)B * H * (S_pad / 32);
   const long long prep_blocks = (tasks + 7) / 8;
   if (prep_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  bwd_prep_kernel<<<(unsigned)prep_blocks, 256, 0, stream>>>(
+  bwd_prep_kernel<false><<<(unsigned)prep_blocks, 256, 0, stream>>>(
       static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(d_out), lse, nlse2, dvec, B,
       H, S, S_pad);
   bwd_zero_kernel<<<1024, 256, 0, stream>>>(reinterpret_cast<float4*>(dk_rope),
@@ -619,7 +802,7 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
       encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides,
                         kr_box) != cudaSuccess)
     return cudaErrorInvalidValue;
-  Params p;
+  Params p = {};
   p.nlse2 = nlse2;
   p.dvec = dvec;
   p.dq_nope = static_cast<uint16_t*>(dq_nope);
@@ -640,10 +823,101 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
   if (2 * per_role > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.n_key_ctas = (int)per_role;
   static unsigned long long smem_set = 0;
-  if ((e = smem_attr_once(prefill_bwd_kernel, kSmemAlloc, &smem_set)) != cudaSuccess) return e;
-  prefill_bwd_kernel<<<(unsigned)(2 * per_role), kThreads, kSmemAlloc, stream>>>(tqn, tqr, tkn,
-                                                                                  tkr, tv, tdo, p);
+  if ((e = smem_attr_once(prefill_bwd_kernel<false>, kSmemAlloc, &smem_set)) != cudaSuccess) return e;
+  prefill_bwd_kernel<false><<<(unsigned)(2 * per_role), kThreads, kSmemAlloc, stream>>>(tqn, tqr, tkn, tkr, tv, tdo, p);
   return cudaGetLastError();
+}
+
+// Whether the CTAs of such a call can be numbered.
+bool cross_bwd_fits(int B, int H, int Sq, int Sk) {
+  return (long long)B * H * ((Sq + 127) / 128 + (long long)((Sk + 127) / 128)) <= 0x40000000LL;
+}
+
+namespace {
+struct CrossBwdWorkspace {
+  size_t nlse2, dvec, rope, kv, q, bytes;  // offsets, and the whole
+  CrossBwdWorkspace(const sm103_bwd::Cut& c, int B, int H, int Sk) {
+    size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t here = at;
+      at += (n + 255) / 256 * 256;
+      return here;
+    };
+    const size_t vec = (size_t)B * H * c.nqt * sm103_bwd::BT * sizeof(float);
+    nlse2 = take(vec);
+    dvec = take(vec);
+    rope = take((size_t)B * H * c.n_qs * Sk * 64 * sizeof(float));
+    kv = take(c.n_qs > 1 ? (size_t)c.key_ctas * sm103_bwd::BT * 256 * sizeof(float) : 0);
+    q = take(c.n_ks > 1 ? (size_t)c.query_ctas * sm103_bwd::BT * 192 * sizeof(float) : 0);
+    bytes = at;
+  }
+};
+}  // namespace
+
+size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
+  return CrossBwdWorkspace(sm103_bwd::cut_of(B, H, Sq, Sk, sms), B, H, Sk).bytes;
+}
+
+cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
+                                   const void* v, const int* key_lens, const void* out, const float* lse,
+                                   const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
+                                   void* dv, int B, int H, int Sq, int Sk, float softmax_scale, void* workspace, int sms,
+                                   unsigned int* err, cudaStream_t stream) {
+  using namespace sm103_bwd;
+  const Cut c = cut_of(B, H, Sq, Sk, sms);
+  const CrossBwdWorkspace w(c, B, H, Sk);
+  CUtensorMap tqn, tqr, tkn, tkr, tv, tdo;
+  uint64_t kr_dims[3] = {64, (uint64_t)Sk, (uint64_t)B};
+  uint64_t kr_strides[2] = {64 * 2, (uint64_t)Sk * 64 * 2};
+  uint32_t kr_box[3] = {64, BT, 1};
+  if (!bwd_map_bshd(&tqn, q_nope, B, Sq, H, 128) || !bwd_map_bshd(&tqr, q_rope, B, Sq, H, 64) ||
+      !bwd_map_bshd(&tkn, k_nope, B, Sk, H, 128) || !bwd_map_bshd(&tv, v, B, Sk, H, 128) ||
+      !bwd_map_bshd(&tdo, d_out, B, Sq, H, 128) ||
+      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  char* base = static_cast<char*>(workspace);
+  auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+  Params p = {};
+  p.nlse2 = at(w.nlse2);
+  p.dvec = at(w.dvec);
+  p.dq_nope = static_cast<uint16_t*>(dq_nope);
+  p.dq_rope = static_cast<uint16_t*>(dq_rope);
+  p.dk_nope = static_cast<uint16_t*>(dk_nope);
+  p.dk_rope_out = static_cast<uint16_t*>(dk_rope);
+  p.dv = static_cast<uint16_t*>(dv);
+  p.err = err;
+  p.B = B;
+  p.H = H;
+  p.S = Sq;
+  p.nt = c.nqt;
+  p.S_pad = c.nqt * BT;
+  p.Sk = Sk;
+  p.nkt = c.nkt;
+  p.n_qs = c.n_qs;
+  p.n_ks = c.n_ks;
+  p.key_lens = key_lens;
+  p.part_rope = at(w.rope);
+  p.part_kv = at(w.kv);
+  p.part_q = at(w.q);
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.n_key_ctas = (int)c.key_ctas;
+  if (c.key_ctas + c.query_ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const long long tasks = (long long)B * H * (p.S_pad / 32);
+  if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  static unsigned long long smem_set = 0;
+  cudaError_t e = smem_attr_once(prefill_bwd_kernel<true>, kSmemAlloc, &smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(bwd_prep_kernel<true>, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
+                       static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.S_pad);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent_smem(prefill_bwd_kernel<true>, (int)(c.key_ctas + c.query_ctas), kThreads, kSmemAlloc, stream, tqn,
+                            tqr, tkn, tkr, tv, tdo, p);
+  if (e != cudaSuccess) return e;
+  const long long joins = (long long)B * Sk * 16 + (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) +
+                          (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
+  const long long blocks = (joins + 255) / 256, most = 8LL * sms;
+  return launch_dependent(bwd_join_kernel, (int)(blocks < most ? blocks : most), 256, stream, p);
 }
 
 }  // namespace mla

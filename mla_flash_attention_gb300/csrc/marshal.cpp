@@ -39,6 +39,8 @@ decltype(&mla_decode_tree) f_tree = nullptr;
 decltype(&mla_decode_workspace_size) f_tree_ws = nullptr;
 decltype(&mla_cross_attention) f_cross = nullptr;
 decltype(&mla_cross_attention_workspace_size) f_cross_ws = nullptr;
+decltype(&mla_cross_attention_backward) f_cross_grad = nullptr;
+decltype(&mla_cross_attention_backward_workspace_size) f_cross_grad_ws = nullptr;
 PyObject* raise_status = nullptr;
 
 [[noreturn]] void fail(PyObject* type, const std::string& msg) {
@@ -508,12 +510,48 @@ PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (q_nope, q_rope, k_nope, k_rope, v, key_lens, out, lse, d_out, softmax_scale, grads, workspace)
+PyObject* cross_attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 12) fail(PyExc_TypeError, "cross_attention_backward takes 12 arguments");
+  const CrossOperands o(a);
+  const Tensor &out = tensor(a[6], "out"), &lse = tensor(a[7], "lse"), &d_out = tensor(a[8], "d_out");
+  need(out, "out", at::kBFloat16, {o.B, o.Sq, o.H, o.dv}, o.dev);
+  need(lse, "lse", at::kFloat, {o.B, o.H, o.Sq}, o.dev);
+  need(d_out, "d_out", at::kBFloat16, {o.B, o.Sq, o.H, o.dv}, o.dev);
+  const float scale = static_cast<float>(number(a[9]));
+  const c10::cuda::CUDAGuard guard(o.dev);
+  const Tensor* of[5] = {&o.qn, &o.qr, &o.kn, &o.kr, &o.v};
+  const char* const names[5] = {"grads[0]", "grads[1]", "grads[2]", "grads[3]", "grads[4]"};
+  Tensor g[5];
+  for (int i = 0; i < 5; ++i) {
+    if (a[10] == Py_None) {
+      g[i] = empty(of[i]->sizes(), at::kBFloat16, o.dev);
+    } else {
+      g[i] = tensor(member(a[10], "grads", 5, i), names[i]);
+      need(g[i], names[i], at::kBFloat16, of[i]->sizes(), o.dev);
+    }
+  }
+  const int B = size_arg(o.B), H = size_arg(o.H), Sq = size_arg(o.Sq), Sk = size_arg(o.Sk);
+  const Tensor ws = workspace_of(a[11], a[11] == Py_None ? f_cross_grad_ws(B, H, Sq, Sk) : 0, o.dev);
+  const size_t ws_bytes = ws.defined() ? ws.nbytes() : 0;
+  void* st = stream_of(o.dev);
+  check(unlocked([&] {
+    return f_cross_grad(ptr(o.qn), ptr(o.qr), ptr(o.kn), ptr(o.kr), ptr(o.v), ints(o.lens), ptr(out),
+                        static_cast<const float*>(ptr(lse)), ptr(d_out), ptr(g[0]), ptr(g[1]), ptr(g[2]), ptr(g[3]),
+                        ptr(g[4]), B, H, Sq, Sk, size_arg(o.dn), size_arg(o.dr), size_arg(o.dv), scale, ptr(ws),
+                        ws_bytes, st);
+  }));
+  return wrap_all(g, 5);
+  END_HANDLE_TH_ERRORS
+}
+
 // connect(addresses of the C functions in the order below, the function that raises for a status)
 PyObject* connect(PyObject*, PyObject* args) {
-  unsigned long long f[11];
+  unsigned long long f[13];
   PyObject* raise;
-  if (!PyArg_ParseTuple(args, "(KKKKKKKKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
-                        &f[10], &raise))
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKKK)O", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                        &f[10], &f[11], &f[12], &raise))
     return nullptr;
   const unsigned long long* next = f;
   const auto take = [&](auto& fn) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(*next++); };
@@ -528,6 +566,8 @@ PyObject* connect(PyObject*, PyObject* args) {
   take(f_tree_ws);
   take(f_cross);
   take(f_cross_ws);
+  take(f_cross_grad);
+  take(f_cross_grad_ws);
   Py_INCREF(raise);
   Py_XSETREF(raise_status, raise);
   Py_RETURN_NONE;
@@ -546,6 +586,7 @@ PyMethodDef methods[] = {{"connect", connect, METH_VARARGS, nullptr},
                          {"rope_append", fast<rope_append<false>>(), METH_FASTCALL, nullptr},
                          {"rope_append_axes", fast<rope_append<true>>(), METH_FASTCALL, nullptr},
                          {"cross_attention", fast<cross_attention>(), METH_FASTCALL, nullptr},
+                         {"cross_attention_backward", fast<cross_attention_backward>(), METH_FASTCALL, nullptr},
                          {"decode_tree", fast<decode_tree>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -61,6 +61,13 @@ size_t cross_workspace_bytes(int B, int H, int Sq, int Sk, int sms);
 cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
                                float softmax_scale, void* workspace, int sms, unsigned int* err, cudaStream_t stream);
+bool cross_bwd_fits(int B, int H, int Sq, int Sk);
+size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms);
+cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
+                                   const void* v, const int* key_lens, const void* out, const float* lse,
+                                   const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
+                                   void* dv, int B, int H, int Sq, int Sk, float softmax_scale, void* workspace, int sms,
+                                   unsigned int* err, cudaStream_t stream);
 size_t norm_rope_grad_workspace_bytes(long long rows, int H, int sms);
 cudaError_t launch_norm_rope_sm103(const void* q, long long q_row, long long q_head, const void* kn,
                                    long long kn_row, long long kn_head, const void* kr, long long kr_row,
@@ -808,6 +815,43 @@ mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const voi
   if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
   const cudaError_t e = mla::launch_cross_sm103(q_nope, q_rope, k_nope, k_rope, v, key_lens, out, lse, B, H, Sq, Sk,
                                                 softmax_scale, workspace, sms, err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return MLA_OK;
+}
+
+size_t mla_cross_attention_backward_workspace_size(int B, int H, int Sq, int Sk) {
+  const char* fn = "mla_cross_attention_backward_workspace_size";
+  if (check_cross(fn, B, H, Sq, Sk, 128, 64, 128, 1.f) != MLA_OK || !mla::cross_bwd_fits(B, H, Sq, Sk)) return 0;
+  const int sms = num_sms_current();
+  return sms > 0 ? mla::cross_bwd_workspace_bytes(B, H, Sq, Sk, sms) : 0;
+}
+
+mla_status mla_cross_attention_backward(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
+                                        const void* v, const int* key_lens, const void* out, const float* lse,
+                                        const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
+                                        void* dv, int B, int H, int Sq, int Sk, int d_nope, int d_rope, int d_v,
+                                        float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "mla_cross_attention_backward";
+  const void* ptrs[] = {q_nope, q_rope, k_nope, k_rope, v, out, lse, d_out, dq_nope, dq_rope, dk_nope, dk_rope, dv};
+  for (const void* p : ptrs)
+    if (!p) return fail(MLA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (const mla_status st = check_cross(fn, B, H, Sq, Sk, d_nope, d_rope, d_v, softmax_scale)) return st;
+  if (!mla::cross_bwd_fits(B, H, Sq, Sk)) return fail(MLA_ERR_UNSUPPORTED, "%s: problem too large", fn);
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return fail(MLA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  if (workspace && !aligned16(workspace)) return fail(MLA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(key_lens) & 3)
+    return fail(MLA_ERR_INVALID_ARG, "%s: key_lens must be 4-byte aligned", fn);
+  const int sms = num_sms_current();
+  if (sms <= 0) return fail(MLA_ERR_CUDA, "%s: cannot query the SM count", fn);
+  const size_t need = mla::cross_bwd_workspace_bytes(B, H, Sq, Sk, sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(MLA_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", fn, workspace_bytes, need);
+  unsigned int* err = device_error_word();
+  if (!err) return fail(MLA_ERR_CUDA, "%s: device error word not reachable", fn);
+  const cudaError_t e = mla::launch_cross_bwd_sm103(q_nope, q_rope, k_nope, k_rope, v, key_lens, out, lse, d_out, dq_nope,
+                                                    dq_rope, dk_nope, dk_rope, dv, B, H, Sq, Sk, softmax_scale, workspace,
+                                                    sms, err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return MLA_OK;
 }

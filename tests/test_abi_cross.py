@@ -12,6 +12,8 @@ FORWARD = OPERANDS + [("out", P), ("lse", P)] + SIZES
 FORWARD0 = dict(qn=16, qr=16, kn=16, kr=16, v=16, lens=16, out=16, lse=16, B=2, H=3, Sq=4, Sk=5, dn=128, dr=64, dv=128,
                 scale=0.1, ws=None, wsb=0, stream=None)
 
+BACKWARD = OPERANDS + [("out", P), ("lse", P)] + [(n, P) for n in ("do", "dqn", "dqr", "dkn", "dkr", "dv_")] + SIZES
+BACKWARD0 = dict(FORWARD0, do=16, dqn=16, dqr=16, dkn=16, dkr=16, dv_=16)
 SHARED = [(1, {n: None}) for n in ("qn", "qr", "kn", "kr", "v", "out", "lse")]
 SHARED += [(1, {n: 24}) for n in ("qn", "qr", "kn", "kr", "v", "out", "lse", "ws")]
 SHARED += [(1, {n: bad}) for n in ("B", "H", "Sq", "Sk") for bad in (0, -1)]
@@ -27,8 +29,16 @@ def test_forward_refuses(clib, want, kw):
     assert b"mla_cross_attention" in clib.mla_last_error()
 
 
-def test_workspace_size_of_refused_sizes(clib):
-    f = clib.mla_cross_attention_workspace_size
+@pytest.mark.parametrize("want,kw", SHARED + [(1, {n: bad}) for n in ("do", "dqn", "dqr", "dkn", "dkr", "dv_")
+                                              for bad in (None, 8)] + [(2, dict(B=65535, H=65535, Sq=1, Sk=3000))])
+def test_backward_refuses(clib, want, kw):
+    assert call(clib.mla_cross_attention_backward, BACKWARD, BACKWARD0, **kw) == want
+    assert b"mla_cross_attention_backward" in clib.mla_last_error()
+
+
+@pytest.mark.parametrize("name", ["mla_cross_attention_workspace_size", "mla_cross_attention_backward_workspace_size"])
+def test_workspace_size_of_refused_sizes(clib, name):
+    f = getattr(clib, name)
     f.restype, f.argtypes = Z, [I, I, I, I]
     assert f(0, 1, 1, 1) == f(1, 0, 1, 1) == f(1, 1, -1, 1) == f(1, 1, 1, 0) == f(65536, 1, 1, 1) == 0
 
@@ -37,6 +47,9 @@ def test_binding_refuses(binding):
     args = [cpu(1, 2, 3, 128), cpu(1, 2, 3, 64), cpu(1, 5, 3, 128), cpu(1, 5, 64), cpu(1, 5, 3, 128)]
     with pytest.raises(ValueError, match="CUDA"):
         binding.mla_cross_attention(*args, softmax_scale=0.1)
+    grads = [cpu(1, 2, 3, 128), cpu(1, 3, 2, dtype=torch.float32), cpu(1, 2, 3, 128)]
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.mla_cross_attention_backward(*args, *grads, softmax_scale=0.1)
     with pytest.raises(TypeError, match="tensor"):
         binding.mla_cross_attention(None, *args[1:], softmax_scale=0.1)
     with pytest.raises(ValueError, match="dimensions"):
