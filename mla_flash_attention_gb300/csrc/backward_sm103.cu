@@ -675,47 +675,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Cross attention: joins what the CTAs left in fp32, one thread for four columns of a row: the rope key's
-// gradient over heads and shares, and the shares' gradients of K and V, and of Q, where those were cut.
+// Cross attention: joins what the CTAs left in fp32.  The rope key's gradient, a sum over heads and shares, a
+// key a block: 16 threads' loads cover its 64 columns and 16 such groups take every 16th head or share each (one
+// thread for all of them waited 150 loads long), joined in group order.  The shares' gradients of K and V, and of
+// Q, where those were cut: a thread for four columns of a row.
 __global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
+  __shared__ float4 groups[16][17];
   wait_for_stream();
-  const long long n_rope = (long long)p.B * p.Sk * 16;
-  const long long n_kv = p.n_qs > 1 ? (long long)p.B * p.Sk * p.H * 64 : 0;
-  const long long n_q = p.n_ks > 1 ? (long long)p.B * p.S * p.H * 48 : 0;
   auto add = [](float4& a, const float4& v) { a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
   auto put = [](uint16_t* dst, const float4& a) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
   };
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_rope + n_kv + n_q;
+  const int c4 = threadIdx.x & 15, group = threadIdx.x >> 4;
+  for (long long row = blockIdx.x; row < (long long)p.B * p.Sk; row += gridDim.x) {
+    const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key < key_len(p, b)) {
+      const float* src = p.part_rope + ((size_t)b * p.H * p.n_qs * p.Sk + key) * 64 + 4 * c4;
+#pragma unroll 4
+      for (int k = group; k < p.H * p.n_qs; k += 16)
+        add(a, ptx::ld_l2(reinterpret_cast<const float4*>(src + (size_t)k * p.Sk * 64)));
+    }
+    groups[group][c4] = a;
+    __syncthreads();
+    if (group == 0) {
+      for (int k = 1; k < 16; ++k) add(a, groups[k][c4]);
+      put(p.dk_rope_out + row * 64 + 4 * c4, a);
+    }
+    __syncthreads();
+  }
+  const long long n_kv = p.n_qs > 1 ? (long long)p.B * p.Sk * p.H * 64 : 0;
+  const long long n_q = p.n_ks > 1 ? (long long)p.B * p.S * p.H * 48 : 0;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_kv + n_q;
        i += (long long)gridDim.x * blockDim.x) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < n_rope) {
-      const long long row = i >> 4;
-      const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk), c = (i & 15) * 4;
-      if (key < key_len(p, b)) {
-        const float* src = p.part_rope + ((size_t)b * p.H * p.n_qs * p.Sk + key) * 64 + c;
-#pragma unroll 8
-        for (int k = 0; k < p.H * p.n_qs; ++k) add(a, ptx::ld_l2(reinterpret_cast<const float4*>(src + (size_t)k * p.Sk * 64)));
-      }
-      put(p.dk_rope_out + row * 64 + c, a);
-    } else if (i < n_rope + n_kv) {
-      const long long at = i - n_rope, bkh = at >> 6;  // (b, key, h)
-      const int c = (at & 63) * 4, h = static_cast<int>(bkh % p.H);
+    if (i < n_kv) {
+      const long long bkh = i >> 6;  // (b, key, h)
+      const int c = (i & 63) * 4, h = static_cast<int>(bkh % p.H);
       const long long bk = bkh / p.H;
       const int b = static_cast<int>(bk / p.Sk), key = static_cast<int>(bk - (long long)b * p.Sk);
       if (key < key_len(p, b)) {
         const size_t cta = (((size_t)b * p.H + h) * p.nkt + key / BT) * p.n_qs;
+#pragma unroll 4
         for (int s = 0; s < p.n_qs; ++s)
           add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_kv + ((cta + s) * BT + key % BT) * 256 + c)));
       }
       put((c < 128 ? p.dv : p.dk_nope) + bkh * 128 + (c & 127), a);
     } else {
-      const long long at = i - n_rope - n_kv, bqh = at / 48;  // (b, query, h)
+      const long long at = i - n_kv, bqh = at / 48;  // (b, query, h)
       const int c = static_cast<int>(at - bqh * 48) * 4, h = static_cast<int>(bqh % p.H);
       const long long bq = bqh / p.H;
       const int b = static_cast<int>(bq / p.S), q = static_cast<int>(bq - (long long)b * p.S);
       const int tiles = (key_len(p, b) + BT - 1) / BT;
       const size_t cta = (((size_t)b * p.H + h) * p.nt + q / BT) * p.n_ks;
+#pragma unroll 4
       for (int s = 0; s < p.n_ks; ++s)
         if (share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
           add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((cta + s) * BT + q % BT) * 192 + c)));
@@ -914,9 +927,8 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   e = launch_dependent_smem(prefill_bwd_kernel<true>, (int)(c.key_ctas + c.query_ctas), kThreads, kSmemAlloc, stream, tqn,
                             tqr, tkn, tkr, tv, tdo, p);
   if (e != cudaSuccess) return e;
-  const long long joins = (long long)B * Sk * 16 + (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) +
-                          (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
-  const long long blocks = (joins + 255) / 256, most = 8LL * sms;
+  const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
+  const long long rows = (long long)B * Sk, blocks = rows > (cut + 255) / 256 ? rows : (cut + 255) / 256, most = 8LL * sms;
   return launch_dependent(bwd_join_kernel, (int)(blocks < most ? blocks : most), 256, stream, p);
 }
 
