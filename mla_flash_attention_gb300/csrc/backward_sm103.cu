@@ -6,12 +6,12 @@
 //   dQ = scale dS K,  dK = scale dS' Q   (the rope key is shared by every head: its gradient
 //   is the sum over heads, accumulated by fp32 atomics).
 //
-// Two CTA roles share one launch, one kernel body and one shared-memory plan:
-//   key-tile CTAs (b, h, 128 keys): K and V stay in shared memory; query tiles stream by.
+// Two roles of units share one launch, one kernel body and one shared-memory plan:
+//   key-tile units (b, h, 128 keys): K and V stay in shared memory; query tiles stream by.
 //     TMEM: X [0,128) S' = K Q' (keys on lanes), then dP' = V dO'; dV [128,256);
 //           dK [256,448) (nope 128 + rope 64); Y [448,512) P', then dS' (bf16 pairs)
 //     MMAs per query tile n: dP'(n), dV += P' dO (TS: A = Y), S'(n+1), dK += dS' Q (TS: A = Y)
-//   query-tile CTAs (b, h, 128 queries): Q and dO stay; key tiles stream by.
+//   query-tile units (b, h, 128 queries): Q and dO stay; key tiles stream by.
 //     TMEM: X [0,128) S = Q K'; [128,256) dP = dO V'; dQ [256,448); Y [448,512) dS (bf16)
 //     MMAs per key tile n: S(n+1), dQ += dS K (TS: A = Y), dP(n+1)
 //   Scores of the next tile are issued as soon as the elementwise warps have read the
@@ -57,7 +57,7 @@ struct Params {
   float* dk_rope;      // [B, S, 64], accumulated (zeroed before the launch)
   uint16_t* dv;        // [B, S, H, 128]
   unsigned int* err;
-  int B, H, S, S_pad, nt, causal, n_key_ctas;
+  int B, H, S, S_pad, nt, causal, n_key_ctas, n_units;
   float scale, scale_log2;
   // cross attention: S is Sq, nt the query tiles
   int Sk, nkt;             // keys, key tiles of Sk
@@ -67,6 +67,7 @@ struct Params {
   float *part_kv;          // n_qs > 1: [key role's CTAs][128][dV 128 | dK nope 128]
   float *part_q;           // n_ks > 1: [query role's CTAs][128][192]
   uint16_t* dk_rope_out;   // [B, Sk, 64]
+  int wide;                // the bf16 gradients are 32-byte aligned
 };
 
 __device__ __forceinline__ int key_len(const Params& p, int b) {
@@ -80,8 +81,8 @@ __device__ __forceinline__ int share_begin(int tiles, int s, int n) {
 struct Bars {
   // one full barrier per 16 KB chunk of a streamed tile, so the MMAs over its first chunk can
   // start while the later ones are still arriving
-  uint64_t fix_full, ring_full[2][3], ring_empty[2], one_full[2], one_empty;
-  uint64_t s_full, x_read, dp_full, dp_read, p_ready, dv_done, ds_ready, acc_step, acc_done;
+  uint64_t fix3_full, fix3_empty, fix2_full, fix2_empty, ring_full[2][3], ring_empty[2], one_full[2], one_empty;
+  uint64_t s_full, x_read, dp_full, dp_read, p_ready, dv_done, ds_ready, acc_step, acc_done, acc_free, drained;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -90,16 +91,13 @@ struct Bars {
 // One warp per (b, h, 32 consecutive queries): each 256-byte row of dO and O is read by the
 // whole warp (8 bytes a lane), the 32 per-lane partial sums are reduced across lanes by a
 // transposing butterfly (16 + 8 + 4 + 2 + 1 exchanges) that leaves row i0 + lane's sum in
-// lane `lane`, so the D and LSE accesses are 128-byte coalesced.  kCross: a row that saw no key (LSE = -inf)
-// gets -inf like the padding, so its weights are 0.
-template <bool kCross>
+// lane `lane`, so the D and LSE accesses are 128-byte coalesced.
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restrict__ out,
                                                        const uint16_t* __restrict__ d_out,
                                                        const float* __restrict__ lse,
                                                        float* __restrict__ nlse2,
                                                        float* __restrict__ dvec, int B, int H,
                                                        int S, int S_pad) {
-  if (kCross) wait_for_stream();
   const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int groups = S_pad / 32;
@@ -142,12 +140,56 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restric
   const size_t vo = (size_t)bh * S_pad + i;
   if (i < S) {
     dvec[vo] = part[0];
-    const float of = lse[(size_t)bh * S + i];
-    nlse2[vo] = kCross && of == -INFINITY ? -INFINITY : -of * 1.4426950408889634f;
+    nlse2[vo] = -lse[(size_t)bh * S + i] * 1.4426950408889634f;
   } else {
     dvec[vo] = 0.f;
     nlse2[vo] = -INFINITY;
   }
+}
+
+// The same for cross attention, whose batches are often too few for that many rows a warp (128 rows of 152 heads:
+// 21 us): a warp takes eight rows of a head, 16 lanes a row, all its loads under way at once.  A row that saw no
+// key (LSE = -inf) gets -inf like the padding, so its weights are 0.
+__global__ void __launch_bounds__(256) cross_prep_kernel(const uint16_t* __restrict__ out,
+                                                         const uint16_t* __restrict__ d_out,
+                                                         const float* __restrict__ lse, float* __restrict__ nlse2,
+                                                         float* __restrict__ dvec, int B, int H, int S, int S_pad) {
+  wait_for_stream();
+  const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, groups = S_pad / 8;
+  if (task >= (long long)B * H * groups) return;
+  const int bh = static_cast<int>(task / groups), i0 = static_cast<int>(task - (long long)bh * groups) * 8;
+  const int b = bh / H, h = bh - b * H;
+  uint4 a[4], o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + 2 * k + (lane >> 4);
+    const size_t ro = (((size_t)b * S + i) * H + h) * 128 + (lane & 15) * 8;
+    a[k] = o[k] = make_uint4(0, 0, 0, 0);
+    if (i < S) {
+      a[k] = __ldg(reinterpret_cast<const uint4*>(d_out + ro));
+      o[k] = __ldg(reinterpret_cast<const uint4*>(out + ro));
+    }
+  }
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+  float mine = 0.f;  // lane 16 r + 2 k: of row 2 k + r
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+    float d = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d = fmaf(hi(x[j]), hi(y[j]), fmaf(lo(x[j]), lo(y[j]), d));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if ((lane & 15) == 2 * k) mine = d;
+  }
+  if ((lane & 15) >= 8 || (lane & 1)) return;
+  const int i = i0 + (lane & 15) + (lane >> 4);
+  const size_t vo = (size_t)bh * S_pad + i;
+  const float of = i < S ? lse[(size_t)bh * S + i] : -INFINITY;
+  dvec[vo] = mine;
+  nlse2[vo] = of == -INFINITY ? -INFINITY : -of * 1.4426950408889634f;
 }
 
 // Zero the rope-key gradient accumulator (n4 float4 stores).
@@ -171,17 +213,42 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t (&u)
   }
 }
 
-// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst
-__device__ __forceinline__ void store_f32x32(float* dst, const uint32_t (&u)[32], float mul) {
-  float4* d = reinterpret_cast<float4*>(dst);
+// The same in two whole sectors, dst 32-byte aligned: a warp's lanes write rows that lie apart, and 16 bytes
+// at a time took a request for every half sector.
+__device__ __forceinline__ void store_bf16x32_wide(uint16_t* dst, const uint32_t (&u)[32], float mul) {
 #pragma unroll
-  for (int x = 0; x < 8; ++x)
-    d[x] = make_float4(__uint_as_float(u[4 * x]) * mul, __uint_as_float(u[4 * x + 1]) * mul,
-                       __uint_as_float(u[4 * x + 2]) * mul, __uint_as_float(u[4 * x + 3]) * mul);
+  for (int x = 0; x < 2; ++x) {
+    uint32_t w[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      w[y] = ptx::pack_bf16x2(__uint_as_float(u[16 * x + 2 * y]) * mul, __uint_as_float(u[16 * x + 2 * y + 1]) * mul);
+    ptx::st_v8(dst + 16 * x, w);
+  }
+}
+
+// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst
+// (a workspace's 32-byte aligned)
+__device__ __forceinline__ void store_f32x32(float* dst, const uint32_t (&u)[32], float mul) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint32_t w[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(__uint_as_float(u[8 * x + y]) * mul);
+    ptx::st_v8(dst + 8 * x, w);
+  }
 }
 
 struct Maps {
   const CUtensorMap *qn, *qr, *kn, *kr, *v, *dout;
+};
+
+// Where a thread's role stands in the run of units that its CTA works through: steps and units before this
+// one (the phases of the barriers go on from unit to unit), and copies under way.
+struct Flow {
+  uint32_t g = 0, u = 0;
+  uint32_t n_fix3 = 0, n_fix2 = 0, n_ring = 0, n_one = 0;
+  bool after_key = false;  // the unit before was of the key role
+  bool ok = true;
 };
 
 // kKeyRole: this CTA owns key tile `tile` and streams query tiles (dK, dV); otherwise it
@@ -189,7 +256,7 @@ struct Maps {
 // role's CTAs.
 template <bool kKeyRole, bool kCross>
 __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigned char* sm,
-                                         Bars& bars, int b, int h, int tile, int share, int cta) {
+                                         Bars& bars, int b, int h, int tile, int share, int cta, Flow& f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = kCross ? key_len(p, b) : p.S;  // keys
   int t_begin, t_end;
@@ -202,6 +269,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     t_end = kKeyRole ? p.nt : (p.causal ? tile + 1 : p.nt);
   }
   const int nsteps = t_end - t_begin;
+  const uint32_t g = f.g;  // step n of this unit is step g + n of the CTA
   const int rows = kCross && kKeyRole ? p.Sk : p.S;  // of the owned operand and its gradients
   const int bh = b * p.H + h;
   const uint32_t tmem = bars.tmem_base;
@@ -228,22 +296,31 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       ptx::prefetch_tensormap(m.qn);
       ptx::prefetch_tensormap(m.kn);
       const int row0 = tile * BT;
-      ptx::mbar_arrive_expect_tx(&bars.fix_full, 5 * kChunk);
-      unsigned char* f3 = sm + kOffFix3;
-      unsigned char* f2_ = sm + kOffFix2;
-      if (kKeyRole) {
-        ptx::tma_load_4d(f3, m.kn, &bars.fix_full, 0, h, row0, b);
-        ptx::tma_load_4d(f3 + kChunk, m.kn, &bars.fix_full, 64, h, row0, b);
-        ptx::tma_load_3d(f3 + 2 * kChunk, m.kr, &bars.fix_full, 0, row0, b);
-        ptx::tma_load_4d(f2_, m.v, &bars.fix_full, 0, h, row0, b);
-        ptx::tma_load_4d(f2_ + kChunk, m.v, &bars.fix_full, 64, h, row0, b);
-      } else {
-        ptx::tma_load_4d(f3, m.qn, &bars.fix_full, 0, h, row0, b);
-        ptx::tma_load_4d(f3 + kChunk, m.qn, &bars.fix_full, 64, h, row0, b);
-        ptx::tma_load_4d(f3 + 2 * kChunk, m.qr, &bars.fix_full, 0, h, row0, b);
-        ptx::tma_load_4d(f2_, m.dout, &bars.fix_full, 0, h, row0, b);
-        ptx::tma_load_4d(f2_ + kChunk, m.dout, &bars.fix_full, 64, h, row0, b);
-      }
+      // the owned tiles, each as soon as the unit before has formed its last products with it
+      auto load_fix3 = [&]() -> bool {
+        if (!ptx::mbar_wait(&bars.fix3_empty, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
+        unsigned char* f3 = sm + kOffFix3;
+        ptx::mbar_arrive_expect_tx(&bars.fix3_full, 3 * kChunk);
+        const CUtensorMap* nope = kKeyRole ? m.kn : m.qn;
+        ptx::tma_load_4d(f3, nope, &bars.fix3_full, 0, h, row0, b);
+        ptx::tma_load_4d(f3 + kChunk, nope, &bars.fix3_full, 64, h, row0, b);
+        if (kKeyRole)
+          ptx::tma_load_3d(f3 + 2 * kChunk, m.kr, &bars.fix3_full, 0, row0, b);
+        else
+          ptx::tma_load_4d(f3 + 2 * kChunk, m.qr, &bars.fix3_full, 0, h, row0, b);
+        ++f.n_fix3;
+        return true;
+      };
+      auto load_fix2 = [&]() -> bool {
+        if (!ptx::mbar_wait(&bars.fix2_empty, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
+        unsigned char* f2_ = sm + kOffFix2;
+        ptx::mbar_arrive_expect_tx(&bars.fix2_full, 2 * kChunk);
+        const CUtensorMap* of = kKeyRole ? m.v : m.dout;
+        ptx::tma_load_4d(f2_, of, &bars.fix2_full, 0, h, row0, b);
+        ptx::tma_load_4d(f2_ + kChunk, of, &bars.fix2_full, 64, h, row0, b);
+        ++f.n_fix2;
+        return true;
+      };
       constexpr int kAhead = 2;  // tiles warmed in L2 ahead of their load
       auto warm = [&](int n) {
         const int r0 = (t_begin + n) * BT;
@@ -265,11 +342,12 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       };
       for (int n = 0; n < kAhead && n < nsteps; ++n) warm(n);
-      int n_ring = 0, n_one = 0;  // tiles under way
-      for (int n = 0; n < nsteps; ++n) {
+      f.ok = load_fix3();
+      for (int n = 0; f.ok && n < nsteps; ++n) {
         if (n + kAhead < nsteps) warm(n + kAhead);
-        const int r0 = (t_begin + n) * BT, s = n & 1;
-        if (!ptx::mbar_wait(&bars.ring_empty[s], ((n >> 1) & 1) ^ 1, abort_flag, p.err)) break;
+        const uint32_t step = g + n;
+        const int r0 = (t_begin + n) * BT, s = step & 1;
+        if (!(f.ok = ptx::mbar_wait(&bars.ring_empty[s], ((step >> 1) & 1) ^ 1, abort_flag, p.err))) break;
         unsigned char* dst = sm + kOffRing + s * 3 * kChunk;
         if (kKeyRole) {
           ptx::mbar_arrive_expect_tx(&bars.ring_full[s][0], kChunk + 2 * BT * 4);
@@ -288,24 +366,19 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tma_load_4d(dst + kChunk, m.kn, &bars.ring_full[s][1], 64, h, r0, b);
           ptx::tma_load_3d(dst + 2 * kChunk, m.kr, &bars.ring_full[s][2], 0, r0, b);
         }
-        n_ring = n + 1;
-        if (!ptx::mbar_wait(&bars.one_empty, (n & 1) ^ 1, abort_flag, p.err)) break;
+        ++f.n_ring;
+        if (n == 0 && !(f.ok = load_fix2())) break;
+        if (!(f.ok = ptx::mbar_wait(&bars.one_empty, (step & 1) ^ 1, abort_flag, p.err))) break;
         unsigned char* one = sm + kOffOne;
         const CUtensorMap* tm = kKeyRole ? m.dout : m.v;
         ptx::mbar_arrive_expect_tx(&bars.one_full[0], kChunk);
         ptx::mbar_arrive_expect_tx(&bars.one_full[1], kChunk);
         ptx::tma_load_4d(one, tm, &bars.one_full[0], 0, h, r0, b);
         ptx::tma_load_4d(one + kChunk, tm, &bars.one_full[1], 64, h, r0, b);
-        n_one = n + 1;
-      }
-      if constexpr (kCross) {  // copies that after an abort nobody may wait for land before the CTA leaves
-        ptx::mbar_wait_drain(&bars.fix_full, 0);
-        for (int v = n_ring > 2 ? n_ring - 2 : 0; v < n_ring; ++v)
-          for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
-        for (int c = 0; c < 2 && n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (n_one - 1) & 1);
+        ++f.n_one;
       }
     }
-    __syncwarp();
+    f.ok = __all_sync(0xffffffffu, f.ok);
   } else if (warp == 1) {
     if (ptx::elect_one()) {
       // ------------------------------------------------------------ MMA issuer
@@ -314,14 +387,14 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       constexpr uint32_t kIdAcc = ptx::make_idesc(1, BT, 192, 0, 1);  // B N-major, N = 192
       const uint32_t base = ptx::smem_u32(sm);
       const uint32_t one = base + kOffOne;
-      auto ring_of = [&](int n) { return base + kOffRing + (n & 1) * 3 * kChunk; };
+      auto ring_of = [&](int n) { return base + kOffRing + ((g + n) & 1) * 3 * kChunk; };
       // scores over the 192-deep nope+rope contraction (key role: transposed, keys on lanes)
       auto issue_s = [&](int n) -> bool {
         const uint32_t ring = ring_of(n);
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
           if ((k & 3) == 0) {  // each 64-deep chunk as soon as it has landed
-            if (!ptx::mbar_wait(&bars.ring_full[n & 1][k >> 2], (n >> 1) & 1, abort_flag, p.err)) return false;
+            if (!ptx::mbar_wait(&bars.ring_full[(g + n) & 1][k >> 2], ((g + n) >> 1) & 1, abort_flag, p.err)) return false;
             ptx::tc_fence_after();
           }
           const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
@@ -329,6 +402,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
                            ptx::sw128_desc(ring + off, 16, 1024), kIdS, k > 0);
         }
         ptx::mma_commit(&bars.s_full);
+        if (n + 1 == nsteps) ptx::mma_commit(&bars.fix3_empty);
         return true;
       };
       // dP = dO V' over d_v = 128 (key role: dP' = V dO' into X; query role: own columns)
@@ -336,7 +410,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if ((k & 3) == 0) {
-            if (!ptx::mbar_wait(&bars.one_full[k >> 2], n & 1, abort_flag, p.err)) return false;
+            if (!ptx::mbar_wait(&bars.one_full[k >> 2], (g + n) & 1, abort_flag, p.err)) return false;
+            if (n == 0 && k == 0 && !ptx::mbar_wait(&bars.fix2_full, f.u & 1, abort_flag, p.err)) return false;
             ptx::tc_fence_after();
           }
           const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
@@ -345,6 +420,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
                            ptx::sw128_desc(one + off, 16, 1024), kIdS, k > 0);
         }
         ptx::mma_commit(&bars.dp_full);
+        if (n + 1 == nsteps) ptx::mma_commit(&bars.fix2_empty);
         return true;
       };
       // dK += dS' Q (key role) or dQ += dS K: A = dS (bf16 pairs in Y), B = the streamed
@@ -356,21 +432,29 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::mma_bf16_ts(tmem + kColAcc, tmem + kColY + k * 8,
                            ptx::sw128_desc(ring + k * 2048, kChunk, 1024), kIdAcc,
                            (n > 0 || k > 0) ? 1u : 0u);
-        ptx::mma_commit(&bars.ring_empty[n & 1]);
+        ptx::mma_commit(&bars.ring_empty[(g + n) & 1]);
         ptx::mma_commit(&bars.acc_step);
       };
       auto wait = [&](uint64_t* bar, int n) -> bool {
-        if (!ptx::mbar_wait(bar, n & 1, abort_flag, p.err)) return false;
+        if (!ptx::mbar_wait(bar, (g + n) & 1, abort_flag, p.err)) return false;
         ptx::tc_fence_after();
         return true;
       };
-      bool ok = ptx::mbar_wait(&bars.fix_full, 0, abort_flag, p.err) && issue_s(0);
+      // the accumulators of the unit before were read
+      auto acc_free = [&]() -> bool {
+        if (!ptx::mbar_wait(&bars.acc_free, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
+        ptx::tc_fence_after();
+        return true;
+      };
+      // (the score columns were read: dP' of the unit before lay in them, or its dP was read after them)
+      bool ok = ptx::mbar_wait(&bars.fix3_full, f.u & 1, abort_flag, p.err) && (g == 0 || wait(&bars.dp_read, -1)) &&
+                issue_s(0);
       if (kKeyRole) {
         // per query tile n: dP'(n) | dV(n) | S'(n+1) | dK(n) -- the next scores run while the
         // elementwise warps turn dP'(n) into dS(n)
         for (int n = 0; ok && n < nsteps; ++n) {
           if (!(ok = wait(&bars.x_read, n) && issue_dp(n))) break;
-          if (!(ok = wait(&bars.p_ready, n))) break;
+          if (!(ok = wait(&bars.p_ready, n) && (n > 0 || acc_free()))) break;
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // dV += P' dO: A = P' (bf16 pairs in Y), B = dO N-major
             ptx::mma_bf16_ts(tmem + kColDV, tmem + kColY + k * 8,
@@ -384,10 +468,12 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       } else {
         // per key tile n: S(n+1) | dQ(n) | dP(n+1), with dP(0) issued up front
+        // (dP's columns are those of dV in the key role)
+        if (ok && f.after_key) ok = acc_free();
         if (ok && (ok = issue_dp(0))) ptx::mma_commit(&bars.one_empty);
         for (int n = 0; ok && n < nsteps; ++n) {
           if (n + 1 < nsteps && !(ok = wait(&bars.x_read, n) && issue_s(n + 1))) break;
-          if (!(ok = wait(&bars.ds_ready, n))) break;
+          if (!(ok = wait(&bars.ds_ready, n) && (n > 0 || acc_free()))) break;
           issue_acc(n);
           if (n + 1 < nsteps) {
             if (!(ok = wait(&bars.dp_read, n) && issue_dp(n + 1))) break;
@@ -395,11 +481,10 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           }
         }
       }
-      if (ok || kCross) ptx::mma_commit(&bars.acc_done);
-      // after an abort: every MMA issued completes before the CTA frees its TMEM
-      if (kCross && !ok) ptx::mbar_wait_drain(&bars.acc_done, 0);
+      if (ok) ptx::mma_commit(&bars.acc_done);
+      f.ok = ok;
     }
-    __syncwarp();
+    f.ok = __all_sync(0xffffffffu, f.ok);
   } else {
     // -------------------------------------------------------------- elementwise warps
     const int q4 = warp & 3, hf = (warp - 2) >> 2;
@@ -429,11 +514,12 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     };
     bool ok = true;
     for (int n = 0; n < nsteps; ++n) {
-      const int t = t_begin + n, s = n & 1;
+      const uint32_t step = g + n;
+      const int t = t_begin + n, s = step & 1;
       const float* vec = reinterpret_cast<const float*>(sm + kOffVec + s * 2 * BT * 4);
-      ok = wait(&bars.s_full, n & 1);
+      ok = wait(&bars.s_full, step & 1);
       // the query vectors of this stage arrived with its TMA transaction: observe it directly
-      if (kKeyRole && ok) ok = wait(&bars.ring_full[s][0], (n >> 1) & 1);
+      if (kKeyRole && ok) ok = wait(&bars.ring_full[s][0], (step >> 1) & 1);
       if (!ok) break;
       uint32_t u[64];
       ptx::tmem_ld32(tX, *reinterpret_cast<uint32_t(*)[32]>(u));
@@ -480,14 +566,14 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       uint32_t pk[32];
       if (kKeyRole) {
         // P' (bf16) into Y once dK(n-1) has consumed the dS' held there
-        if (n > 0 && !(ok = wait(&bars.acc_step, (n - 1) & 1))) break;
+        if (n > 0 && !(ok = wait(&bars.acc_step, (step - 1) & 1))) break;
 #pragma unroll
         for (int x = 0; x < 32; ++x) pk[x] = ptx::pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
         ptx::tmem_st32(tY, pk);
         ptx::tmem_st_wait();
         arrive(&bars.p_ready);
       }
-      if (!(ok = wait(&bars.dp_full, n & 1))) break;
+      if (!(ok = wait(&bars.dp_full, step & 1))) break;
       ptx::tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(u));
       ptx::tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
       ptx::tmem_ld_wait();
@@ -499,7 +585,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (hf * 64 + x >= lim) u[x] = 0u;
-          for (int c = 0; c < 3 && ok; ++c) ok = wait(&bars.ring_full[s][c], (n >> 1) & 1);
+          for (int c = 0; c < 3 && ok; ++c) ok = wait(&bars.ring_full[s][c], (step >> 1) & 1);
           if (!ok) break;
           if (r >= lim) {
             for (int c = hf; c < 3; c += 2) {
@@ -533,8 +619,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       // dS into Y once its previous reader is done: dV(n) (key role: P' lives there) or
       // dQ(n-1)
       if (kKeyRole) {
-        if (!(ok = wait(&bars.dv_done, n & 1))) break;
-      } else if (n > 0 && !(ok = wait(&bars.acc_step, (n - 1) & 1))) {
+        if (!(ok = wait(&bars.dv_done, step & 1))) break;
+      } else if (n > 0 && !(ok = wait(&bars.acc_step, (step - 1) & 1))) {
         break;
       }
       ptx::tmem_st32(tY, pk);
@@ -542,10 +628,16 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       arrive(&bars.ds_ready);
     }
     // ---------------------------------------------------------------- epilogue
-    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.acc_done, 0, abort_flag, p.err));
+    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.acc_done, f.u & 1, abort_flag, p.err));
     if (ok) {
       ptx::tc_fence_after();
       const bool store = row_idx < rows;
+      auto put = [&](uint16_t* dst, const uint32_t(&w)[32], float mul) {
+        if (kCross && p.wide)
+          store_bf16x32_wide(dst, w, mul);
+        else
+          store_bf16x32(dst, w, mul);
+      };
       const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
       if (kKeyRole) {
         // half 0: dV (4 chunks) and rope columns 0..31 of dK; half 1: dK nope (4 chunks) and
@@ -563,7 +655,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
               if (c < 4 && p.n_qs == 1) {
 #pragma unroll
                 for (int x = 0; x < 32; ++x) w[x] = 0u;
-                store_bf16x32((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, 1.f);
+                put((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, 1.f);
               }
               continue;
             }
@@ -573,7 +665,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
             else if (p.n_qs > 1)
               store_f32x32(p.part_kv + ((size_t)cta * BT + r) * 256 + hf * 128 + 32 * c, w, mul);
             else
-              store_bf16x32((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, mul);
+              put((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, mul);
             continue;
           }
           if (c < 4) {
@@ -603,13 +695,18 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           if (kCross && p.n_ks > 1)
             store_f32x32(p.part_q + ((size_t)cta * BT + r) * 192 + 32 * cc, w, p.scale);
           else if (cc < 4)
-            store_bf16x32(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
+            put(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
           else
-            store_bf16x32(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
+            put(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
         }
       }
+      arrive(&bars.acc_free);
     }
+    f.ok = ok;
   }
+  f.g += nsteps;
+  ++f.u;
+  f.after_key = kKeyRole;
 }
 
 template <bool kCross>
@@ -625,20 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ Bars bars;
   const int warp = threadIdx.x >> 5;
-  // key-tile CTAs first, then query-tile CTAs; within a role the tiles of one (b, h) are
-  // consecutive (most work first), so CTAs that run together stream the same (b, h)'s tiles
-  // and find them in L2
-  const bool key_role = static_cast<int>(blockIdx.x) < p.n_key_ctas;
-  const int cta = key_role ? blockIdx.x : blockIdx.x - p.n_key_ctas;
-  const int shares = !kCross ? 1 : key_role ? p.n_qs : p.n_ks, idx = cta / shares, share = cta % shares;
-  const int tiles = kCross && key_role ? p.nkt : p.nt;
-  const int bh = idx / tiles;
-  const int tile = key_role || kCross ? idx % tiles : tiles - 1 - idx % tiles;
-  const int b = bh / p.H, h = bh % p.H;
-
   if (threadIdx.x == 0) {
     bars.abort_flag = 0;
-    ptx::mbar_init(&bars.fix_full, 1);
+    ptx::mbar_init(&bars.fix3_full, 1);
+    ptx::mbar_init(&bars.fix3_empty, 1);
+    ptx::mbar_init(&bars.fix2_full, 1);
+    ptx::mbar_init(&bars.fix2_empty, 1);
     for (int s = 0; s < 2; ++s) {
       for (int c = 0; c < 3; ++c) ptx::mbar_init(&bars.ring_full[s][c], 1);
       ptx::mbar_init(&bars.ring_empty[s], 1);
@@ -655,6 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&bars.dv_done, 1);
     ptx::mbar_init(&bars.ds_ready, 8);
     ptx::mbar_init(&bars.acc_done, 1);
+    ptx::mbar_init(&bars.acc_free, 8);
+    ptx::mbar_init(&bars.drained, 1);
     ptx::fence_barrier_init();
   }
   if (warp == 0) ptx::tmem_alloc(&bars.tmem_base, 512);
@@ -663,10 +754,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   if (kCross) wait_for_stream();
   const Maps m{&tm_qn, &tm_qr, &tm_kn, &tm_kr, &tm_v, &tm_do};
-  if (key_role)
-    bwd_body<true, kCross>(m, p, sm, bars, b, h, tile, share, cta);
-  else
-    bwd_body<false, kCross>(m, p, sm, bars, b, h, tile, share, cta);
+  // Key-tile units first, then query-tile units; within a role the tiles of one (b, h) are consecutive (most
+  // work first), so CTAs that run together stream the same (b, h)'s tiles and find them in L2.  A CTA takes
+  // every gridDim.x-th unit (the prefill's has one): the next unit's tiles are loaded, and its first scores
+  // formed, while this one's accumulators are stored.
+  Flow f;
+  for (unsigned unit = blockIdx.x; f.ok && unit < static_cast<unsigned>(p.n_units); unit += gridDim.x) {
+    const bool key_role = unit < static_cast<unsigned>(p.n_key_ctas);
+    const unsigned cta = key_role ? unit : unit - p.n_key_ctas;
+    const unsigned shares = !kCross ? 1 : key_role ? p.n_qs : p.n_ks, idx = cta / shares, share = cta % shares;
+    const unsigned tiles = kCross && key_role ? p.nkt : p.nt;
+    const int bh = idx / tiles;
+    const int tile = key_role || kCross ? idx % tiles : tiles - 1 - idx % tiles;
+    const int b = bh / p.H, h = bh % p.H;
+    if (key_role)
+      bwd_body<true, kCross>(m, p, sm, bars, b, h, tile, share, cta, f);
+    else
+      bwd_body<false, kCross>(m, p, sm, bars, b, h, tile, share, cta, f);
+  }
+  if (!f.ok && warp < 2) {
+    // after an abort: copies that nobody may wait for land, and every MMA issued completes, before the CTA
+    // gives its memory back
+    if (ptx::elect_one()) {
+      if (warp == 0) {
+        if (f.n_fix3 > 0) ptx::mbar_wait_drain(&bars.fix3_full, (f.n_fix3 - 1) & 1);
+        if (f.n_fix2 > 0) ptx::mbar_wait_drain(&bars.fix2_full, (f.n_fix2 - 1) & 1);
+        for (uint32_t v = f.n_ring > 2 ? f.n_ring - 2 : 0; v < f.n_ring; ++v)
+          for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
+        for (int c = 0; c < 2 && f.n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (f.n_one - 1) & 1);
+      } else {
+        ptx::mma_commit(&bars.drained);
+        ptx::mbar_wait_drain(&bars.drained, 0);
+      }
+    }
+    __syncwarp();
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -797,7 +919,7 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
   const long long tasks = (long long)B * H * (S_pad / 32);
   const long long prep_blocks = (tasks + 7) / 8;
   if (prep_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  bwd_prep_kernel<false><<<(unsigned)prep_blocks, 256, 0, stream>>>(
+  bwd_prep_kernel<<<(unsigned)prep_blocks, 256, 0, stream>>>(
       static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(d_out), lse, nlse2, dvec, B,
       H, S, S_pad);
   bwd_zero_kernel<<<1024, 256, 0, stream>>>(reinterpret_cast<float4*>(dk_rope),
@@ -835,6 +957,7 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
   const long long per_role = (long long)B * H * nt;
   if (2 * per_role > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.n_key_ctas = (int)per_role;
+  p.n_units = (int)(2 * per_role);
   static unsigned long long smem_set = 0;
   if ((e = smem_attr_once(prefill_bwd_kernel<false>, kSmemAlloc, &smem_set)) != cudaSuccess) return e;
   prefill_bwd_kernel<false><<<(unsigned)(2 * per_role), kThreads, kSmemAlloc, stream>>>(tqn, tqr, tkn, tkr, tv, tdo, p);
@@ -862,7 +985,7 @@ struct CrossBwdWorkspace {
     rope = take((size_t)B * H * c.n_qs * Sk * 64 * sizeof(float));
     kv = take(c.n_qs > 1 ? (size_t)c.key_ctas * sm103_bwd::BT * 256 * sizeof(float) : 0);
     q = take(c.n_ks > 1 ? (size_t)c.query_ctas * sm103_bwd::BT * 192 * sizeof(float) : 0);
-    bytes = at;
+    bytes = at + 32;
   }
 };
 }  // namespace
@@ -888,7 +1011,8 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
       !bwd_map_bshd(&tdo, d_out, B, Sq, H, 128) ||
       encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
     return cudaErrorInvalidValue;
-  char* base = static_cast<char*>(workspace);
+  // (the workspace is 16-byte aligned, its parts 32)
+  char* base = static_cast<char*>(workspace) + (reinterpret_cast<uintptr_t>(workspace) & 16);
   auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
   Params p = {};
   p.nlse2 = at(w.nlse2);
@@ -909,22 +1033,26 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   p.n_qs = c.n_qs;
   p.n_ks = c.n_ks;
   p.key_lens = key_lens;
+  const void* grads[] = {dq_nope, dq_rope, dk_nope, dv};
+  p.wide = 1;
+  for (const void* g : grads) p.wide &= (reinterpret_cast<uintptr_t>(g) & 31) == 0;
   p.part_rope = at(w.rope);
   p.part_kv = at(w.kv);
   p.part_q = at(w.q);
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.n_key_ctas = (int)c.key_ctas;
-  if (c.key_ctas + c.query_ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const long long tasks = (long long)B * H * (p.S_pad / 32);
+  p.n_units = (int)(c.key_ctas + c.query_ctas);
+  if (c.key_ctas + c.query_ctas > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
+  const long long tasks = (long long)B * H * (p.S_pad / 8);
   if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   static unsigned long long smem_set = 0;
   cudaError_t e = smem_attr_once(prefill_bwd_kernel<true>, kSmemAlloc, &smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(bwd_prep_kernel<true>, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
+  e = launch_dependent(cross_prep_kernel, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
                        static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.S_pad);
   if (e != cudaSuccess) return e;
-  e = launch_dependent_smem(prefill_bwd_kernel<true>, (int)(c.key_ctas + c.query_ctas), kThreads, kSmemAlloc, stream, tqn,
+  e = launch_dependent_smem(prefill_bwd_kernel<true>, p.n_units < sms ? p.n_units : sms, kThreads, kSmemAlloc, stream, tqn,
                             tqr, tkn, tkr, tv, tdo, p);
   if (e != cudaSuccess) return e;
   const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
