@@ -529,14 +529,18 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       // P = exp2(s * scale * log2(e) - LSE * log2(e)), two columns per packed instruction
       float pr[64];
       if (kKeyRole) {
-        const float2* nl = reinterpret_cast<const float2*>(vec) + hf * 32;  // per query
+        const float4* nl = reinterpret_cast<const float4*>(vec) + hf * 16;  // per query
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float2 l = nl[x];
-          const uint64_t a2 = ptx::fma2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
-                                        sc2, ptx::f2(l.x, l.y));
-          pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
-          pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
+        for (int x4 = 0; x4 < 16; ++x4) {
+          const float4 l4 = nl[x4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = 2 * x4 + e;
+            const uint64_t a2 = ptx::fma2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), sc2,
+                                          e == 0 ? ptx::f2(l4.x, l4.y) : ptx::f2(l4.z, l4.w));
+            pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
+            pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
+          }
         }
         if (!kCross && p.causal && t == tile) {  // diagonal tile: a query before the key sees nothing
 #pragma unroll
@@ -598,14 +602,18 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       }
       // dS = P * (dP - D) as bf16 pairs
       if (kKeyRole) {
-        const float2* dd = reinterpret_cast<const float2*>(vec + BT) + hf * 32;  // per query
+        const float4* dd = reinterpret_cast<const float4*>(vec + BT) + hf * 16;  // per query
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float2 d = dd[x];
-          const uint64_t g = ptx::mul2(ptx::f2(pr[2 * x], pr[2 * x + 1]),
-                                       ptx::sub2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
-                                                 ptx::f2(d.x, d.y)));
-          pk[x] = ptx::pack_bf16x2(ptx::f2_lo(g), ptx::f2_hi(g));
+        for (int x4 = 0; x4 < 16; ++x4) {
+          const float4 d4 = dd[x4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = 2 * x4 + e;
+            const uint64_t ds = ptx::mul2(ptx::f2(pr[2 * x], pr[2 * x + 1]),
+                                          ptx::sub2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
+                                                    e == 0 ? ptx::f2(d4.x, d4.y) : ptx::f2(d4.z, d4.w)));
+            pk[x] = ptx::pack_bf16x2(ptx::f2_lo(ds), ptx::f2_hi(ds));
+          }
         }
       } else {
         const uint64_t d2 = ptx::f2(d_row, d_row);
