@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/DimVector.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -18,14 +19,13 @@
 #include <optional>
 #include <string>
 #include <type_traits>
-#include <vector>
 
 #include "../../include/mla.h"
 
 namespace {
 
 using at::Tensor;
-using Shape = std::vector<int64_t>;
+using Shape = at::DimVector;  // (on the stack: a call checks up to twenty tensors)
 
 // The C entry points of the loaded library and the Python function that raises for a status.
 decltype(&mla_qk_norm_rope) f_norm = nullptr;
@@ -75,20 +75,24 @@ const Tensor& tensor(PyObject* o, const char* name, int dims = -1) {
   return t;
 }
 
-// The checks of one tensor; strided: any strides with the last dimension contiguous.
-void need(const Tensor& t, const char* name, at::ScalarType dtype, c10::IntArrayRef shape,
-          const std::optional<at::Device>& dev, bool strided = false) {
+// What need() says of a tensor that does not fit.
+[[noreturn]] void misfit(const Tensor& t, const char* name, at::ScalarType dtype, c10::IntArrayRef shape,
+                         const std::optional<at::Device>& dev, bool strided) {
   const std::string n(name);
   if (t.scalar_type() != dtype)
     fail(PyExc_TypeError, n + " must have dtype " + show(dtype) + " (got " + show(t.scalar_type()) + ")");
   if (t.sizes() != shape) fail(PyExc_ValueError, n + " must have shape " + show(shape) + " (got " + show(t.sizes()) + ")");
   if (!t.is_cuda()) fail(PyExc_ValueError, n + " must be a CUDA tensor");
   if (dev && t.device() != *dev) fail(PyExc_ValueError, n + " must be on " + dev->str() + " (got " + t.device().str() + ")");
-  if (strided) {
-    if (t.size(-1) != 1 && t.stride(-1) != 1) fail(PyExc_ValueError, n + " must have a contiguous last dimension");
-  } else if (!t.is_contiguous()) {
-    fail(PyExc_ValueError, n + " must be contiguous");
-  }
+  fail(PyExc_ValueError, n + (strided ? " must have a contiguous last dimension" : " must be contiguous"));
+}
+
+// The checks of one tensor; strided: any strides with the last dimension contiguous.
+void need(const Tensor& t, const char* name, at::ScalarType dtype, c10::IntArrayRef shape,
+          const std::optional<at::Device>& dev, bool strided = false) {
+  const bool fits = t.scalar_type() == dtype && t.sizes() == shape && t.is_cuda() && (!dev || t.device() == *dev) &&
+                    (strided ? t.size(-1) == 1 || t.stride(-1) == 1 : t.is_contiguous());
+  if (!fits) misfit(t, name, dtype, shape, dev, strided);
 }
 
 void* ptr(const Tensor& t) { return t.defined() ? const_cast<void*>(t.const_data_ptr()) : nullptr; }
@@ -114,6 +118,14 @@ int64_t row_stride(const Tensor& t, const char* name) {
 
 Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, const at::Device& dev) {
   return at::detail::empty_cuda(shape, dtype, dev, std::nullopt);
+}
+
+// Elements [first, first + n) of t, one-dimensional, as a tensor that shares its storage.
+Tensor part(const Tensor& t, int64_t first, int64_t n) {
+  Tensor r = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+  r.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  r.unsafeGetTensorImpl()->set_storage_offset(first);
+  return r;
 }
 
 // A size as the C entry points take it.  One past an int's range is one that they refuse, not its low bits.
@@ -288,16 +300,22 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const Tensor* given[7] = {&o.q, &o.kn, &o.kr, &o.w[0], &o.w[1], &o.w[2], &o.w[3]};
   const char* const names[7] = {"grads[0]", "grads[1]", "grads[2]", "grads[3]", "grads[4]", "grads[5]", "grads[6]"};
-  Tensor g[7];
+  Tensor g[7], sums;  // the weights' gradients made here are parts of one allocation
   bool weights = false;
+  if (a[15] == Py_None && (o.w[0].defined() || o.w[1].defined() || o.w[2].defined() || o.w[3].defined()))
+    sums = empty({2 * (o.dn + o.dr)}, at::kFloat, o.dev);
   for (int i = 0; i < 7; ++i) {
     const Tensor& of = *given[i];
     if (a[15] != Py_None) member(a[15], "grads", 7, i);
     if (!of.defined()) continue;
     weights |= i >= 3;
     const at::ScalarType dtype = i < 3 ? at::kBFloat16 : at::kFloat;
+    if (a[15] == Py_None && i >= 3) {
+      g[i] = part(sums, (i - 3) / 2 * (o.dn + o.dr) + (i - 3) % 2 * o.dn, of.size(0));
+      continue;
+    }
     if (a[15] == Py_None) {
-      g[i] = i < 3 && !of.is_contiguous()
+      g[i] = !of.is_contiguous()
                  ? at::empty_strided(of.sizes(), of.strides(), at::TensorOptions().dtype(dtype).device(o.dev))
                  : empty(of.sizes(), dtype, o.dev);
       continue;
