@@ -30,6 +30,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "sm103_ptx.cuh"
 
@@ -68,6 +70,8 @@ struct Params {
   float *part_q;           // n_ks > 1: [query role's CTAs][128][192]
   uint16_t* dk_rope_out;   // [B, Sk, 64]
   int wide;                // the bf16 gradients are 32-byte aligned
+  size_t q_bytes, k_bytes, rope_bytes;                   // of dq_nope (dq_rope half), dk_nope and dv, dk_rope: for the
+  size_t part_rope_bytes, part_kv_bytes, part_q_bytes;   // store checks
 };
 
 __device__ __forceinline__ int key_len(const Params& p, int b) {
@@ -213,9 +217,23 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t (&u)
   }
 }
 
-// The same in two whole sectors, dst 32-byte aligned: a warp's lanes write rows that lie apart, and 16 bytes
-// at a time took a request for every half sector.
-__device__ __forceinline__ void store_bf16x32_wide(uint16_t* dst, const uint32_t (&u)[32], float mul) {
+// What one store_row writes, checked as a whole.
+struct alignas(16) Row64 {
+  uint4 v[4];
+};
+struct alignas(16) Row128 {
+  uint4 v[8];
+};
+
+// store_bf16x32 in two whole sectors where dst is 32-byte aligned: a warp's lanes write rows that lie apart, and
+// 16 bytes at a time took a request for every half sector.
+__device__ __forceinline__ void store_row(uint16_t* dst, const uint32_t (&u)[32], float mul, bool wide, const void* base,
+                                          size_t bytes, unsigned int* err) {
+  if (!MLA_STORE_OK(reinterpret_cast<Row64*>(dst), base, bytes, err)) return;
+  if (!wide) {
+    store_bf16x32(dst, u, mul);
+    return;
+  }
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     uint32_t w[8];
@@ -225,10 +243,10 @@ __device__ __forceinline__ void store_bf16x32_wide(uint16_t* dst, const uint32_t
     ptx::st_v8(dst + 16 * x, w);
   }
 }
-
-// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst
-// (a workspace's 32-byte aligned)
-__device__ __forceinline__ void store_f32x32(float* dst, const uint32_t (&u)[32], float mul) {
+// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst (32-byte aligned)
+__device__ __forceinline__ void store_row(float* dst, const uint32_t (&u)[32], float mul, const void* base, size_t bytes,
+                                          unsigned int* err) {
+  if (!MLA_STORE_OK(reinterpret_cast<Row128*>(dst), base, bytes, err)) return;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     uint32_t w[8];
@@ -281,11 +299,13 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     if (warp >= 2 && row_idx < rows && (kKeyRole ? p.n_qs : p.n_ks) == 1) {
       const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4* wide = reinterpret_cast<uint4*>((kKeyRole ? (hf == 0 ? p.dv : p.dk_nope) : p.dq_nope) + ro * 128);
+      uint16_t* to = kKeyRole ? (hf == 0 ? p.dv : p.dk_nope) : p.dq_nope;
+      uint4* wide = reinterpret_cast<uint4*>(to + ro * 128);
       for (int x = 0; x < 16; ++x)
-        if (kKeyRole || x / 8 == hf) wide[x] = zero;
-      if (!kKeyRole && hf == 0)
-        for (int x = 0; x < 8; ++x) reinterpret_cast<uint4*>(p.dq_rope + ro * 64)[x] = zero;
+        if ((kKeyRole || x / 8 == hf) && MLA_STORE_OK(wide + x, to, kKeyRole ? p.k_bytes : p.q_bytes, p.err)) wide[x] = zero;
+      uint4* narrow = reinterpret_cast<uint4*>(p.dq_rope + ro * 64);
+      for (int x = 0; x < 8; ++x)
+        if (!kKeyRole && hf == 0 && MLA_STORE_OK(narrow + x, p.dq_rope, p.q_bytes / 2, p.err)) narrow[x] = zero;
     }
     return;
   }
@@ -293,8 +313,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
   if (warp == 0) {
     if (ptx::elect_one()) {
       // ------------------------------------------------------------ TMA producer
-      ptx::prefetch_tensormap(m.qn);
-      ptx::prefetch_tensormap(m.kn);
       const int row0 = tile * BT;
       // the owned tiles, each as soon as the unit before has formed its last products with it
       auto load_fix3 = [&]() -> bool {
@@ -640,12 +658,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     if (ok) {
       ptx::tc_fence_after();
       const bool store = row_idx < rows;
-      auto put = [&](uint16_t* dst, const uint32_t(&w)[32], float mul) {
-        if (kCross && p.wide)
-          store_bf16x32_wide(dst, w, mul);
-        else
-          store_bf16x32(dst, w, mul);
-      };
       const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
       if (kKeyRole) {
         // half 0: dV (4 chunks) and rope columns 0..31 of dK; half 1: dK nope (4 chunks) and
@@ -657,25 +669,27 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           uint32_t w[32];
           ptx::tmem_ld32(tmem + lane_off + col, w);
           ptx::tmem_ld_wait();
-          if (!store) continue;
           if constexpr (kCross) {
             if (row_idx >= len) {  // lanes of no key
-              if (c < 4 && p.n_qs == 1) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) w[x] = 0u;
-                put((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, 1.f);
-              }
-              continue;
+              for (int x = 0; x < 32; ++x) w[x] = 0u;
             }
             const float mul = c < 4 && hf == 0 ? 1.f : p.scale;
-            if (c == 4)
-              store_f32x32(p.part_rope + (((size_t)bh * p.n_qs + share) * p.Sk + row_idx) * 64 + 32 * hf, w, mul);
-            else if (p.n_qs > 1)
-              store_f32x32(p.part_kv + ((size_t)cta * BT + r) * 256 + hf * 128 + 32 * c, w, mul);
-            else
-              put((hf == 0 ? p.dv : p.dk_nope) + ro * 128 + 32 * c, w, mul);
+            uint16_t* to = hf == 0 ? p.dv : p.dk_nope;
+            if (store) {
+              if (c == 4)
+                store_row(p.part_rope + (((size_t)bh * p.n_qs + share) * p.Sk + row_idx) * 64 + 32 * hf, w, mul, p.part_rope,
+                          p.part_rope_bytes, p.err);
+              else if (p.n_qs > 1)
+                store_row(p.part_kv + ((size_t)cta * BT + r) * 256 + hf * 128 + 32 * c, w, mul, p.part_kv, p.part_kv_bytes,
+                          p.err);
+              else
+                store_row(to + ro * 128 + 32 * c, w, mul, p.wide, to, p.k_bytes, p.err);
+            }
+            __syncwarp();
             continue;
           }
+          if (!store) continue;
           if (c < 4) {
             if (hf == 0)
               store_bf16x32(p.dv + ro * 128 + 32 * c, w, 1.f);
@@ -699,13 +713,23 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           uint32_t w[32];
           ptx::tmem_ld32(tmem + lane_off + kColAcc + 32 * cc, w);
           ptx::tmem_ld_wait();
+          if constexpr (kCross) {
+            if (store) {
+              if (p.n_ks > 1)
+                store_row(p.part_q + ((size_t)cta * BT + r) * 192 + 32 * cc, w, p.scale, p.part_q, p.part_q_bytes, p.err);
+              else if (cc < 4)
+                store_row(p.dq_nope + ro * 128 + 32 * cc, w, p.scale, p.wide, p.dq_nope, p.q_bytes, p.err);
+              else
+                store_row(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale, p.wide, p.dq_rope, p.q_bytes / 2, p.err);
+            }
+            __syncwarp();
+            continue;
+          }
           if (!store) continue;
-          if (kCross && p.n_ks > 1)
-            store_f32x32(p.part_q + ((size_t)cta * BT + r) * 192 + 32 * cc, w, p.scale);
-          else if (cc < 4)
-            put(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
+          if (cc < 4)
+            store_bf16x32(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
           else
-            put(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
+            store_bf16x32(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
         }
       }
       arrive(&bars.acc_free);
@@ -731,6 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tm_qn);
+    ptx::prefetch_tensormap(&tm_kn);
     bars.abort_flag = 0;
     ptx::mbar_init(&bars.fix3_full, 1);
     ptx::mbar_init(&bars.fix3_empty, 1);
@@ -780,23 +806,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       bwd_body<false, kCross>(m, p, sm, bars, b, h, tile, share, cta, f);
   }
-  if (!f.ok && warp < 2) {
-    // after an abort: copies that nobody may wait for land, and every MMA issued completes, before the CTA
-    // gives its memory back
-    if (ptx::elect_one()) {
-      if (warp == 0) {
-        if (f.n_fix3 > 0) ptx::mbar_wait_drain(&bars.fix3_full, (f.n_fix3 - 1) & 1);
-        if (f.n_fix2 > 0) ptx::mbar_wait_drain(&bars.fix2_full, (f.n_fix2 - 1) & 1);
-        for (uint32_t v = f.n_ring > 2 ? f.n_ring - 2 : 0; v < f.n_ring; ++v)
-          for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
-        for (int c = 0; c < 2 && f.n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (f.n_one - 1) & 1);
-      } else {
-        ptx::mma_commit(&bars.drained);
-        ptx::mbar_wait_drain(&bars.drained, 0);
-      }
+  // Nothing asynchronous outlives the CTA: commits arrive in its shared memory, and after an abort copies and
+  // products may be under way that nobody waits for.
+  if (warp < 2 && ptx::elect_one()) {
+    if (warp == 1) {
+      ptx::mma_commit(&bars.drained);
+      ptx::mbar_wait_drain(&bars.drained, 0);
+    } else if (!f.ok) {
+      if (f.n_fix3 > 0) ptx::mbar_wait_drain(&bars.fix3_full, (f.n_fix3 - 1) & 1);
+      if (f.n_fix2 > 0) ptx::mbar_wait_drain(&bars.fix2_full, (f.n_fix2 - 1) & 1);
+      for (uint32_t v = f.n_ring > 2 ? f.n_ring - 2 : 0; v < f.n_ring; ++v)
+        for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
+      for (int c = 0; c < 2 && f.n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (f.n_one - 1) & 1);
     }
-    __syncwarp();
   }
+  __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -813,8 +837,9 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
   __shared__ float4 groups[16][17];
   wait_for_stream();
   auto add = [](float4& a, const float4& v) { a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
-  auto put = [](uint16_t* dst, const float4& a) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
+  auto put = [&](uint16_t* base, size_t at, size_t bytes, const float4& a) {
+    uint2* dst = reinterpret_cast<uint2*>(base + at);
+    if (MLA_STORE_OK(dst, base, bytes, p.err)) *dst = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
   };
   const int c4 = threadIdx.x & 15, group = threadIdx.x >> 4;
   for (long long row = blockIdx.x; row < (long long)p.B * p.Sk; row += gridDim.x) {
@@ -830,7 +855,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
     __syncthreads();
     if (group == 0) {
       for (int k = 1; k < 16; ++k) add(a, groups[k][c4]);
-      put(p.dk_rope_out + row * 64 + 4 * c4, a);
+      put(p.dk_rope_out, row * 64 + 4 * c4, p.rope_bytes, a);
     }
     __syncthreads();
   }
@@ -850,7 +875,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
         for (int s = 0; s < p.n_qs; ++s)
           add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_kv + ((cta + s) * BT + key % BT) * 256 + c)));
       }
-      put((c < 128 ? p.dv : p.dk_nope) + bkh * 128 + (c & 127), a);
+      put(c < 128 ? p.dv : p.dk_nope, bkh * 128 + (c & 127), p.k_bytes, a);
     } else {
       const long long at = i - n_kv, bqh = at / 48;  // (b, query, h)
       const int c = static_cast<int>(at - bqh * 48) * 4, h = static_cast<int>(bqh % p.H);
@@ -862,7 +887,10 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
       for (int s = 0; s < p.n_ks; ++s)
         if (share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
           add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((cta + s) * BT + q % BT) * 192 + c)));
-      put(c < 128 ? p.dq_nope + bqh * 128 + c : p.dq_rope + bqh * 64 + (c - 128), a);
+      if (c < 128)
+        put(p.dq_nope, bqh * 128 + c, p.q_bytes, a);
+      else
+        put(p.dq_rope, bqh * 64 + (c - 128), p.q_bytes / 2, a);
     }
   }
 }
@@ -1044,6 +1072,13 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   const void* grads[] = {dq_nope, dq_rope, dk_nope, dv};
   p.wide = 1;
   for (const void* g : grads) p.wide &= (reinterpret_cast<uintptr_t>(g) & 31) == 0;
+  p.q_bytes = (size_t)B * Sq * H * 128 * 2;
+  p.q_bytes -= std::min(p.q_bytes, testing_out_shrink());
+  p.k_bytes = (size_t)B * Sk * H * 128 * 2;
+  p.rope_bytes = (size_t)B * Sk * 64 * 2;
+  p.part_rope_bytes = w.kv - w.rope;
+  p.part_kv_bytes = w.q - w.kv;
+  p.part_q_bytes = w.bytes - 32 - w.q;
   p.part_rope = at(w.rope);
   p.part_kv = at(w.kv);
   p.part_q = at(w.q);

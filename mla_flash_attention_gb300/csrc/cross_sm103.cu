@@ -337,10 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_q;
       }
-      if (!ok) {  // every MMA issued completes before the CTA frees its TMEM
-        ptx::mma_commit(&bars.drained);
-        ptx::mbar_wait_drain(&bars.drained, 0);
-      }
+      // every MMA issued completes, and every commit arrives, before the CTA gives its memory back
+      ptx::mma_commit(&bars.drained);
+      ptx::mbar_wait_drain(&bars.drained, 0);
     }
   } else {
     // -------------------------------------------------------------- softmax warpgroups
