@@ -1,4 +1,4 @@
-// Backward pass of the MLA prefill and of cross attention on tcgen05 / TMEM / TMA, bf16 operands.
+// MLA prefill backward on tcgen05 / TMEM / TMA, bf16 operands.
 //
 // For one (batch, head), with s = scale * [Qn|Qr][Kn|Kr]' and P = exp(s - LSE) (the forward's
 // log-sum-exp reused, so no row statistics are recomputed):
@@ -6,12 +6,12 @@
 //   dQ = scale dS K,  dK = scale dS' Q   (the rope key is shared by every head: its gradient
 //   is the sum over heads, accumulated by fp32 atomics).
 //
-// Two roles of units share one launch, one kernel body and one shared-memory plan:
-//   key-tile units (b, h, 128 keys): K and V stay in shared memory; query tiles stream by.
+// Two CTA roles share one launch, one kernel body and one shared-memory plan:
+//   key-tile CTAs (b, h, 128 keys): K and V stay in shared memory; query tiles stream by.
 //     TMEM: X [0,128) S' = K Q' (keys on lanes), then dP' = V dO'; dV [128,256);
 //           dK [256,448) (nope 128 + rope 64); Y [448,512) P', then dS' (bf16 pairs)
 //     MMAs per query tile n: dP'(n), dV += P' dO (TS: A = Y), S'(n+1), dK += dS' Q (TS: A = Y)
-//   query-tile units (b, h, 128 queries): Q and dO stay; key tiles stream by.
+//   query-tile CTAs (b, h, 128 queries): Q and dO stay; key tiles stream by.
 //     TMEM: X [0,128) S = Q K'; [128,256) dP = dO V'; dQ [256,448); Y [448,512) dS (bf16)
 //     MMAs per key tile n: S(n+1), dQ += dS K (TS: A = Y), dP(n+1)
 //   Scores of the next tile are issued as soon as the elementwise warps have read the
@@ -19,18 +19,10 @@
 // Shared memory (both roles): fixed 3-chunk tile (K | Q) + fixed 2-chunk tile (V | dO), a
 // 2-stage ring of streamed 3-chunk tiles (Q | K), one streamed 2-chunk tile (dO | V), and
 // the streamed query tiles' -LSE*log2(e) and D vectors (key-tile role).
-// Cross attention (kCross) has queries and keys of unlike counts, each sequence its own number of keys, no
-// causal mask.  In the key role the keys are TMEM lanes, so what stands behind a sequence's last key stays in
-// lanes that are stored as zeros; in the query role those keys' weights and dP are masked and their K rows
-// zeroed in shared memory (0 * NaN is NaN).  The tiles that a CTA streams are cut in shares where few tiles
-// of the one kind meet many of the other, and the rope key's gradient is summed over the heads from fp32
-// partial results by a kernel of its own, in a fixed order: gradients do not depend on the run.
 // Warps: 0 TMA producer, 1 MMA issuer, 2-9 elementwise (TMEM lane quarter = warp % 4,
 // column half = (warp - 2) / 4; each half owns 64 score columns and 32 packed columns of Y).
 #include <cuda.h>
 #include <cudaTypedefs.h>
-
-#include <algorithm>
 
 #include "common.cuh"
 #include "sm103_ptx.cuh"
@@ -51,7 +43,7 @@ constexpr int kThreads = 320;
 constexpr uint32_t kColX = 0, kColDP = 128, kColDV = 128, kColAcc = 256, kColY = 448;
 
 struct Params {
-  const float* nlse2;  // [B*H, S_pad]: -LSE * log2(e); +padding rows hold -inf  (S_pad: of the queries)
+  const float* nlse2;  // [B*H, S_pad]: -LSE * log2(e); +padding rows hold -inf
   const float* dvec;   // [B*H, S_pad]: D = rowsum(dO * O); padding rows hold 0
   uint16_t* dq_nope;   // [B, S, H, 128]
   uint16_t* dq_rope;   // [B, S, H, 64]
@@ -59,34 +51,15 @@ struct Params {
   float* dk_rope;      // [B, S, 64], accumulated (zeroed before the launch)
   uint16_t* dv;        // [B, S, H, 128]
   unsigned int* err;
-  int B, H, S, S_pad, nt, causal, n_key_ctas, n_units;
+  int B, H, S, S_pad, nt, causal, n_key_ctas;
   float scale, scale_log2;
-  // cross attention: S is Sq, nt the query tiles
-  int Sk, nkt;             // keys, key tiles of Sk
-  int n_qs, n_ks;          // shares of the query tiles (key role) and of the key tiles (query role)
-  const int* key_lens;     // or null
-  float *part_rope;        // [B*H][n_qs][Sk][64]: dk_rope of one head and share
-  float *part_kv;          // n_qs > 1: [key role's CTAs][128][dV 128 | dK nope 128]
-  float *part_q;           // n_ks > 1: [query role's CTAs][128][192]
-  uint16_t* dk_rope_out;   // [B, Sk, 64]
-  int wide;                // the bf16 gradients are 32-byte aligned
-  size_t q_bytes, k_bytes, rope_bytes;                   // of dq_nope (dq_rope half), dk_nope and dv, dk_rope: for the
-  size_t part_rope_bytes, part_kv_bytes, part_q_bytes;   // store checks
 };
-
-__device__ __forceinline__ int key_len(const Params& p, int b) {
-  return p.key_lens ? min(max(__ldg(p.key_lens + b), 0), p.Sk) : p.Sk;
-}
-// first tile of share s
-__device__ __forceinline__ int share_begin(int tiles, int s, int n) {
-  return static_cast<int>(static_cast<long long>(tiles) * s / n);
-}
 
 struct Bars {
   // one full barrier per 16 KB chunk of a streamed tile, so the MMAs over its first chunk can
   // start while the later ones are still arriving
-  uint64_t fix3_full, fix3_empty, fix2_full, fix2_empty, ring_full[2][3], ring_empty[2], one_full[2], one_empty;
-  uint64_t s_full, x_read, dp_full, dp_read, p_ready, dv_done, ds_ready, acc_step, acc_done, acc_free, drained;
+  uint64_t fix_full, ring_full[2][3], ring_empty[2], one_full[2], one_empty;
+  uint64_t s_full, x_read, dp_full, dp_read, p_ready, dv_done, ds_ready, acc_step, acc_done;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -151,51 +124,6 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restric
   }
 }
 
-// The same for cross attention, whose batches are often too few for that many rows a warp (128 rows of 152 heads:
-// 21 us): a warp takes eight rows of a head, 16 lanes a row, all its loads under way at once.  A row that saw no
-// key (LSE = -inf) gets -inf like the padding, so its weights are 0.
-__global__ void __launch_bounds__(256) cross_prep_kernel(const uint16_t* __restrict__ out,
-                                                         const uint16_t* __restrict__ d_out,
-                                                         const float* __restrict__ lse, float* __restrict__ nlse2,
-                                                         float* __restrict__ dvec, int B, int H, int S, int S_pad) {
-  wait_for_stream();
-  const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, groups = S_pad / 8;
-  if (task >= (long long)B * H * groups) return;
-  const int bh = static_cast<int>(task / groups), i0 = static_cast<int>(task - (long long)bh * groups) * 8;
-  const int b = bh / H, h = bh - b * H;
-  uint4 a[4], o[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = i0 + 2 * k + (lane >> 4);
-    const size_t ro = (((size_t)b * S + i) * H + h) * 128 + (lane & 15) * 8;
-    a[k] = o[k] = make_uint4(0, 0, 0, 0);
-    if (i < S) {
-      a[k] = __ldg(reinterpret_cast<const uint4*>(d_out + ro));
-      o[k] = __ldg(reinterpret_cast<const uint4*>(out + ro));
-    }
-  }
-  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  float mine = 0.f;  // lane 16 r + 2 k: of row 2 k + r
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
-    float d = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d = fmaf(hi(x[j]), hi(y[j]), fmaf(lo(x[j]), lo(y[j]), d));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if ((lane & 15) == 2 * k) mine = d;
-  }
-  if ((lane & 15) >= 8 || (lane & 1)) return;
-  const int i = i0 + (lane & 15) + (lane >> 4);
-  const size_t vo = (size_t)bh * S_pad + i;
-  const float of = i < S ? lse[(size_t)bh * S + i] : -INFINITY;
-  dvec[vo] = mine;
-  nlse2[vo] = of == -INFINITY ? -INFINITY : -of * 1.4426950408889634f;
-}
-
 // Zero the rope-key gradient accumulator (n4 float4 stores).
 __global__ void __launch_bounds__(256) bwd_zero_kernel(float4* __restrict__ p, long long n4) {
   for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < n4;
@@ -217,128 +145,45 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const uint32_t (&u)
   }
 }
 
-// What one store_row writes, checked as a whole.
-struct alignas(16) Row64 {
-  uint4 v[4];
-};
-struct alignas(16) Row128 {
-  uint4 v[8];
-};
-
-// store_bf16x32 in two whole sectors where dst is 32-byte aligned: a warp's lanes write rows that lie apart, and
-// 16 bytes at a time took a request for every half sector.
-__device__ __forceinline__ void store_row(uint16_t* dst, const uint32_t (&u)[32], float mul, bool wide, const void* base,
-                                          size_t bytes, unsigned int* err) {
-  if (!MLA_STORE_OK(reinterpret_cast<Row64*>(dst), base, bytes, err)) return;
-  if (!wide) {
-    store_bf16x32(dst, u, mul);
-    return;
-  }
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    uint32_t w[8];
-#pragma unroll
-    for (int y = 0; y < 8; ++y)
-      w[y] = ptx::pack_bf16x2(__uint_as_float(u[16 * x + 2 * y]) * mul, __uint_as_float(u[16 * x + 2 * y + 1]) * mul);
-    ptx::st_v8(dst + 16 * x, w);
-  }
-}
-// 32 fp32 accumulator columns (times `mul`) -> 32 fp32 at dst (32-byte aligned)
-__device__ __forceinline__ void store_row(float* dst, const uint32_t (&u)[32], float mul, const void* base, size_t bytes,
-                                          unsigned int* err) {
-  if (!MLA_STORE_OK(reinterpret_cast<Row128*>(dst), base, bytes, err)) return;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    uint32_t w[8];
-#pragma unroll
-    for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(__uint_as_float(u[8 * x + y]) * mul);
-    ptx::st_v8(dst + 8 * x, w);
-  }
-}
-
 struct Maps {
   const CUtensorMap *qn, *qr, *kn, *kr, *v, *dout;
 };
 
-// Where a thread's role stands in the run of units that its CTA works through: steps and units before this
-// one (the phases of the barriers go on from unit to unit), and copies under way.
-struct Flow {
-  uint32_t g = 0, u = 0;
-  uint32_t n_fix3 = 0, n_fix2 = 0, n_ring = 0, n_one = 0;
-  bool after_key = false;  // the unit before was of the key role
-  bool ok = true;
-};
-
 // kKeyRole: this CTA owns key tile `tile` and streams query tiles (dK, dV); otherwise it
-// owns query tile `tile` and streams key tiles (dQ).  kCross: share `share` of them; `cta` numbers the
-// role's CTAs.
-template <bool kKeyRole, bool kCross>
+// owns query tile `tile` and streams key tiles (dQ).
+template <bool kKeyRole>
 __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigned char* sm,
-                                         Bars& bars, int b, int h, int tile, int share, int cta, Flow& f) {
+                                         Bars& bars, int b, int h, int tile) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = kCross ? key_len(p, b) : p.S;  // keys
-  int t_begin, t_end;
-  if constexpr (kCross) {
-    const int of = kKeyRole ? (tile * BT < len ? p.nt : 0) : (len + BT - 1) / BT, n = kKeyRole ? p.n_qs : p.n_ks;
-    t_begin = share_begin(of, share, n);
-    t_end = share_begin(of, share + 1, n);
-  } else {
-    t_begin = kKeyRole ? (p.causal ? tile : 0) : 0;
-    t_end = kKeyRole ? p.nt : (p.causal ? tile + 1 : p.nt);
-  }
+  const int t_begin = kKeyRole ? (p.causal ? tile : 0) : 0;
+  const int t_end = kKeyRole ? p.nt : (p.causal ? tile + 1 : p.nt);
   const int nsteps = t_end - t_begin;
-  const uint32_t g = f.g;  // step n of this unit is step g + n of the CTA
-  const int rows = kCross && kKeyRole ? p.Sk : p.S;  // of the owned operand and its gradients
   const int bh = b * p.H + h;
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort_flag;
 
-  if (kCross && nsteps == 0) {
-    // queries without a key, keys behind their sequence's last: zeros (shares are joined without them)
-    const int r = (warp & 3) * 32 + lane, hf = (warp - 2) >> 2, row_idx = tile * BT + r;
-    if (warp >= 2 && row_idx < rows && (kKeyRole ? p.n_qs : p.n_ks) == 1) {
-      const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint16_t* to = kKeyRole ? (hf == 0 ? p.dv : p.dk_nope) : p.dq_nope;
-      uint4* wide = reinterpret_cast<uint4*>(to + ro * 128);
-      for (int x = 0; x < 16; ++x)
-        if ((kKeyRole || x / 8 == hf) && MLA_STORE_OK(wide + x, to, kKeyRole ? p.k_bytes : p.q_bytes, p.err)) wide[x] = zero;
-      uint4* narrow = reinterpret_cast<uint4*>(p.dq_rope + ro * 64);
-      for (int x = 0; x < 8; ++x)
-        if (!kKeyRole && hf == 0 && MLA_STORE_OK(narrow + x, p.dq_rope, p.q_bytes / 2, p.err)) narrow[x] = zero;
-    }
-    return;
-  }
-
   if (warp == 0) {
     if (ptx::elect_one()) {
       // ------------------------------------------------------------ TMA producer
+      ptx::prefetch_tensormap(m.qn);
+      ptx::prefetch_tensormap(m.kn);
       const int row0 = tile * BT;
-      // the owned tiles, each as soon as the unit before has formed its last products with it
-      auto load_fix3 = [&]() -> bool {
-        if (!ptx::mbar_wait(&bars.fix3_empty, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
-        unsigned char* f3 = sm + kOffFix3;
-        ptx::mbar_arrive_expect_tx(&bars.fix3_full, 3 * kChunk);
-        const CUtensorMap* nope = kKeyRole ? m.kn : m.qn;
-        ptx::tma_load_4d(f3, nope, &bars.fix3_full, 0, h, row0, b);
-        ptx::tma_load_4d(f3 + kChunk, nope, &bars.fix3_full, 64, h, row0, b);
-        if (kKeyRole)
-          ptx::tma_load_3d(f3 + 2 * kChunk, m.kr, &bars.fix3_full, 0, row0, b);
-        else
-          ptx::tma_load_4d(f3 + 2 * kChunk, m.qr, &bars.fix3_full, 0, h, row0, b);
-        ++f.n_fix3;
-        return true;
-      };
-      auto load_fix2 = [&]() -> bool {
-        if (!ptx::mbar_wait(&bars.fix2_empty, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
-        unsigned char* f2_ = sm + kOffFix2;
-        ptx::mbar_arrive_expect_tx(&bars.fix2_full, 2 * kChunk);
-        const CUtensorMap* of = kKeyRole ? m.v : m.dout;
-        ptx::tma_load_4d(f2_, of, &bars.fix2_full, 0, h, row0, b);
-        ptx::tma_load_4d(f2_ + kChunk, of, &bars.fix2_full, 64, h, row0, b);
-        ++f.n_fix2;
-        return true;
-      };
+      ptx::mbar_arrive_expect_tx(&bars.fix_full, 5 * kChunk);
+      unsigned char* f3 = sm + kOffFix3;
+      unsigned char* f2_ = sm + kOffFix2;
+      if (kKeyRole) {
+        ptx::tma_load_4d(f3, m.kn, &bars.fix_full, 0, h, row0, b);
+        ptx::tma_load_4d(f3 + kChunk, m.kn, &bars.fix_full, 64, h, row0, b);
+        ptx::tma_load_3d(f3 + 2 * kChunk, m.kr, &bars.fix_full, 0, row0, b);
+        ptx::tma_load_4d(f2_, m.v, &bars.fix_full, 0, h, row0, b);
+        ptx::tma_load_4d(f2_ + kChunk, m.v, &bars.fix_full, 64, h, row0, b);
+      } else {
+        ptx::tma_load_4d(f3, m.qn, &bars.fix_full, 0, h, row0, b);
+        ptx::tma_load_4d(f3 + kChunk, m.qn, &bars.fix_full, 64, h, row0, b);
+        ptx::tma_load_4d(f3 + 2 * kChunk, m.qr, &bars.fix_full, 0, h, row0, b);
+        ptx::tma_load_4d(f2_, m.dout, &bars.fix_full, 0, h, row0, b);
+        ptx::tma_load_4d(f2_ + kChunk, m.dout, &bars.fix_full, 64, h, row0, b);
+      }
       constexpr int kAhead = 2;  // tiles warmed in L2 ahead of their load
       auto warm = [&](int n) {
         const int r0 = (t_begin + n) * BT;
@@ -360,12 +205,10 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       };
       for (int n = 0; n < kAhead && n < nsteps; ++n) warm(n);
-      f.ok = load_fix3();
-      for (int n = 0; f.ok && n < nsteps; ++n) {
+      for (int n = 0; n < nsteps; ++n) {
         if (n + kAhead < nsteps) warm(n + kAhead);
-        const uint32_t step = g + n;
-        const int r0 = (t_begin + n) * BT, s = step & 1;
-        if (!(f.ok = ptx::mbar_wait(&bars.ring_empty[s], ((step >> 1) & 1) ^ 1, abort_flag, p.err))) break;
+        const int r0 = (t_begin + n) * BT, s = n & 1;
+        if (!ptx::mbar_wait(&bars.ring_empty[s], ((n >> 1) & 1) ^ 1, abort_flag, p.err)) break;
         unsigned char* dst = sm + kOffRing + s * 3 * kChunk;
         if (kKeyRole) {
           ptx::mbar_arrive_expect_tx(&bars.ring_full[s][0], kChunk + 2 * BT * 4);
@@ -384,19 +227,16 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tma_load_4d(dst + kChunk, m.kn, &bars.ring_full[s][1], 64, h, r0, b);
           ptx::tma_load_3d(dst + 2 * kChunk, m.kr, &bars.ring_full[s][2], 0, r0, b);
         }
-        ++f.n_ring;
-        if (n == 0 && !(f.ok = load_fix2())) break;
-        if (!(f.ok = ptx::mbar_wait(&bars.one_empty, (step & 1) ^ 1, abort_flag, p.err))) break;
+        if (!ptx::mbar_wait(&bars.one_empty, (n & 1) ^ 1, abort_flag, p.err)) break;
         unsigned char* one = sm + kOffOne;
         const CUtensorMap* tm = kKeyRole ? m.dout : m.v;
         ptx::mbar_arrive_expect_tx(&bars.one_full[0], kChunk);
         ptx::mbar_arrive_expect_tx(&bars.one_full[1], kChunk);
         ptx::tma_load_4d(one, tm, &bars.one_full[0], 0, h, r0, b);
         ptx::tma_load_4d(one + kChunk, tm, &bars.one_full[1], 64, h, r0, b);
-        ++f.n_one;
       }
     }
-    f.ok = __all_sync(0xffffffffu, f.ok);
+    __syncwarp();
   } else if (warp == 1) {
     if (ptx::elect_one()) {
       // ------------------------------------------------------------ MMA issuer
@@ -405,14 +245,14 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       constexpr uint32_t kIdAcc = ptx::make_idesc(1, BT, 192, 0, 1);  // B N-major, N = 192
       const uint32_t base = ptx::smem_u32(sm);
       const uint32_t one = base + kOffOne;
-      auto ring_of = [&](int n) { return base + kOffRing + ((g + n) & 1) * 3 * kChunk; };
+      auto ring_of = [&](int n) { return base + kOffRing + (n & 1) * 3 * kChunk; };
       // scores over the 192-deep nope+rope contraction (key role: transposed, keys on lanes)
       auto issue_s = [&](int n) -> bool {
         const uint32_t ring = ring_of(n);
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
           if ((k & 3) == 0) {  // each 64-deep chunk as soon as it has landed
-            if (!ptx::mbar_wait(&bars.ring_full[(g + n) & 1][k >> 2], ((g + n) >> 1) & 1, abort_flag, p.err)) return false;
+            if (!ptx::mbar_wait(&bars.ring_full[n & 1][k >> 2], (n >> 1) & 1, abort_flag, p.err)) return false;
             ptx::tc_fence_after();
           }
           const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
@@ -420,7 +260,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
                            ptx::sw128_desc(ring + off, 16, 1024), kIdS, k > 0);
         }
         ptx::mma_commit(&bars.s_full);
-        if (n + 1 == nsteps) ptx::mma_commit(&bars.fix3_empty);
         return true;
       };
       // dP = dO V' over d_v = 128 (key role: dP' = V dO' into X; query role: own columns)
@@ -428,8 +267,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if ((k & 3) == 0) {
-            if (!ptx::mbar_wait(&bars.one_full[k >> 2], (g + n) & 1, abort_flag, p.err)) return false;
-            if (n == 0 && k == 0 && !ptx::mbar_wait(&bars.fix2_full, f.u & 1, abort_flag, p.err)) return false;
+            if (!ptx::mbar_wait(&bars.one_full[k >> 2], n & 1, abort_flag, p.err)) return false;
             ptx::tc_fence_after();
           }
           const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
@@ -438,7 +276,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
                            ptx::sw128_desc(one + off, 16, 1024), kIdS, k > 0);
         }
         ptx::mma_commit(&bars.dp_full);
-        if (n + 1 == nsteps) ptx::mma_commit(&bars.fix2_empty);
         return true;
       };
       // dK += dS' Q (key role) or dQ += dS K: A = dS (bf16 pairs in Y), B = the streamed
@@ -450,29 +287,21 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::mma_bf16_ts(tmem + kColAcc, tmem + kColY + k * 8,
                            ptx::sw128_desc(ring + k * 2048, kChunk, 1024), kIdAcc,
                            (n > 0 || k > 0) ? 1u : 0u);
-        ptx::mma_commit(&bars.ring_empty[(g + n) & 1]);
+        ptx::mma_commit(&bars.ring_empty[n & 1]);
         ptx::mma_commit(&bars.acc_step);
       };
       auto wait = [&](uint64_t* bar, int n) -> bool {
-        if (!ptx::mbar_wait(bar, (g + n) & 1, abort_flag, p.err)) return false;
+        if (!ptx::mbar_wait(bar, n & 1, abort_flag, p.err)) return false;
         ptx::tc_fence_after();
         return true;
       };
-      // the accumulators of the unit before were read
-      auto acc_free = [&]() -> bool {
-        if (!ptx::mbar_wait(&bars.acc_free, (f.u & 1) ^ 1, abort_flag, p.err)) return false;
-        ptx::tc_fence_after();
-        return true;
-      };
-      // (the score columns were read: dP' of the unit before lay in them, or its dP was read after them)
-      bool ok = ptx::mbar_wait(&bars.fix3_full, f.u & 1, abort_flag, p.err) && (g == 0 || wait(&bars.dp_read, -1)) &&
-                issue_s(0);
+      bool ok = ptx::mbar_wait(&bars.fix_full, 0, abort_flag, p.err) && issue_s(0);
       if (kKeyRole) {
         // per query tile n: dP'(n) | dV(n) | S'(n+1) | dK(n) -- the next scores run while the
         // elementwise warps turn dP'(n) into dS(n)
         for (int n = 0; ok && n < nsteps; ++n) {
           if (!(ok = wait(&bars.x_read, n) && issue_dp(n))) break;
-          if (!(ok = wait(&bars.p_ready, n) && (n > 0 || acc_free()))) break;
+          if (!(ok = wait(&bars.p_ready, n))) break;
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // dV += P' dO: A = P' (bf16 pairs in Y), B = dO N-major
             ptx::mma_bf16_ts(tmem + kColDV, tmem + kColY + k * 8,
@@ -486,12 +315,10 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       } else {
         // per key tile n: S(n+1) | dQ(n) | dP(n+1), with dP(0) issued up front
-        // (dP's columns are those of dV in the key role)
-        if (ok && f.after_key) ok = acc_free();
         if (ok && (ok = issue_dp(0))) ptx::mma_commit(&bars.one_empty);
         for (int n = 0; ok && n < nsteps; ++n) {
           if (n + 1 < nsteps && !(ok = wait(&bars.x_read, n) && issue_s(n + 1))) break;
-          if (!(ok = wait(&bars.ds_ready, n) && (n > 0 || acc_free()))) break;
+          if (!(ok = wait(&bars.ds_ready, n))) break;
           issue_acc(n);
           if (n + 1 < nsteps) {
             if (!(ok = wait(&bars.dp_read, n) && issue_dp(n + 1))) break;
@@ -500,9 +327,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         }
       }
       if (ok) ptx::mma_commit(&bars.acc_done);
-      f.ok = ok;
     }
-    f.ok = __all_sync(0xffffffffu, f.ok);
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- elementwise warps
     const int q4 = warp & 3, hf = (warp - 2) >> 2;
@@ -532,12 +358,11 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
     };
     bool ok = true;
     for (int n = 0; n < nsteps; ++n) {
-      const uint32_t step = g + n;
-      const int t = t_begin + n, s = step & 1;
+      const int t = t_begin + n, s = n & 1;
       const float* vec = reinterpret_cast<const float*>(sm + kOffVec + s * 2 * BT * 4);
-      ok = wait(&bars.s_full, step & 1);
+      ok = wait(&bars.s_full, n & 1);
       // the query vectors of this stage arrived with its TMA transaction: observe it directly
-      if (kKeyRole && ok) ok = wait(&bars.ring_full[s][0], (step >> 1) & 1);
+      if (kKeyRole && ok) ok = wait(&bars.ring_full[s][0], (n >> 1) & 1);
       if (!ok) break;
       uint32_t u[64];
       ptx::tmem_ld32(tX, *reinterpret_cast<uint32_t(*)[32]>(u));
@@ -547,20 +372,16 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       // P = exp2(s * scale * log2(e) - LSE * log2(e)), two columns per packed instruction
       float pr[64];
       if (kKeyRole) {
-        const float4* nl = reinterpret_cast<const float4*>(vec) + hf * 16;  // per query
+        const float2* nl = reinterpret_cast<const float2*>(vec) + hf * 32;  // per query
 #pragma unroll
-        for (int x4 = 0; x4 < 16; ++x4) {
-          const float4 l4 = nl[x4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = 2 * x4 + e;
-            const uint64_t a2 = ptx::fma2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), sc2,
-                                          e == 0 ? ptx::f2(l4.x, l4.y) : ptx::f2(l4.z, l4.w));
-            pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
-            pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
-          }
+        for (int x = 0; x < 32; ++x) {
+          const float2 l = nl[x];
+          const uint64_t a2 = ptx::fma2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
+                                        sc2, ptx::f2(l.x, l.y));
+          pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
+          pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
         }
-        if (!kCross && p.causal && t == tile) {  // diagonal tile: a query before the key sees nothing
+        if (p.causal && t == tile) {  // diagonal tile: a query before the key sees nothing
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (hf * 64 + x < r) pr[x] = 0.f;
@@ -574,12 +395,12 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           pr[2 * x] = ptx::ex2(ptx::f2_lo(a2));
           pr[2 * x + 1] = ptx::ex2(ptx::f2_hi(a2));
         }
-        if (!kCross && p.causal && t == tile) {  // diagonal tile: keys after the query are masked
+        if (p.causal && t == tile) {  // diagonal tile: keys after the query are masked
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (hf * 64 + x > r) pr[x] = 0.f;
-        } else if ((kCross || !p.causal) && (t + 1) * BT > len) {  // keys past the sequence end
-          const int lim = len - t * BT - hf * 64;
+        } else if (!p.causal && (t + 1) * BT > p.S) {  // keys past the sequence end
+          const int lim = p.S - t * BT - hf * 64;
 #pragma unroll
           for (int x = 0; x < 64; ++x)
             if (x >= lim) pr[x] = 0.f;
@@ -588,50 +409,28 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       uint32_t pk[32];
       if (kKeyRole) {
         // P' (bf16) into Y once dK(n-1) has consumed the dS' held there
-        if (n > 0 && !(ok = wait(&bars.acc_step, (step - 1) & 1))) break;
+        if (n > 0 && !(ok = wait(&bars.acc_step, (n - 1) & 1))) break;
 #pragma unroll
         for (int x = 0; x < 32; ++x) pk[x] = ptx::pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
         ptx::tmem_st32(tY, pk);
         ptx::tmem_st_wait();
         arrive(&bars.p_ready);
       }
-      if (!(ok = wait(&bars.dp_full, step & 1))) break;
+      if (!(ok = wait(&bars.dp_full, n & 1))) break;
       ptx::tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(u));
       ptx::tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
       ptx::tmem_ld_wait();
       arrive(&bars.dp_read);
-      if constexpr (kCross && !kKeyRole) {
-        if ((t + 1) * BT > len && len < p.Sk) {
-          // what stands behind the last key may be NaN: out of dP, and out of the product with K
-          const int lim = len - t * BT;
-#pragma unroll
-          for (int x = 0; x < 64; ++x)
-            if (hf * 64 + x >= lim) u[x] = 0u;
-          for (int c = 0; c < 3 && ok; ++c) ok = wait(&bars.ring_full[s][c], (step >> 1) & 1);
-          if (!ok) break;
-          if (r >= lim) {
-            for (int c = hf; c < 3; c += 2) {
-              uint4* row = reinterpret_cast<uint4*>(sm + kOffRing + (s * 3 + c) * kChunk + r * 128);
-              for (int x = 0; x < 8; ++x) row[x] = make_uint4(0, 0, 0, 0);
-            }
-          }
-          ptx::fence_proxy_async();
-        }
-      }
       // dS = P * (dP - D) as bf16 pairs
       if (kKeyRole) {
-        const float4* dd = reinterpret_cast<const float4*>(vec + BT) + hf * 16;  // per query
+        const float2* dd = reinterpret_cast<const float2*>(vec + BT) + hf * 32;  // per query
 #pragma unroll
-        for (int x4 = 0; x4 < 16; ++x4) {
-          const float4 d4 = dd[x4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = 2 * x4 + e;
-            const uint64_t ds = ptx::mul2(ptx::f2(pr[2 * x], pr[2 * x + 1]),
-                                          ptx::sub2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
-                                                    e == 0 ? ptx::f2(d4.x, d4.y) : ptx::f2(d4.z, d4.w)));
-            pk[x] = ptx::pack_bf16x2(ptx::f2_lo(ds), ptx::f2_hi(ds));
-          }
+        for (int x = 0; x < 32; ++x) {
+          const float2 d = dd[x];
+          const uint64_t g = ptx::mul2(ptx::f2(pr[2 * x], pr[2 * x + 1]),
+                                       ptx::sub2(ptx::f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])),
+                                                 ptx::f2(d.x, d.y)));
+          pk[x] = ptx::pack_bf16x2(ptx::f2_lo(g), ptx::f2_hi(g));
         }
       } else {
         const uint64_t d2 = ptx::f2(d_row, d_row);
@@ -645,8 +444,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       // dS into Y once its previous reader is done: dV(n) (key role: P' lives there) or
       // dQ(n-1)
       if (kKeyRole) {
-        if (!(ok = wait(&bars.dv_done, step & 1))) break;
-      } else if (n > 0 && !(ok = wait(&bars.acc_step, (step - 1) & 1))) {
+        if (!(ok = wait(&bars.dv_done, n & 1))) break;
+      } else if (n > 0 && !(ok = wait(&bars.acc_step, (n - 1) & 1))) {
         break;
       }
       ptx::tmem_st32(tY, pk);
@@ -654,11 +453,11 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
       arrive(&bars.ds_ready);
     }
     // ---------------------------------------------------------------- epilogue
-    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.acc_done, f.u & 1, abort_flag, p.err));
+    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars.acc_done, 0, abort_flag, p.err));
     if (ok) {
       ptx::tc_fence_after();
-      const bool store = row_idx < rows;
-      const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
+      const bool store = row_idx < p.S;
+      const size_t ro = ((size_t)b * p.S + row_idx) * p.H + h;  // row of a [B, S, H, d] tensor
       if (kKeyRole) {
         // half 0: dV (4 chunks) and rope columns 0..31 of dK; half 1: dK nope (4 chunks) and
         // rope columns 32..63
@@ -669,26 +468,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           uint32_t w[32];
           ptx::tmem_ld32(tmem + lane_off + col, w);
           ptx::tmem_ld_wait();
-          if constexpr (kCross) {
-            if (row_idx >= len) {  // lanes of no key
-#pragma unroll
-              for (int x = 0; x < 32; ++x) w[x] = 0u;
-            }
-            const float mul = c < 4 && hf == 0 ? 1.f : p.scale;
-            uint16_t* to = hf == 0 ? p.dv : p.dk_nope;
-            if (store) {
-              if (c == 4)
-                store_row(p.part_rope + (((size_t)bh * p.n_qs + share) * p.Sk + row_idx) * 64 + 32 * hf, w, mul, p.part_rope,
-                          p.part_rope_bytes, p.err);
-              else if (p.n_qs > 1)
-                store_row(p.part_kv + ((size_t)cta * BT + r) * 256 + hf * 128 + 32 * c, w, mul, p.part_kv, p.part_kv_bytes,
-                          p.err);
-              else
-                store_row(to + ro * 128 + 32 * c, w, mul, p.wide, to, p.k_bytes, p.err);
-            }
-            __syncwarp();
-            continue;
-          }
           if (!store) continue;
           if (c < 4) {
             if (hf == 0)
@@ -713,18 +492,6 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           uint32_t w[32];
           ptx::tmem_ld32(tmem + lane_off + kColAcc + 32 * cc, w);
           ptx::tmem_ld_wait();
-          if constexpr (kCross) {
-            if (store) {
-              if (p.n_ks > 1)
-                store_row(p.part_q + ((size_t)cta * BT + r) * 192 + 32 * cc, w, p.scale, p.part_q, p.part_q_bytes, p.err);
-              else if (cc < 4)
-                store_row(p.dq_nope + ro * 128 + 32 * cc, w, p.scale, p.wide, p.dq_nope, p.q_bytes, p.err);
-              else
-                store_row(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale, p.wide, p.dq_rope, p.q_bytes / 2, p.err);
-            }
-            __syncwarp();
-            continue;
-          }
           if (!store) continue;
           if (cc < 4)
             store_bf16x32(p.dq_nope + ro * 128 + 32 * cc, w, p.scale);
@@ -732,16 +499,10 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
             store_bf16x32(p.dq_rope + ro * 64 + 32 * (cc - 4), w, p.scale);
         }
       }
-      arrive(&bars.acc_free);
     }
-    f.ok = ok;
   }
-  f.g += nsteps;
-  ++f.u;
-  f.after_key = kKeyRole;
 }
 
-template <bool kCross>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_bwd_kernel(const __grid_constant__ CUtensorMap tm_qn,
                        const __grid_constant__ CUtensorMap tm_qr,
@@ -754,14 +515,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ Bars bars;
   const int warp = threadIdx.x >> 5;
+  // key-tile CTAs first, then query-tile CTAs; within a role the tiles of one (b, h) are
+  // consecutive (most work first), so CTAs that run together stream the same (b, h)'s tiles
+  // and find them in L2
+  const bool key_role = static_cast<int>(blockIdx.x) < p.n_key_ctas;
+  const int idx = key_role ? blockIdx.x : blockIdx.x - p.n_key_ctas;
+  const int bh = idx / p.nt;
+  const int tile = key_role ? idx % p.nt : p.nt - 1 - idx % p.nt;
+  const int b = bh / p.H, h = bh % p.H;
+
   if (threadIdx.x == 0) {
-    ptx::prefetch_tensormap(&tm_qn);
-    ptx::prefetch_tensormap(&tm_kn);
     bars.abort_flag = 0;
-    ptx::mbar_init(&bars.fix3_full, 1);
-    ptx::mbar_init(&bars.fix3_empty, 1);
-    ptx::mbar_init(&bars.fix2_full, 1);
-    ptx::mbar_init(&bars.fix2_empty, 1);
+    ptx::mbar_init(&bars.fix_full, 1);
     for (int s = 0; s < 2; ++s) {
       for (int c = 0; c < 3; ++c) ptx::mbar_init(&bars.ring_full[s][c], 1);
       ptx::mbar_init(&bars.ring_empty[s], 1);
@@ -778,142 +543,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&bars.dv_done, 1);
     ptx::mbar_init(&bars.ds_ready, 8);
     ptx::mbar_init(&bars.acc_done, 1);
-    ptx::mbar_init(&bars.acc_free, 8);
-    ptx::mbar_init(&bars.drained, 1);
     ptx::fence_barrier_init();
   }
   if (warp == 0) ptx::tmem_alloc(&bars.tmem_base, 512);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (kCross) wait_for_stream();
   const Maps m{&tm_qn, &tm_qr, &tm_kn, &tm_kr, &tm_v, &tm_do};
-  // Key-tile units first, then query-tile units; within a role the tiles of one (b, h) are consecutive (most
-  // work first), so CTAs that run together stream the same (b, h)'s tiles and find them in L2.  A CTA takes
-  // every gridDim.x-th unit (the prefill's has one): the next unit's tiles are loaded, and its first scores
-  // formed, while this one's accumulators are stored.
-  Flow f;
-  for (unsigned unit = blockIdx.x; f.ok && unit < static_cast<unsigned>(p.n_units); unit += gridDim.x) {
-    const bool key_role = unit < static_cast<unsigned>(p.n_key_ctas);
-    const unsigned cta = key_role ? unit : unit - p.n_key_ctas;
-    const unsigned shares = !kCross ? 1 : key_role ? p.n_qs : p.n_ks, idx = cta / shares, share = cta % shares;
-    const unsigned tiles = kCross && key_role ? p.nkt : p.nt;
-    const int bh = idx / tiles;
-    const int tile = key_role || kCross ? idx % tiles : tiles - 1 - idx % tiles;
-    const int b = bh / p.H, h = bh % p.H;
-    if (key_role)
-      bwd_body<true, kCross>(m, p, sm, bars, b, h, tile, share, cta, f);
-    else
-      bwd_body<false, kCross>(m, p, sm, bars, b, h, tile, share, cta, f);
-  }
-  // Nothing asynchronous outlives the CTA: commits arrive in its shared memory, and after an abort copies and
-  // products may be under way that nobody waits for.
-  if (warp < 2 && ptx::elect_one()) {
-    if (warp == 1) {
-      ptx::mma_commit(&bars.drained);
-      ptx::mbar_wait_drain(&bars.drained, 0);
-    } else if (!f.ok) {
-      if (f.n_fix3 > 0) ptx::mbar_wait_drain(&bars.fix3_full, (f.n_fix3 - 1) & 1);
-      if (f.n_fix2 > 0) ptx::mbar_wait_drain(&bars.fix2_full, (f.n_fix2 - 1) & 1);
-      for (uint32_t v = f.n_ring > 2 ? f.n_ring - 2 : 0; v < f.n_ring; ++v)
-        for (int c = 0; c < 3; ++c) ptx::mbar_wait_drain(&bars.ring_full[v & 1][c], (v >> 1) & 1);
-      for (int c = 0; c < 2 && f.n_one > 0; ++c) ptx::mbar_wait_drain(&bars.one_full[c], (f.n_one - 1) & 1);
-    }
-  }
-  __syncwarp();
+  if (key_role)
+    bwd_body<true>(m, p, sm, bars, b, h, tile);
+  else
+    bwd_body<false>(m, p, sm, bars, b, h, tile);
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(bars.tmem_base, 512);
   }
-}
-
-// Cross attention: joins what the CTAs left in fp32.  The rope key's gradient, a sum over heads and shares, a
-// key a block: 16 threads' loads cover its 64 columns and 16 such groups take every 16th head or share each (one
-// thread for all of them waited 150 loads long), joined in group order.  The shares' gradients of K and V, and of
-// Q, where those were cut: a thread for four columns of a row.
-__global__ void __launch_bounds__(256) bwd_join_kernel(const Params p) {
-  __shared__ float4 groups[16][17];
-  wait_for_stream();
-  auto add = [](float4& a, const float4& v) { a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
-  auto put = [&](uint16_t* base, size_t at, size_t bytes, const float4& a) {
-    uint2* dst = reinterpret_cast<uint2*>(base + at);
-    if (MLA_STORE_OK(dst, base, bytes, p.err)) *dst = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
-  };
-  const int c4 = threadIdx.x & 15, group = threadIdx.x >> 4;
-  for (long long row = blockIdx.x; row < (long long)p.B * p.Sk; row += gridDim.x) {
-    const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key < key_len(p, b)) {
-      const float* src = p.part_rope + ((size_t)b * p.H * p.n_qs * p.Sk + key) * 64 + 4 * c4;
-#pragma unroll 4
-      for (int k = group; k < p.H * p.n_qs; k += 16)
-        add(a, ptx::ld_l2(reinterpret_cast<const float4*>(src + (size_t)k * p.Sk * 64)));
-    }
-    groups[group][c4] = a;
-    __syncthreads();
-    if (group == 0) {
-      for (int k = 1; k < 16; ++k) add(a, groups[k][c4]);
-      put(p.dk_rope_out, row * 64 + 4 * c4, p.rope_bytes, a);
-    }
-    __syncthreads();
-  }
-  const long long n_kv = p.n_qs > 1 ? (long long)p.B * p.Sk * p.H * 64 : 0;
-  const long long n_q = p.n_ks > 1 ? (long long)p.B * p.S * p.H * 48 : 0;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_kv + n_q;
-       i += (long long)gridDim.x * blockDim.x) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < n_kv) {
-      const long long bkh = i >> 6;  // (b, key, h)
-      const int c = (i & 63) * 4, h = static_cast<int>(bkh % p.H);
-      const long long bk = bkh / p.H;
-      const int b = static_cast<int>(bk / p.Sk), key = static_cast<int>(bk - (long long)b * p.Sk);
-      if (key < key_len(p, b)) {
-        const size_t cta = (((size_t)b * p.H + h) * p.nkt + key / BT) * p.n_qs;
-#pragma unroll 4
-        for (int s = 0; s < p.n_qs; ++s)
-          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_kv + ((cta + s) * BT + key % BT) * 256 + c)));
-      }
-      put(c < 128 ? p.dv : p.dk_nope, bkh * 128 + (c & 127), p.k_bytes, a);
-    } else {
-      const long long at = i - n_kv, bqh = at / 48;  // (b, query, h)
-      const int c = static_cast<int>(at - bqh * 48) * 4, h = static_cast<int>(bqh % p.H);
-      const long long bq = bqh / p.H;
-      const int b = static_cast<int>(bq / p.S), q = static_cast<int>(bq - (long long)b * p.S);
-      const int tiles = (key_len(p, b) + BT - 1) / BT;
-      const size_t cta = (((size_t)b * p.H + h) * p.nt + q / BT) * p.n_ks;
-#pragma unroll 4
-      for (int s = 0; s < p.n_ks; ++s)
-        if (share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
-          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((cta + s) * BT + q % BT) * 192 + c)));
-      if (c < 128)
-        put(p.dq_nope, bqh * 128 + c, p.q_bytes, a);
-      else
-        put(p.dq_rope, bqh * 64 + (c - 128), p.q_bytes / 2, a);
-    }
-  }
-}
-
-// How a cross attention's backward is cut: the tiles that one CTA streams go in shares where their
-// steps would last longer than half of what an SM has to do in all.
-struct Cut {
-  int nqt, nkt, n_qs, n_ks;
-  long long key_ctas, query_ctas;
-};
-constexpr int kLeastSteps = 4;
-
-inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
-  Cut c;
-  c.nqt = (Sq + BT - 1) / BT;
-  c.nkt = (Sk + BT - 1) / BT;
-  const double each = (double)B * H * c.nqt * c.nkt / sms;  // half of both roles' steps, an SM
-  const double most = each > kLeastSteps ? each : kLeastSteps;
-  c.n_qs = c.nqt > most ? (int)(c.nqt / most + 0.999) : 1;
-  c.n_ks = c.nkt > most ? (int)(c.nkt / most + 0.999) : 1;
-  c.key_ctas = (long long)B * H * c.nkt * c.n_qs;
-  c.query_ctas = (long long)B * H * c.nqt * c.n_ks;
-  return c;
 }
 
 }  // namespace sm103_bwd
@@ -973,7 +619,7 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
       encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides,
                         kr_box) != cudaSuccess)
     return cudaErrorInvalidValue;
-  Params p = {};
+  Params p;
   p.nlse2 = nlse2;
   p.dvec = dvec;
   p.dq_nope = static_cast<uint16_t*>(dq_nope);
@@ -993,114 +639,11 @@ cudaError_t launch_prefill_bwd_sm103(const void* q_nope, const void* q_rope, con
   const long long per_role = (long long)B * H * nt;
   if (2 * per_role > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.n_key_ctas = (int)per_role;
-  p.n_units = (int)(2 * per_role);
   static unsigned long long smem_set = 0;
-  if ((e = smem_attr_once(prefill_bwd_kernel<false>, kSmemAlloc, &smem_set)) != cudaSuccess) return e;
-  prefill_bwd_kernel<false><<<(unsigned)(2 * per_role), kThreads, kSmemAlloc, stream>>>(tqn, tqr, tkn, tkr, tv, tdo, p);
+  if ((e = smem_attr_once(prefill_bwd_kernel, kSmemAlloc, &smem_set)) != cudaSuccess) return e;
+  prefill_bwd_kernel<<<(unsigned)(2 * per_role), kThreads, kSmemAlloc, stream>>>(tqn, tqr, tkn,
+                                                                                  tkr, tv, tdo, p);
   return cudaGetLastError();
-}
-
-// Whether the CTAs of such a call can be numbered.
-bool cross_bwd_fits(int B, int H, int Sq, int Sk) {
-  return (long long)B * H * ((Sq + 127) / 128 + (long long)((Sk + 127) / 128)) <= 0x40000000LL;
-}
-
-namespace {
-struct CrossBwdWorkspace {
-  size_t nlse2, dvec, rope, kv, q, bytes;  // offsets, and the whole
-  CrossBwdWorkspace(const sm103_bwd::Cut& c, int B, int H, int Sk) {
-    size_t at = 0;
-    auto take = [&](size_t n) {
-      const size_t here = at;
-      at += (n + 255) / 256 * 256;
-      return here;
-    };
-    const size_t vec = (size_t)B * H * c.nqt * sm103_bwd::BT * sizeof(float);
-    nlse2 = take(vec);
-    dvec = take(vec);
-    rope = take((size_t)B * H * c.n_qs * Sk * 64 * sizeof(float));
-    kv = take(c.n_qs > 1 ? (size_t)c.key_ctas * sm103_bwd::BT * 256 * sizeof(float) : 0);
-    q = take(c.n_ks > 1 ? (size_t)c.query_ctas * sm103_bwd::BT * 192 * sizeof(float) : 0);
-    bytes = at + 32;
-  }
-};
-}  // namespace
-
-size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
-  return CrossBwdWorkspace(sm103_bwd::cut_of(B, H, Sq, Sk, sms), B, H, Sk).bytes;
-}
-
-cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
-                                   const void* v, const int* key_lens, const void* out, const float* lse,
-                                   const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
-                                   void* dv, int B, int H, int Sq, int Sk, float softmax_scale, void* workspace, int sms,
-                                   unsigned int* err, cudaStream_t stream) {
-  using namespace sm103_bwd;
-  const Cut c = cut_of(B, H, Sq, Sk, sms);
-  const CrossBwdWorkspace w(c, B, H, Sk);
-  CUtensorMap tqn, tqr, tkn, tkr, tv, tdo;
-  uint64_t kr_dims[3] = {64, (uint64_t)Sk, (uint64_t)B};
-  uint64_t kr_strides[2] = {64 * 2, (uint64_t)Sk * 64 * 2};
-  uint32_t kr_box[3] = {64, BT, 1};
-  if (!bwd_map_bshd(&tqn, q_nope, B, Sq, H, 128) || !bwd_map_bshd(&tqr, q_rope, B, Sq, H, 64) ||
-      !bwd_map_bshd(&tkn, k_nope, B, Sk, H, 128) || !bwd_map_bshd(&tv, v, B, Sk, H, 128) ||
-      !bwd_map_bshd(&tdo, d_out, B, Sq, H, 128) ||
-      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
-    return cudaErrorInvalidValue;
-  // (the workspace is 16-byte aligned, its parts 32)
-  char* base = static_cast<char*>(workspace) + (reinterpret_cast<uintptr_t>(workspace) & 16);
-  auto at = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
-  Params p = {};
-  p.nlse2 = at(w.nlse2);
-  p.dvec = at(w.dvec);
-  p.dq_nope = static_cast<uint16_t*>(dq_nope);
-  p.dq_rope = static_cast<uint16_t*>(dq_rope);
-  p.dk_nope = static_cast<uint16_t*>(dk_nope);
-  p.dk_rope_out = static_cast<uint16_t*>(dk_rope);
-  p.dv = static_cast<uint16_t*>(dv);
-  p.err = err;
-  p.B = B;
-  p.H = H;
-  p.S = Sq;
-  p.nt = c.nqt;
-  p.S_pad = c.nqt * BT;
-  p.Sk = Sk;
-  p.nkt = c.nkt;
-  p.n_qs = c.n_qs;
-  p.n_ks = c.n_ks;
-  p.key_lens = key_lens;
-  const void* grads[] = {dq_nope, dq_rope, dk_nope, dv};
-  p.wide = 1;
-  for (const void* g : grads) p.wide &= (reinterpret_cast<uintptr_t>(g) & 31) == 0;
-  p.q_bytes = (size_t)B * Sq * H * 128 * 2;
-  p.q_bytes -= std::min(p.q_bytes, testing_out_shrink());
-  p.k_bytes = (size_t)B * Sk * H * 128 * 2;
-  p.rope_bytes = (size_t)B * Sk * 64 * 2;
-  p.part_rope_bytes = w.kv - w.rope;
-  p.part_kv_bytes = w.q - w.kv;
-  p.part_q_bytes = w.bytes - 32 - w.q;
-  p.part_rope = at(w.rope);
-  p.part_kv = at(w.kv);
-  p.part_q = at(w.q);
-  p.scale = softmax_scale;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.n_key_ctas = (int)c.key_ctas;
-  p.n_units = (int)(c.key_ctas + c.query_ctas);
-  if (c.key_ctas + c.query_ctas > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
-  const long long tasks = (long long)B * H * (p.S_pad / 8);
-  if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  static unsigned long long smem_set = 0;
-  cudaError_t e = smem_attr_once(prefill_bwd_kernel<true>, kSmemAlloc, &smem_set);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(cross_prep_kernel, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
-                       static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.S_pad);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent_smem(prefill_bwd_kernel<true>, p.n_units < sms ? p.n_units : sms, kThreads, kSmemAlloc, stream, tqn,
-                            tqr, tkn, tkr, tv, tdo, p);
-  if (e != cudaSuccess) return e;
-  const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
-  const long long rows = (long long)B * Sk, blocks = rows > (cut + 255) / 256 ? rows : (cut + 255) / 256, most = 8LL * sms;
-  return launch_dependent(bwd_join_kernel, (int)(blocks < most ? blocks : most), 256, stream, p);
 }
 
 }  // namespace mla
