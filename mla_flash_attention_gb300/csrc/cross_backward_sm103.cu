@@ -291,10 +291,8 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
           ptx::tma_prefetch_4d(m.v, 64, h, r0, b);
         }
       };
-      for (int n = 0; n < kAhead && n < nsteps; ++n) warm(n);
       f.ok = load_fix3();
       for (int n = 0; f.ok && n < nsteps; ++n) {
-        if (n + kAhead < nsteps) warm(n + kAhead);
         const uint32_t step = g + n;
         const int r0 = (t_begin + n) * BT, s = step & 1;
         if (!(f.ok = ptx::mbar_wait(&bars.ring_empty[s], ((step >> 1) & 1) ^ 1, abort_flag, p.err))) break;
@@ -326,6 +324,9 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
         ptx::tma_load_4d(one, tm, &bars.one_full[0], 0, h, r0, b);
         ptx::tma_load_4d(one + kChunk, tm, &bars.one_full[1], 64, h, r0, b);
         ++f.n_one;
+        // (behind this step's own loads, which the unit waits for)
+        for (int a = n == 0 ? 1 : kAhead; a <= kAhead; ++a)
+          if (n + a < nsteps) warm(n + a);
       }
     }
     f.ok = __all_sync(0xffffffffu, f.ok);
