@@ -73,8 +73,9 @@ struct Params {
   unsigned int* err;
   int B, H, Sq, Sk, q_pad;
   int nqt, nkt;            // query tiles, key tiles of Sk
+  int n_query_units;
   int n_qs, n_ks;          // shares of the query tiles (key role) and of the key tiles (query role)
-  int n_key_units, n_units;
+  int by_lens;             // units pass over the key tiles that hold no key
   int wide;                // the bf16 gradients are 32-byte aligned
   float scale, scale_log2;
   size_t q_bytes, k_bytes, rope_bytes;                   // of dq_nope (dq_rope half), dk_nope and dv, dk_rope: for the
@@ -200,6 +201,64 @@ struct Maps {
   const CUtensorMap *qn, *qr, *kn, *kr, *v, *dout;
 };
 
+// The units of a CTA: every gridDim.x-th, the key-tile units first; if there are more units than CTAs, only the tiles that
+// hold keys (with the empty ones in the order, which a CTA passes in no time, other CTAs had more than their share: 8 x 16
+// heads, 448 queries, up to 1500 keys 207 us, so 178; 4 x 32 heads, 1024 queries, up to 1024 keys 251, so 198).  Every
+// warp walks them by itself, 32 sequences' lengths at a time; where it stands is kept in shared memory, the products'
+// loops having no register for it.
+struct Walk {
+  unsigned id, base;  // base: key-tile units of the sequences before b
+  int b;
+};
+__device__ __forceinline__ bool next_unit(Walk& walk, const Params& p, bool& key_role, int& bh, int& tile, int& share) {
+  const int lane = threadIdx.x & 31;
+  const unsigned id = walk.id, each = static_cast<unsigned>(p.H) * p.n_qs;  // units of a sequence's key tile
+  unsigned base = p.by_lens ? walk.base : static_cast<unsigned>(p.B) * p.nkt * each, at = id, tiles = p.nkt;
+  int b = 0;
+  key_role = id < base;
+  if (p.by_lens) {
+    for (b = walk.b; b < p.B; b += 32) {
+      const unsigned mine = b + lane < p.B ? (key_len(p, b + lane) + BT - 1) / BT : 0;
+      unsigned upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const unsigned low = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += low;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, id - base >= upto * each);
+      key_role = past != 0xffffffffu;
+      if (key_role) {
+        const int first = __ffs(~past) - 1;
+        tiles = __shfl_sync(0xffffffffu, mine, first);
+        at = id - base - (__shfl_sync(0xffffffffu, upto, first) - tiles) * each;
+        __syncwarp();
+        if (lane == 0) walk.base = base, walk.b = b;
+        b += first;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31) * each;
+    }
+    if (!key_role) {
+      __syncwarp();
+      if (lane == 0) walk.base = base, walk.b = b;
+    }
+  }
+  const unsigned shares = key_role ? p.n_qs : p.n_ks;
+  if (!key_role) {
+    at = id - base;
+    tiles = p.nqt;
+    if (at >= static_cast<unsigned>(p.n_query_units)) return false;
+  }
+  const unsigned unit = at / shares, h = unit / tiles;
+  share = at - unit * shares;
+  tile = unit - h * tiles;
+  bh = (key_role ? b * p.H : 0) + h;
+  __syncwarp();
+  if (lane == 0) walk.id = id + gridDim.x;
+  __syncwarp();
+  return true;
+}
+
 // Where a thread's role stands in the run of units that its CTA works through: steps and units before this
 // one (the phases of the barriers go on from unit to unit), and copies under way.
 struct Flow {
@@ -225,19 +284,17 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort_flag;
 
-  if (nsteps == 0) {
-    // queries without a key, keys behind their sequence's last: zeros (shares are joined without them)
+  if (nsteps == 0) {  // queries without a key: zeros (shares are joined without them)
     const int r = (warp & 3) * 32 + lane, hf = (warp - 2) >> 2, row_idx = tile * BT + r;
-    if (warp >= 2 && row_idx < rows && shares == 1) {
+    if (!kKeyRole && warp >= 2 && row_idx < rows && shares == 1) {
       const size_t ro = ((size_t)b * rows + row_idx) * p.H + h;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint16_t* to = kKeyRole ? (hf == 0 ? p.dv : p.dk_nope) : p.dq_nope;
-      uint4* wide = reinterpret_cast<uint4*>(to + ro * 128);
-      for (int x = 0; x < 16; ++x)
-        if ((kKeyRole || x / 8 == hf) && MLA_STORE_OK(wide + x, to, kKeyRole ? p.k_bytes : p.q_bytes, p.err)) wide[x] = zero;
-      uint4* narrow = reinterpret_cast<uint4*>(p.dq_rope + ro * 64);
+      uint4* wide = reinterpret_cast<uint4*>(p.dq_nope + ro * 128) + 8 * hf;
+      uint4* narrow = reinterpret_cast<uint4*>(p.dq_rope + ro * 64) + 4 * hf;
       for (int x = 0; x < 8; ++x)
-        if (!kKeyRole && hf == 0 && MLA_STORE_OK(narrow + x, p.dq_rope, p.q_bytes / 2, p.err)) narrow[x] = zero;
+        if (MLA_STORE_OK(wide + x, p.dq_nope, p.q_bytes, p.err)) wide[x] = zero;
+      for (int x = 0; x < 4; ++x)
+        if (MLA_STORE_OK(narrow + x, p.dq_rope, p.q_bytes / 2, p.err)) narrow[x] = zero;
     }
     return;
   }
@@ -685,18 +742,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   wait_for_stream();
   const Maps m{&tm_qn, &tm_qr, &tm_kn, &tm_kr, &tm_v, &tm_do};
-  // Key-tile units first, then query-tile units; within a role the tiles of one (b, h) are consecutive, so CTAs
-  // that run together stream the same (b, h)'s tiles and find them in L2.
+  // Within a role the tiles of one (b, h) are consecutive, so CTAs that run together stream the same (b, h)'s
+  // tiles and find them in L2.
   Flow f;
-  for (unsigned id = blockIdx.x; f.ok && id < static_cast<unsigned>(p.n_units); id += gridDim.x) {
-    const bool key_role = id < static_cast<unsigned>(p.n_key_units);
-    const unsigned unit = key_role ? id : id - p.n_key_units, shares = key_role ? p.n_qs : p.n_ks;
-    const unsigned tiles = key_role ? p.nkt : p.nqt, idx = unit / shares, bh = idx / tiles;
-    const int share = unit - idx * shares, tile = idx - bh * tiles, b = bh / p.H, h = bh - b * p.H;
+  if (p.key_lens && p.n_qs == 1 && warp >= 2) {  // key tiles that no unit has, while the first tiles are on their way
+    const int lane = threadIdx.x & 31, each = p.H * 32;  // 16-byte pieces of a key's dV and dK nope
+    for (long long row = blockIdx.x * 8LL + warp - 2; row < (long long)p.B * p.Sk; row += gridDim.x * 8LL) {
+      const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk);
+      if (key < (key_len(p, b) + BT - 1) / BT * BT) continue;
+      for (int i = lane; i < each; i += 32) {
+        uint16_t* to = i < each / 2 ? p.dv : p.dk_nope;
+        uint4* dst = reinterpret_cast<uint4*>(to + row * p.H * 128) + (i < each / 2 ? i : i - each / 2);
+        if (MLA_STORE_OK(dst, to, p.k_bytes, p.err)) *dst = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  __shared__ Walk walks[kThreads / 32];
+  Walk& walk = walks[warp];
+  if (ptx::elect_one()) walk = {blockIdx.x, 0, 0};
+  __syncwarp();
+  bool key_role;
+  int bh, tile, share;
+  while (f.ok && next_unit(walk, p, key_role, bh, tile, share)) {
+    const int b = bh / p.H, h = bh - b * p.H;
     if (key_role)
-      bwd_body<true>(m, p, sm, bars, b, h, tile, share, unit, f);
+      bwd_body<true>(m, p, sm, bars, b, h, tile, share, (bh * p.nkt + tile) * p.n_qs + share, f);
     else
-      bwd_body<false>(m, p, sm, bars, b, h, tile, share, unit, f);
+      bwd_body<false>(m, p, sm, bars, b, h, tile, share, (bh * p.nqt + tile) * p.n_ks + share, f);
   }
   // Nothing asynchronous outlives the CTA: commits arrive in its shared memory, and after an abort copies and
   // products may be under way that nobody waits for.
@@ -909,9 +981,10 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   p.part_q = at(w.q);
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.n_key_units = (int)c.key_units;
-  p.n_units = (int)(c.key_units + c.query_units);
-  if (c.key_units + c.query_units > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
+  p.n_query_units = (int)c.query_units;
+  const long long units = c.key_units + c.query_units;
+  p.by_lens = key_lens && units > sms;
+  if (units > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
   const long long tasks = (long long)B * H * (p.q_pad / 8);
   if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   static unsigned long long smem_set = 0;
@@ -920,7 +993,7 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   e = launch_dependent(prep_kernel, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
                        static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.q_pad);
   if (e != cudaSuccess) return e;
-  e = launch_dependent_smem(cross_bwd_kernel, p.n_units < sms ? p.n_units : sms, kThreads, kSmemAlloc, stream, tqn,
+  e = launch_dependent_smem(cross_bwd_kernel, (int)(units < sms ? units : sms), kThreads, kSmemAlloc, stream, tqn,
                             tqr, tkn, tkr, tv, tdo, p);
   if (e != cudaSuccess) return e;
   const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
