@@ -15,6 +15,7 @@
 // awaited first it was 36 us.  (Blocks of two warps at 64 registers: with four 27.0, at 56
 // registers 29.5.)
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "rope.cuh"
@@ -37,7 +38,6 @@ struct Params {
   float* kv_scale;
   const int *page_table, *cache_lens, *new_lens;
   int rows, T, max_pages, num_pages;
-  int drop;  // rows of padding are not read
   unsigned int* err;
 };
 
@@ -65,7 +65,8 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
-template <bool kFp8, bool kPairs, bool kAxes>
+// kDrop: rows of padding are passed over before they are read.
+template <bool kFp8, bool kPairs, bool kAxes, bool kDrop>
 __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Params p) {
   wait_for_stream();
   const int lane = threadIdx.x & 31, l = lane & 15;
@@ -80,7 +81,9 @@ __global__ void __launch_bounds__(kWarps * 32, 16) rope_append_kernel(const Para
     L = __ldg(p.cache_lens + b);
     n = p.new_lens ? __ldg(p.new_lens + b) : p.T;
   }
-  if (p.drop && !__any_sync(0xffffffffu, t < n)) return;
+  if constexpr (kDrop) {
+    if (!__any_sync(0xffffffffu, t < n)) return;
+  }
   if (in_range) {
     if (!kAxes && p.positions) pos = __ldg(p.positions + id);
     const uint16_t* src = p.c_new + (long long)id * p.row_stride;
@@ -247,18 +250,22 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.err = err;
-  // Rows of padding are passed over before they are read where the rows are three times what stands on the GPU at once, and
-  // the length that this waits for is hidden (8 x 8191 rows, half of them padding, 3 axes: bf16 16.9, so 11.0 us; e4m3
-  // 17.5, so 14.1; 16384 rows the same either way; 64 to 4096 rows 0.3 us more)
-  p.drop = new_lens != nullptr && p.rows >= 32768;
   const int grid = (p.rows + 2 * kWarps - 1) / (2 * kWarps);
-  auto one = fp8 ? (pairs ? rope_append_kernel<true, true, false> : rope_append_kernel<true, false, false>)
-                 : (pairs ? rope_append_kernel<false, true, false> : rope_append_kernel<false, false, false>);
-  auto more = fp8 ? (pairs ? rope_append_kernel<true, true, true> : rope_append_kernel<true, false, true>)
-                  : (pairs ? rope_append_kernel<false, true, true> : rope_append_kernel<false, false, true>);
+  // Rows of padding are passed over where the rows are three times what stands on the GPU at once, which hides the length
+  // that this waits for (8 x 8191 rows, half of them padding, 3 axes: bf16 16.9, so 11.0 us; e4m3 17.5, so 14.1; 16384
+  // rows the same either way; 64 to 4096 rows 0.3 us more)
+  const bool drop = new_lens && p.rows >= 32768;
+  auto pick = [&](auto fp8_, auto pairs_) {
+    constexpr bool f = decltype(fp8_)::value, r = decltype(pairs_)::value;
+    return drop ? (axes > 1 ? rope_append_kernel<f, r, true, true> : rope_append_kernel<f, r, false, true>)
+                : (axes > 1 ? rope_append_kernel<f, r, true, false> : rope_append_kernel<f, r, false, false>);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  auto kernel = fp8 ? (pairs ? pick(yes, yes) : pick(yes, no)) : (pairs ? pick(no, yes) : pick(no, no));
   // (a programmatic dependent: calls of 128 x 7 rows in a row take 3.3 instead of 6.2 us, of 65536 rows
   // 26.2 instead of 28.7)
-  return launch_dependent(axes > 1 ? more : one, grid, kWarps * 32, stream, p);
+  return launch_dependent(kernel, grid, kWarps * 32, stream, p);
 }
 
 }  // namespace mla
