@@ -21,6 +21,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "sm103_ptx.cuh"
@@ -28,7 +29,7 @@
 namespace mla {
 namespace sm103_cross {
 
-constexpr int BM = 128, BN = 128;
+constexpr int BM = 128, BN = 128, DV = 128;
 constexpr int kChunk = 128 * 128;   // one 128-row x 128-byte swizzled chunk
 constexpr int kQTile = 3 * kChunk;  // nope (2 chunks) + rope (1 chunk)
 constexpr int kSlot = 2 * kChunk;   // a K_nope or V tile
@@ -53,6 +54,7 @@ struct Params {
   int nrb;        // row blocks of a (batch, head)
   int n_split;    // shares of the keys of a row block
   int units;      // B * H * nrb * n_split
+  int chunk;      // few rows: keys of a share
   int slot_rows;  // rows of a partial result
   float scale_log2;
   const int* key_lens;  // or null: Sk everywhere
@@ -82,6 +84,13 @@ __device__ __forceinline__ int key_len(const Params& p, int b) {
 // first key tile of share s
 __device__ __forceinline__ int share_begin(int tiles, int s, int n_split) {
   return static_cast<int>(static_cast<long long>(tiles) * s / n_split);
+}
+
+// share s of a sequence of len keys holds none
+__device__ __forceinline__ bool share_empty(const Params& p, int len, int s) {
+  if (p.chunk > 0) return static_cast<long long>(s) * p.chunk >= len;
+  const int tiles = (len + BN - 1) / BN;
+  return share_begin(tiles, s, p.n_split) == share_begin(tiles, s + 1, p.n_split);
 }
 
 struct Unit {
@@ -571,6 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+}  // namespace sm103_cross
+}  // namespace mla
+
+#include "cross_few_sm103.cuh"
+
+namespace mla {
+namespace sm103_cross {
+
 // Joins the shares of a row: with the largest of their log2 sums as reference, weights 2^(lse_s - max)
 // over their sum, in the order of the shares.  kWarps warps a row, every kWarps-th share each.
 template <int kWarps>
@@ -584,14 +601,14 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   const bool live = row < rows;
   const long long bh = live ? row / p.Sq : 0;
   const int i = live ? static_cast<int>(row - bh * p.Sq) : 0, b = static_cast<int>(bh / p.H);
-  const int tiles = live ? (key_len(p, b) + BN - 1) / BN : 0;
+  const int len = live ? key_len(p, b) : 0;
   const int block = i / p.slot_rows, r = i - block * p.slot_rows;
   const size_t first = (static_cast<size_t>(bh) * p.nrb + block) * p.n_split;
   float m = -INFINITY, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = part; s < p.n_split; s += kWarps) {
-    if (share_begin(tiles, s, p.n_split) == share_begin(tiles, s + 1, p.n_split)) continue;  // no keys of this sequence
+    if (share_empty(p, len, s)) continue;  // no keys of this sequence
     const size_t at = (first + s) * p.slot_rows + r;
     const float lse = ptx::ld_l2(p.part_lse + at);
     const float4 v = ptx::ld_l2(reinterpret_cast<const float4*>(p.part_o + at * 128) + lane);
@@ -626,18 +643,46 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
+// Whether a call of so many rows takes the form without tiles: one row always (1 x 8 heads x 77 keys 6.2, so 3.1 us; 64 x 32 x up
+// to 1500 155, so 128; 64 x 128 x 1000 679, so 624), two to four, whose products take longer than the keys' bytes, where
+// latency counts more (1 x 8 x 600: two rows 8.2, so 5.6, four 8.2, so 7.2; 2 x 1 x 20000: two 15.4, so 13.3, four 15, and
+// 18.5; 32 x 16 x 1500: two 73, and 104).
+inline bool few_rows(int B, int H, int Sq, int Sk) {
+  const long long keys = (long long)B * H * Sk;
+  return Sq == 1 || (Sq == 2 && keys <= 65536) || (Sq <= kFewRows && keys <= 32768);
+}
+
 // How a call is cut: row blocks of up to 256 rows (128 where that is all), and each block's keys in
 // n_split shares.  A share costs its key tiles and about kEnds of them more for its two ends, the join
 // about kJoin; the CTAs work in rounds of one unit each.
 struct Cut {
   bool one_tile;
-  int nrb, n_split, slot_rows;
-  long long units;
+  int nrb, n_split, slot_rows, chunk;
+  long long units;  // of tiles; a partial result each where split
 };
+constexpr int kFewStep = 128;  // few rows: keys of a CTA's step
 constexpr int kEnds = 2, kJoin = 3, kMaxSlots = 4;  // slots: units of a split call, times the SMs
 
-inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
-  Cut c;
+inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
+  Cut c = {};
+  if (few_rows(B, H, Sq, Sk)) {
+    const long long items = (long long)B * H, slots = (long long)sms * (Sq == 1 ? 2 : 1);
+    const int steps = (Sk + kFewStep - 1) / kFewStep;
+    double best = 1e300;
+    for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
+      const double unit = (double)((steps + s - 1) / s) + kEnds, rounds = (double)(items * s) / slots;
+      const double cost = (ragged ? std::max(rounds, 1.) + 0.5 : std::ceil(rounds)) * unit + (s > 1 ? 2 + s / 32. : 0);
+      if (cost < best) {
+        best = cost;
+        c.chunk = (int)std::min((steps + s - 1) / s * kFewStep, 0x7fffffffLL);
+      }
+    }
+    c.n_split = (int)(((long long)Sk + c.chunk - 1) / c.chunk);
+    c.nrb = 1;
+    c.slot_rows = Sq;
+    c.units = items * c.n_split;
+    return c;
+  }
   c.one_tile = Sq <= BM;
   c.nrb = c.one_tile ? 1 : (Sq + 2 * BM - 1) / (2 * BM);
   c.slot_rows = std::min(Sq, c.one_tile ? BM : 2 * BM);
@@ -699,6 +744,14 @@ cudaError_t launch_cross(const CUtensorMap& tqn, const CUtensorMap& tqr, const C
                                tkr, tv, p);
 }
 
+cudaError_t launch_join(const sm103_cross::Params& p, cudaStream_t stream) {
+  using namespace sm103_cross;
+  // few shares: a warp a row; many: the warps of a block share one
+  const long long rows = (long long)p.B * p.H * p.Sq;
+  if (p.n_split <= 4) return launch_dependent(join_kernel<1>, (int)((rows + 7) / 8), 256, stream, p);
+  return launch_dependent(join_kernel<8>, (int)rows, 256, stream, p);
+}
+
 }  // namespace
 
 // Whether the units of such a call can be numbered.
@@ -707,23 +760,19 @@ bool cross_fits(int B, int H, int Sq) {
 }
 
 size_t cross_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
-  const sm103_cross::Cut c = sm103_cross::cut_of(B, H, Sq, Sk, sms);
-  return c.n_split > 1 ? part_o_bytes(c) + part_lse_bytes(c) : 0;
+  size_t most = 0;  // with and without key lengths
+  for (const bool ragged : {false, true}) {
+    const sm103_cross::Cut c = sm103_cross::cut_of(B, H, Sq, Sk, ragged, sms);
+    if (c.n_split > 1) most = std::max(most, part_o_bytes(c) + part_lse_bytes(c));
+  }
+  return most;
 }
 
 cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
                                float softmax_scale, void* workspace, int sms, unsigned int* err, cudaStream_t stream) {
   using namespace sm103_cross;
-  CUtensorMap tqn, tqr, tkn, tkr, tv;
-  uint64_t kr_dims[3] = {64, (uint64_t)Sk, (uint64_t)B};
-  uint64_t kr_strides[2] = {64 * 2, (uint64_t)Sk * 64 * 2};
-  uint32_t kr_box[3] = {64, BN, 1};
-  if (!cross_map(&tqn, q_nope, B, Sq, H, 128) || !cross_map(&tqr, q_rope, B, Sq, H, 64) ||
-      !cross_map(&tkn, k_nope, B, Sk, H, 128) || !cross_map(&tv, v, B, Sk, H, 128) ||
-      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
-    return cudaErrorInvalidValue;
-  const Cut c = cut_of(B, H, Sq, Sk, sms);
+  const Cut c = cut_of(B, H, Sq, Sk, key_lens != nullptr, sms);
   Params p = {};
   p.B = B;
   p.H = H;
@@ -732,6 +781,7 @@ cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const voi
   p.nrb = c.nrb;
   p.n_split = c.n_split;
   p.units = (int)c.units;
+  p.chunk = c.chunk;
   p.slot_rows = c.slot_rows;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.key_lens = key_lens;
@@ -747,13 +797,27 @@ cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const voi
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_o_bytes);
   }
-  const cudaError_t e = c.one_tile ? launch_cross<true>(tqn, tqr, tkn, tkr, tv, p, sms, stream)
-                                   : launch_cross<false>(tqn, tqr, tkn, tkr, tv, p, sms, stream);
+  cudaError_t e;
+  if (c.chunk > 0) {
+    auto kernel = Sq == 1 ? few_rows_kernel<1, 4> : Sq == 2 ? few_rows_kernel<2, 2> : few_rows_kernel<4, 2>;
+    auto in = [](const void* x) { return static_cast<const uint16_t*>(x); };
+    e = launch_dependent(kernel, p.units, kFewWarps * 32, stream, in(q_nope), in(q_rope), in(k_nope), in(k_rope),
+                         in(v), p);
+    if (e != cudaSuccess || c.n_split == 1) return e;
+    return launch_join(p, stream);
+  }
+  CUtensorMap tqn, tqr, tkn, tkr, tv;
+  uint64_t kr_dims[3] = {64, (uint64_t)Sk, (uint64_t)B};
+  uint64_t kr_strides[2] = {64 * 2, (uint64_t)Sk * 64 * 2};
+  uint32_t kr_box[3] = {64, BN, 1};
+  if (!cross_map(&tqn, q_nope, B, Sq, H, 128) || !cross_map(&tqr, q_rope, B, Sq, H, 64) ||
+      !cross_map(&tkn, k_nope, B, Sk, H, 128) || !cross_map(&tv, v, B, Sk, H, 128) ||
+      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  e = c.one_tile ? launch_cross<true>(tqn, tqr, tkn, tkr, tv, p, sms, stream)
+                 : launch_cross<false>(tqn, tqr, tkn, tkr, tv, p, sms, stream);
   if (e != cudaSuccess || c.n_split == 1) return e;
-  // few shares: a warp a row; many: the warps of a block share one
-  const long long rows = (long long)B * H * Sq;
-  if (c.n_split <= 4) return launch_dependent(join_kernel<1>, (int)((rows + 7) / 8), 256, stream, p);
-  return launch_dependent(join_kernel<8>, (int)rows, 256, stream, p);
+  return launch_join(p, stream);
 }
 
 }  // namespace mla
