@@ -9,10 +9,11 @@
 //   - A CTA is persistent and walks work units of (batch, head, row block, share of the keys): the next
 //     unit's keys are on their way, and its first scores are formed, while this one's last rows are
 //     stored.  With encoder lengths of ten tiles a CTA a unit spent a fifth of its time on its two ends.
-//   - Row blocks of up to 128 rows (decode steps, short prompts) give both score buffers the same rows
-//     and every other key tile each (`by_keys`): each softmax warpgroup keeps its own maximum, sum and
-//     output accumulator and the two are joined at the end.  Such blocks are bound by the keys' bytes: four ring
-//     slots instead of three then take the shared memory that the second query tile would.
+//   - Up to eight rows (decode steps) take no tiles: cross_few_sm103.cuh.
+//   - Row blocks of up to 128 rows (short prompts) give both score buffers the same rows and every other key
+//     tile each (`by_keys`): each softmax warpgroup keeps its own maximum, sum and output accumulator and the
+//     two are joined at the end.  Such blocks are bound by the keys' bytes: four ring slots instead of three
+//     then take the shared memory that the second query tile would.
 //   - Few units (few rows, long keys) are split along the keys; a second kernel joins the shares by their
 //     log-sum-exp.
 //   - Keys behind a sequence's last are masked, and the value rows there zeroed in shared memory before
@@ -643,30 +644,22 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
-// Whether a call of so many rows takes the form without tiles: one row always (1 x 8 heads x 77 keys 6.2, so 3.1 us; 64 x 32 x up
-// to 1500 155, so 128; 64 x 128 x 1000 679, so 624), two to four, whose products take longer than the keys' bytes, where
-// latency counts more (1 x 8 x 600: two rows 8.2, so 5.6, four 8.2, so 7.2; 2 x 1 x 20000: two 15.4, so 13.3, four 15, and
-// 18.5; 32 x 16 x 1500: two 73, and 104).
-inline bool few_rows(int B, int H, int Sq, int Sk) {
-  const long long keys = (long long)B * H * Sk;
-  return Sq == 1 || (Sq == 2 && keys <= 65536) || (Sq <= kFewRows && keys <= 32768);
-}
-
 // How a call is cut: row blocks of up to 256 rows (128 where that is all), and each block's keys in
 // n_split shares.  A share costs its key tiles and about kEnds of them more for its two ends, the join
-// about kJoin; the CTAs work in rounds of one unit each.
+// about kJoin; the CTAs work in rounds of one unit each.  Few rows (the form without tiles): runs of whole steps, two
+// CTAs an SM that start as others end; where lengths are given they may be ragged, and half a unit more is charged
+// for the longest (16 x 8 heads, one row, up to 6000 keys: 44 us, 52 without).
 struct Cut {
   bool one_tile;
   int nrb, n_split, slot_rows, chunk;
   long long units;  // of tiles; a partial result each where split
 };
-constexpr int kFewStep = 128;  // few rows: keys of a CTA's step
 constexpr int kEnds = 2, kJoin = 3, kMaxSlots = 4;  // slots: units of a split call, times the SMs
 
 inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
   Cut c = {};
-  if (few_rows(B, H, Sq, Sk)) {
-    const long long items = (long long)B * H, slots = (long long)sms * (Sq == 1 ? 2 : 1);
+  if (Sq <= kFewRows) {
+    const long long items = (long long)B * H, slots = 2LL * sms;
     const int steps = (Sk + kFewStep - 1) / kFewStep;
     double best = 1e300;
     for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
@@ -799,7 +792,7 @@ cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const voi
   }
   cudaError_t e;
   if (c.chunk > 0) {
-    auto kernel = Sq == 1 ? few_rows_kernel<1, 4> : Sq == 2 ? few_rows_kernel<2, 2> : few_rows_kernel<4, 2>;
+    auto kernel = Sq == 1 ? one_row_kernel : eight_rows_kernel;
     auto in = [](const void* x) { return static_cast<const uint16_t*>(x); };
     e = launch_dependent(kernel, p.units, kFewWarps * 32, stream, in(q_nope), in(q_rope), in(k_nope), in(k_rope),
                          in(v), p);
