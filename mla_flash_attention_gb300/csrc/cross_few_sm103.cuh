@@ -1,5 +1,5 @@
-// Cross attention of at most eight queries a sequence (a decode step's token, a few drafted ones or beams), part of
-// cross_sm103.cu: loads straight into registers instead of tiles.
+// Cross attention of at most eight queries a sequence (a decode step's token, a few drafted ones or beams), and of more in
+// small calls, part of cross_sm103.cu: loads straight into registers instead of tiles.
 //
 // Such a call does 2 to 16 operations a byte of K and V, so their bytes bound it, and a tile of 128 rows would be
 // padding but for these rows: nothing is staged.  A CTA has one (batch, head) and a run of `chunk` keys, of which each
@@ -9,7 +9,7 @@
 //   one query: fp32 products, eight lanes a key (16 columns of nope and 8 of rope each, three shuffles a score),
 //     weights in fp32.  64 sequences x 32 heads, up to 1500 keys: 128 us (155 as tiles; the keys' bytes take 120); 64
 //     x 128 x 1000 keys 624 us (7.0 TB/s; 679 as tiles); 1 x 8 x 77 3.1 us (6.2).
-//   two to eight: 16 keys x 8 rows mma.sync, whose rate does here (20 of them for 16 keys, a fifth of a tile's padding):
+//   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (20 of them for 16 keys, a fifth of a tile's padding):
 //     scores as K Q', so that the rows fill the narrow side, and O' += V' P', P' being the scores' own registers
 //     transposed.  As Q K' with the rows on the wide side, half of it empty and twice the products, they took 158 instead of
 //     133 us.  64 x 32 x up to 1500 keys, 8 rows: 136 us (159 as tiles); 8 x 32 x 300 7.4 us (15.4).
@@ -19,7 +19,7 @@
 namespace mla {
 namespace sm103_cross {
 
-constexpr int kFewRows = 8;  // most queries a sequence of this form
+constexpr int kFewRows = 8;  // queries of a block
 constexpr int kFewWarps = 8, kFewStep = 16 * kFewWarps;  // keys of a step
 
 __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
@@ -190,15 +190,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   __shared__ float joined[kFewWarps][8][DV + 4];  // each warp's O, maximum, sums of exact and of rounded weights
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int heads = p.B * p.H, share = blockIdx.x / static_cast<unsigned>(heads), bh = blockIdx.x - share * heads;
+  const unsigned item = blockIdx.x / p.row_blocks, heads = p.B * p.H;
+  const int row0 = (blockIdx.x - item * p.row_blocks) * kFewRows, share = item / heads, bh = item - share * heads;
   const int b = bh / p.H, h = bh - b * p.H;
   const unsigned len = key_len(p, b), first = static_cast<unsigned>(share) * p.chunk, end = min(first + p.chunk, len);
   if (p.n_split > 1 && first >= len) return;  // (the join passes over it)
   if (threadIdx.x < 8 * 24) {
     const int r = threadIdx.x / 24, x = threadIdx.x - 24 * r;
     uint4 val = make_uint4(0, 0, 0, 0);
-    if (r < p.Sq) {
-      const size_t row = (static_cast<size_t>(b) * p.Sq + r) * p.H + h;
+    if (row0 + r < p.Sq) {
+      const size_t row = (static_cast<size_t>(b) * p.Sq + row0 + r) * p.H + h;
       val = x < 16 ? load_once(q_nope + row * 128 + 8 * x) : load_once(q_rope + row * 64 + 8 * (x - 16));
     }
     qs[r * kPadQ + x] = val;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   }
   __syncthreads();
   // the eight warps' results, in their order: a warp a row, four columns a lane
-  if (warp >= p.Sq) return;
+  if (row0 + warp >= p.Sq) return;
   float ref = -INFINITY, sum = 0.f, rounded = 0.f;
   for (int k = 0; k < kFewWarps; ++k) ref = fmaxf(ref, joined[k][warp][DV]);
   const float top = ref;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     a = make_float4(a.x + x.x * e, a.y + x.y * e, a.z + x.z * e, a.w + x.w * e);
   }
   const float inv = rounded == 0.f ? 0.f : 1.f / rounded, lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
-  finish_row(p, b, h, bh, share, warp, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), lse2);
+  finish_row(p, b, h, bh, share, row0 + warp, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), lse2);
 }
 
 }  // namespace sm103_cross

@@ -9,7 +9,7 @@
 //   - A CTA is persistent and walks work units of (batch, head, row block, share of the keys): the next
 //     unit's keys are on their way, and its first scores are formed, while this one's last rows are
 //     stored.  With encoder lengths of ten tiles a CTA a unit spent a fifth of its time on its two ends.
-//   - Up to eight rows (decode steps) take no tiles: cross_few_sm103.cuh.
+//   - Up to eight rows (decode steps), and small calls, take no tiles: cross_few_sm103.cuh.
 //   - Row blocks of up to 128 rows (short prompts) give both score buffers the same rows and every other key
 //     tile each (`by_keys`): each softmax warpgroup keeps its own maximum, sum and output accumulator and the
 //     two are joined at the end.  Such blocks are bound by the keys' bytes: four ring slots instead of three
@@ -55,7 +55,7 @@ struct Params {
   int nrb;        // row blocks of a (batch, head)
   int n_split;    // shares of the keys of a row block
   int units;      // B * H * nrb * n_split
-  int chunk;      // few rows: keys of a share
+  int chunk, row_blocks;  // few rows: keys of a share; blocks of eight rows
   unsigned shift;  // 1: see Walk
   int slot_rows;  // rows of a partial result
   float scale_log2;
@@ -657,6 +657,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
+// Whether a call takes the form without tiles: up to eight rows always; more, in blocks of eight that read the keys
+// once each, where a tile's latency is more than these reads (1 x 8 heads x 77 keys, 64 rows 6.5, so 3.6 us; 1 x 8 x 600, 100
+// rows 12.3, so 8.7; 8 x 8 x 300, 16 rows 8.7, so 6.2, 24 the same either way, 48 8.7, and 13.3), or where it would be
+// padding both ways (64 x 64 x 50, 16 rows 130, so 93; 24 rows 133 and 136).
+inline bool few_rows(int B, int H, int Sq, int Sk) {
+  const long long visits = (long long)B * H * ((Sq + kFewRows - 1) / kFewRows) * Sk;
+  return Sq <= kFewRows || visits <= 65536 || (Sq <= 24 && Sk <= 64 && visits <= 0x40000000);
+}
+
 // How a call is cut: row blocks of up to 256 rows (128 where that is all), and each block's keys in
 // n_split shares.  A share costs its key tiles and about kEnds of them more for its two ends, the join
 // about kJoin; the CTAs work in rounds of one unit each.  Few rows (the form without tiles): runs of whole steps, two
@@ -671,8 +680,9 @@ constexpr int kEnds = 2, kJoin = 3, kMaxSlots = 4;  // slots: units of a split c
 
 inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
   Cut c = {};
-  if (Sq <= kFewRows) {
-    const long long items = (long long)B * H, slots = 2LL * sms;
+  if (few_rows(B, H, Sq, Sk)) {
+    const int blocks = (Sq + kFewRows - 1) / kFewRows;
+    const long long items = (long long)B * H * blocks, slots = 2LL * sms;
     const int steps = (Sk + kFewStep - 1) / kFewStep;
     double best = 1e300;
     for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
@@ -686,7 +696,7 @@ inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
     c.n_split = (int)(((long long)Sk + c.chunk - 1) / c.chunk);
     c.nrb = 1;
     c.slot_rows = Sq;
-    c.units = items * c.n_split;
+    c.units = (long long)B * H * c.n_split;
     return c;
   }
   c.one_tile = Sq <= BM;
@@ -788,6 +798,7 @@ cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const voi
   p.n_split = c.n_split;
   p.units = (int)c.units;
   p.chunk = c.chunk;
+  p.row_blocks = (Sq + kFewRows - 1) / kFewRows;
   p.shift = c.nrb > 1 && (Sq - 1) % (2 * BM) < BM;
   p.slot_rows = c.slot_rows;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -808,7 +819,7 @@ cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const voi
   if (c.chunk > 0) {
     auto kernel = Sq == 1 ? one_row_kernel : eight_rows_kernel;
     auto in = [](const void* x) { return static_cast<const uint16_t*>(x); };
-    e = launch_dependent(kernel, p.units, kFewWarps * 32, stream, in(q_nope), in(q_rope), in(k_nope), in(k_rope),
+    e = launch_dependent(kernel, p.units * p.row_blocks, kFewWarps * 32, stream, in(q_nope), in(q_rope), in(k_nope), in(k_rope),
                          in(v), p);
     if (e != cudaSuccess || c.n_split == 1) return e;
     return launch_join(p, stream);
