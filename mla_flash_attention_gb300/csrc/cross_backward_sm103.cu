@@ -793,35 +793,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds what the units left in fp32.  The rope key's gradient, a sum over heads and shares, a
-// key a block: 16 threads' loads cover its 64 columns and 16 such groups take every 16th head or share each (one
-// thread for all of them waited 150 loads long), joined in group order.  The shares' gradients of K and V, and of
-// Q, where those were cut: a thread for four columns of a row.
+// Adds what the units left in fp32.  The rope key's gradient of a key, a sum over heads and shares: 16 threads' loads cover
+// its 64 columns, and kGroups such groups (one for four terms or fewer, up to a block's 16) take every kGroups-th
+// term each, joined in group order; a block has 16 / kGroups keys at a time (with one key a block, however few terms, the
+// gradient of 6 x 1 heads, 6 queries and up to 29241 keys took 274 us, so 118; one thread for all of 152 terms waited 150 loads
+// long).  The shares'
+// gradients of K and V, and of Q, where those were cut: a thread for four columns of a row.
+template <int kGroups>
 __global__ void __launch_bounds__(256) sum_kernel(const Params p) {
-  __shared__ float4 groups[16][17];
+  __shared__ float4 sums[16][17];
   wait_for_stream();
   auto add = [](float4& a, const float4& v) { a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
   auto put = [&](uint16_t* base, size_t at, size_t bytes, const float4& a) {
     uint2* dst = reinterpret_cast<uint2*>(base + at);
     if (MLA_STORE_OK(dst, base, bytes, p.err)) *dst = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
   };
-  const int c4 = threadIdx.x & 15, group = threadIdx.x >> 4;
-  for (long long row = blockIdx.x; row < (long long)p.B * p.Sk; row += gridDim.x) {
+  const int c4 = threadIdx.x & 15, place = threadIdx.x >> 4, terms = p.H * p.n_qs;
+  const int group = place % kGroups;
+  constexpr int keys = 16 / kGroups;
+  for (long long row0 = (long long)blockIdx.x * keys; row0 < (long long)p.B * p.Sk; row0 += (long long)gridDim.x * keys) {
+    const long long row = row0 + place / kGroups;
     const int b = static_cast<int>(row / p.Sk), key = static_cast<int>(row - (long long)b * p.Sk);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key < key_len(p, b)) {
-      const float* src = p.part_rope + ((size_t)b * p.H * p.n_qs * p.Sk + key) * 64 + 4 * c4;
+    if (b < p.B && key < key_len(p, b)) {
+      const float* src = p.part_rope + ((size_t)b * terms * p.Sk + key) * 64 + 4 * c4;
 #pragma unroll 4
-      for (int k = group; k < p.H * p.n_qs; k += 16)
+      for (int k = group; k < terms; k += kGroups)
         add(a, ptx::ld_l2(reinterpret_cast<const float4*>(src + (size_t)k * p.Sk * 64)));
     }
-    groups[group][c4] = a;
-    __syncthreads();
-    if (group == 0) {
-      for (int k = 1; k < 16; ++k) add(a, groups[k][c4]);
-      put(p.dk_rope, row * 64 + 4 * c4, p.rope_bytes, a);
+    if constexpr (kGroups > 1) {
+      sums[place][c4] = a;
+      __syncthreads();
+      if (group == 0)
+        for (int k = 1; k < kGroups; ++k) add(a, sums[place + k][c4]);
     }
-    __syncthreads();
+    if (group == 0 && b < p.B) put(p.dk_rope, row * 64 + 4 * c4, p.rope_bytes, a);
+    if constexpr (kGroups > 1) __syncthreads();
   }
   const long long n_kv = p.n_qs > 1 ? (long long)p.B * p.Sk * p.H * 64 : 0;
   const long long n_q = p.n_ks > 1 ? (long long)p.B * p.Sq * p.H * 48 : 0;
@@ -997,8 +1004,13 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
                             tqr, tkn, tkr, tv, tdo, p);
   if (e != cudaSuccess) return e;
   const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
-  const long long rows = (long long)B * Sk, blocks = rows > (cut + 255) / 256 ? rows : (cut + 255) / 256, most = 8LL * sms;
-  return launch_dependent(sum_kernel, (int)(blocks < most ? blocks : most), 256, stream, p);
+  // four terms a group, fewer while there are blocks for it
+  const long long keys = (long long)B * Sk, terms = (long long)H * c.n_qs;
+  int groups = 1;
+  while (groups < 16 && groups < terms && (groups * 4 < terms || keys * groups < 16 * 4LL * sms)) groups *= 2;
+  const long long blocks = std::max((keys * groups + 15) / 16, (cut + 255) / 256);
+  auto sum = groups == 1 ? sum_kernel<1> : groups == 2 ? sum_kernel<2> : groups == 4 ? sum_kernel<4> : groups == 8 ? sum_kernel<8> : sum_kernel<16>;
+  return launch_dependent(sum, (int)std::min(blocks, 8LL * sms), 256, stream, p);
 }
 
 }  // namespace mla

@@ -657,15 +657,6 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
-// Whether a call takes the form without tiles: up to eight rows always; more, in blocks of eight that read the keys
-// once each, where a tile's latency is more than these reads (1 x 8 heads x 77 keys, 64 rows 6.5, so 3.6 us; 1 x 8 x 600, 100
-// rows 12.3, so 8.7; 8 x 8 x 300, 16 rows 8.7, so 6.2, 24 the same either way, 48 8.7, and 13.3), or where it would be
-// padding both ways (64 x 64 x 50, 16 rows 130, so 93; 24 rows 133 and 136).
-inline bool few_rows(int B, int H, int Sq, int Sk) {
-  const long long visits = (long long)B * H * ((Sq + kFewRows - 1) / kFewRows) * Sk;
-  return Sq <= kFewRows || visits <= 65536 || (Sq <= 24 && Sk <= 64 && visits <= 0x40000000);
-}
-
 // How a call is cut: row blocks of up to 256 rows (128 where that is all), and each block's keys in
 // n_split shares.  A share costs its key tiles and about kEnds of them more for its two ends, the join
 // about kJoin; the CTAs work in rounds of one unit each.  Few rows (the form without tiles): runs of whole steps, two
@@ -678,27 +669,29 @@ struct Cut {
 };
 constexpr int kEnds = 2, kJoin = 3, kMaxSlots = 4;  // slots: units of a split call, times the SMs
 
-inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
+inline Cut few_cut(int B, int H, int Sq, int Sk, bool ragged, int sms) {
   Cut c = {};
-  if (few_rows(B, H, Sq, Sk)) {
-    const int blocks = (Sq + kFewRows - 1) / kFewRows;
-    const long long items = (long long)B * H * blocks, slots = 2LL * sms;
-    const int steps = (Sk + kFewStep - 1) / kFewStep;
-    double best = 1e300;
-    for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
-      const double unit = (double)((steps + s - 1) / s) + kEnds, rounds = (double)(items * s) / slots;
-      const double cost = (ragged ? std::max(rounds, 1.) + 0.5 : std::ceil(rounds)) * unit + (s > 1 ? 2 + s / 32. : 0);
-      if (cost < best) {
-        best = cost;
-        c.chunk = (int)std::min((steps + s - 1) / s * kFewStep, 0x7fffffffLL);
-      }
+  const int blocks = (Sq + kFewRows - 1) / kFewRows;
+  const long long items = (long long)B * H * blocks, slots = 2LL * sms;
+  const int steps = (Sk + kFewStep - 1) / kFewStep;
+  double best = 1e300;
+  for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
+    const double unit = (double)((steps + s - 1) / s) + kEnds, rounds = (double)(items * s) / slots;
+    const double cost = (ragged ? std::max(rounds, 1.) + 0.5 : std::ceil(rounds)) * unit + (s > 1 ? 2 + s / 32. : 0);
+    if (cost < best) {
+      best = cost;
+      c.chunk = (int)std::min((steps + s - 1) / s * kFewStep, 0x7fffffffLL);
     }
-    c.n_split = (int)(((long long)Sk + c.chunk - 1) / c.chunk);
-    c.nrb = 1;
-    c.slot_rows = Sq;
-    c.units = (long long)B * H * c.n_split;
-    return c;
   }
+  c.n_split = (int)(((long long)Sk + c.chunk - 1) / c.chunk);
+  c.nrb = 1;
+  c.slot_rows = Sq;
+  c.units = (long long)B * H * c.n_split;
+  return c;
+}
+
+inline Cut tile_cut(int B, int H, int Sq, int Sk, int sms) {
+  Cut c = {};
   c.one_tile = Sq <= BM;
   c.nrb = c.one_tile ? 1 : (Sq + 2 * BM - 1) / (2 * BM);
   c.slot_rows = std::min(Sq, c.one_tile ? BM : 2 * BM);
@@ -716,6 +709,23 @@ inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
   }
   c.units = items * c.n_split;
   return c;
+}
+
+// Up to eight rows take the form without tiles, more of them, in blocks of eight that read the keys once each, where that is
+// expected to be faster.  Microseconds, fitted to calls of 8 to 100 rows: a CTA of few rows has 2.2 beside its keys, of which
+// 128 take 1.1 alone and 2.9 with all SMs full; a unit of tiles 3 beside 1.5 a tile, and 1.7 to start with (1 x 8
+// heads x 77 keys, 64 rows 6.5, so 3.6; 1 x 8 x 600, 100 rows 12.3, so 8.7; 64 x 64 x 50, 16 rows 130, so 93, 32 rows 134,
+// not 181; 8 x 8 x 300, 16 rows 8.7, so 6.2, 48 rows 8.7, not 13.3).
+inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
+  const Cut few = few_cut(B, H, Sq, Sk, ragged, sms);
+  if (Sq <= kFewRows) return few;
+  const Cut tiles = tile_cut(B, H, Sq, Sk, sms);
+  const double ctas = (double)few.units * ((Sq + kFewRows - 1) / kFewRows), slots = 2. * sms;
+  const double keys = (double)std::min(few.chunk, Sk) / kFewStep, full = std::min(ctas / slots, 1.);
+  const double t_few = std::ceil(ctas / slots) * (keys * (1.1 + 1.8 * full) + 2.2) + (few.n_split > 1 ? 2.2 : 0);
+  const double t_tiles = 1.7 + std::ceil((double)tiles.units / sms) * ((Sk + BN - 1) / BN / tiles.n_split * 1.5 + 3) +
+                         (tiles.n_split > 1 ? 3 : 0);
+  return t_few < t_tiles && ctas < 0x40000000 ? few : tiles;
 }
 
 }  // namespace sm103_cross
