@@ -27,6 +27,7 @@
 //   - In the key role the keys are TMEM lanes, so what stands behind a sequence's last key stays in lanes that are
 //     stored as zeros; in the query role those keys' weights and dP are masked and their K rows zeroed in shared
 //     memory (0 * NaN is NaN).
+//   - Few queries and keys take no tiles: cross_backward_few_sm103.cuh.
 //   - The tiles that a CTA streams are cut in shares where few tiles of the one kind meet many of the other.  Shares,
 //     and the rope key's gradient of each head, are fp32 partial results that a third kernel adds in a fixed
 //     order: gradients do not depend on the run.
@@ -75,6 +76,7 @@ struct Params {
   int nqt, nkt;            // query tiles, key tiles of Sk
   int n_query_units;
   int n_qs, n_ks;          // shares of the query tiles (key role) and of the key tiles (query role)
+  int few_chunk;           // few queries: keys of a CTA; else 0
   int by_lens;             // units pass over the key tiles that hold no key
   int wide;                // the bf16 gradients are 32-byte aligned
   float scale, scale_log2;
@@ -852,12 +854,12 @@ __global__ void __launch_bounds__(256) sum_kernel(const Params p) {
       const int c = static_cast<int>(at - bqh * 48) * 4, h = static_cast<int>(bqh % p.H);
       const long long bq = bqh / p.H;
       const int b = static_cast<int>(bq / p.Sq), q = static_cast<int>(bq - (long long)b * p.Sq);
-      const int tiles = (key_len(p, b) + BT - 1) / BT;
+      const int len = key_len(p, b), tiles = (len + BT - 1) / BT, rows = p.few_chunk ? p.Sq : BT;
       const size_t unit = (((size_t)b * p.H + h) * p.nqt + q / BT) * p.n_ks;
 #pragma unroll 4
       for (int s = 0; s < p.n_ks; ++s)
-        if (share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
-          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((unit + s) * BT + q % BT) * 192 + c)));
+        if (p.few_chunk ? (long long)s * p.few_chunk < len : share_begin(tiles, s, p.n_ks) < share_begin(tiles, s + 1, p.n_ks))
+          add(a, ptx::ld_l2(reinterpret_cast<const float4*>(p.part_q + ((unit + s) * rows + q % BT) * 192 + c)));
       if (c < 128)
         put(p.dq_nope, bqh * 128 + c, p.q_bytes, a);
       else
@@ -866,18 +868,46 @@ __global__ void __launch_bounds__(256) sum_kernel(const Params p) {
   }
 }
 
+}  // namespace sm103_cross_bwd
+}  // namespace mla
+
+#include "cross_backward_few_sm103.cuh"
+
+namespace mla {
+namespace sm103_cross_bwd {
+
 // How a call is cut: the tiles that one CTA streams go in shares where their
 // steps would last longer than half of what an SM has to do in all.
 struct Cut {
-  int nqt, nkt, n_qs, n_ks;
+  int nqt, nkt, n_qs, n_ks, few_chunk;
   long long key_units, query_units;
 };
 constexpr int kLeastSteps = 4;
 
 inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
-  Cut c;
+  Cut c = {};
   c.nqt = (Sq + BT - 1) / BT;
   c.nkt = (Sk + BT - 1) / BT;
+  // Few queries and keys without tiles (microseconds, 8 | 32 queries: 53 x 56 heads, up to 9 keys 228 | 234, so 35 | 79; 26 x 15 x up to
+  // 112 44 | 44, so 21 | 26; 4 x 99 x up to 524 118, so 97 | 122 either way; 8 x 16 x 1000 81 | 85, not 93 | 110)
+  if ((Sq <= 16 && Sk <= 512) || (Sq <= kFewRows && Sk <= 256)) {
+    // runs of whole steps, two CTAs an SM; a CTA takes about as long as three steps beside its own, a sum of shares as two
+    const long long items = (long long)B * H, slots = 2LL * sms;
+    const int steps = (Sk + kFewKeys - 1) / kFewKeys;
+    double best = 1e300;
+    for (long long s = 1; s <= steps && (s == 1 || items * s <= 4 * slots); ++s) {
+      const double cost = (double)((items * s + slots - 1) / slots) * ((double)((steps + s - 1) / s) + 3) + (s > 1 ? 2 + s / 16. : 0);
+      if (cost < best) {
+        best = cost;
+        c.few_chunk = (int)std::min((steps + s - 1) / s * kFewKeys, 0x7fffffc0LL);
+      }
+    }
+    c.n_qs = 1;
+    c.n_ks = (int)(((long long)Sk + c.few_chunk - 1) / c.few_chunk);
+    c.key_units = 0;
+    c.query_units = items * c.n_ks;
+    return c;
+  }
   const double each = (double)B * H * c.nqt * c.nkt / sms;  // half of both roles' steps, an SM
   const double most = each > kLeastSteps ? each : kLeastSteps;
   c.n_qs = c.nqt > most ? (int)(c.nqt / most + 0.999) : 1;
@@ -912,26 +942,26 @@ bool cross_bwd_fits(int B, int H, int Sq, int Sk) {
 namespace {
 struct CrossBwdWorkspace {
   size_t nlse2, dvec, rope, kv, q, bytes;  // offsets, and the whole
-  CrossBwdWorkspace(const sm103_cross_bwd::Cut& c, int B, int H, int Sk) {
+  CrossBwdWorkspace(const sm103_cross_bwd::Cut& c, int B, int H, int Sq, int Sk) {
     size_t at = 0;
     auto take = [&](size_t n) {
       const size_t here = at;
       at += (n + 255) / 256 * 256;
       return here;
     };
-    const size_t vec = (size_t)B * H * c.nqt * sm103_cross_bwd::BT * sizeof(float);
+    const size_t vec = c.few_chunk ? 0 : (size_t)B * H * c.nqt * sm103_cross_bwd::BT * sizeof(float);
     nlse2 = take(vec);
     dvec = take(vec);
     rope = take((size_t)B * H * c.n_qs * Sk * 64 * sizeof(float));
     kv = take(c.n_qs > 1 ? (size_t)c.key_units * sm103_cross_bwd::BT * 256 * sizeof(float) : 0);
-    q = take(c.n_ks > 1 ? (size_t)c.query_units * sm103_cross_bwd::BT * 192 * sizeof(float) : 0);
+    q = take(c.n_ks > 1 ? (size_t)c.query_units * (c.few_chunk ? Sq : sm103_cross_bwd::BT) * 192 * sizeof(float) : 0);
     bytes = at + 32;
   }
 };
 }  // namespace
 
 size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
-  return CrossBwdWorkspace(sm103_cross_bwd::cut_of(B, H, Sq, Sk, sms), B, H, Sk).bytes;
+  return CrossBwdWorkspace(sm103_cross_bwd::cut_of(B, H, Sq, Sk, sms), B, H, Sq, Sk).bytes;
 }
 
 cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
@@ -941,15 +971,16 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
                                    unsigned int* err, cudaStream_t stream) {
   using namespace sm103_cross_bwd;
   const Cut c = cut_of(B, H, Sq, Sk, sms);
-  const CrossBwdWorkspace w(c, B, H, Sk);
+  const CrossBwdWorkspace w(c, B, H, Sq, Sk);
   CUtensorMap tqn, tqr, tkn, tkr, tv, tdo;
   uint64_t kr_dims[3] = {64, (uint64_t)Sk, (uint64_t)B};
   uint64_t kr_strides[2] = {64 * 2, (uint64_t)Sk * 64 * 2};
   uint32_t kr_box[3] = {64, BT, 1};
-  if (!cross_bwd_map(&tqn, q_nope, B, Sq, H, 128) || !cross_bwd_map(&tqr, q_rope, B, Sq, H, 64) ||
+  if (c.few_chunk == 0 &&
+      (!cross_bwd_map(&tqn, q_nope, B, Sq, H, 128) || !cross_bwd_map(&tqr, q_rope, B, Sq, H, 64) ||
       !cross_bwd_map(&tkn, k_nope, B, Sk, H, 128) || !cross_bwd_map(&tv, v, B, Sk, H, 128) ||
       !cross_bwd_map(&tdo, d_out, B, Sq, H, 128) ||
-      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess)
+      encode_tensor_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_rope, kr_dims, kr_strides, kr_box) != cudaSuccess))
     return cudaErrorInvalidValue;
   // (the workspace is 16-byte aligned, its parts 32)
   char* base = static_cast<char*>(workspace) + (reinterpret_cast<uintptr_t>(workspace) & 16);
@@ -972,6 +1003,7 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   p.nkt = c.nkt;
   p.n_qs = c.n_qs;
   p.n_ks = c.n_ks;
+  p.few_chunk = c.few_chunk;
   p.key_lens = key_lens;
   const void* grads[] = {dq_nope, dq_rope, dk_nope, dv};
   p.wide = 1;
@@ -992,17 +1024,30 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   const long long units = c.key_units + c.query_units;
   p.by_lens = key_lens && units > sms;
   if (units > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
-  const long long tasks = (long long)B * H * (p.q_pad / 8);
-  if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  static unsigned long long smem_set = 0;
-  cudaError_t e = smem_attr_once(cross_bwd_kernel, kSmemAlloc, &smem_set);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(prep_kernel, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
-                       static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.q_pad);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent_smem(cross_bwd_kernel, (int)(units < sms ? units : sms), kThreads, kSmemAlloc, stream, tqn,
-                            tqr, tkn, tkr, tv, tdo, p);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (c.few_chunk) {
+    auto at16 = [](const void* x) { return static_cast<const uint16_t*>(x); };
+    const FewInputs in{at16(q_nope), at16(q_rope), at16(k_nope), at16(k_rope), at16(v), at16(out), at16(d_out), lse};
+    static unsigned long long few_set[2] = {0, 0};
+    auto kernel = Sq <= 16 ? few_rows_kernel<16> : few_rows_kernel<32>;
+    const int bytes = Sq <= 16 ? FewSmem<16>::kBytes : FewSmem<32>::kBytes;
+    e = smem_attr_once(kernel, bytes, &few_set[Sq > 16]);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent_smem(kernel, (int)units, 256, bytes, stream, in, p);
+    if (e != cudaSuccess) return e;
+  } else {
+    const long long tasks = (long long)B * H * (p.q_pad / 8);
+    if ((tasks + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    static unsigned long long smem_set = 0;
+    e = smem_attr_once(cross_bwd_kernel, kSmemAlloc, &smem_set);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(prep_kernel, (int)((tasks + 7) / 8), 256, stream, static_cast<const uint16_t*>(out),
+                         static_cast<const uint16_t*>(d_out), lse, at(w.nlse2), at(w.dvec), B, H, Sq, p.q_pad);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent_smem(cross_bwd_kernel, (int)(units < sms ? units : sms), kThreads, kSmemAlloc, stream, tqn,
+                              tqr, tkn, tkr, tv, tdo, p);
+    if (e != cudaSuccess) return e;
+  }
   const long long cut = (c.n_qs > 1 ? (long long)B * Sk * H * 64 : 0) + (c.n_ks > 1 ? (long long)B * Sq * H * 48 : 0);
   // four terms a group, fewer while there are blocks for it
   const long long keys = (long long)B * Sk, terms = (long long)H * c.n_qs;

@@ -167,12 +167,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   finish_row(p, b, h, bh, share, 0, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), lse2);
 }
 
-// d (16 x 8) += a (16 x 16) b (16 x 8)
-__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // an 8 x 8 matrix of 16-bit values, two of a row a lane, transposed
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -234,8 +228,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
 #pragma unroll
     for (int j = 0; j < 6; ++j) {
       const uint4 q = qs[g * kPadQ + 4 * j + t];
-      mma_16x8(s, kk[0][j].x, kk[1][j].x, kk[0][j].y, kk[1][j].y, q.x, q.y);
-      mma_16x8(s1, kk[0][j].z, kk[1][j].z, kk[0][j].w, kk[1][j].w, q.z, q.w);
+      ptx::mma_16x8(s, kk[0][j].x, kk[1][j].x, kk[0][j].y, kk[1][j].y, q.x, q.y);
+      ptx::mma_16x8(s1, kk[0][j].z, kk[1][j].z, kk[0][j].w, kk[1][j].w, q.z, q.w);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -280,7 +274,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     for (int i = 0; i < 8; ++i) {
       auto word = [&](const uint4& x) { return (i & 6) == 0 ? x.x : (i & 6) == 2 ? x.y : (i & 6) == 4 ? x.z : x.w; };
       const uint32_t pick = i & 1 ? 0x7632 : 0x5410;
-      mma_16x8(o[i], __byte_perm(word(vv[0][0]), word(vv[1][0]), pick), __byte_perm(word(vv[0][1]), word(vv[1][1]), pick),
+      ptx::mma_16x8(o[i], __byte_perm(word(vv[0][0]), word(vv[1][0]), pick), __byte_perm(word(vv[0][1]), word(vv[1][1]), pick),
                __byte_perm(word(vv[2][0]), word(vv[3][0]), pick), __byte_perm(word(vv[2][1]), word(vv[3][1]), pick), w[0], w[1]);
     }
   }
