@@ -1,4 +1,4 @@
-// Gradient of cross attention for few queries and keys (at most 32 queries a sequence), part of cross_backward_sm103.cu: 128-row
+// Gradient of cross attention for few queries and keys (at most 64 queries a sequence), part of cross_backward_sm103.cu: 128-row
 // tiles would be padding but for these, and a unit of tiles takes 6 us however little there is in it (53 x 56 heads, 29
 // queries, up to 9 keys 234 us, so 76; 26 x 15 heads, 3 queries, up to 112 keys 44, so 21; 11 x 48, 18 queries, 165 keys 97, so
 // 77).  Bound by latency: a step is a load, three barriers and chains of 20 products, 7 us of two CTAs an SM, so that long
@@ -16,7 +16,7 @@
 namespace mla {
 namespace sm103_cross_bwd {
 
-constexpr int kFewRows = 32;  // most queries of this form
+constexpr int kFewRows = 64;  // most queries of this form
 constexpr int kFewKeys = 64;  // keys of a step
 
 template <int kRows>
@@ -100,9 +100,43 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
   // rows of the fragments: of A (16 x 16 at row, column) and of B from rows [n][k]; both from rows [k][m or n] by transposing
   const int ar = lane & 15, ac = (lane >> 4) * 16, br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 16;
   constexpr int kQueryStrips = kRows / 16;
-  const bool has_dq = warp < 3 * kQueryStrips;
+  constexpr bool kSteps = kRows <= 32;  // more rows: no more keys than a step's, dQ a product like the others
+  const bool has_dq = kSteps && warp < 3 * kQueryStrips;
   const int dq_strip = warp / 3, dq_block = warp - 3 * dq_strip;
   float dq[8][4] = {};
+  auto add_dq = [&](float (&acc)[8][4], int strip, int block, int strips) {  // dS K of one step
+    for (int k = 0; k < strips; ++k) {
+      uint32_t a[4];
+      ptx::ldmatrix_x4<true>(a, base + L::kDs + (16 * k + br) * L::kStrideP + 32 * strip + bc);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t kb[4];
+        ptx::ldmatrix_x4<true>(kb, base + L::kK + (16 * k + ar) * L::kStride3 + 128 * block + 32 * n + ac);
+        ptx::mma_16x8(acc[2 * n], a[0], a[1], a[2], a[3], kb[0], kb[1]);
+        ptx::mma_16x8(acc[2 * n + 1], a[0], a[1], a[2], a[3], kb[2], kb[3]);
+      }
+    }
+  };
+  auto store_dq = [&](const float (&acc)[8][4], int strip, int block) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int q = 16 * strip + g + 8 * half;
+      if (p.n_ks > 1) {
+        if (q >= p.Sq) continue;
+        float* row = p.part_q + (((size_t)bh * p.n_ks + share) * p.Sq + q) * 192 + 64 * block + 2 * t;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          float2* dst = reinterpret_cast<float2*>(row + 8 * n);
+          if (MLA_STORE_OK(dst, p.part_q, p.part_q_bytes, p.err)) *dst = make_float2(acc[n][2 * half] * p.scale, acc[n][2 * half + 1] * p.scale);
+        }
+      } else {
+        const size_t at = ((size_t)b * p.Sq + q) * p.H + h;
+        uint16_t* to = block < 2 ? p.dq_nope : p.dq_rope;
+        store_piece(block < 2 ? to + at * 128 + 64 * block : to + at * 64, acc, half, p.scale, t, q < p.Sq, to,
+                    block < 2 ? p.q_bytes : p.q_bytes / 2, p.err);
+      }
+    }
+  };
   for (long long k0l = first; k0l < end; k0l += kFewKeys) {
     const int k0 = static_cast<int>(k0l), strips = (min(kFewKeys, end - k0) + 15) / 16;
     __syncthreads();  // (the keys before are done with)
@@ -163,21 +197,16 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
       }
     }
     __syncthreads();
-    if (has_dq) {
-      for (int k = 0; k < strips; ++k) {
-        uint32_t a[4];
-        ptx::ldmatrix_x4<true>(a, base + L::kDs + (16 * k + br) * L::kStrideP + 32 * dq_strip + bc);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t kb[4];
-          ptx::ldmatrix_x4<true>(kb, base + L::kK + (16 * k + ar) * L::kStride3 + 128 * dq_block + 32 * n + ac);
-          ptx::mma_16x8(dq[2 * n], a[0], a[1], a[2], a[3], kb[0], kb[1]);
-          ptx::mma_16x8(dq[2 * n + 1], a[0], a[1], a[2], a[3], kb[2], kb[3]);
-        }
-      }
-    }
+    if (has_dq) add_dq(dq, dq_strip, dq_block, strips);
     // pieces 0, 1 of a strip: dV; 2, 3: dK nope; 4: dK rope
-    for (int task = 7 - warp; task < 5 * strips; task += 8) {
+    for (int task = 7 - warp; task < 5 * strips + (kSteps ? 0 : 3 * kQueryStrips); task += 8) {
+      if (!kSteps && task >= 5 * strips) {
+        float acc[8][4] = {};
+        const int piece = task - 5 * strips;
+        add_dq(acc, piece / 3, piece % 3, strips);
+        store_dq(acc, piece / 3, piece % 3);
+        continue;
+      }
       const int strip = task / 5, piece = task - 5 * strip;
       const uint32_t from = base + (piece < 2 ? L::kP : L::kDs), with = base + (piece < 2 ? L::kDo + 128 * piece : L::kQ + 128 * (piece - 2));
       const int stride = piece < 2 ? L::kStride2 : L::kStride3;
@@ -213,25 +242,9 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
       }
     }
   }
-  if (!has_dq) return;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int q = 16 * dq_strip + g + 8 * half;
-    if (p.n_ks > 1) {
-      if (q >= p.Sq) continue;
-      float* row = p.part_q + (((size_t)bh * p.n_ks + share) * p.Sq + q) * 192 + 64 * dq_block + 2 * t;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float2* dst = reinterpret_cast<float2*>(row + 8 * n);
-        if (MLA_STORE_OK(dst, p.part_q, p.part_q_bytes, p.err)) *dst = make_float2(dq[n][2 * half] * p.scale, dq[n][2 * half + 1] * p.scale);
-      }
-    } else {
-      const size_t at = ((size_t)b * p.Sq + q) * p.H + h;
-      uint16_t* to = dq_block < 2 ? p.dq_nope : p.dq_rope;
-      store_piece(dq_block < 2 ? to + at * 128 + 64 * dq_block : to + at * 64, dq, half, p.scale, t, q < p.Sq, to,
-                  dq_block < 2 ? p.q_bytes : p.q_bytes / 2, p.err);
-    }
-  }
+  if (has_dq) store_dq(dq, dq_strip, dq_block);
+  if (!kSteps && len == 0)  // zeros
+    for (int piece = warp; piece < 3 * kQueryStrips; piece += 8) store_dq(dq, piece / 3, piece % 3);
 }
 
 }  // namespace sm103_cross_bwd

@@ -889,8 +889,9 @@ inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
   c.nqt = (Sq + BT - 1) / BT;
   c.nkt = (Sk + BT - 1) / BT;
   // Few queries and keys without tiles (microseconds, 8 | 32 queries: 53 x 56 heads, up to 9 keys 228 | 234, so 35 | 79; 26 x 15 x up to
-  // 112 44 | 44, so 21 | 26; 4 x 99 x up to 524 118, so 97 | 122 either way; 8 x 16 x 1000 81 | 85, not 93 | 110)
-  if ((Sq <= 16 && Sk <= 512) || (Sq <= kFewRows && Sk <= 256)) {
+  // 112 44 | 44, so 21 | 26; 4 x 99 x up to 524 118, so 97 | 122 either way; 8 x 16 x 1000 81 | 85, not 93 | 110; 33 | 64: 37 x 49 x
+  // 13 121 | 127, so 68 | 87; 64 x 64 x 40 269 | 277, 244 | 286; 11 x 48 x 128 55 | 57, not 97 | 121)
+  if ((Sq <= 16 && Sk <= 512) || (Sq <= 32 && Sk <= 256) || (Sq <= kFewRows && Sk <= kFewKeys / 2)) {
     // runs of whole steps, two CTAs an SM; a CTA takes about as long as three steps beside its own, a sum of shares as two
     const long long items = (long long)B * H, slots = 2LL * sms;
     const int steps = (Sk + kFewKeys - 1) / kFewKeys;
@@ -1028,10 +1029,11 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   if (c.few_chunk) {
     auto at16 = [](const void* x) { return static_cast<const uint16_t*>(x); };
     const FewInputs in{at16(q_nope), at16(q_rope), at16(k_nope), at16(k_rope), at16(v), at16(out), at16(d_out), lse};
-    static unsigned long long few_set[2] = {0, 0};
-    auto kernel = Sq <= 16 ? few_rows_kernel<16> : few_rows_kernel<32>;
-    const int bytes = Sq <= 16 ? FewSmem<16>::kBytes : FewSmem<32>::kBytes;
-    e = smem_attr_once(kernel, bytes, &few_set[Sq > 16]);
+    static unsigned long long few_set[3] = {0, 0, 0};
+    const int rows = Sq <= 16 ? 0 : Sq <= 32 ? 1 : 2;
+    auto kernel = rows == 0 ? few_rows_kernel<16> : rows == 1 ? few_rows_kernel<32> : few_rows_kernel<64>;
+    const int bytes = rows == 0 ? FewSmem<16>::kBytes : rows == 1 ? FewSmem<32>::kBytes : FewSmem<64>::kBytes;
+    e = smem_attr_once(kernel, bytes, &few_set[rows]);
     if (e != cudaSuccess) return e;
     e = launch_dependent_smem(kernel, (int)units, 256, bytes, stream, in, p);
     if (e != cudaSuccess) return e;

@@ -9,7 +9,7 @@
 //   one query: fp32 products, eight lanes a key (16 columns of nope and 8 of rope each, three shuffles a score),
 //     weights in fp32.  64 sequences x 32 heads, up to 1500 keys: 128 us (155 as tiles; the keys' bytes take 120); 64
 //     x 128 x 1000 keys 624 us (7.0 TB/s; 679 as tiles); 1 x 8 x 77 3.1 us (6.2).
-//   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (20 of them for 16 keys, a fifth of a tile's padding):
+//   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (20 of them for 16 keys):
 //     scores as K Q', so that the rows fill the narrow side, and O' += V' P', P' being the scores' own registers
 //     transposed.  As Q K' with the rows on the wide side, half of it empty and twice the products, they took 158 instead of
 //     133 us.  64 x 32 x up to 1500 keys, 8 rows: 136 us (159 as tiles); 8 x 32 x 300 7.4 us (15.4).

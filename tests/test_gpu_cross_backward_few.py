@@ -1,5 +1,5 @@
-"""Gradients of cross attention of few queries and keys, which take a form without tiles (up to 16 queries and 512 keys, or 32
-and 256), and of the sizes next to it: strips of 16, steps of 64 keys, runs of several CTAs, sequences without
+"""Gradients of cross attention of few queries and keys, which take a form without tiles (up to 16 queries and 512 keys, 32
+and 256, or 64 and 32), and of the sizes next to it: strips of 16, steps of 64 keys, runs of several CTAs, sequences without
 keys, NaN behind the last key, repeated bit for bit.  Bounds as in test_gpu_cross_backward.py."""
 import pytest
 import torch
@@ -17,8 +17,8 @@ def lengths(B, Sk):
     return lens.tolist()
 
 
-@pytest.mark.parametrize("Sq", [1, 2, 15, 16, 17, 31, 32, 33])
-@pytest.mark.parametrize("Sk", [1, 15, 16, 17, 63, 64, 65, 200, 256, 257])
+@pytest.mark.parametrize("Sq", [1, 2, 15, 16, 17, 31, 32, 33, 50, 64, 65])
+@pytest.mark.parametrize("Sk", [1, 15, 16, 17, 32, 33, 63, 64, 65, 128, 129, 200, 256, 257])
 def test_counts(lib, Sq, Sk):
     for lens in (None, lengths(5, Sk)):
         p = Grad(lib, 5, 3, Sq, Sk, lens=lens)
@@ -29,7 +29,7 @@ def test_counts(lib, Sq, Sk):
 
 @pytest.mark.parametrize("B,H,Sq,Sk,lens", [
     (1, 1, 16, 512, None), (2, 2, 9, 511, [511, 65]), (1, 1, 16, 513, None), (3, 1, 30, 250, [250, 129, 0]), (40, 17, 12, 130, None),
-    (130, 5, 7, 90, "any"), (60, 40, 3, 20, "any")])
+    (130, 5, 7, 90, "any"), (60, 40, 3, 20, "any"), (60, 40, 60, 20, "any"), (40, 30, 47, 128, "any")])
 def test_runs_and_many_heads_repeat_exactly(lib, B, H, Sq, Sk, lens):
     p = Grad(lib, B, H, Sq, Sk, lens=lengths(B, Sk) if lens == "any" else lens)
     grads = p.backward(lib)
@@ -71,7 +71,7 @@ def test_non_finite_values_stay_in_their_sequence_and_head(lib):
 def test_writes_only_its_outputs_and_workspace(lib):
     from tests.test_gpu_canaries import Guarded
 
-    for B, H, Sq, Sk in ((2, 3, 16, 200), (1, 1, 11, 500), (1, 1, 32, 256), (3, 5, 1, 3)):
+    for B, H, Sq, Sk in ((2, 3, 16, 200), (1, 1, 11, 500), (1, 1, 32, 256), (3, 5, 1, 3), (2, 3, 61, 33), (2, 3, 64, 128)):
         p = Grad(lib, B, H, Sq, Sk)
         grads = [Guarded(t.shape, torch.bfloat16) for t in p.args()[:5]]
         ws = Guarded((lib.cross_attention_backward_workspace_size(B, H, Sq, Sk),), torch.uint8)
