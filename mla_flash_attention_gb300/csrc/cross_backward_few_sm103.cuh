@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
           float2* dst = reinterpret_cast<float2*>(row + 8 * n);
-          if (MLA_STORE_OK(dst, p.part_q, p.part_q_bytes, p.err)) *dst = make_float2(acc[n][2 * half] * p.scale, acc[n][2 * half + 1] * p.scale);
+          if (MLA_STORE_OK(dst, p.part_q, p.part_q_bytes, p.err))
+            *dst = make_float2(acc[n][2 * half] * p.scale, acc[n][2 * half + 1] * p.scale);
         }
       } else {
         const size_t at = ((size_t)b * p.Sq + q) * p.H + h;
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
         continue;
       }
       const int strip = task / 5, piece = task - 5 * strip;
-      const uint32_t from = base + (piece < 2 ? L::kP : L::kDs), with = base + (piece < 2 ? L::kDo + 128 * piece : L::kQ + 128 * (piece - 2));
+      const uint32_t from = base + (piece < 2 ? L::kP : L::kDs);
+      const uint32_t with = base + (piece < 2 ? L::kDo + 128 * piece : L::kQ + 128 * (piece - 2));
       const int stride = piece < 2 ? L::kStride2 : L::kStride3;
       float acc[8][4] = {};
 #pragma unroll
@@ -234,10 +236,12 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             float2* dst = reinterpret_cast<float2*>(row + 8 * n);
-            if (MLA_STORE_OK(dst, p.part_rope, p.part_rope_bytes, p.err)) *dst = make_float2(acc[n][2 * half] * mul, acc[n][2 * half + 1] * mul);
+            if (MLA_STORE_OK(dst, p.part_rope, p.part_rope_bytes, p.err))
+              *dst = make_float2(acc[n][2 * half] * mul, acc[n][2 * half + 1] * mul);
           }
         } else {
-          store_piece(to + (((size_t)b * p.Sk + key) * p.H + h) * 128 + 64 * (piece & 1), acc, half, mul, t, key < end, to, p.k_bytes, p.err);
+          store_piece(to + (((size_t)b * p.Sk + key) * p.H + h) * 128 + 64 * (piece & 1), acc, half, mul, t, key < end, to,
+                      p.k_bytes, p.err);
         }
       }
     }

@@ -1056,7 +1056,11 @@ cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const
   int groups = 1;
   while (groups < 16 && groups < terms && (groups * 4 < terms || keys * groups < 16 * 4LL * sms)) groups *= 2;
   const long long blocks = std::max((keys * groups + 15) / 16, (cut + 255) / 256);
-  auto sum = groups == 1 ? sum_kernel<1> : groups == 2 ? sum_kernel<2> : groups == 4 ? sum_kernel<4> : groups == 8 ? sum_kernel<8> : sum_kernel<16>;
+  auto sum = groups == 1   ? sum_kernel<1>
+             : groups == 2 ? sum_kernel<2>
+             : groups == 4 ? sum_kernel<4>
+             : groups == 8 ? sum_kernel<8>
+                           : sum_kernel<16>;
   return launch_dependent(sum, (int)std::min(blocks, 8LL * sms), 256, stream, p);
 }
 
