@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(256, 2) few_rows_kernel(const FewInputs in, co
     if (has_dq) add_dq(dq, dq_strip, dq_block, strips);
     // pieces 0, 1 of a strip: dV; 2, 3: dK nope; 4: dK rope
     for (int task = 7 - warp; task < 5 * strips + (kSteps ? 0 : 3 * kQueryStrips); task += 8) {
+      __syncwarp();  // (lanes of no key or query stored nothing of the task before)
       if (!kSteps && task >= 5 * strips) {
         float acc[8][4] = {};
         const int piece = task - 5 * strips;

@@ -599,6 +599,7 @@ __device__ __forceinline__ void bwd_body(const Maps& m, const Params& p, unsigne
             }
           }
           ptx::fence_proxy_async();
+          __syncwarp();  // (the store of dS is the whole warp's, and the first step has no wait before it)
         }
       }
       // dS = P * (dP - D) as bf16 pairs

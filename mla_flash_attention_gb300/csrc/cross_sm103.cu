@@ -553,23 +553,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * w0);
           }
-          if (!row_live) continue;
-          if (p.n_split > 1) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * 128 + c * 32);
+          if (row_live) {
+            if (p.n_split > 1) {
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * 128 + c * 32);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (MLA_STORE_OK(dst + x, p.part_o, p.part_o_bytes, p.err))
-                dst[x] = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(out_row + c * 32);
-            const float* f = reinterpret_cast<const float*>(v);
+              for (int x = 0; x < 8; ++x)
+                if (MLA_STORE_OK(dst + x, p.part_o, p.part_o_bytes, p.err))
+                  dst[x] = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(out_row + c * 32);
+              const float* f = reinterpret_cast<const float*>(v);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (MLA_STORE_OK(dst + x, p.out, p.out_bytes, p.err))
-                dst[x] = make_uint4(
-                    ptx::pack_bf16x2(f[8 * x], f[8 * x + 1]), ptx::pack_bf16x2(f[8 * x + 2], f[8 * x + 3]),
-                    ptx::pack_bf16x2(f[8 * x + 4], f[8 * x + 5]), ptx::pack_bf16x2(f[8 * x + 6], f[8 * x + 7]));
+              for (int x = 0; x < 4; ++x)
+                if (MLA_STORE_OK(dst + x, p.out, p.out_bytes, p.err))
+                  dst[x] = make_uint4(
+                      ptx::pack_bf16x2(f[8 * x], f[8 * x + 1]), ptx::pack_bf16x2(f[8 * x + 2], f[8 * x + 3]),
+                      ptx::pack_bf16x2(f[8 * x + 4], f[8 * x + 5]), ptx::pack_bf16x2(f[8 * x + 6], f[8 * x + 7]));
+            }
           }
+          __syncwarp();  // the next columns are loaded by the whole warp, rows of padding included
         }
         if (row_live) {
           if (p.n_split > 1) {
