@@ -440,8 +440,9 @@ size_t mla_cross_attention_workspace_size(int B, int H, int Sq, int Sk);
  * Queries that share their keys (beams of one sequence) are rows of one sequence: Sq counts them all.
  * Attention to two sources, or to a prefix and then causally to the rest, joins by the two LSEs.
  * Softmax weights enter the product with V as bf16, as in mla_prefill (with one query a sequence as fp32).
- * Supported: d_nope = 128, d_rope = 64, d_v = 128; B, H <= 65535; B * H * ceil(Sq / 256) <= 2^30,
- * B * H * Sq <= 8e9 and Sq * H, Sk * H below 2^32.
+ * Supported: d_nope = 128, d_rope = 64, d_v = 128; B, H from 1 to 65535, Sq, Sk from 1 to 2^31 - 512 (a
+ * sequence without keys is one of key length 0); B * H * ceil(Sq / 256) <= 2^30, B * H * Sq <= 8e9 and
+ * Sq * H, Sk * H below 2^32.
  */
 mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const void* k_nope,
                                const void* k_rope, const void* v, const int* key_lens, void* out,

@@ -238,8 +238,9 @@ mla_status check_cross(const char* fn, int B, int H, int Sq, int Sk, int d_nope,
     return fail(MLA_ERR_UNSUPPORTED, "%s: only d_nope=128, d_rope=64, d_v=128 are built (got %d, %d, %d)", fn, d_nope,
                 d_rope, d_v);
   if (B > 65535 || H > 65535) return fail(MLA_ERR_UNSUPPORTED, "%s: B and H must be at most 65535", fn);
-  // (a sequence's bytes have to fit a tensor map's stride of 40 bits)
-  if (!mla::cross_fits(B, H, Sq) || (long long)Sq * H >= (1LL << 32) || (long long)Sk * H >= (1LL << 32))
+  // (counts rounded up to whole tiles are ints, and a sequence's bytes have to fit a tensor map's stride of 40 bits)
+  if (std::max(Sq, Sk) > 0x7fffffff - 511 || !mla::cross_fits(B, H, Sq) || (long long)Sq * H >= (1LL << 32) ||
+      (long long)Sk * H >= (1LL << 32))
     return fail(MLA_ERR_UNSUPPORTED, "%s: problem too large", fn);
   if (!std::isfinite(softmax_scale) || softmax_scale <= 0.f)
     return fail(MLA_ERR_INVALID_ARG, "%s: softmax_scale must be finite and positive", fn);
