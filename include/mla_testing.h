@@ -39,6 +39,17 @@ int mla_testing_bounds_checked(void);
  */
 void mla_testing_bounds_shrink(long long bytes);
 
+/*
+ * mla_testing_cross_plan, mla_testing_cross_backward_plan -- the form that mla_cross_attention, with key
+ * lengths (`ragged`) or without, and its backward take for calls of these sizes on a GPU of `sms` SMs (<= 0: the
+ * current one), so that a test can name the form that it means.  Forward: 0 without tiles, 1 by key tiles and
+ * one query tile, 2 by key tiles and two; *shares: into how many the keys are cut.  Backward: 0 without tiles, 1 by
+ * tiles; *query_shares, *key_shares: into how many the tiles that a unit streams are cut.  -1 for sizes that the
+ * calls refuse.  Host arithmetic alone.
+ */
+int mla_testing_cross_plan(int B, int H, int Sq, int Sk, int ragged, int sms, int* shares);
+int mla_testing_cross_backward_plan(int B, int H, int Sq, int Sk, int sms, int* query_shares, int* key_shares);
+
 #ifdef __cplusplus
 }
 #endif

@@ -121,6 +121,10 @@ _lib.mla_testing_bounds_checked.restype = _i
 _lib.mla_testing_bounds_checked.argtypes = []
 _lib.mla_testing_bounds_shrink.restype = None
 _lib.mla_testing_bounds_shrink.argtypes = [ctypes.c_longlong]
+_lib.mla_testing_cross_plan.restype = _i
+_lib.mla_testing_cross_plan.argtypes = [_i, _i, _i, _i, _i, _i, _ip]
+_lib.mla_testing_cross_backward_plan.restype = _i
+_lib.mla_testing_cross_backward_plan.argtypes = [_i, _i, _i, _i, _i, _ip, _ip]
 
 EXPORTED = ("mla_prefill", "mla_decode_workspace_size", "mla_decode", "mla_decode_noalloc",
             "mla_decode_noalloc_max_workspace", "mla_cache_append", "mla_absorb",
@@ -132,7 +136,7 @@ EXPORTED = ("mla_prefill", "mla_decode_workspace_size", "mla_decode", "mla_decod
             "mla_cross_attention_backward_workspace_size", "mla_cross_attention_backward",
             "mla_check_device_error",
             "mla_last_error", "mla_version", "mla_testing_decode_stall", "mla_testing_bounds_checked",
-            "mla_testing_bounds_shrink")
+            "mla_testing_bounds_shrink", "mla_testing_cross_plan", "mla_testing_cross_backward_plan")
 
 
 class MLAError(RuntimeError):
@@ -192,6 +196,21 @@ def testing_bounds_shrink(nbytes: int = 0) -> None:
     """Test hook (include/mla_testing.h): later launches report `out` as `nbytes` smaller to
     the store checks of the bounds-checked build; ``testing_bounds_shrink()`` restores them."""
     _lib.mla_testing_bounds_shrink(int(nbytes))
+
+
+def testing_cross_plan(B: int, H: int, Sq: int, Sk: int, ragged: bool = False, sms: int = 0):
+    """Test hook (include/mla_testing.h): (form, shares) of mla_cross_attention with key lengths or
+    without; form 0 without tiles, 1 one query tile, 2 two."""
+    n = _i()
+    return int(_lib.mla_testing_cross_plan(B, H, Sq, Sk, int(ragged), sms, ctypes.addressof(n))), n.value
+
+
+def testing_cross_backward_plan(B: int, H: int, Sq: int, Sk: int, sms: int = 0):
+    """Test hook (include/mla_testing.h): (form, query shares, key shares) of
+    mla_cross_attention_backward; form 0 without tiles, 1 by tiles."""
+    q, k = _i(), _i()
+    form = _lib.mla_testing_cross_backward_plan(B, H, Sq, Sk, sms, ctypes.addressof(q), ctypes.addressof(k))
+    return int(form), q.value, k.value
 
 
 def check_device_error(stream=None) -> None:

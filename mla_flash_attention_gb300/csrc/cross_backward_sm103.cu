@@ -966,6 +966,14 @@ size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
   return CrossBwdWorkspace(sm103_cross_bwd::cut_of(B, H, Sq, Sk, sms), B, H, Sq, Sk).bytes;
 }
 
+// Of a call's plan, for tests: 0 without tiles, 1 by tiles.
+int cross_bwd_form(int B, int H, int Sq, int Sk, int sms, int* query_shares, int* key_shares) {
+  const sm103_cross_bwd::Cut c = sm103_cross_bwd::cut_of(B, H, Sq, Sk, sms);
+  *query_shares = c.n_qs;
+  *key_shares = c.n_ks;
+  return c.few_chunk > 0 ? 0 : 1;
+}
+
 cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                    const void* v, const int* key_lens, const void* out, const float* lse,
                                    const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,

@@ -796,6 +796,13 @@ size_t cross_workspace_bytes(int B, int H, int Sq, int Sk, int sms) {
   return most;
 }
 
+// Of a call's plan, for tests: 0 without tiles, 1 one query tile, 2 two.
+int cross_form(int B, int H, int Sq, int Sk, bool ragged, int sms, int* shares) {
+  const sm103_cross::Cut c = sm103_cross::cut_of(B, H, Sq, Sk, ragged, sms);
+  *shares = c.n_split;
+  return c.chunk > 0 ? 0 : c.one_tile ? 1 : 2;
+}
+
 cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
                                float softmax_scale, void* workspace, int sms, unsigned int* err, cudaStream_t stream) {

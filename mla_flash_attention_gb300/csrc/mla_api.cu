@@ -58,11 +58,13 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
                                int max_pages, int num_pages, bool fp8, unsigned int* err, cudaStream_t stream);
 bool cross_fits(int B, int H, int Sq);
 size_t cross_workspace_bytes(int B, int H, int Sq, int Sk, int sms);
+int cross_form(int B, int H, int Sq, int Sk, bool ragged, int sms, int* shares);
 cudaError_t launch_cross_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                const void* v, const int* key_lens, void* out, float* lse, int B, int H, int Sq, int Sk,
                                float softmax_scale, void* workspace, int sms, unsigned int* err, cudaStream_t stream);
 bool cross_bwd_fits(int B, int H, int Sq, int Sk);
 size_t cross_bwd_workspace_bytes(int B, int H, int Sq, int Sk, int sms);
+int cross_bwd_form(int B, int H, int Sq, int Sk, int sms, int* query_shares, int* key_shares);
 cudaError_t launch_cross_bwd_sm103(const void* q_nope, const void* q_rope, const void* k_nope, const void* k_rope,
                                    const void* v, const int* key_lens, const void* out, const float* lse,
                                    const void* d_out, void* dq_nope, void* dq_rope, void* dk_nope, void* dk_rope,
@@ -404,6 +406,19 @@ void mla_testing_decode_stall(int skip_unit, long long wait_limit_cycles) {
 }
 
 void mla_testing_bounds_shrink(long long bytes) { g_out_shrink.store(bytes > 0 ? (size_t)bytes : 0); }
+
+int mla_testing_cross_plan(int B, int H, int Sq, int Sk, int ragged, int sms, int* shares) {
+  if (check_cross("mla_testing_cross_plan", B, H, Sq, Sk, 128, 64, 128, 1.f) != MLA_OK) return -1;
+  if (sms <= 0) sms = num_sms_current();
+  return sms > 0 ? mla::cross_form(B, H, Sq, Sk, ragged != 0, sms, shares) : -1;
+}
+
+int mla_testing_cross_backward_plan(int B, int H, int Sq, int Sk, int sms, int* query_shares, int* key_shares) {
+  const char* fn = "mla_testing_cross_backward_plan";
+  if (check_cross(fn, B, H, Sq, Sk, 128, 64, 128, 1.f) != MLA_OK || !mla::cross_bwd_fits(B, H, Sq, Sk)) return -1;
+  if (sms <= 0) sms = num_sms_current();
+  return sms > 0 ? mla::cross_bwd_form(B, H, Sq, Sk, sms, query_shares, key_shares) : -1;
+}
 
 int mla_testing_bounds_checked(void) {
 #ifdef MLA_DEBUG
