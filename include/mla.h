@@ -439,7 +439,8 @@ size_t mla_cross_attention_workspace_size(int B, int H, int Sq, int Sk);
  *           overlap on the GPU need one each
  * Queries that share their keys (beams of one sequence) are rows of one sequence: Sq counts them all.
  * Attention to two sources, or to a prefix and then causally to the rest, joins by the two LSEs.
- * Softmax weights enter the product with V as bf16, as in mla_prefill (with one query a sequence as fp32).
+ * Softmax weights enter the product with V rounded to bf16, as in mla_prefill; with up to eight queries a
+ * sequence, and in small calls of more, to 2^-15 of themselves or better.
  * Supported: d_nope = 128, d_rope = 64, d_v = 128; B, H from 1 to 65535, Sq, Sk from 1 to 2^31 - 512 (a
  * sequence without keys is one of key length 0); B * H * ceil(Sq / 256) <= 2^30, B * H * Sq <= 8e9 and
  * Sq * H, Sk * H below 2^32.

@@ -9,7 +9,7 @@
 //   one query: fp32 products, eight lanes a key (16 columns of nope and 8 of rope each, three shuffles a score),
 //     weights in fp32.  64 sequences x 32 heads, up to 1500 keys: 128 us (155 as tiles; the keys' bytes take 120); 64
 //     x 128 x 1000 keys 624 us (7.0 TB/s; 679 as tiles); 1 x 8 x 77 3.1 us (6.2).
-//   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (20 of them for 16 keys):
+//   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (28 of them for 16 keys):
 //     scores as K Q', so that the rows fill the narrow side, and O' += V' P', P' being the scores' own registers
 //     transposed.  As Q K' with the rows on the wide side, half of it empty and twice the products, they took 158 instead of
 //     133 us.  64 x 32 x up to 1500 keys, 8 rows: 136 us (159 as tiles); 8 x 32 x 300 7.4 us (15.4).
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
                       const uint16_t* __restrict__ k_nope, const uint16_t* __restrict__ k_rope,
                       const uint16_t* __restrict__ v, const Params p) {
   __shared__ uint4 qs[8 * kPadQ];
-  __shared__ float joined[kFewWarps][8][DV + 4];  // each warp's O, maximum, sums of exact and of rounded weights
+  __shared__ float joined[kFewWarps][8][DV + 4];  // each warp's O, maximum, sum
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const unsigned item = blockIdx.x / p.row_blocks, heads = p.B * p.H;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   }
   __syncthreads();
   float o[8][4] = {};  // O': columns 8 g + i and 64 + 8 g + i, rows 2 t and 2 t + 1 each
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, lr[2] = {};  // of rows 2 t, 2 t + 1; the sums of this lane's keys
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {};  // of rows 2 t, 2 t + 1; the sums of this lane's keys
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (unsigned key0 = first + warp * 16; key0 < end; key0 += kFewStep) {
     uint4 kk[2][6], vv[4][2];
@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         const float to = fmaxf(m[r], top[r]), keep = ptx::ex2(m[r] - (to == -INFINITY ? 0.f : to));
         m[r] = to;
         l[r] *= keep;
-        lr[r] *= keep;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[i][r] *= keep;
@@ -257,34 +256,38 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         }
       }
     }
-    uint32_t w[2];
+    // A weight enters the products as two bf16 terms, its upper half and the rest rounded, which gives it to 2^-15 and not 2^-8
+    // (with one term O was off by 0.0023 of itself, RMS, where its own rounding is 0.0017) and takes no time here: 64 x 32 x
+    // up to 1500 keys, 2 rows 134.4, so 135.0 us, 8 rows 137.2 either way.  The rest is taken 2^-20 of the weight too large,
+    // so that neither term is 0: times an infinite value both are that.
+    uint32_t w[2], rest[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const float x = ptx::ex2(fmaf(s[2 * n], p.scale_log2, m[0] == -INFINITY ? 0.f : -m[0]));
       const float y = ptx::ex2(fmaf(s[2 * n + 1], p.scale_log2, m[1] == -INFINITY ? 0.f : -m[1]));
-      w[n] = ptx::pack_bf16x2(x, y);
+      w[n] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+      rest[n] = ptx::pack_bf16x2(fmaf(x, 0x1p-20f, x - __uint_as_float(__float_as_uint(x) & 0xffff0000u)),
+                                 fmaf(y, 0x1p-20f, y - __uint_as_float(__float_as_uint(y) & 0xffff0000u)));
       l[0] += x;
       l[1] += y;
-      lr[0] += __uint_as_float(w[n] << 16);
-      lr[1] += __uint_as_float(w[n] & 0xffff0000u);
       w[n] = transposed(w[n]);  // keys 2 t, 2 t + 1 of row g
+      rest[n] = transposed(rest[n]);
     }
     // O' += V' P': column i of a lane's 16 bytes in both halves of the row
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       auto word = [&](const uint4& x) { return (i & 6) == 0 ? x.x : (i & 6) == 2 ? x.y : (i & 6) == 4 ? x.z : x.w; };
       const uint32_t pick = i & 1 ? 0x7632 : 0x5410;
-      ptx::mma_16x8(o[i], __byte_perm(word(vv[0][0]), word(vv[1][0]), pick), __byte_perm(word(vv[0][1]), word(vv[1][1]), pick),
-               __byte_perm(word(vv[2][0]), word(vv[3][0]), pick), __byte_perm(word(vv[2][1]), word(vv[3][1]), pick), w[0], w[1]);
+      const uint32_t a[4] = {__byte_perm(word(vv[0][0]), word(vv[1][0]), pick), __byte_perm(word(vv[0][1]), word(vv[1][1]), pick),
+                             __byte_perm(word(vv[2][0]), word(vv[3][0]), pick), __byte_perm(word(vv[2][1]), word(vv[3][1]), pick)};
+      ptx::mma_16x8(o[i], a[0], a[1], a[2], a[3], w[0], w[1]);
+      ptx::mma_16x8(o[i], a[0], a[1], a[2], a[3], rest[0], rest[1]);
     }
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
 #pragma unroll
-    for (int off = 4; off < 32; off *= 2) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-      lr[r] += __shfl_xor_sync(0xffffffffu, lr[r], off);
-    }
+    for (int off = 4; off < 32; off *= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
     float* to = joined[warp][2 * t + r];
 #pragma unroll
     for (int half = 0; half < 2; ++half)
@@ -295,13 +298,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     if (g == 0) {
       to[DV] = m[r];
       to[DV + 1] = l[r];
-      to[DV + 2] = lr[r];
     }
   }
   __syncthreads();
   // the eight warps' results, in their order: a warp a row, four columns a lane
   if (row0 + warp >= p.Sq) return;
-  float ref = -INFINITY, sum = 0.f, rounded = 0.f;
+  float ref = -INFINITY, sum = 0.f;
   for (int k = 0; k < kFewWarps; ++k) ref = fmaxf(ref, joined[k][warp][DV]);
   const float top = ref;
   if (ref == -INFINITY) ref = 0.f;
@@ -312,10 +314,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     const float e = ptx::ex2(from[DV] - ref);
     const float4 x = reinterpret_cast<const float4*>(from)[lane];
     sum += from[DV + 1] * e;
-    rounded += from[DV + 2] * e;
     a = make_float4(a.x + x.x * e, a.y + x.y * e, a.z + x.z * e, a.w + x.w * e);
   }
-  const float inv = rounded == 0.f ? 0.f : 1.f / rounded, lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum, lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
   finish_row(p, b, h, bh, share, row0 + warp, lane, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), lse2);
 }
 

@@ -457,8 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m = m_use;
           const float neg_m = m == -INFINITY ? 0.f : -m;
-          // as in the prefill: O is normalised by the sum of the bf16-rounded weights that the product
-          // with V uses, the LSE is that of the exact ones
+          // as in the prefill: the weights enter the product with V as one bf16 term (a second one, as the forms without
+          // tiles have it, would double that product, 1024 of the 2560 clocks of MMAs that bound a step of long prompts),
+          // O is normalised by the sum of the rounded weights that the product uses, the LSE is that of the exact ones
           const uint64_t sc2 = ptx::f2(p.scale_log2, p.scale_log2), nm2 = ptx::f2(neg_m, neg_m);
           uint64_t ps2[2] = {ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f)};
           float pr[4] = {0.f, 0.f, 0.f, 0.f};
