@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import numbers
 import os
 from typing import Optional
 
@@ -487,13 +488,13 @@ def rope_turns_axes(inv_freq, pair_axes, device=None) -> torch.Tensor:
     [d_rope / 2] names the axis whose position turns each pair (0, 1, ..), in any order: sections one
     after another ([0] * 8 + [1] * 12 + [2] * 12), axes in turn, halves for rows and columns."""
     freqs = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else list(inv_freq)
-    axis = pair_axes.tolist() if isinstance(pair_axes, torch.Tensor) else list(pair_axes)
+    axis = pair_axes.tolist() if isinstance(pair_axes, torch.Tensor) else list(pair_axes)  # (an array's integers too)
     if len(freqs) != len(axis) or not axis:
         raise ValueError("pair_axes must name an axis for each of the %d pairs (got %d)" % (len(freqs), len(axis)))
-    if not all(isinstance(a, int) and not isinstance(a, bool) and 0 <= a < 4 for a in axis):
+    if not all(isinstance(a, numbers.Integral) and not isinstance(a, bool) and 0 <= a < 4 for a in axis):
         raise ValueError("pair_axes must be integers from 0 to 3")
     return torch.stack([rope_turns([f if a == row else 0.0 for f, a in zip(freqs, axis)], device)
-                        for row in range(max(axis) + 1)])
+                        for row in range(int(max(axis)) + 1)])
 
 
 def tree_mask_from_parents(parents):
