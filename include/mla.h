@@ -359,7 +359,8 @@ mla_status mla_qk_norm_rope_axes(const void* q, int64_t q_row_stride, int64_t q_
  * mla_qk_norm_rope_axes_backward -- gradients of mla_qk_norm_rope_axes.  dk_rope, the upstream
  * gradient of the rope key, is fp32 (as mla_prefill_backward gives it) or bf16 (as
  * mla_cross_attention_backward does), by dk_rope_dtype; the rest, the workspace included, is as for
- * mla_qk_norm_rope_backward.
+ * mla_qk_norm_rope_backward.  With axes = 1 it is that call for a bf16 dk_rope, which
+ * mla_qk_norm_rope_backward does not take.
  */
 mla_status mla_qk_norm_rope_axes_backward(
     const void* dq_nope, const void* dq_rope, const void* dk_nope, const void* dk_rope,
@@ -453,7 +454,11 @@ mla_status mla_cross_attention(const void* q_nope, const void* q_rope, const voi
 
 /*
  * mla_cross_attention_backward_workspace_size -- bytes of device workspace
- * mla_cross_attention_backward needs (0 for sizes it refuses).
+ * mla_cross_attention_backward needs (0 for sizes it refuses).  The rope key's gradient of each head is kept
+ * there in fp32 until the heads are summed in a fixed order: 256 bytes a (key, head), 1.07 GB for 128 heads of
+ * 32768 keys; the vectors of the rows' sums 8 bytes a (query, head).  Where few tiles of 128 queries meet many
+ * of keys, or the reverse, and streams are cut in shares, 768 bytes a (query, head) and share of the keys, or
+ * 1024 + 256 bytes a (key, head) and share of the queries.
  */
 size_t mla_cross_attention_backward_workspace_size(int B, int H, int Sq, int Sk);
 

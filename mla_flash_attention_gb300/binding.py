@@ -3,7 +3,7 @@
 Argument marshalling only: torch tensors are checked for device, dtype, shape and
 contiguity, then their device pointers and the current CUDA stream are passed to
 the library, through ctypes or, for the calls around the attention (norms, rotated
-append, drafted trees), through the compiled module ``_marshal``.  Every step of the
+append, drafted trees) and cross attention, through the compiled module ``_marshal``.  Every step of the
 attention runs inside the library's CUDA kernels; there is no fallback of any kind:
 if the shared library is missing, importing this module raises, and if ``_marshal``
 is missing or does not fit the installed torch, the calls that it marshals raise.
@@ -576,7 +576,8 @@ def mla_qk_norm_rope_axes_backward(dq_nope, dq_rope, dk_nope, dk_rope, q=None, k
                                    k_rope_weight=None, eps: float = 1e-6, interleaved: bool = True, grads=None,
                                    workspace=None, stream=None):
     """Gradients of mla_qk_norm_rope_axes.  dk_rope is fp32 (from mla_prefill_backward) or bf16 (from
-    mla_cross_attention_backward); everything else is as for mla_qk_norm_rope_backward."""
+    mla_cross_attention_backward; with positions on one axis too: positions [B,S,1], rope_turns [1, dr/2]);
+    everything else is as for mla_qk_norm_rope_backward."""
     return _call(stream, q if q is not None else k_nope if k_nope is not None else k_rope,
                  _marshal.qk_norm_rope_axes_backward, q, k_nope, k_rope, positions, rope_turns, q_nope_weight,
                  q_rope_weight, k_nope_weight, k_rope_weight, eps, interleaved, dq_nope, dq_rope, dk_nope, dk_rope,

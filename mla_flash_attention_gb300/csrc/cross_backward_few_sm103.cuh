@@ -6,8 +6,8 @@
 //
 // A CTA has one (batch, head) and a run of keys, 64 at a time; Q and dO stay in shared memory.  For each 64 keys
 //   S' = K Q', dP' = V dO' in pieces of 16 keys x 16 queries, P' = exp2(.. - LSE) and dS' = P' * (dP' - D) to shared memory
-//   as bf16; dV = P' dO and dK = dS' Q in pieces of 16 keys x 64 columns, written at once; dQ += dS K in pieces of 16 x 64
-//   that stay in registers of a warp each,
+//   as bf16 (as the form by tiles has them: a row has one precision in both); dV = P' dO and dK = dS' Q in pieces of 16 keys
+//   x 64 columns, written at once; dQ += dS K in pieces of 16 x 64 that stay in registers of a warp each,
 // all by mma.sync on ldmatrix fragments (rows of an odd number of 16 bytes: no bank conflicts), scores formed once.  D
 // is made by the CTA itself.  The rope key's gradient and, where a (batch, head) has several CTAs, dQ go to
 // the sum kernel in fp32.

@@ -6,6 +6,10 @@
 //   dV = P' dO,  dP = dO V',  D_i = sum_d dO_id O_id,  dS = P * (dP - D),
 //   dQ = scale dS K,  dK = scale dS' Q   (the rope key is shared by the heads: its gradient is the sum over them)
 //
+// P and dS are rounded to bf16 where they enter products as operands beside bf16 ones, as in the prefill's: gradients are
+// off by 0.0024 of themselves, RMS, where their own rounding is 0.0017; a second term of each would add
+// 44 % to the MMAs.  The rope key's gradient, the whole sum in fp32, is rounded once and to bf16 like the other gradients.
+//
 // Two roles of units with the products, tiles and roles of warps of the prefill's backward:
 //   key-tile units (b, h, 128 keys): K and V stay in shared memory; query tiles stream by.
 //     TMEM: X [0,128) S' = K Q' (keys on lanes), then dP' = V dO'; dV [128,256);

@@ -251,9 +251,10 @@ cudaError_t launch_rope_append(const void* c_new, long long row_stride, const vo
   p.num_pages = num_pages;
   p.err = err;
   const int grid = (p.rows + 2 * kWarps - 1) / (2 * kWarps);
-  // Rows of padding are passed over where the rows are three times what stands on the GPU at once, which hides the length
-  // that this waits for (8 x 8191 rows, half of them padding, 3 axes: bf16 16.9, so 11.0 us; e4m3 17.5, so 14.1; 16384
-  // rows the same either way; 64 to 4096 rows 0.3 us more)
+  // Rows of padding are passed over where the rows are three times what stands on a GPU of 152 SMs at once, which hides the
+  // length that this waits for (8 sequences of up to 8191 new rows, 44 % of the rows padding, 3 axes, from DRAM: bf16 21.5, so
+  // 17.6 us; e4m3 23.5, so 21.7; with the rows in L2 20.4, so 14.4, and 21.0, so 18.5; 16384 rows the same either way; 64 to
+  // 4096 rows 0.3 us more)
   const bool drop = new_lens && p.rows >= 32768;
   auto pick = [&](auto fp8_, auto pairs_) {
     constexpr bool f = decltype(fp8_)::value, r = decltype(pairs_)::value;
