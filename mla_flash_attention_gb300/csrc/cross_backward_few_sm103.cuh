@@ -1,7 +1,7 @@
 // Gradient of cross attention for few queries and keys (at most 64 queries a sequence), part of cross_backward_sm103.cu: 128-row
 // tiles would be padding but for these, and a unit of tiles takes 6 us however little there is in it (53 x 56 heads, 29
-// queries, up to 9 keys 234 us, so 76; 26 x 15 heads, 3 queries, up to 112 keys 44, so 21; 11 x 48, 18 queries, 165 keys 97, so
-// 77).  Bound by latency: a step is a load, three barriers and chains of 20 products, 7 us of two CTAs an SM, so that long
+// queries, up to 9 keys 242 us, so 79; 26 x 15 heads, 3 queries, up to 112 keys 45, so 21; 11 x 48, 18 queries, 165 keys 98, so
+// 79).  Bound by latency: a step is a load, three barriers and chains of 20 products, 7 us of two CTAs an SM, so that long
 // keys stay with the tiles.
 //
 // A CTA has one (batch, head) and a run of keys, 64 at a time; Q and dO stay in shared memory.  For each 64 keys

@@ -893,9 +893,11 @@ inline Cut cut_of(int B, int H, int Sq, int Sk, int sms) {
   Cut c = {};
   c.nqt = (Sq + BT - 1) / BT;
   c.nkt = (Sk + BT - 1) / BT;
-  // Few queries and keys without tiles (microseconds, 8 | 32 queries: 53 x 56 heads, up to 9 keys 228 | 234, so 35 | 79; 26 x 15 x up to
-  // 112 44 | 44, so 21 | 26; 4 x 99 x up to 524 118, so 97 | 122 either way; 8 x 16 x 1000 81 | 85, not 93 | 110; 33 | 64: 37 x 49 x
-  // 13 121 | 127, so 68 | 87; 64 x 64 x 40 269 | 277, 244 | 286; 11 x 48 x 128 55 | 57, not 97 | 121)
+  // Few queries and keys without tiles (microseconds as tiles and without, 8 | 32 queries: 53 x 56 heads, up to 9 keys 236 | 246, so
+  // 35 | 80; 26 x 15 x up to 112 45 | 45, so 21 | 25; 8 x 16 x 1000 81 | 86, not 93 | 110; 33 | 64: 37 x 49 x 13 121 | 128, so 68 | 89;
+  // 64 x 64 x 40 270 | 280, not 244 | 286; 11 x 48 x 128 57 | 59, not 97 | 121).  Towards its ends the rule errs where heads fill two
+  // CTAs an SM once and a bit: 11 x 48 x 128, 8 queries 54, so 46, but 32 queries 56, and 63 without; 4 x 99 x up to 512, 8
+  // queries 92, and 115 without.
   if ((Sq <= 16 && Sk <= 512) || (Sq <= 32 && Sk <= 256) || (Sq <= kFewRows && Sk <= kFewKeys / 2)) {
     // runs of whole steps, two CTAs an SM; a CTA takes about as long as three steps beside its own, a sum of shares as two
     const long long items = (long long)B * H, slots = 2LL * sms;

@@ -12,7 +12,7 @@
 //   two to eight (a CTA each eight of more): 16 keys x 8 rows mma.sync, whose rate does here (28 of them for 16 keys):
 //     scores as K Q', so that the rows fill the narrow side, and O' += V' P', P' being the scores' own registers
 //     transposed.  As Q K' with the rows on the wide side, half of it empty and twice the products, they took 158 instead of
-//     133 us.  64 x 32 x up to 1500 keys, 8 rows: 136 us (159 as tiles); 8 x 32 x 300 7.4 us (15.4).
+//     133 us.  64 x 32 x up to 1500 keys, 8 rows: 137 us (159 as tiles); 8 x 32 x 300 8.7 us.
 // Eight heads a CTA, a warp each, with shorter runs, took 134-140 us for the first.
 #pragma once
 

@@ -716,9 +716,11 @@ inline Cut tile_cut(int B, int H, int Sq, int Sk, int sms) {
 
 // Up to eight rows take the form without tiles, more of them, in blocks of eight that read the keys once each, where that is
 // expected to be faster.  Microseconds, fitted to calls of 8 to 100 rows: a CTA of few rows has 2.2 beside its keys, of which
-// 128 take 1.1 alone and 2.9 with all SMs full; a unit of tiles 3 beside 1.5 a tile (of a share: rounded down), and 1.7 to start with (1 x 8
-// heads x 77 keys, 64 rows 6.5, so 3.6; 1 x 8 x 600, 100 rows 12.3, so 8.7; 64 x 64 x 50, 16 rows 130, so 93, 32 rows 134,
-// not 181; 8 x 8 x 300, 16 rows 8.7, so 6.2, 48 rows 8.7, not 13.3).
+// 128 take 1.1 alone and 2.9 with all SMs full; a unit of tiles 3 beside 1.5 a tile (of a share: rounded down), and 1.7 to
+// start with.  Measured as tiles and without: 1 x 8 heads x 77 keys, 64 rows 6.9, so 3.6; 8 x 8 x 300, 16 rows 9.2, so 6.2, 48 rows
+// 9.2, not 13.3; 64 x 64 x 50, 16 rows 117, so 101, 32 rows 119, not 190.  Next to the border it errs by up to 4 us for tiles, where
+// shares take about 3 more than it expects (1 x 8 x 600, 100 rows 12.3, not 8.7) or lengths are ragged (8 x 32 x up to 300, 16 rows
+// 15.4, not 12.3).
 inline Cut cut_of(int B, int H, int Sq, int Sk, bool ragged, int sms) {
   const Cut few = few_cut(B, H, Sq, Sk, ragged, sms);
   if (Sq <= kFewRows) return few;
